@@ -30,6 +30,7 @@ __all__ = [
     "h32_q4_0_blocks_to_planes", "h32_q4_0_planes_to_blocks",
     "h32_gemm_tc_workspace_bytes", "h32_gemm_tc_schedule",
     "q4_0_x_q4_gemm_tc_noalloc", "q4_0_x_q8_gemm_tc_noalloc",
+    "h32_add_rms_norm_quantize",
 ]
 
 
@@ -92,6 +93,9 @@ _SIGS = {
                                          _I64, _P, _I64, _P, _P]),
     "h32_moe_route": (_INT, [_P, _I64, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P]),
     "h32_moe_combine": (_INT, [_P, _I64, _I64, _P, _P, _I64, _I32, _I64, _P, _I64, _P]),
+    "h32_add_rms_norm_quantize": (_INT, [_P, _INT, _I64, _P, _INT, _I64, _P, _INT, ctypes.c_float,
+                                         _I64, _I64, _P, _I64, _P, _INT, _I64, _I32, _INT, _P, _P,
+                                         _I64, _P]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGS)
 
@@ -166,6 +170,15 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _raw(t):
+    return None if t is None else t.data_ptr()
+
+
+def _pitch(t):
+    """Row pitch of a checked 2-D tensor (0 for None)."""
+    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
 def _check(fn: str, st: int):
     if st != H32_OK:
         raise H32Error(fn, st)
@@ -228,6 +241,25 @@ def _same_gpu(*named):
             dev = t.device
         elif t.device != dev:
             raise ValueError(f"{name} is on {t.device}, the call's other tensors on {dev}")
+
+
+def _on_stream(dev, stream, body):
+    """body(stream handle) with `dev` current and torch allocating for `stream` (None:
+    the device's current stream; a torch stream, or a raw handle), so that outputs
+    allocated inside belong to the stream the kernels run on."""
+    torch = _torch()
+    if stream is None:
+        if torch.cuda.current_device() == dev.index:
+            return body(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(dev):
+            return body(torch.cuda.current_stream().cuda_stream)
+    if not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(int(stream), device=dev) if int(stream)
+                  else torch.cuda.default_stream(dev))
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the call's tensors on {dev}")
+    with torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
 
 
 def _act_dtype(x, name="x"):
@@ -853,6 +885,87 @@ def h32_moe_combine(y, row_of, topk_w, out=None, stream=None):
     return out
 
 
+ACT_FORMS = {"q4": 0, "q8": 1, "q4_tc": 2, "q8_tc": 3, "q4_tc_e5m2": 4}
+# code bytes per value, in halves
+_FORM_HALF_BYTES = {"q4": 1, "q8": 2, "q4_tc": 2, "q8_tc": 4, "q4_tc_e5m2": 2}
+
+
+def h32_add_rms_norm_quantize(x, weight, residual=None, eps=1e-6, form="q4_tc", rotate=True,
+                              residual_out=None, norm_out=None, xq=None, xd=None, stream=None):
+    """Residual addition, root-mean-square norm and the activation quantizer in one pass.
+
+    x [M][K] bf16/fp32, weight [K] bf16/fp32, residual [M][K] bf16/fp32 or None ->
+    (xq, xd, residual_out, norm_out): h = x + residual rounded to the residual's type,
+    n = h / sqrt(mean(h^2) + eps) * weight, and n rotated and quantized as by the
+    quantizer of `form` ("q4", "q8", "q4_tc", "q8_tc", "q4_tc_e5m2": its xq and xd or
+    xdt layouts; None: no quantization, xq = xd = None).
+    residual_out: None allocates it (with a residual), False leaves h unstored, a
+    tensor (residual or x themselves allowed) receives it.  norm_out: None (not
+    returned), a dtype (torch.bfloat16, torch.float32) or a tensor for n."""
+    torch = _torch()
+    bf16, f32 = torch.bfloat16, torch.float32
+    either = (bf16, f32)
+    _need(x, "x", either, (_ge(0), _ge(0)), pitched=True)
+    M, K = x.shape
+    _need(weight, "weight", either, (K,))
+    if form is not None and form not in ACT_FORMS:
+        raise ValueError(f"form must be None or one of {', '.join(ACT_FORMS)}")
+    if residual is not None:
+        _need(residual, "residual", either, (M, K), pitched=True)
+    elif residual_out is not None and residual_out is not False:
+        raise ValueError("residual_out needs a residual")
+    if form is None and norm_out is None:
+        raise ValueError("form=None needs norm_out")
+    if residual_out is not None and residual_out is not False:
+        _need(residual_out, "residual_out", (residual.dtype,), (_ge(M), _ge(K)), pitched=True)
+    if isinstance(norm_out, torch.dtype):
+        if norm_out not in either:
+            raise ValueError("norm_out must be bf16 or fp32")
+    elif norm_out is not None:
+        _need(norm_out, "norm_out", either, (_ge(M), _ge(K)), pitched=True)
+    tc = form is not None and form.endswith(("_tc", "_e5m2"))
+    qshape = None
+    if form is None:
+        if xq is not None or xd is not None:
+            raise ValueError("form=None writes no xq or xd")
+    else:
+        qshape = (M, K * _FORM_HALF_BYTES[form] // 2)
+        if xq is not None:
+            _need(xq, "xq", (torch.int8, torch.uint8) if form == "q8" else (torch.uint8,),
+                  (_ge(M), qshape[1]))
+        if xd is not None:
+            _need(xd, "xd", (f32,), (_ge(K // 32), _ge(M)) if tc else (_ge(M), K // 32))
+    keep = residual_out if isinstance(residual_out, torch.Tensor) else None
+    nrm = norm_out if isinstance(norm_out, torch.Tensor) else None
+    _same_gpu(("x", x), ("weight", weight), ("residual", residual), ("residual_out", keep),
+              ("norm_out", nrm), ("xq", xq), ("xd", xd))
+    dev = x.device
+
+    def body(raw, res_out=keep, nrm=nrm, xq=xq, xd=xd):
+        if residual is not None and residual_out is None:
+            res_out = torch.empty((M, K), dtype=residual.dtype, device=dev)
+        if nrm is None and norm_out is not None:
+            nrm = torch.empty((M, K), dtype=norm_out, device=dev)
+        if form is not None:
+            if xq is None:
+                xq = torch.empty(qshape, dtype=torch.int8 if form == "q8" else torch.uint8,
+                                 device=dev)
+            if xd is None:
+                xd = torch.empty((K // 32, _round4(M)) if tc else (M, K // 32), dtype=f32,
+                                 device=dev)
+        st = lib().h32_add_rms_norm_quantize(
+            x.data_ptr(), x.dtype == bf16, _rows(x, "x"),
+            _raw(residual), residual is not None and residual.dtype == bf16, _pitch(residual),
+            weight.data_ptr(), weight.dtype == bf16, eps, M, K,
+            _raw(res_out), _pitch(res_out), _raw(nrm), nrm is not None and nrm.dtype == bf16,
+            _pitch(nrm), ACT_FORMS.get(form, 0), _rot_arg(rotate), _raw(xq), _raw(xd),
+            xd.shape[1] if tc else 0, raw)
+        _check("h32_add_rms_norm_quantize", st)
+        return xq, xd, res_out, nrm
+
+    return _on_stream(dev, stream, body)
+
+
 # --------------------------------------------------------------------------
 # optional per-call tracing (H32_TRACE=1: device time per call; H32_TRACE=hash:
 # also a hash of every output), off by default; see trace.py
@@ -868,7 +981,7 @@ _COMPUTE_CALLS = (
     "h32_quantize_act_q4_tc_e5m2", "h32_quantize_act_q4_tc_e5m2_gather",
     "q4_0_x_q4_gemm_tc_widen", "q4_0_x_q4_gemm_tc_widen_experts",
     "h32_q4_0_blocks_to_planes", "h32_q4_0_planes_to_blocks",
-    "q4_0_x_q4_gemm_tc_noalloc", "q4_0_x_q8_gemm_tc_noalloc",
+    "q4_0_x_q4_gemm_tc_noalloc", "q4_0_x_q8_gemm_tc_noalloc", "h32_add_rms_norm_quantize",
 )
 for _name in _COMPUTE_CALLS:
     globals()[_name] = _trace.traced(_name)(globals()[_name])

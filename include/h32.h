@@ -61,6 +61,16 @@ typedef enum h32_in_dtype {
     H32_IN_BF16 = 1  /* bf16 activations, widened to fp32 exactly            */
 } h32_in_dtype;
 
+/* the layouts in which a quantizer writes codes and scales (h32_quantize_act_q4,
+ * _q8, _q4_tc, _q8_tc and _q4_tc_e5m2 below) */
+typedef enum h32_act_form {
+    H32_ACT_Q4 = 0,         /* xq [M][K/2] nibbles, xd [M][K/32]                 */
+    H32_ACT_Q8 = 1,         /* xq [M][K] int8, xd [M][K/32]                      */
+    H32_ACT_Q4_TC = 2,      /* xq [M][K] e4m3 bytes, xd [K/32][ldxd]             */
+    H32_ACT_Q8_TC = 3,      /* xq [M][2K] e4m3 bytes (16 h, l), xd [K/32][ldxd]  */
+    H32_ACT_Q4_TC_E5M2 = 4  /* xq [M][K] e5m2 bytes, xd [K/32][ldxd]             */
+} h32_act_form;
+
 /*
  * Rotate and quantize activations to 4-bit codes (the activation quantizer of
  * "The rotation" / "Prompt processing: 4-bit activations, rotated first").
@@ -514,6 +524,42 @@ h32_status h32_moe_route(const float *logits, int64_t T, int32_t E, int64_t ldl,
 h32_status h32_moe_combine(const float *y, int64_t R, int64_t ldy, const int32_t *row_of,
                            const float *topk_w, int64_t T, int32_t k, int64_t H, float *out,
                            int64_t ldo, void *stream);
+
+/*
+ * What runs between two products of a decoder layer, in one pass: the residual
+ * addition, the root-mean-square norm, and the next product's activation
+ * quantizer ("The rotation": every projection's input is rotated and quantized).
+ * Per row:
+ *   h = x + residual in fp32, rounded to the residual's type (h = x without one);
+ *   S = sum of h^2 in fp32: fma over each 32-block from +0, groups of 32 blocks
+ *       by the xor tree of strides 1, 2, 4, 8, 16 (absent blocks 0), then the
+ *       groups in order;
+ *   r = 1 / sqrt(S / K + eps), every step rounded to fp32; n = (h r) w, two fp32
+ *       roundings; where S overflows fp32 the row is scaled by 2^-80 first;
+ *   then n is rotated and quantized exactly as by the quantizer of `form`.
+ * Bit-identical to that sequential evaluation.
+ *   x            [M][ldx] of type x_dt
+ *   residual     nullable [M][ldr] of type res_dt
+ *   w            [K] norm weights of type w_dt
+ *   eps          > 0, finite
+ *   residual_out nullable (null without a residual) [M][ldro] out, res_dt: h
+ *   norm_out     nullable [M][ldn] out, norm_dt: n rounded once (for a router, or
+ *                for h32_quantize_act_q4_tc_gather)
+ *   form         an h32_act_form: the layout of xq, xd and ldxd (used by the _TC
+ *                forms: >= M, a multiple of 4; entries m >= M are left untouched).
+ *                xq and xd both null: norm_out alone (then it must be given)
+ *   rotate       as for h32_quantize_act_q4
+ * residual_out may be residual or x itself, and norm_out may be x or residual
+ * itself (same type and pitch, element for element); any other overlap of
+ * outputs and inputs is undefined.  Requires K % 32 == 0 and K <= 32768.
+ * Non-finite inputs are outside the contract, as for the quantizers.
+ */
+h32_status h32_add_rms_norm_quantize(const void *x, h32_in_dtype x_dt, int64_t ldx,
+                                     const void *residual, h32_in_dtype res_dt, int64_t ldr,
+                                     const void *w, h32_in_dtype w_dt, float eps, int64_t M,
+                                     int64_t K, void *residual_out, int64_t ldro, void *norm_out,
+                                     h32_in_dtype norm_dt, int64_t ldn, int32_t form, int rotate,
+                                     void *xq, float *xd, int64_t ldxd, void *stream);
 
 /*
  * Synchronize `stream`, then report and clear the device status words that

@@ -68,6 +68,7 @@ def _load():
                                            _P, _P, _P, _P, _P],
                 "o_moe_route": [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P],
                 "o_moe_combine": [_P, _I64, _P, _P, _I64, _I64, _I64, _P],
+                "o_add_rms_norm": [_P, _P, ctypes.c_int, _P, ctypes.c_float, _I64, _I64, _P, _P],
             }
             for name, args in sigs.items():
                 fn = getattr(lib, name)
@@ -336,6 +337,25 @@ def moe_combine(y: np.ndarray, row_of: np.ndarray, topk_w: np.ndarray) -> np.nda
     out = np.empty((T, H), np.float32)
     _load().o_moe_combine(_ptr(y), H, _ptr(row_of), _ptr(topk_w), T, k, H, _ptr(out))
     return out
+
+
+# --------------------------------------------------------------------------
+# residual addition and root-mean-square norm in front of the quantizers
+# --------------------------------------------------------------------------
+def add_rms_norm(x: np.ndarray, w: np.ndarray, residual: np.ndarray | None = None,
+                 eps: float = 1e-6):
+    """x, residual [M][K] (fp32, or bf16 as uint16 bits), w [K] -> (h, n) fp32 [M][K]:
+    h = x + residual in fp32, rounded to bf16 where the residual is bf16;
+    n = h / sqrt(mean(h^2) + eps) * w, every step rounded to fp32, the sum in the
+    order the C file states.  Quantize n with quantize_act_q4 / _q8."""
+    res_bf16 = residual is not None and residual.dtype == np.uint16
+    xf, wf = _widen(x), _widen(w)
+    rf = None if residual is None else _widen(residual)
+    M, K = xf.shape
+    assert K % 32 == 0
+    h, n = np.empty((M, K), np.float32), np.empty((M, K), np.float32)
+    _load().o_add_rms_norm(_ptr(xf), _ptr(rf), int(res_bf16), _ptr(wf), eps, M, K, _ptr(h), _ptr(n))
+    return h, n
 
 
 # --------------------------------------------------------------------------

@@ -591,3 +591,71 @@ void o_moe_combine(const float *y, int64_t ldy, const int32_t *row_of, const flo
             out[t * H + h] = acc;
         }
 }
+
+/* ------------------------------------------------------------------------ */
+/* Residual addition and root-mean-square norm in front of the quantizer     */
+/* ------------------------------------------------------------------------ */
+
+/* fp32 -> the nearest bf16 (ties to even), widened again */
+static float round_bf16(float f)
+{
+    uint32_t u;
+    memcpy(&u, &f, 4);
+    u = (u + 0x7FFFu + ((u >> 16) & 1u)) & 0xFFFF0000u;
+    memcpy(&f, &u, 4);
+    return f;
+}
+
+/* sum of squares of a row: fma over each 32-block from +0, then groups of 32
+ * blocks by the xor tree of strides 1 .. 16 (absent blocks 0), then the groups
+ * in order */
+static float row_sum_squares(const float *h, int64_t K)
+{
+    float total = 0.0f;
+    const int64_t nb = K / 32;
+    for (int64_t g = 0; g < nb; g += 32) {
+        float part[32] = {0.0f};
+        for (int64_t b = 0; b < 32 && g + b < nb; ++b) {
+            float acc = 0.0f;
+            for (int i = 0; i < 32; ++i) {
+                const float v = h[(g + b) * 32 + i];
+                acc = fmaf(v, v, acc);
+            }
+            part[b] = acc;
+        }
+        for (int o = 1; o < 32; o <<= 1) {
+            float next[32];
+            for (int b = 0; b < 32; ++b) next[b] = part[b] + part[b ^ o];
+            memcpy(part, next, sizeof part);
+        }
+        total = g == 0 ? part[0] : total + part[0];
+    }
+    return total;
+}
+
+/* x, res [M][K] fp32 (res may be null), w [K] -> h [M][K] (rounded to bf16
+ * where res_bf16 is set and there is a residual), n [M][K] = the normed rows */
+void o_add_rms_norm(const float *x, const float *res, int res_bf16, const float *w, float eps,
+                    int64_t M, int64_t K, float *h, float *n)
+{
+    for (int64_t m = 0; m < M; ++m) {
+        float *hr = h + m * K, *nr = n + m * K;
+        for (int64_t i = 0; i < K; ++i) {
+            hr[i] = res ? x[m * K + i] + res[m * K + i] : x[m * K + i];
+            if (res && res_bf16) hr[i] = round_bf16(hr[i]);
+            nr[i] = hr[i];
+        }
+        float s = row_sum_squares(nr, K);
+        float r;
+        if (s < INFINITY) {
+            r = 1.0f / sqrtf(s / (float)K + eps);
+        } else {
+            for (int64_t i = 0; i < K; ++i) nr[i] = nr[i] * 0x1p-80f;
+            r = 1.0f / sqrtf(row_sum_squares(nr, K) / (float)K);
+        }
+        for (int64_t i = 0; i < K; ++i) {
+            const float t = nr[i] * r;
+            nr[i] = t * w[i];
+        }
+    }
+}

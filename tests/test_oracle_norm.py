@@ -1,0 +1,66 @@
+"""Pins for the oracle's residual addition and root-mean-square norm, against
+float64 and closed forms (the norm itself; its quantized output is the
+quantizers', pinned on their own)."""
+import numpy as np
+import pytest
+
+import oracle
+from hadamard_rotated_bit_gb300 import workloads as wl
+
+U = 2.0 ** -24   # half a step of fp32
+
+
+@pytest.mark.parametrize("M,K", [(1, 32), (3, 96), (5, 1024), (2, 1056), (4, 5120), (2, 17408)])
+def test_norm_against_float64(M, K):
+    """n within the forward bound: a 32-term fma chain and the trees above it keep
+    the sum of squares (all positive) within (32 + 5 + K/1024 + 1) half steps, the
+    square root halves that, and divide, add, sqrt, divide and two products add
+    one half step each (the first two halved too)."""
+    r = np.random.default_rng(M * K)
+    x = (r.standard_normal((M, K)) * 3).astype(np.float32)
+    res = (r.standard_normal((M, K)) * 2).astype(np.float32)
+    w = (1 + 0.1 * r.standard_normal(K)).astype(np.float32)
+    h, n = oracle.add_rms_norm(x, w, res, 1e-6)
+    assert np.array_equal(h, x + res)
+    h64 = h.astype(np.float64)
+    want = h64 / np.sqrt((h64 ** 2).mean(1, keepdims=True) + np.float64(np.float32(1e-6))) * w
+    bound = ((32 + 5 + K / 1024 + 1 + 2) / 2 + 4) * U * (1 + 1e-4)
+    assert np.all(np.abs(n - want) <= bound * np.abs(want))
+
+
+def test_bf16_residual_is_rounded_before_the_norm():
+    r = np.random.default_rng(1)
+    x = r.standard_normal((4, 256)).astype(np.float32)
+    res = wl.f32_to_bf16_bits(r.standard_normal((4, 256)).astype(np.float32))
+    h, n = oracle.add_rms_norm(x, np.ones(256, np.float32), res)
+    stored = wl.bf16_bits_to_f32(wl.f32_to_bf16_bits(x + wl.bf16_bits_to_f32(res)))
+    assert np.array_equal(h, stored) and not np.array_equal(h, x + wl.bf16_bits_to_f32(res))
+    _, n2 = oracle.add_rms_norm(stored, np.ones(256, np.float32), None)
+    assert np.array_equal(n, n2)
+
+
+def test_closed_forms():
+    one = np.ones(64, np.float32)
+    # constant rows: mean square exact, r = 1/c
+    h, n = oracle.add_rms_norm(np.full((1, 64), 4.0, np.float32), one, None, 1e-30)
+    assert np.all(n == 1.0)
+    # zero rows: n = 0 whatever r = 1/sqrt(eps) is
+    _, n = oracle.add_rms_norm(np.zeros((1, 64), np.float32), one, None, 1e-30)
+    assert np.all(n == 0.0)
+    # a sum of squares above fp32's range: the row is scaled first
+    big = np.full((1, 64), 2.0 ** 100, np.float32)
+    big[0, 1] = -(2.0 ** 100)
+    _, n = oracle.add_rms_norm(big, one, None, 1e-6)
+    assert n[0, 0] == 1.0 and n[0, 1] == -1.0
+
+
+def test_sum_order_is_the_stated_one():
+    """1 + 2^-24 terms are lost one by one but kept when their group is summed first."""
+    x = np.zeros((1, 64), np.float32)
+    x[0, 0] = 1.0
+    x[0, 1:32] = 2.0 ** -13        # squares 2^-26 (a quarter step): lost in the chain of block 0
+    x[0, 32:64] = 2.0 ** -13       # block 1 sums to 2^-21, then joins
+    _, n = oracle.add_rms_norm(x, np.ones(64, np.float32), None, 1e-30)
+    s = np.float32(1.0) + np.float32(2.0 ** -21)
+    r = np.float32(1) / np.sqrt(s / np.float32(64))
+    assert n[0, 0] == r
