@@ -115,6 +115,8 @@ class H32Error(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(library_path):
@@ -145,15 +147,29 @@ def h32_set_wait_limit(polls: int) -> None:
 # --------------------------------------------------------------------------
 # marshalling helpers
 # --------------------------------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _current_raw_stream(index):
+    """Handle of the current stream of CUDA device `index` (0.1 us; building the
+    torch.cuda.Stream object for it takes 3)."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw else torch.cuda.current_stream(index).cuda_stream
 
 
 def _stream(stream):
     torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return ctypes.c_void_p(_current_raw_stream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -215,14 +231,20 @@ def _need(t, name, dtypes, shape, pitched=False):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected " + " or ".join(map(str, dtypes)))
-    want = "(" + ", ".join((">=" if isinstance(d, _AtLeast) else "") + str(int(d))
-                           for d in shape) + ")"
-    if t.dim() != len(shape) or any(h < d or (not isinstance(d, _AtLeast) and h != d)
-                                    for h, d in zip(t.shape, shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {want}")
+    got = t.shape
+    ok = len(got) == len(shape)
+    if ok:
+        for h, d in zip(got, shape):
+            if h != d and (h < d or not isinstance(d, _AtLeast)):
+                ok = False
+    if not ok:
+        want = "(" + ", ".join((">=" if isinstance(d, _AtLeast) else "") + str(int(d))
+                               for d in shape) + ")"
+        raise ValueError(f"{name}: shape {tuple(got)}, expected {want}")
     if pitched:
-        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or \
-                (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        if not (len(got) == 2 and t.is_contiguous()) and \
+                (len(got) != 2 or (got[1] > 1 and t.stride(1) != 1) or
+                 (got[0] > 1 and t.stride(0) < got[1])):
             raise ValueError(f"{name} must be 2-D with contiguous, non-overlapping rows")
     elif not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -250,9 +272,9 @@ def _on_stream(dev, stream, body):
     torch = _torch()
     if stream is None:
         if torch.cuda.current_device() == dev.index:
-            return body(torch.cuda.current_stream().cuda_stream)
+            return body(_current_raw_stream(dev.index))
         with torch.cuda.device(dev):
-            return body(torch.cuda.current_stream().cuda_stream)
+            return body(_current_raw_stream(dev.index))
     if not hasattr(stream, "cuda_stream"):
         stream = (torch.cuda.ExternalStream(int(stream), device=dev) if int(stream)
                   else torch.cuda.default_stream(dev))
