@@ -30,7 +30,7 @@ __all__ = [
     "h32_q4_0_blocks_to_planes", "h32_q4_0_planes_to_blocks",
     "h32_gemm_tc_workspace_bytes", "h32_gemm_tc_schedule",
     "q4_0_x_q4_gemm_tc_noalloc", "q4_0_x_q8_gemm_tc_noalloc",
-    "h32_add_rms_norm_quantize",
+    "h32_add_rms_norm_quantize", "h32_moe_route_scored",
 ]
 
 
@@ -93,6 +93,8 @@ _SIGS = {
                                          _I64, _P, _I64, _P, _P]),
     "h32_moe_route": (_INT, [_P, _I64, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P]),
     "h32_moe_combine": (_INT, [_P, _I64, _I64, _P, _P, _I64, _I32, _I64, _P, _I64, _P]),
+    "h32_moe_route_scored": (_INT, [_P, _I64, _I32, _I64, _I32, _P, _I32, _I32, _I32, _I32, _I32,
+                                    ctypes.c_float, _P, _P, _P, _P, _P, _P]),
     "h32_add_rms_norm_quantize": (_INT, [_P, _INT, _I64, _P, _INT, _I64, _P, _INT, ctypes.c_float,
                                          _I64, _I64, _P, _I64, _P, _INT, _I64, _I32, _INT, _P, _P,
                                          _I64, _P]),
@@ -907,6 +909,68 @@ def h32_moe_combine(y, row_of, topk_w, out=None, stream=None):
     return out
 
 
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def h32_moe_route_scored(logits, k, score="softmax", bias=None, n_group=1, topk_group=1,
+                         group_top=1, renormalize=True, scale=1.0, topk_id=None, topk_w=None,
+                         expert_off=None, row_idx=None, row_of=None, stream=None):
+    """Router by scores: logits [T][E] fp32, bias [E] fp32 or None -> the outputs of
+    h32_moe_route (topk_id, topk_w, expert_off, row_idx, row_of).
+
+    Scores are the softmax or the sigmoids of the logits, keys = scores + bias; of the
+    n_group groups of consecutive experts the topk_group with the largest sums of their
+    group_top (1 or 2) best keys stay, and the k experts of largest key in them are
+    chosen (ties: lower id).  Weights are scale * score, with `renormalize` divided by
+    the sum over the choices."""
+    torch = _torch()
+    i32, f32 = (torch.int32,), (torch.float32,)
+    _need(logits, "logits", f32, (_ge(0), _ge(0)), pitched=True)
+    T, E = logits.shape
+    k, n_group, topk_group, group_top = int(k), int(n_group), int(topk_group), int(group_top)
+    if score not in ROUTE_SCORES:
+        raise ValueError(f"score must be one of {', '.join(ROUTE_SCORES)}")
+    if k < 1:
+        raise ValueError("k must be at least 1")
+    if bias is not None:
+        _need(bias, "bias", f32, (E,))
+    if topk_id is not None:
+        _need(topk_id, "topk_id", i32, (_ge(T), k))
+    if topk_w is not None:
+        _need(topk_w, "topk_w", f32, (_ge(T), k))
+    if expert_off is not None:
+        _need(expert_off, "expert_off", i32, (_ge(E + 1),))
+    if row_idx is not None:
+        _need(row_idx, "row_idx", i32, (_ge(T * k),))
+    if row_of is not None:
+        _need(row_of, "row_of", i32, (_ge(T), k))
+    _same_gpu(("logits", logits), ("bias", bias), ("topk_id", topk_id), ("topk_w", topk_w),
+              ("expert_off", expert_off), ("row_idx", row_idx), ("row_of", row_of))
+    dev = logits.device
+
+    def body(raw, topk_id=topk_id, topk_w=topk_w, expert_off=expert_off, row_idx=row_idx,
+             row_of=row_of):
+        if topk_id is None:
+            topk_id = torch.empty((T, k), dtype=torch.int32, device=dev)
+        if topk_w is None:
+            topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        if expert_off is None:
+            expert_off = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        if row_idx is None:
+            row_idx = torch.empty(T * k, dtype=torch.int32, device=dev)
+        if row_of is None:
+            row_of = torch.empty((T, k), dtype=torch.int32, device=dev)
+        st = lib().h32_moe_route_scored(
+            logits.data_ptr(), T, E, _pitch(logits) if T > 0 else E, ROUTE_SCORES[score],
+            _raw(bias), n_group, topk_group, group_top, k, bool(renormalize), scale,
+            topk_id.data_ptr(), topk_w.data_ptr(), expert_off.data_ptr(), row_idx.data_ptr(),
+            row_of.data_ptr(), raw)
+        _check("h32_moe_route_scored", st)
+        return topk_id, topk_w, expert_off, row_idx, row_of
+
+    return _on_stream(dev, stream, body)
+
+
 ACT_FORMS = {"q4": 0, "q8": 1, "q4_tc": 2, "q8_tc": 3, "q4_tc_e5m2": 4}
 # code bytes per value, in halves
 _FORM_HALF_BYTES = {"q4": 1, "q8": 2, "q4_tc": 2, "q8_tc": 4, "q4_tc_e5m2": 2}
@@ -1004,6 +1068,7 @@ _COMPUTE_CALLS = (
     "q4_0_x_q4_gemm_tc_widen", "q4_0_x_q4_gemm_tc_widen_experts",
     "h32_q4_0_blocks_to_planes", "h32_q4_0_planes_to_blocks",
     "q4_0_x_q4_gemm_tc_noalloc", "q4_0_x_q8_gemm_tc_noalloc", "h32_add_rms_norm_quantize",
+    "h32_moe_route_scored",
 )
 for _name in _COMPUTE_CALLS:
     globals()[_name] = _trace.traced(_name)(globals()[_name])

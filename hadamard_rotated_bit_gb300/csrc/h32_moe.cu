@@ -21,14 +21,13 @@
 //   combine_kernel      one block per token (x) and 128 float4 columns (y): 16-byte
 //                       loads of the token's k rows, fma in choice order
 #include "h32_common.cuh"
+#include "h32_moe.cuh"
 
 namespace h32 {
 namespace {
 
 __device__ uint32_t g_moe_status;   // kStatusGuard: a combine row index out of range
 
-constexpr int kMaxE = 1024;         // experts a router call handles
-constexpr int kMaxK = 32;           // choices per token (one lane each)
 constexpr int kTopkWarps = 8;       // tokens per block of route_topk_kernel
 constexpr int kGroupThreads = 1024;
 constexpr int kCombineThreads = 128;   // one float4 column each
@@ -238,6 +237,13 @@ __global__ void __launch_bounds__(kCombineThreads)
 
 }  // namespace
 
+// with T = 0 this writes all-zero offsets
+cudaError_t launch_route_group(const int32_t *topk_id, int T, int E, int k, int32_t *expert_off,
+                               int32_t *row_idx, int32_t *row_of, cudaStream_t s) {
+    return launch_pdl(route_group_kernel, dim3(E), dim3(kGroupThreads), 0, s, topk_id, T, E, k,
+                      expert_off, row_idx, row_of);
+}
+
 __device__ uint32_t g_moe_status_taken;
 __global__ void take_g_moe_status() { g_moe_status_taken = atomicExch(&g_moe_status, 0u); }
 
@@ -288,11 +294,7 @@ extern "C" h32_status h32_moe_route(const float *logits, int64_t T, int32_t E, i
             e1 = launch_pdl(route_topk_kernel<32>, grid, block, 0, s, logits, t32, ei, ldl, ki, topk_id, topk_w);
         if (e1 != cudaSuccess) return launch_status(e1);
     }
-    // with T = 0 this writes all-zero offsets
-    const cudaError_t e2 = launch_pdl(route_group_kernel, dim3(E), dim3(kGroupThreads), 0, s,
-                                      static_cast<const int32_t *>(topk_id), t32,
-                                      static_cast<int>(E), static_cast<int>(k), expert_off,
-                                      row_idx, row_of);
+    const cudaError_t e2 = launch_route_group(topk_id, t32, E, k, expert_off, row_idx, row_of, s);
     return launch_status(e2 != cudaSuccess ? e2 : cudaGetLastError());
 }
 

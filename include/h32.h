@@ -509,6 +509,47 @@ h32_status h32_moe_route(const float *logits, int64_t T, int32_t E, int64_t ldl,
                          int32_t *topk_id, float *topk_w, int32_t *expert_off, int32_t *row_idx,
                          int32_t *row_of, void *stream);
 
+typedef enum h32_score {
+    H32_SCORE_SOFTMAX = 0,  /* softmax over all E logits */
+    H32_SCORE_SIGMOID = 1   /* 1 / (1 + exp(-l))         */
+} h32_score;
+
+/*
+ * Routing by scores, for mixture-of-experts layers whose router does more than
+ * h32_moe_route: sigmoid scores, a bias that balances the experts' load, groups
+ * of experts, weights that need not be renormalised.  Per token:
+ *   - scores s_e: the softmax over the E logits, or their sigmoids;
+ *   - keys s_e + bias_e (bias null: the scores);
+ *   - the E experts form n_group groups of E / n_group consecutive ids; a group
+ *     scores the sum of its group_top (1 or 2) largest keys (those above -inf;
+ *     -inf where it has none), and the topk_group groups of largest score stay,
+ *     ties to the lower group;
+ *   - the k experts of largest key in those groups are chosen, ties to the lower
+ *     id, listed by decreasing key;
+ *   - choice j weighs scale * s_j (the score, without the bias), or with
+ *     `renormalize` scale * s_j / sum of the k chosen scores, in fp32;
+ * then the rows are grouped by expert as by h32_moe_route, with the same outputs
+ * topk_id, topk_w, expert_off, row_idx, row_of (and their alignment).
+ * Keys and group scores are ordered by their values in double precision, so ids,
+ * offsets and row maps do not depend on fp32 rounding; the weights are within a
+ * few ulps.  Deterministic.
+ * Logits that are not finite: a -inf logit masks its expert (score 0, key -inf
+ * whatever the bias); a NaN logit or bias ranks below it; +inf logits share the
+ * softmax equally.  Masked experts are chosen only when fewer than k others are
+ * left, and weigh 0; where every choice is masked, `renormalize` gives equal
+ * weights.
+ * Requires 1 <= E <= 1024, 1 <= n_group <= 32 dividing E, 1 <= topk_group <=
+ * n_group, 1 <= k <= min(32, topk_group E / n_group), T k < 2^31, a finite scale;
+ * logits (row pitch ldl >= E) and bias [E] 4-byte aligned.  T = 0 writes all-zero
+ * offsets.
+ */
+h32_status h32_moe_route_scored(const float *logits, int64_t T, int32_t E, int64_t ldl,
+                                int32_t score, const float *bias, int32_t n_group,
+                                int32_t topk_group, int32_t group_top, int32_t k,
+                                int32_t renormalize, float scale, int32_t *topk_id, float *topk_w,
+                                int32_t *expert_off, int32_t *row_idx, int32_t *row_of,
+                                void *stream);
+
 /*
  * The weighted combine after the expert GEMMs: the k expert outputs of each
  * token, in grouped order, added back in token order:

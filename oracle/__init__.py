@@ -326,6 +326,65 @@ def moe_route(logits: np.ndarray, k: int):
     return topk_id, topk_w, off, row_idx, row_of
 
 
+def moe_route_scored(logits: np.ndarray, k: int, score: str = "softmax",
+                     bias: np.ndarray | None = None, n_group: int = 1, topk_group: int = 1,
+                     group_top: int = 1, renormalize: bool = True, scale: float = 1.0):
+    """Routing by scores in float64, token by token as the rule is stated: returns the
+    five outputs of moe_route, the weights in float64.
+
+    score s = softmax or sigmoid of the logits (0 for a NaN or -inf logit); key = s +
+    bias (-inf for a -inf logit, NaN for a NaN logit or bias); a group scores the sum
+    of its group_top largest keys above -inf; the topk_group best groups stay (ties:
+    lower group); the k largest keys in them (NaN below -inf; ties: lower id)."""
+    logits = _c(logits, np.float32)
+    T, E = logits.shape
+    size = E // n_group
+    ids = np.empty((T, k), np.int32)
+    w = np.empty((T, k), np.float64)
+    with np.errstate(over="ignore", invalid="ignore", under="ignore"):
+        for t in range(T):
+            l = logits[t].astype(np.float64)
+            masked = np.isnan(l) | (l == -np.inf)
+            if score == "sigmoid":
+                s = 1.0 / (1.0 + np.exp(-l))
+            else:
+                top = l[~masked].max() if (~masked).any() else 0.0
+                s = (l == np.inf).astype(np.float64) if top == np.inf else np.exp(l - top)
+                s = np.where(masked, 0.0, s)
+                s = s / s.sum() if s.sum() > 0 else s
+            s = np.where(masked, 0.0, s)
+            b = np.zeros(E) if bias is None else np.asarray(bias, np.float32).astype(np.float64)
+            key = np.where(l == -np.inf, -np.inf, s + b)
+            key = np.where(np.isnan(l) | np.isnan(b), np.nan, key)
+            gs = []
+            for g in range(n_group):
+                kg = key[g * size:(g + 1) * size]
+                kg = np.sort(kg[kg > -np.inf])[::-1][:group_top]
+                gs.append(kg.sum() if kg.size else -np.inf)
+            stay = sorted(range(n_group), key=lambda g: (-gs[g], g))[:topk_group]
+            cand = [e for e in range(E) if e // size in stay]
+            cand.sort(key=lambda e: (np.isnan(key[e]), 0.0 if np.isnan(key[e]) else -key[e], e))
+            ids[t] = cand[:k]
+            c = s[ids[t]]
+            if renormalize:
+                lc = l[ids[t]]
+                ok = ~masked[ids[t]]
+                if not ok.any():
+                    c = np.full(k, 1.0 / k)
+                elif c.sum() < 1e-200:     # ratios of scores that underflow together
+                    c = np.where(ok, np.exp(lc - lc[ok].max()), 0.0)
+                    c = c / c.sum()
+                else:
+                    c = c / c.sum()
+            w[t] = c * scale
+    tok = np.repeat(np.arange(T), k)
+    order = np.lexsort((tok, ids.reshape(-1)))
+    row_of = np.empty(T * k, np.int32)
+    row_of[order] = np.arange(T * k, dtype=np.int32)
+    off = np.concatenate(([0], np.cumsum(np.bincount(ids.reshape(-1), minlength=E)))).astype(np.int32)
+    return ids, w, off, tok[order].astype(np.int32), row_of.reshape(T, k)
+
+
 def moe_combine(y: np.ndarray, row_of: np.ndarray, topk_w: np.ndarray) -> np.ndarray:
     """y [R][H] fp32 (grouped rows) -> out [T][H]: sum over the token's k
     choices in order of w_j * y[row_of[t][j]], fp32 fma from +0."""

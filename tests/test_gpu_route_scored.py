@@ -1,0 +1,192 @@
+"""GPU parity of h32_moe_route_scored against a float64 evaluation of its rule.
+
+Ids, offsets and row maps are exact (near ties included: the rule orders keys by
+their values in double).  Weights: relative to the exact value within
+  - a score: expf within 2 ulp (4 half steps), the argument's rounding |l - lmax|
+    half steps (at most 104, softmax), 1 + or the sum over E in trees (up to 37 adds
+    of terms with 4 + |d| half steps each: below 37 + 4 + 104), one divide and one
+    product: below 260 half steps of 2^-24;
+  - renormalised: the exps of the choices (4 + |d| with |d| <= 104), their sum over
+    k <= 32 (31 more), one divide, one product: below 260 as well;
+floor 2^-126 * scale where a weight underflows."""
+import numpy as np
+import pytest
+
+import oracle
+from tests._gpu import np_of, torch_of
+
+pytestmark = pytest.mark.gpu
+
+TOL = 260 * 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def h32():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import hadamard_rotated_bit_gb300 as m
+    from hadamard_rotated_bit_gb300 import _build
+    _build.build()
+    return m
+
+
+def _check(h32, l, k, bias=None, pad=0, **kw):
+    import torch
+    T, E = l.shape
+    if pad:
+        wide = np.full((T, E + pad), 1e9, np.float32)
+        wide[:, :E] = l
+        lt = torch_of(wide)[:, :E]
+    else:
+        lt = torch_of(l)
+    bt = None if bias is None else torch_of(np.asarray(bias, np.float32))
+    ids, w, off, ridx, row_of = h32.h32_moe_route_scored(lt, k, bias=bt, **kw)
+    torch.cuda.synchronize()
+    assert h32.h32_device_status() == 0
+    rid, rw, roff, rridx, rrow = oracle.moe_route_scored(l, k, bias=bias, **kw)
+    assert np.array_equal(np_of(ids), rid)
+    assert np.array_equal(np_of(off), roff)
+    assert np.array_equal(np_of(ridx), rridx)
+    assert np.array_equal(np_of(row_of), rrow)
+    gw = np_of(w).astype(np.float64)
+    floor = 2.0 ** -126 * abs(kw.get("scale", 1.0)) + 2.0 ** -149
+    assert np.all(np.abs(gw - rw) <= TOL * np.abs(rw) + floor)
+
+
+def _logits(T, E, seed, sigma=1.5):
+    return (np.random.default_rng(seed).standard_normal((T, E)) * sigma).astype(np.float32)
+
+
+CASES = [  # T, E, k, n_group, topk_group, group_top
+    (1, 1, 1, 1, 1, 1), (1, 128, 8, 1, 1, 1), (7, 5, 5, 1, 1, 2), (33, 64, 6, 8, 3, 1),
+    (40, 256, 8, 8, 4, 2), (65, 160, 6, 8, 3, 1), (9, 40, 4, 8, 2, 2), (20, 1000, 32, 5, 3, 2),
+    (31, 1024, 32, 32, 31, 2), (17, 1022, 8, 2, 1, 2), (50, 33, 32, 1, 1, 1), (64, 32, 4, 32, 4, 1),
+    (12, 36, 12, 4, 2, 2), (300, 37, 8, 1, 1, 1), (8, 512, 1, 16, 1, 1)]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,k,G,tg,gt", CASES)
+def test_matches_the_rule(h32, score, renorm, T, E, k, G, tg, gt):
+    l = _logits(T, E, T * 31 + E)
+    bias = 0.05 * np.random.default_rng(E).standard_normal(E)
+    for b in (None, bias.astype(np.float32)):
+        _check(h32, l, k, b, score=score, n_group=G, topk_group=tg, group_top=gt,
+               renormalize=renorm, scale=2.5)
+
+
+def test_row_pitch(h32):
+    l = _logits(19, 64, 3)
+    for pad in (1, 4, 64):
+        _check(h32, l, 5, pad=pad, score="sigmoid", n_group=4, topk_group=2, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_near_and_exact_ties(h32, score):
+    """Logits one fp32 step apart, equal logits with equal and with different biases,
+    biases that undo a difference of scores to the last bit, whole rows equal, scores
+    that saturate or underflow in fp32, groups that tie."""
+    r = np.random.default_rng(5)
+    T, E = 48, 64
+    l = _logits(T, E, 8, 0.5)
+    for t in range(T):
+        p = r.permutation(E)
+        l[t, p[1]] = l[t, p[0]]
+        l[t, p[2]] = np.nextafter(l[t, p[0]], np.float32(9))
+        l[t, p[3]] = np.nextafter(l[t, p[0]], np.float32(-9))
+    l[0] = 0.25
+    l[1, ::2] = 20.0
+    l[1, 1::2] = 25.0                       # sigmoids that round to 1
+    l[2] = -120.0 + np.arange(E) * 0.01     # sigmoids that underflow
+    l[3] = np.arange(E) * -3.0              # softmax scores that underflow
+    l[4, 32:] = l[4, :32]                   # groups equal pairwise
+    s0 = 1 / (1 + np.exp(-l[5].astype(np.float64)))
+    cancel = (0.75 - s0).astype(np.float32)  # every key of row 5 near 0.75
+    some = np.zeros(E, np.float32)
+    some[::3] = 0.125
+    for b in (None, np.zeros(E, np.float32), some, cancel):
+        for G, tg, gt in ((1, 1, 1), (8, 3, 2), (2, 1, 1), (4, 2, 2)):
+            for renorm in (True, False):
+                _check(h32, l, 7, b, score=score, n_group=G, topk_group=tg, group_top=gt,
+                       renormalize=renorm)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_masked_and_non_finite_logits(h32, score):
+    """-inf (masked), NaN and +inf logits, masked whole groups and rows, fewer
+    unmasked experts than choices, non-finite biases."""
+    r = np.random.default_rng(9)
+    T, E = 60, 48
+    l = _logits(T, E, 10)
+    for t in range(T):
+        m = r.random(E)
+        l[t, m < 0.3] = -np.inf
+        l[t, (m >= 0.3) & (m < 0.35)] = np.nan
+    l[0] = -np.inf
+    l[1] = np.nan
+    l[2, :5] = np.inf
+    l[3, 12:] = -np.inf                     # one group of four left
+    l[4] = -np.inf
+    l[4, 20] = 0.5                          # one expert left
+    l[5, ::2] = np.nan
+    l[5, 1::2] = -np.inf
+    bias = 0.1 * r.standard_normal(E)
+    odd = bias.copy()
+    odd[3], odd[4], odd[5] = np.nan, -np.inf, np.inf
+    for b in (None, bias.astype(np.float32), odd.astype(np.float32)):
+        for G, tg, gt in ((1, 1, 1), (4, 2, 2), (4, 1, 1), (12, 5, 2)):
+            for renorm in (True, False):
+                _check(h32, l, 4, b, score=score, n_group=G, topk_group=tg, group_top=gt,
+                       renormalize=renorm)
+
+
+@pytest.mark.parametrize("T,E,k", [(4096, 64, 2), (2500, 256, 8), (3001, 128, 8)])
+def test_many_tokens(h32, T, E, k):
+    _check(h32, _logits(T, E, T), k, 0.02 * np.random.default_rng(1).standard_normal(E).astype(np.float32),
+           score="sigmoid", n_group=8, topk_group=4, group_top=2, scale=2.5)
+
+
+def test_softmax_without_bias_equals_the_plain_router(h32):
+    """The same ids, offsets and row maps as h32_moe_route, weights within both bounds."""
+    import torch
+    l = torch_of(_logits(700, 128, 4))
+    a = h32.h32_moe_route(l, 8)
+    b = h32.h32_moe_route_scored(l, 8)
+    for i in (0, 2, 3, 4):
+        assert torch.equal(a[i], b[i])
+    assert torch.all((a[1] - b[1]).abs() <= 2 * TOL * a[1])
+
+
+def test_empty_given_outputs_stream_and_graph(h32):
+    import torch
+    E, k = 32, 4
+    out = h32.h32_moe_route_scored(torch.empty((0, E), device="cuda"), k)
+    torch.cuda.synchronize()
+    assert out[0].shape == (0, k) and out[2].tolist() == [0] * (E + 1)
+    T = 21
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ids, w = torch.full((T + 2, k), -7, **i32), torch.full((T + 2, k), -7.0, device="cuda")
+    off, ridx, rof = (torch.full((E + 3,), -7, **i32), torch.full((T * k + 5,), -7, **i32),
+                      torch.full((T + 1, k), -7, **i32))
+    l = torch_of(_logits(T, E, 2))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    h32.h32_moe_route_scored(l, k, score="sigmoid", topk_id=ids, topk_w=w, expert_off=off,
+                             row_idx=ridx, row_of=rof, stream=s)
+    s.synchronize()
+    rid, rw, roff, rridx, rrow = oracle.moe_route_scored(np_of(l), k, score="sigmoid")
+    assert np.array_equal(np_of(ids[:T]), rid) and np.array_equal(np_of(off[:E + 1]), roff)
+    assert np.array_equal(np_of(ridx[:T * k]), rridx) and np.array_equal(np_of(rof[:T]), rrow)
+    for t, n in ((ids, T), (w, T), (off, E + 1), (ridx, T * k), (rof, T)):
+        assert torch.all(t[n:] == -7)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = h32.h32_moe_route_scored(l, k, score="sigmoid")
+    for seed in (5, 6):
+        l.copy_(torch_of(_logits(T, E, seed)))
+        g.replay()
+        torch.cuda.synchronize()
+        rid, rw, roff, rridx, rrow = oracle.moe_route_scored(np_of(l), k, score="sigmoid")
+        assert np.array_equal(np_of(out[0]), rid) and np.array_equal(np_of(out[3]), rridx)
+        assert np.array_equal(np_of(out[2]), roff) and np.array_equal(np_of(out[4]), rrow)
