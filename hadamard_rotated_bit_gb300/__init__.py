@@ -31,6 +31,7 @@ __all__ = [
     "h32_gemm_tc_workspace_bytes", "h32_gemm_tc_schedule",
     "q4_0_x_q4_gemm_tc_noalloc", "q4_0_x_q8_gemm_tc_noalloc",
     "h32_add_rms_norm_quantize", "h32_moe_route_scored",
+    "q4_0_x_q4_gemm_tc_epilogue", "q4_0_x_q8_gemm_tc_epilogue",
 ]
 
 
@@ -93,6 +94,10 @@ _SIGS = {
                                          _I64, _P, _I64, _P, _P]),
     "h32_moe_route": (_INT, [_P, _I64, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P]),
     "h32_moe_combine": (_INT, [_P, _I64, _I64, _P, _P, _I64, _I32, _I64, _P, _I64, _P]),
+    "q4_0_x_q4_gemm_tc_epilogue": (_INT, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P, _I32, _P,
+                                          _INT, _I64, _P, _INT, _I64, _P, ctypes.c_size_t, _P]),
+    "q4_0_x_q8_gemm_tc_epilogue": (_INT, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P, _I32, _P,
+                                          _INT, _I64, _P, _INT, _I64, _P, ctypes.c_size_t, _P]),
     "h32_moe_route_scored": (_INT, [_P, _I64, _I32, _I64, _I32, _P, _I32, _I32, _I32, _I32, _I32,
                                     ctypes.c_float, _P, _P, _P, _P, _P, _P]),
     "h32_add_rms_norm_quantize": (_INT, [_P, _INT, _I64, _P, _INT, _I64, _P, _INT, ctypes.c_float,
@@ -909,6 +914,74 @@ def h32_moe_combine(y, row_of, topk_w, out=None, stream=None):
     return out
 
 
+EPI_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu_tanh": 3, "gelu_erf": 4, "swiglu": 5}
+
+
+def q4_0_x_q4_gemm_tc_epilogue(wp, wsc, xw, xdt, M=None, bias=None, act="none", residual=None,
+                               y=None, y_dtype=None, stream=None, workspace=None):
+    """y = act(z + bias) + residual, z the product of q4_0_x_q4_gemm_tc, in one kernel.
+
+    bias [N] fp32 or None; act "none", "relu", "silu", "gelu_tanh", "gelu_erf" or
+    "swiglu" (the weights' gate and up rows interleaved: silu(gate) * up, N/2 outputs);
+    residual [M][outputs] bf16/fp32 or None (may be y); y [M][outputs] bf16/fp32, by
+    default allocated as y_dtype (fp32).  Few tokens run a kernel of their own.
+    workspace as for q4_0_x_q4_gemm_tc."""
+    return _gemm_epilogue("q4_0_x_q4_gemm_tc_epilogue", wp, wsc, xw, xdt, M, bias, act, residual,
+                          y, y_dtype, stream, workspace)
+
+
+def q4_0_x_q8_gemm_tc_epilogue(wp, wsc, xw8, xdt, M=None, bias=None, act="none", residual=None,
+                               y=None, y_dtype=None, stream=None, workspace=None):
+    """The same on 8-bit activations (z the product of q4_0_x_q8_gemm_tc)."""
+    return _gemm_epilogue("q4_0_x_q8_gemm_tc_epilogue", wp, wsc, xw8, xdt, M, bias, act, residual,
+                          y, y_dtype, stream, workspace)
+
+
+def _gemm_epilogue(fn, wp, wsc, xw, xdt, M, bias, act, residual, y, y_dtype, stream, workspace):
+    torch = _torch()
+    bf16, f32 = torch.bfloat16, torch.float32
+    if M is None:
+        M = xw.shape[0]
+    if act is None:
+        act = "none"
+    if act not in EPI_ACTS:
+        raise ValueError(f"act must be one of {', '.join(EPI_ACTS)}")
+    N, K = _tc_operands(wp, wsc, xw, xdt, M, 2 if fn == "q4_0_x_q8_gemm_tc_epilogue" else 1)
+    n_out = N // 2 if act == "swiglu" else N
+    if bias is not None:
+        _need(bias, "bias", (f32,), (N,))
+    if residual is not None:
+        _need(residual, "residual", (bf16, f32), (_ge(M), _ge(n_out)), pitched=True)
+    if y is not None:
+        _need(y, "y", (bf16, f32), (_ge(M), _ge(n_out)), pitched=True)
+        if y_dtype is not None and y_dtype != y.dtype:
+            raise ValueError(f"y is {y.dtype}, y_dtype {y_dtype}")
+    elif y_dtype is not None and y_dtype not in (bf16, f32):
+        raise ValueError("y_dtype must be bf16 or fp32")
+    explicit_ws = workspace is not None and workspace is not False
+    if explicit_ws:
+        _need(workspace, "workspace", (torch.uint8,), (_ge(0),))
+    _same_gpu(("wp", wp), ("wsc", wsc), ("xw", xw), ("xdt", xdt), ("bias", bias),
+              ("residual", residual), ("y", y), ("workspace", workspace if explicit_ws else None))
+    dev = wp.device
+
+    def body(raw, y=y):
+        if y is None:
+            y = torch.empty((M, n_out), dtype=y_dtype or f32, device=dev)
+        ws = workspace if explicit_ws else None
+        if workspace is None and M > 0:
+            ws = _workspace_for(M, N, K, dev, raw)
+        st = getattr(lib(), fn)(
+            wp.data_ptr(), wsc.data_ptr(), wsc.shape[1], xw.data_ptr(), xdt.data_ptr(), xdt.shape[1],
+            M, N, K, _raw(bias), EPI_ACTS[act], _raw(residual),
+            residual is not None and residual.dtype == bf16, _pitch(residual), y.data_ptr(),
+            y.dtype == bf16, _pitch(y), _raw(ws), 0 if ws is None else ws.numel(), raw)
+        _check(fn, st)
+        return y
+
+    return _on_stream(dev, stream, body)
+
+
 ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 
 
@@ -1068,7 +1141,7 @@ _COMPUTE_CALLS = (
     "q4_0_x_q4_gemm_tc_widen", "q4_0_x_q4_gemm_tc_widen_experts",
     "h32_q4_0_blocks_to_planes", "h32_q4_0_planes_to_blocks",
     "q4_0_x_q4_gemm_tc_noalloc", "q4_0_x_q8_gemm_tc_noalloc", "h32_add_rms_norm_quantize",
-    "h32_moe_route_scored",
+    "h32_moe_route_scored", "q4_0_x_q4_gemm_tc_epilogue", "q4_0_x_q8_gemm_tc_epilogue",
 )
 for _name in _COMPUTE_CALLS:
     globals()[_name] = _trace.traced(_name)(globals()[_name])

@@ -68,6 +68,7 @@
 
 #include "h32_common.cuh"
 #include "h32_epilogue.cuh"
+#include "h32_finish.cuh"
 #include "h32_tcform.cuh"
 
 namespace h32 {
@@ -164,6 +165,7 @@ struct TcArgs {
     float *ws_acc;
     int32_t split_p, split_kh, ws_ld;
     uint64_t wait_limit;
+    EpiArgs fin;                 // the finished output (kEpi == 3); y is unused then
 };
 
 __device__ __forceinline__ void record(uint32_t bits) { atomicOr(&g_tc_status, bits); }
@@ -348,6 +350,53 @@ __device__ __forceinline__ void stage_dw(const float *s_sa, int s, int row, int 
     }
 }
 
+// The finished output of a warp's share of a tile (kEpi == 3): bias, activation,
+// residual, one rounding to y's type.  A lane holds one weight row (output
+// feature) and 16 token columns per chunk, so for each column the warp's 32 lanes
+// read and write 32 consecutive features.  For the gated activation the lanes of
+// a pair hold a gate row and its up row: they exchange halves of the chunk (8
+// shuffles), the even lane finishes columns 0..7, the odd lane 8..15.
+template <int kMaxChunks>
+__device__ __forceinline__ void finish_tile(const TcArgs &a, const TcTile &ti, int row, int lane,
+                                            int c0, int nch, const uint64_t *acc) {
+    const EpiArgs &f = a.fin;
+    const int n = ti.n0 + row;
+    const bool in = n < a.N;
+    const float bias = (f.bias && in) ? __ldg(f.bias + ti.wrow + row) : 0.0f;
+    const bool gated = f.act == H32_EPI_SWIGLU;
+#pragma unroll
+    for (int c = 0; c < kMaxChunks; ++c) {
+        if (c < nch) {
+            float z[16];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint64_t pr = acc[8 * c + q];
+                z[2 * q] = __uint_as_float(static_cast<uint32_t>(pr));
+                z[2 * q + 1] = __uint_as_float(static_cast<uint32_t>(pr >> 32));
+            }
+            if (f.bias) {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) z[q] = __fadd_rn(z[q], bias);
+            }
+            const int col = c0 + 16 * c;
+            if (gated) {
+                const bool odd = lane & 1;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float v = __shfl_xor_sync(0xFFFFFFFFu, odd ? z[q] : z[8 + q], 1);
+                    z[q] = odd ? swiglu(v, z[8 + q]) : swiglu(z[q], v);
+                }
+                const int first = col + (odd ? 8 : 0);
+                if (in) finish_columns<8>(f, z, ti.g0 + first, ti.clo - first, ti.chi - first, n >> 1);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) z[q] = activate(z[q], f.act);
+                if (in) finish_columns<16>(f, z, ti.g0 + col, ti.clo - col, ti.chi - col, n);
+            }
+        }
+    }
+}
+
 // The ring positions of an epilogue warp: shared-memory stage and TMEM buffer,
 // each a counter and a phase bit.
 struct EpiRing {
@@ -361,7 +410,7 @@ struct EpiRing {
 // come from one elected lane.  Returns false when a wait gave up.  A warp holds
 // its lane quarter's 32 weight rows (one a thread, the 32x32b TMEM fragment)
 // times its share of the tile's columns.
-template <int EPQ, int XB, bool kQN, bool kTail, bool kWQ, int kMode>
+template <int EPQ, int XB, bool kQN, bool kTail, bool kWQ, int kMode, bool kFin>
 __device__ __forceinline__ bool epi_item(const TcArgs &a, int t, int st0, int nstage,
                                          const int *s_off, const int *s_tpre, uint64_t *bars,
                                          const float *s_sa, const float *s_sb, float *s_q,
@@ -476,7 +525,9 @@ __device__ __forceinline__ bool epi_item(const TcArgs &a, int t, int st0, int ns
         return true;
     }
     const int64_t n = ti.n0 + row;
-    if (n < a.N && (!kQN || a.y)) {
+    if constexpr (kFin) {
+        finish_tile<C::kMaxChunks>(a, ti, row, lane, c0, nch, acc);
+    } else if (n < a.N && (!kQN || a.y)) {
 #pragma unroll
         for (int c = 0; c < C::kMaxChunks; ++c) {
             if (c < nch) {
@@ -547,7 +598,7 @@ __device__ __forceinline__ bool epi_item(const TcArgs &a, int t, int st0, int ns
 // a loop over items whose K range is a variable made every tile of the
 // instance about 6% slower), the two parts of a split piece before and after
 // it.
-template <int EPQ, int XB, bool kQN, bool kTail, bool kWQ, bool kSplit>
+template <int EPQ, int XB, bool kQN, bool kTail, bool kWQ, bool kSplit, bool kFin>
 __device__ __forceinline__ bool epilogue_tiles(const TcArgs &a, int total, const int *s_off,
                                                const int *s_tpre, uint64_t *bars, const float *s_sa,
                                                const float *s_sb, float *s_q, uint32_t tmem,
@@ -560,7 +611,7 @@ __device__ __forceinline__ bool epilogue_tiles(const TcArgs &a, int total, const
         if (a.split_p > 0) {
             main_end = a.tail_first;
             if (b < a.split_p &&
-                !epi_item<EPQ, XB, kQN, kTail, kWQ, 1>(a, a.tail_first + b, 0, a.split_kh, s_off,
+                !epi_item<EPQ, XB, kQN, kTail, kWQ, 1, kFin>(a, a.tail_first + b, 0, a.split_kh, s_off,
                                                         s_tpre, bars, s_sa, s_sb, s_q, tmem, warp,
                                                         lane, abort_flag, r))
                 return false;
@@ -568,12 +619,12 @@ __device__ __forceinline__ bool epilogue_tiles(const TcArgs &a, int total, const
     }
     const int nit = b < main_end ? (main_end - 1 - b) / g + 1 : 0;
     for (int k = 0; k < nit; ++k)
-        if (!epi_item<EPQ, XB, kQN, kTail, kWQ, 0>(a, b + k * g, 0, nst, s_off, s_tpre, bars, s_sa,
+        if (!epi_item<EPQ, XB, kQN, kTail, kWQ, 0, kFin>(a, b + k * g, 0, nst, s_off, s_tpre, bars, s_sa,
                                                     s_sb, s_q, tmem, warp, lane, abort_flag, r))
             return false;
     if constexpr (kSplit) {
         if (a.split_p > 0 && b >= a.split_p && b < 2 * a.split_p &&
-            !epi_item<EPQ, XB, kQN, kTail, kWQ, 2>(a, a.tail_first + b - a.split_p, a.split_kh,
+            !epi_item<EPQ, XB, kQN, kTail, kWQ, 2, kFin>(a, a.tail_first + b - a.split_p, a.split_kh,
                                                     nst - a.split_kh, s_off, s_tpre, bars, s_sa,
                                                     s_sb, s_q, tmem, warp, lane, abort_flag, r))
             return false;
@@ -590,7 +641,7 @@ __device__ __forceinline__ bool epilogue_tiles(const TcArgs &a, int total, const
 // counters and phase bits, arrivals come from one elected lane.  Returns false
 // when a wait gave up.  A warp holds its lane quarter's 32 weight rows (one a
 // thread, the 32x32b TMEM fragment) times its share of the tile's columns.
-template <int EPQ, int XB, bool kQN, bool kTail, bool kWQ>
+template <int EPQ, int XB, bool kQN, bool kTail, bool kWQ, bool kFin>
 __device__ __forceinline__ bool epilogue_tiles_plain(const TcArgs &a, int total, const int *s_off,
                                                const int *s_tpre, uint64_t *bars, const float *s_sa,
                                                const float *s_sb, float *s_q, uint32_t tmem,
@@ -657,7 +708,9 @@ __device__ __forceinline__ bool epilogue_tiles_plain(const TcArgs &a, int total,
             }
         }
         const int64_t n = ti.n0 + row;
-        if (n < a.N && (!kQN || a.y)) {
+        if constexpr (kFin) {
+            finish_tile<C::kMaxChunks>(a, ti, row, lane, c0, nch, acc);
+        } else if (n < a.N && (!kQN || a.y)) {
 #pragma unroll
             for (int c = 0; c < C::kMaxChunks; ++c) {
                 if (c < nch) {
@@ -775,8 +828,8 @@ __device__ __forceinline__ bool widen_tiles(const TcArgs &a, int total, const in
 }
 
 // kEpi: 0 = y only, 1 = y and the block sums, 2 = y (optional) and the output
-// quantized for the next projection.  kTail: the last partial wave's tiles are
-// cut into pieces (TcArgs::tail_first, tail_k).  kWQ: the widening instance
+// quantized for the next projection, 3 = the finished output (TcArgs::fin).
+// kTail: the last partial wave's tiles are cut into pieces (TcArgs::tail_first, tail_k).  kWQ: the widening instance
 // (map_a over the Q4_0 nibbles, map_sa over the fp16 scales).  kSplit: the cut
 // pieces also run in two parts along K (TcArgs::split_p, TcItem); an instance
 // of its own, as the cut instance without that code measured about 4% faster
@@ -1027,10 +1080,10 @@ __global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ>::kThreads, 1)
         if constexpr (C::kRegSplit) reg_alloc<C::kEpiRegs>();
         bool eok;
         if constexpr (!kTail)
-            eok = epilogue_tiles_plain<EPQ, XB, kEpi == 2, kTail, kWQ>(
+            eok = epilogue_tiles_plain<EPQ, XB, kEpi == 2, kTail, kWQ, kEpi == 3>(
                 a, total, s_off, s_tpre, bars, s_sa, s_sb, s_q, tmem, warp, lane, abort_flag);
         else
-            eok = epilogue_tiles<EPQ, XB, kEpi == 2, kTail, kWQ, kSplit>(
+            eok = epilogue_tiles<EPQ, XB, kEpi == 2, kTail, kWQ, kSplit, kEpi == 3>(
                 a, total, s_off, s_tpre, bars, s_sa, s_sb, s_q, tmem, warp, lane, abort_flag);
         if (!eok) set_abort(misc);
     } else {
@@ -1402,7 +1455,8 @@ h32_status run_gemm_tc(int xbits, const uint8_t *wp, const float *wsc, int64_t l
                        const int32_t *expert_off, int64_t M, int64_t N, int64_t K, float *y,
                        int64_t ldy, int32_t *block_sums, void *stream, uint8_t *qn = nullptr,
                        float *qnd = nullptr, int64_t ldqnd = 0, int qn_rot = 0,
-                       const uint16_t *wd16 = nullptr, void *ws = nullptr, size_t ws_bytes = 0) {
+                       const uint16_t *wd16 = nullptr, void *ws = nullptr, size_t ws_bytes = 0,
+                       const EpiArgs *fin = nullptr) {
     if (wd16) ldws = K / 32;
     if (M < 0 || N <= 0 || K <= 0 || (K % 128) != 0 || (N % 16) != 0 || (y && ldy < N) ||
         ldws < K / 32 || (ldws % 4) != 0 || ldxd < M || (ldxd % 4) != 0 || E < 1 ||
@@ -1415,7 +1469,8 @@ h32_status run_gemm_tc(int xbits, const uint8_t *wp, const float *wsc, int64_t l
     // for their tensor map
     if (wd16 && ((K % 256) != 0 || xbits != 4 || qn)) return H32_ERR_INVALID_ARG;
     if (M == 0) return H32_OK;
-    if (!wp || (!wsc && !wd16) || !xw || !xdt || (!y && !qn)) return H32_ERR_INVALID_ARG;
+    if (!wp || (!wsc && !wd16) || !xw || !xdt || (!y && !qn && !fin))
+        return H32_ERR_INVALID_ARG;
     if (!aligned16(wp) || (wsc && !aligned16(wsc)) || (wd16 && !aligned16(wd16)) ||
         !aligned16(xw) || !aligned16(xdt) ||
         (y && !aligned16(y)) || (qn && (!aligned16(qn) || !aligned16(qnd))) ||
@@ -1487,12 +1542,34 @@ h32_status run_gemm_tc(int xbits, const uint8_t *wp, const float *wsc, int64_t l
         a.ws_ld = static_cast<int32_t>(plan.ws_ld);
     }
     a.wait_limit = wait_limit();
+    if (fin) a.fin = *fin;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int g = static_cast<int>(grid);
     if (wd16) {
         if (block_sums) return launch_tc<4, 4, 1, false, true>(maps, a, g, s);
         return plan.tail_k > 1 ? launch_tc<4, 4, 0, true, true>(maps, a, g, s)
                                : launch_tc<4, 4, 0, false, true>(maps, a, g, s);
+    }
+    constexpr int kEPQ = H32_TC_EPI_PER_QUAD;
+    // the tile's 16-column chunks in even shares: 12 epilogue warps (3 per lane
+    // quarter) when 16 would leave one warp with twice the others' chunks
+    // (5 or 6 chunks: measured 5-8% faster on the pp512 attention and FFN-down
+    // shapes), 16 otherwise
+    const int n16 = bn / 16;
+    const bool narrow = n16 % 4 == 1 || n16 % 4 == 2;
+    if (fin) {
+        if (xbits == 8) {
+            if (plan.split_p > 0) return launch_tc<kEPQ, 8, 3, true, false, true>(maps, a, g, s);
+            return plan.tail_k > 1 ? launch_tc<kEPQ, 8, 3, true>(maps, a, g, s)
+                                   : launch_tc<kEPQ, 8, 3>(maps, a, g, s);
+        }
+        if (plan.split_p > 0)
+            return narrow ? launch_tc<3, 4, 3, true, false, true>(maps, a, g, s)
+                          : launch_tc<kEPQ, 4, 3, true, false, true>(maps, a, g, s);
+        if (plan.tail_k > 1)
+            return narrow ? launch_tc<3, 4, 3, true>(maps, a, g, s)
+                          : launch_tc<kEPQ, 4, 3, true>(maps, a, g, s);
+        return narrow ? launch_tc<3, 4, 3>(maps, a, g, s) : launch_tc<kEPQ, 4, 3>(maps, a, g, s);
     }
     if (xbits == 8) {
         if (block_sums) return launch_tc<H32_TC_EPI_PER_QUAD, 8, 1>(maps, a, g, s);
@@ -1506,12 +1583,6 @@ h32_status run_gemm_tc(int xbits, const uint8_t *wp, const float *wsc, int64_t l
                                : launch_tc<H32_TC_EPI_PER_QUAD, 4, 2>(maps, a, g, s);
     }
     if (block_sums) return launch_tc<H32_TC_EPI_PER_QUAD, 4, 1>(maps, a, g, s);
-    // the tile's 16-column chunks in even shares: 12 epilogue warps (3 per lane
-    // quarter) when 16 would leave one warp with twice the others' chunks
-    // (5 or 6 chunks: measured 5-8% faster on the pp512 attention and FFN-down
-    // shapes), 16 otherwise
-    const int n16 = bn / 16;
-    const bool narrow = n16 % 4 == 1 || n16 % 4 == 2;
     if (plan.split_p > 0)
         return narrow ? launch_tc<3, 4, 0, true, false, true>(maps, a, g, s)
                       : launch_tc<H32_TC_EPI_PER_QUAD, 4, 0, true, false, true>(maps, a, g, s);
@@ -1695,4 +1766,55 @@ extern "C" h32_status q4_0_x_q4_gemm_tc_experts(const uint8_t *wp, const float *
     if (!expert_off) return H32_ERR_INVALID_ARG;
     return h32::run_gemm_tc(4, wp, wsc, ldws, E, xw, xdt, ldxd, expert_off, R, N, K, y, ldy,
                             block_sums, stream);
+}
+
+namespace h32 {
+namespace {
+h32_status run_epilogue(int xbits, const uint8_t *wp, const float *wsc, int64_t ldws,
+                        const uint8_t *xw, const float *xdt, int64_t ldxd, int64_t M, int64_t N,
+                        int64_t K, const float *bias, int32_t act, const void *residual,
+                        h32_in_dtype residual_dt, int64_t ldr, void *y, h32_in_dtype y_dt,
+                        int64_t ldy, void *ws, size_t ws_bytes, void *stream) {
+    if (act < H32_EPI_NONE || act > H32_EPI_SWIGLU) return H32_ERR_INVALID_ARG;
+    const int64_t n_out = act == H32_EPI_SWIGLU ? N / 2 : N;
+    auto dtype_ok = [](h32_in_dtype d) { return d == H32_IN_F32 || d == H32_IN_BF16; };
+    if (ldy < n_out || !dtype_ok(y_dt) || (residual && (ldr < n_out || !dtype_ok(residual_dt))))
+        return H32_ERR_INVALID_ARG;
+    if (M > 0 && (!y || (y == residual && (ldy != ldr || y_dt != residual_dt))))
+        return H32_ERR_INVALID_ARG;
+    auto esize = [](h32_in_dtype d) { return d == H32_IN_BF16 ? 2 : 4; };
+    if (!aligned16(y) || (ldy * esize(y_dt)) % 16 != 0 || (reinterpret_cast<uintptr_t>(bias) & 3u) ||
+        (residual && (!aligned16(residual) || (ldr * esize(residual_dt)) % 16 != 0)))
+        return H32_ERR_ALIGNMENT;
+    EpiArgs f{};
+    f.bias = bias;
+    f.res = residual;
+    f.y = y;
+    f.ldr = ldr;
+    f.ldy = ldy;
+    f.act = act;
+    f.res_bf16 = residual_dt == H32_IN_BF16;
+    f.y_bf16 = y_dt == H32_IN_BF16;
+    return run_gemm_tc(xbits, wp, wsc, ldws, 1, xw, xdt, ldxd, nullptr, M, N, K, nullptr, 0, nullptr,
+                       stream, nullptr, nullptr, 0, 0, nullptr, ws, ws_bytes, &f);
+}
+}  // namespace
+}  // namespace h32
+
+extern "C" h32_status q4_0_x_q4_gemm_tc_epilogue(
+    const uint8_t *wp, const float *wsc, int64_t ldws, const uint8_t *xw, const float *xdt,
+    int64_t ldxd, int64_t M, int64_t N, int64_t K, const float *bias, int32_t act,
+    const void *residual, h32_in_dtype residual_dt, int64_t ldr, void *y, h32_in_dtype y_dt,
+    int64_t ldy, void *workspace, size_t workspace_bytes, void *stream) {
+    return h32::run_epilogue(4, wp, wsc, ldws, xw, xdt, ldxd, M, N, K, bias, act, residual,
+                             residual_dt, ldr, y, y_dt, ldy, workspace, workspace_bytes, stream);
+}
+
+extern "C" h32_status q4_0_x_q8_gemm_tc_epilogue(
+    const uint8_t *wp, const float *wsc, int64_t ldws, const uint8_t *xw8, const float *xdt,
+    int64_t ldxd, int64_t M, int64_t N, int64_t K, const float *bias, int32_t act,
+    const void *residual, h32_in_dtype residual_dt, int64_t ldr, void *y, h32_in_dtype y_dt,
+    int64_t ldy, void *workspace, size_t workspace_bytes, void *stream) {
+    return h32::run_epilogue(8, wp, wsc, ldws, xw8, xdt, ldxd, M, N, K, bias, act, residual,
+                             residual_dt, ldr, y, y_dt, ldy, workspace, workspace_bytes, stream);
 }

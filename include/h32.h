@@ -437,6 +437,45 @@ h32_status q4_0_x_q8_gemm_tc_ws(const uint8_t *wp, const float *wsc, int64_t ldw
                                 int64_t N, int64_t K, float *y, int64_t ldy, int32_t *block_sums,
                                 void *workspace, size_t workspace_bytes, void *stream);
 
+typedef enum h32_epi_act {
+    H32_EPI_NONE = 0,
+    H32_EPI_RELU = 1,
+    H32_EPI_SILU = 2,       /* z / (1 + exp(-z))                                  */
+    H32_EPI_GELU_TANH = 3,  /* z / (1 + exp(-2 u)), u = sqrt(2/pi)(z + 0.044715 z^3) */
+    H32_EPI_GELU_ERF = 4,   /* z erfc(-z / sqrt(2)) / 2                           */
+    H32_EPI_SWIGLU = 5      /* rows 2i gate, 2i + 1 up: silu(z_gate) z_up, N/2 outputs */
+} h32_epi_act;
+
+/*
+ * The tc products with what usually follows them, in the same kernel:
+ *   z[m][n] = the product of q4_0_x_q4_gemm_tc (q4_0_x_q8_gemm_tc), bit for bit;
+ *   v = act(z + bias[n]);  y[m][j] = v + residual[m][j], all in fp32, rounded
+ *   once to y's type.
+ * For any M: a few tokens (one new token of each sequence) run a kernel of their
+ * own that reads every weight byte once; the results do not depend on M.
+ *   bias            nullable fp32 [N], 4-byte aligned
+ *   act             an h32_epi_act; H32_EPI_SWIGLU takes the weights' gate and up
+ *                   rows interleaved and gives N / 2 outputs a token
+ *   residual        nullable [M][ldr] of type residual_dt, ldr >= outputs; may be
+ *                   y itself (same type and pitch)
+ *   y               [M][ldy] out of type y_dt, ldy >= outputs
+ *   workspace       as for q4_0_x_q4_gemm_tc_ws (null: no split)
+ * z is bit-exact; v is within a few ulps of the formula (the CUDA expf, erfcf).
+ * Other arguments and conditions as for q4_0_x_q4_gemm_tc.
+ */
+h32_status q4_0_x_q4_gemm_tc_epilogue(const uint8_t *wp, const float *wsc, int64_t ldws,
+                                      const uint8_t *xw, const float *xdt, int64_t ldxd, int64_t M,
+                                      int64_t N, int64_t K, const float *bias, int32_t act,
+                                      const void *residual, h32_in_dtype residual_dt, int64_t ldr,
+                                      void *y, h32_in_dtype y_dt, int64_t ldy, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+h32_status q4_0_x_q8_gemm_tc_epilogue(const uint8_t *wp, const float *wsc, int64_t ldws,
+                                      const uint8_t *xw8, const float *xdt, int64_t ldxd,
+                                      int64_t M, int64_t N, int64_t K, const float *bias,
+                                      int32_t act, const void *residual, h32_in_dtype residual_dt,
+                                      int64_t ldr, void *y, h32_in_dtype y_dt, int64_t ldy,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
 /*
  * q4_0_x_q4_gemm_tc / q4_0_x_q8_gemm_tc with the K split, without a caller's
  * workspace and without allocating: the workspace is a 4 MB array the library
