@@ -31,7 +31,7 @@ __all__ = [
     "h32_gemm_tc_workspace_bytes", "h32_gemm_tc_schedule",
     "q4_0_x_q4_gemm_tc_noalloc", "q4_0_x_q8_gemm_tc_noalloc",
     "h32_add_rms_norm_quantize", "h32_moe_route_scored",
-    "q4_0_x_q4_gemm_tc_epilogue", "q4_0_x_q8_gemm_tc_epilogue",
+    "h32_moe_route_scored_workspace_bytes", "q4_0_x_q4_gemm_tc_epilogue", "q4_0_x_q8_gemm_tc_epilogue",
 ]
 
 
@@ -99,7 +99,8 @@ _SIGS = {
     "q4_0_x_q8_gemm_tc_epilogue": (_INT, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P, _I32, _P,
                                           _INT, _I64, _P, _INT, _I64, _P, ctypes.c_size_t, _P]),
     "h32_moe_route_scored": (_INT, [_P, _I64, _I32, _I64, _I32, _P, _I32, _I32, _I32, _I32, _I32,
-                                    ctypes.c_float, _P, _P, _P, _P, _P, _P]),
+                                    ctypes.c_float, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "h32_moe_route_scored_workspace_bytes": (_INT, [_I64, _I32, ctypes.POINTER(ctypes.c_size_t)]),
     "h32_add_rms_norm_quantize": (_INT, [_P, _INT, _I64, _P, _INT, _I64, _P, _INT, ctypes.c_float,
                                          _I64, _I64, _P, _I64, _P, _INT, _I64, _I32, _INT, _P, _P,
                                          _I64, _P]),
@@ -983,6 +984,15 @@ def _gemm_epilogue(fn, wp, wsc, xw, xdt, M, bias, act, residual, y, y_dtype, str
 
 
 ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
+ROUTE_SOLO_TOKENS = 64   # up to here h32_moe_route_scored needs no workspace
+
+
+def h32_moe_route_scored_workspace_bytes(T: int, E: int) -> int:
+    """Workspace bytes of h32_moe_route_scored for T tokens and E experts."""
+    n = ctypes.c_size_t(0)
+    _check("h32_moe_route_scored_workspace_bytes",
+           lib().h32_moe_route_scored_workspace_bytes(int(T), int(E), ctypes.byref(n)))
+    return int(n.value)
 
 
 def h32_moe_route_scored(logits, k, score="softmax", bias=None, n_group=1, topk_group=1,
@@ -1033,11 +1043,16 @@ def h32_moe_route_scored(logits, k, score="softmax", bias=None, n_group=1, topk_
             row_idx = torch.empty(T * k, dtype=torch.int32, device=dev)
         if row_of is None:
             row_of = torch.empty((T, k), dtype=torch.int32, device=dev)
+        ws, ws_bytes = None, 0
+        if T > ROUTE_SOLO_TOKENS:
+            # the call's own: freed with it, reused only by later work of the stream
+            ws_bytes = h32_moe_route_scored_workspace_bytes(T, E)
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         st = lib().h32_moe_route_scored(
             logits.data_ptr(), T, E, _pitch(logits) if T > 0 else E, ROUTE_SCORES[score],
             _raw(bias), n_group, topk_group, group_top, k, bool(renormalize), scale,
             topk_id.data_ptr(), topk_w.data_ptr(), expert_off.data_ptr(), row_idx.data_ptr(),
-            row_of.data_ptr(), raw)
+            row_of.data_ptr(), _raw(ws), ws_bytes, raw)
         _check("h32_moe_route_scored", st)
         return topk_id, topk_w, expert_off, row_idx, row_of
 

@@ -4,36 +4,46 @@
 // topk_group groups of experts with the largest sums of their group_top best
 // keys, the k experts of largest key in those groups, their weights from the
 // scores alone, and the (token, choice) rows grouped by expert as by
-// h32_moe_route.  The order of keys is that of their values in double: keys are
-// computed in fp32 with a bound on their error, and where two keys whose order
-// matters are nearer than their bounds (about one token in a thousand on random
-// logits) the token is decided again in double.
+// h32_moe_route.
 //
-// One warp per token.  Lane i holds `per` consecutive experts, so a lower lane
-// holds lower ids and, with `per` dividing a group's size, a group is a run of
-// whole lanes.  Keys become unsigned integers of the same order; a round of the
-// selection is one warp-wide integer maximum, one ballot (ties: the lowest
-// lane) and the winner's rescan of its own keys.
+// The order of keys is exact.  Without a bias (and with groups by their best key)
+// it is the order of the logits.  Else it is that of the keys' values in double:
+// keys are computed in fp32 with a bound on their error, and where two keys whose
+// order matters are nearer than their bounds (about one token in a thousand on
+// random logits) the token is decided again in double.
 //
-// Bound: instruction issue.  The data are 4 bytes a logit (16.8 MB for 16384
-// tokens x 256 experts, 2.5 us at the copy rate) against about 70 instructions a
-// token and round.
+// route_token: one warp per token.  Lane i holds `per` consecutive experts, so a
+// lower lane holds lower ids and, with `per` dividing a group's size, a group is a
+// run of whole lanes.  Keys become unsigned integers of the same order; each lane
+// keeps its two largest, and a round of the selection is one warp-wide integer
+// maximum, one ballot (ties: the lowest lane) and the winner's step to its next.
+//
+// Grouping: a block counts its chunk of tokens per expert while it routes them,
+// and a second kernel places the rows of one chunk a block: an expert's rows start
+// at the counts of lower experts and of its own in earlier chunks, and a choice's
+// rank within the chunk is a population count over the expert's bitmap of tokens.
+// Up to 64 tokens one block does both, in one launch.
+//
+// Bound: instruction issue.  The data are 4 bytes a logit (16.8 MB for 16384 tokens
+// x 256 experts, 2.5 us at the copy rate).
 #include "h32_common.cuh"
 #include "h32_moe.cuh"
 
 namespace h32 {
 namespace {
 
-constexpr int kScoreWarps = 8;   // tokens a block
+constexpr int kSoloTokens = 64;       // tokens one block routes and groups in one launch
+constexpr int kPlaceThreads = 1024;
 
 struct ScoreArgs {
     const float *logits, *bias;
     int64_t ldl;
     int32_t T, E, k, n_group, topk_group, group_top, per;
-    int32_t sigmoid, renorm, vec;
+    int32_t sigmoid, renorm, vec, lanes;   // lanes: a group's lanes where `per` divides its size, else 0
     float scale;
     int32_t *topk_id;
     float *topk_w;
+    int32_t chunk;                         // tokens a block
 };
 
 // A key as an unsigned integer of the same order: 0 = not a candidate, 1 = NaN,
@@ -54,7 +64,7 @@ struct Norm {
     F lmax, inv;
 };
 
-// score of a logit; a NaN or -inf logit scores 0
+// score of a logit, to a few ulps; a NaN or -inf logit scores 0
 __device__ __forceinline__ float score_of(float l, const Norm<float> &n, bool sigmoid) {
     if (isnan(l) || l == -INFINITY) return 0.0f;
     if (sigmoid) return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l)));
@@ -111,38 +121,53 @@ __device__ __forceinline__ F group_score(F a, F b, int top) {
     return (top == 1 || b == none) ? a : a + b;
 }
 
-// The token decided in double: lane j returns choice j's expert.  Slow (the
-// card's double rate is low) and rare.
+__device__ __forceinline__ uint64_t ordered(double key) {
+    if (isnan(key)) return 1ull;
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(key + 0.0));
+    return (u >> 63) ? ~u : u | 0x8000000000000000ull;
+}
+
+// The token decided in double: lane j returns choice j's expert.  Rare; the
+// card's double rate is low, so every key is computed once and kept.
+template <int NPER>
 __device__ __noinline__ int route_exact(const ScoreArgs &a, const float *row) {
     const int lane = threadIdx.x & 31;
     const bool sg = a.sigmoid != 0;
     const double none = -static_cast<double>(INFINITY);
-    const int e0 = lane * a.per, e1 = min(e0 + a.per, a.E);
-    Norm<double> nm{none, 0.0};
+    const int e0 = lane * a.per;
+    double kd[NPER];
+    Norm<double> nm{none, 1.0};
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+        kd[i] = (i < a.per && e0 + i < a.E) ? static_cast<double>(row[e0 + i]) : none;
+        if (kd[i] > nm.lmax) nm.lmax = kd[i];   // false for NaN
+    }
     if (!sg) {
-        for (int e = e0; e < e1; ++e) {
-            const double l = row[e];
-            if (l > nm.lmax) nm.lmax = l;   // false for NaN
-        }
         nm.lmax = warp_max(nm.lmax);
         double sum = 0.0;
-        nm.inv = 1.0;
-        for (int e = e0; e < e1; ++e) sum += score_of(static_cast<double>(row[e]), nm, false);
+#pragma unroll
+        for (int i = 0; i < NPER; ++i) sum += score_of(kd[i], nm, false);
         sum = warp_sum(sum);
         nm.inv = sum > 0.0 ? 1.0 / sum : 0.0;
     }
-    auto key = [&](int e) {
-        const float l = row[e];
-        return key_of<double>(l, score_of(static_cast<double>(l), nm, sg),
-                              a.bias ? a.bias[e] : 0.0f);
-    };
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+        const int e = e0 + i;
+        const bool in = i < a.per && e < a.E;
+        kd[i] = key_of<double>(in ? row[e] : -INFINITY, score_of(kd[i], nm, sg),
+                               (in && a.bias) ? a.bias[e] : 0.0f);
+    }
     uint32_t groups = 0xFFFFFFFFu;   // the groups chosen, one bit each
+    const int size = a.E / a.n_group;
     if (a.n_group > 1) {
-        const int size = a.E / a.n_group;
         double mine = none;   // lane g: group g's score
         for (int g = 0; g < a.n_group; ++g) {
             double b1 = none, b2 = none;
-            for (int e = max(e0, g * size); e < min(e1, (g + 1) * size); ++e) insert2(b1, b2, key(e));
+#pragma unroll
+            for (int i = 0; i < NPER; ++i) {
+                const int e = e0 + i;
+                if (i < a.per && e >= g * size && e < (g + 1) * size) insert2(b1, b2, kd[i]);
+            }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 const double c1 = __shfl_xor_sync(0xFFFFFFFFu, b1, o);
@@ -159,73 +184,67 @@ __device__ __noinline__ int route_exact(const ScoreArgs &a, const float *row) {
         }
         groups = __ballot_sync(0xFFFFFFFFu, lane < a.n_group && rank < a.topk_group);
     }
-    // k rounds: the best expert after the previous choice in (key, id) order
-    double last = 0.0;
-    int last_id = -1, my = -1;
-    const int size = a.n_group > 1 ? a.E / a.n_group : a.E;
-    auto before = [](double ka, int ia, double kb, int ib) {   // (ka, ia) ranks above (kb, ib)
-        if (ib < 0) return ia >= 0;
-        if (ia < 0) return false;
-        const bool na = isnan(ka), nb = isnan(kb);
-        if (na || nb) return na && nb ? ia < ib : nb;
-        return ka > kb || (ka == kb && ia < ib);
-    };
-    for (int j = 0; j < a.k; ++j) {
-        double bk = 0.0;
-        int bi = -1;
-        for (int e = e0; e < e1; ++e) {
-            if (a.n_group > 1 && !((groups >> (e / size)) & 1u)) continue;
-            const double ke = key(e);
-            if (last_id >= 0 && !before(last, last_id, ke, e)) continue;
-            if (before(ke, e, bk, bi)) {
-                bk = ke;
-                bi = e;
-            }
-        }
+    uint64_t key[NPER];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const double ok = __shfl_xor_sync(0xFFFFFFFFu, bk, o);
-            const int oi = __shfl_xor_sync(0xFFFFFFFFu, bi, o);
-            if (before(ok, oi, bk, bi)) {
-                bk = ok;
-                bi = oi;
+    for (int i = 0; i < NPER; ++i) {
+        const int e = e0 + i;
+        const bool in = i < a.per && e < a.E && ((groups >> min(e / size, 31)) & 1u);
+        key[i] = in ? ordered(kd[i]) : 0ull;
+    }
+    int my = -1;
+    for (int j = 0; j < a.k; ++j) {
+        uint64_t best = 0ull;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < NPER; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
             }
-        }
-        last = bk;
-        last_id = bi;
-        if (lane == j) my = bi;
+        const uint32_t bh = static_cast<uint32_t>(best >> 32), bl = static_cast<uint32_t>(best);
+        const uint32_t mh = __reduce_max_sync(0xFFFFFFFFu, bh);
+        const uint32_t ml = __reduce_max_sync(0xFFFFFFFFu, bh == mh ? bl : 0u);
+        const int w = __ffs(__ballot_sync(0xFFFFFFFFu, bh == mh && bl == ml)) - 1;
+        const int id = __shfl_sync(0xFFFFFFFFu, e0 + at, w);
+        if (lane == j) my = id;
+#pragma unroll
+        for (int i = 0; i < NPER; ++i)
+            if (lane == w && i == at) key[i] = 0ull;
     }
     return my;
 }
 
-template <int NPER>
-__global__ void __launch_bounds__(kScoreWarps * 32) route_scored_kernel(const ScoreArgs a) {
-    pdl_wait();
-    pdl_trigger();
+// exp(-l) and the reciprocal by the fast units; its error is in the bounds below
+__device__ __forceinline__ float fast_sigmoid(float l) {
+    return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-l)));
+}
+
+// Routes the warp's token: writes its choices and weights; lane j returns choice
+// j's expert (lanes >= k: -1).  kLogit: the keys are ordered as the logits.
+template <int NPER, bool kLogit>
+__device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
     const int lane = threadIdx.x & 31;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kScoreWarps + (threadIdx.x >> 5);
-    if (t >= a.T) return;
     const float *row = a.logits + t * a.ldl;
     const bool sg = a.sigmoid != 0;
     const int e0 = lane * a.per;
+    const float none = -INFINITY;
     float l[NPER];
-    if (a.vec) {   // per == NPER, a multiple of 4, everything on 16-byte boundaries
+    if (NPER % 4 == 0 && a.vec) {   // per == NPER, everything on 16-byte boundaries
 #pragma unroll
-        for (int i = 0; i < NPER; i += 4) {
-            float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        for (int i = 0; i + 3 < NPER; i += 4) {
+            float4 f = make_float4(none, none, none, none);
             if (e0 + i < a.E) f = *reinterpret_cast<const float4 *>(row + e0 + i);
             l[i] = f.x;
-            if (NPER > 1) l[i + (NPER > 1)] = f.y;
-            if (NPER > 2) l[i + (NPER > 2) * 2] = f.z;
-            if (NPER > 3) l[i + (NPER > 3) * 3] = f.w;
+            l[i + 1] = f.y;
+            l[i + 2] = f.z;
+            l[i + 3] = f.w;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < NPER; ++i)
-            l[i] = (i < a.per && e0 + i < a.E) ? row[e0 + i] : -INFINITY;
+        for (int i = 0; i < NPER; ++i) l[i] = (i < a.per && e0 + i < a.E) ? row[e0 + i] : none;
     }
-    Norm<float> nm{-INFINITY, 1.0f};
-    if (!sg) {
+    Norm<float> nm{none, 1.0f};
+    if (!sg && (!kLogit || !a.renorm)) {
 #pragma unroll
         for (int i = 0; i < NPER; ++i) nm.lmax = fmaxf(nm.lmax, l[i]);   // skips NaN
         nm.lmax = warp_max(nm.lmax);
@@ -240,127 +259,193 @@ __global__ void __launch_bounds__(kScoreWarps * 32) route_scored_kernel(const Sc
     for (int i = 0; i < NPER; ++i) {
         const int e = e0 + i;
         const bool in = i < a.per && e < a.E;
-        const float s = score_of(l[i], nm, sg);
-        key[i] = in ? ordered(key_of<float>(l[i], s, (a.bias && in) ? a.bias[e] : 0.0f)) : 0u;
+        float k = l[i];
+        if constexpr (!kLogit) {
+            // a NaN logit gives a NaN score and key; a -inf logit masks its expert
+            k = sg ? fast_sigmoid(k) : score_of(k, nm, false);
+            if (a.bias && in) k = __fadd_rn(k, a.bias[e]);
+            if (l[i] == none && !isnan(k)) k = none;
+            if (isnan(l[i])) k = l[i];
+        }
+        key[i] = in ? ordered(k) : 0u;
     }
-    // Bounds on the fp32 errors, in units of 2^-23.  With a bias: a sigmoid is
-    // within 4, a softmax score within (32 + |l - lmax|) s <= 32 smax (expf, the
-    // difference's rounding, a sum of up to 1024 terms in trees), and the key's own
-    // rounding adds |key|.  Without one the key is the score: a sigmoid is within 4 s,
-    // and of a softmax score what all share (the sum) leaves their order alone and
-    // the rest is within (5 + |l - lmax|) s, |l - lmax| <= 104 where it is not 0.
-    const float u = 0x1p-23f, tiny = 0x1p-140f;   // tiny: subnormal results
-    const float cap = a.bias ? (sg ? 4.0f : 32.0f * nm.inv) * u : 0.0f;
-    const float rel = (a.bias ? 1.0f : sg ? 5.0f : 110.0f) * u;
+    // the lane's two largest keys (0: none), the lower id first among equals
+    uint32_t k1 = 0u, k2 = 0u;
+    int i1 = 0, i2 = 0;
+    auto scan = [&]() {
+        k1 = k2 = 0u;
+#pragma unroll
+        for (int i = 0; i < NPER; ++i) {
+            if (key[i] > k1) {
+                k2 = k1;
+                i2 = i1;
+                k1 = key[i];
+                i1 = i;
+            } else if (key[i] > k2) {
+                k2 = key[i];
+                i2 = i;
+            }
+        }
+    };
+    scan();
+    // Bounds on the fp32 errors of keys, in units of u = 2^-23 (kLogit: none needed).
+    // Scores: the fast sigmoid is within (2 + 1.2 |l|) (1 - s) + 2.5 relative, at most
+    // 5 absolute; a softmax score within 2.5 + 1.7 d relative (expf, the rounding of
+    // d = lmax - l) and what all share, the sum of up to 1024 terms (38).  With a bias
+    // that is absolute: 5, or 40 smax, and the key's rounding adds |key|.  Without one
+    // what all share leaves the order alone: (8 + 2 d) s, d = -ln(s / smax) >= |l|, d.
+    const float u = 0x1p-23f, tiny = 0x1p-124f;   // tiny: below the fast units' range
+    const float cap = a.bias ? (sg ? 5.0f : 40.0f * nm.inv) * u : 0.0f;
+    auto err_of = [&](float k) {
+        if (a.bias) return cap + fabsf(k) * u;
+        const float d = k > 0.0f ? fmaxf(0.0f, -__logf(sg ? k : __fdividef(k, nm.inv))) : 104.0f;
+        return fabsf(k) * (8.0f + 2.0f * d) * u + tiny;
+    };
     bool near = false;
     if (a.n_group > 1) {
         const int size = a.E / a.n_group;
-        const float none = -INFINITY;
-        float mine = none, err = 0.0f;   // lane g: group g's score and its bound
-        for (int g = 0; g < a.n_group; ++g) {
-            float b1 = none, b2 = none;
+        float mine = none, err = 0.0f;   // group g's score and its bound, in lane `at_g`
+        auto finish = [&](uint32_t b1, uint32_t b2) {
+            const float f1 = from_ordered(b1), f2 = from_ordered(b2);
+            mine = group_score(f1, f2, a.group_top);
+            if constexpr (!kLogit) {
+                if (f1 > none) err = err_of(f1);
+                if (a.group_top == 2 && f2 > none) err += err_of(f2) + fabsf(mine) * u;
+            }
+        };
+        const uint32_t floor = 0x007FFFFFu;   // -inf: NaN and absent keys count as that
+        int my_group;                          // the group this lane's score is of (n_group: none)
+        if (a.lanes) {
+            // a group is `lanes` whole lanes: all groups at once
+            uint32_t b1 = max(k1, floor), b2 = max(k2, floor);
+            auto merge = [&](uint32_t c1, uint32_t c2) {
+                b2 = max(min(b1, c1), max(b2, c2));
+                b1 = max(b1, c1);
+            };
+            if ((a.lanes & (a.lanes - 1)) == 0) {
+                for (int o = 1; o < a.lanes; o <<= 1) {
+                    const uint32_t c1 = __shfl_xor_sync(0xFFFFFFFFu, b1, o);
+                    const uint32_t c2 = __shfl_xor_sync(0xFFFFFFFFu, b2, o);
+                    merge(c1, c2);
+                }
+            } else {
+                const uint32_t m1 = b1, m2 = b2;
+                const int first = lane - lane % a.lanes, me = lane - first;
+                for (int j = 1; j < a.lanes; ++j) {
+                    const int from = first + (me + j >= a.lanes ? me + j - a.lanes : me + j);
+                    const uint32_t c1 = __shfl_sync(0xFFFFFFFFu, m1, from & 31);
+                    const uint32_t c2 = __shfl_sync(0xFFFFFFFFu, m2, from & 31);
+                    merge(c1, c2);
+                }
+            }
+            finish(b1, b2);
+            my_group = min(lane / a.lanes, a.n_group);
+        } else {
+            uint32_t s1 = floor, s2 = floor;
+            for (int g = 0; g < a.n_group; ++g) {
+                uint32_t b1 = floor, b2 = floor;
 #pragma unroll
-            for (int i = 0; i < NPER; ++i) {
-                const int e = e0 + i;
-                if (key[i] > 1u && e >= g * size && e < (g + 1) * size)
-                    insert2(b1, b2, from_ordered(key[i]));
-            }
+                for (int i = 0; i < NPER; ++i) {
+                    const int e = e0 + i;
+                    const uint32_t v = (e >= g * size && e < (g + 1) * size) ? max(key[i], floor) : floor;
+                    b2 = max(min(b1, v), b2);
+                    b1 = max(b1, v);
+                }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const float c1 = __shfl_xor_sync(0xFFFFFFFFu, b1, o);
-                const float c2 = __shfl_xor_sync(0xFFFFFFFFu, b2, o);
-                insert2(b1, b2, c1);
-                insert2(b1, b2, c2);
+                for (int o = 16; o > 0; o >>= 1) {
+                    const uint32_t c1 = __shfl_xor_sync(0xFFFFFFFFu, b1, o);
+                    const uint32_t c2 = __shfl_xor_sync(0xFFFFFFFFu, b2, o);
+                    b2 = max(min(b1, c1), max(b2, c2));
+                    b1 = max(b1, c1);
+                }
+                if (lane == g) {
+                    s1 = b1;
+                    s2 = b2;
+                }
             }
-            if (lane == g) {
-                mine = group_score(b1, b2, a.group_top);
-                if (b1 > none) err = cap + fabsf(b1) * rel + tiny;
-                if (a.group_top == 2 && b2 > none)
-                    err += cap + fabsf(b2) * rel + fabsf(mine) * u + tiny;
-            }
+            finish(s1, s2);
+            my_group = min(lane, a.n_group);
         }
+        const int step = a.lanes ? a.lanes : 1;
         int rank = 0;
         for (int g = 0; g < a.n_group; ++g) {
-            const float o = __shfl_sync(0xFFFFFFFFu, mine, g);
-            rank += o > mine || (o == mine && g < lane);
+            const float o = __shfl_sync(0xFFFFFFFFu, mine, g * step);
+            rank += o > mine || (o == mine && g < my_group);
         }
-        const bool have = lane < a.n_group;
-        const uint32_t groups = __ballot_sync(0xFFFFFFFFu, have && rank < a.topk_group);
-        if (a.topk_group < a.n_group) {
+        const bool have = my_group < a.n_group;
+        const bool stays = have && rank < a.topk_group;
+        if constexpr (!kLogit) {
             const int in_at = __ffs(__ballot_sync(0xFFFFFFFFu, have && rank == a.topk_group - 1)) - 1;
             const int out_at = __ffs(__ballot_sync(0xFFFFFFFFu, have && rank == a.topk_group)) - 1;
-            const float in = __shfl_sync(0xFFFFFFFFu, mine, max(in_at, 0));
-            const float out = __shfl_sync(0xFFFFFFFFu, mine, max(out_at, 0));
-            const float worst = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(err)));
+            const float in = __shfl_sync(0xFFFFFFFFu, mine, in_at);
+            const float out = __shfl_sync(0xFFFFFFFFu, mine, out_at);
+            const float worst = __uint_as_float(
+                __reduce_max_sync(0xFFFFFFFFu, have ? __float_as_uint(err) : 0u));
             // (both -inf: no key in either; they go by id)
             near = out > none && !(in - out > 2.0f * worst);
+        }
+        if (a.lanes) {
+            if (!stays) k1 = k2 = 0u;
+            if (!stays)
+#pragma unroll
+                for (int i = 0; i < NPER; ++i) key[i] = 0u;
+        } else {
+            const uint32_t groups = __ballot_sync(0xFFFFFFFFu, stays);
 #pragma unroll
             for (int i = 0; i < NPER; ++i)
                 if (!((groups >> min((e0 + i) / size, 31)) & 1u)) key[i] = 0u;
+            scan();
         }
     }
-    // k rounds, and one more for the best key left out
-    uint32_t best = 0u, next_u = 0u;
-    int at = 0, my = -1, next = -1;
+    // k rounds; then the best key left out
+    int my = -1;
     uint32_t my_u = 0u;
-    auto rescan = [&]() {
-        best = 0u;
-#pragma unroll
-        for (int i = 0; i < NPER; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-            }
-    };
-    rescan();
-    for (int j = 0; j <= a.k; ++j) {
-        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
-        const int w = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
-        const int id = __shfl_sync(0xFFFFFFFFu, e0 + at, w);
-        if (j == a.k) {
-            next = m ? id : -1;
-            next_u = m;
-        } else if (lane == j) {
+    for (int j = 0; j < a.k; ++j) {
+        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, k1);
+        const int w = __ffs(__ballot_sync(0xFFFFFFFFu, k1 == m)) - 1;
+        const int id = __shfl_sync(0xFFFFFFFFu, e0 + i1, w);
+        if (lane == j) {
             my = id;
             my_u = m;
         }
         if (lane == w) {
 #pragma unroll
             for (int i = 0; i < NPER; ++i)
-                if (i == at) key[i] = 0u;
-            rescan();
+                if (i == i1) key[i] = 0u;
+            if (k2) {
+                k1 = k2;
+                i1 = i2;
+                k2 = 0u;
+            } else {
+                scan();
+            }
         }
     }
-    // choice j against the one after it (the last against the best left out)
-    float ml = 0.0f, mb = 0.0f;
-    if (lane < a.k) {
-        ml = row[my];
-        mb = a.bias ? a.bias[my] : 0.0f;
-    }
-    {
-        const float nl = next >= 0 ? row[next] : 0.0f;
-        const float nb = (next >= 0 && a.bias) ? a.bias[next] : 0.0f;
+    float ml = lane < a.k ? row[my] : 0.0f;
+    if constexpr (!kLogit) {
+        // choice j against the one after it, the last against the best left out
+        const uint32_t next_u = __reduce_max_sync(0xFFFFFFFFu, k1);
+        const int w = __ffs(__ballot_sync(0xFFFFFFFFu, k1 == next_u)) - 1;
+        const int next = __shfl_sync(0xFFFFFFFFu, e0 + i1, w);
+        const float mb = (lane < a.k && a.bias) ? a.bias[my] : 0.0f;
         uint32_t ou = __shfl_down_sync(0xFFFFFFFFu, my_u, 1);
         float ol = __shfl_down_sync(0xFFFFFFFFu, ml, 1);
         float ob = __shfl_down_sync(0xFFFFFFFFu, mb, 1);
-        const bool last = lane == a.k - 1;
-        if (last) {
+        if (lane == a.k - 1) {
             ou = next_u;
-            ol = nl;
-            ob = nb;
+            ol = next_u ? row[next] : 0.0f;
+            ob = (next_u && a.bias) ? a.bias[next] : 0.0f;
         }
-        // both finite (above -inf and below +inf as ordered integers)
-        const uint32_t lo = 0x007FFFFFu, hi = 0xFF800000u;
-        if (lane < a.k && ou > lo && my_u < hi) {
+        // both finite: above -inf and below +inf as ordered integers
+        if (lane < a.k && ou > 0x007FFFFFu && my_u < 0xFF800000u) {
             const float ka = from_ordered(my_u), kb = from_ordered(ou);
-            const float bound = 2.0f * cap + (fabsf(ka) + fabsf(kb)) * rel + tiny;
             const bool same = my_u == ou && ml == ol && mb == ob;
-            near = near || (!same && !(ka - kb > bound));
+            near = near || (!same && !(ka - kb > err_of(ka) + err_of(kb)));
         }
-    }
-    if (__any_sync(0xFFFFFFFFu, near)) {
-        my = route_exact(a, row);
-        if (lane < a.k) ml = row[my];
+        if (__any_sync(0xFFFFFFFFu, near)) {
+            my = route_exact<NPER>(a, row);
+            if (lane < a.k) ml = row[my];
+        }
     }
     // weights, from the scores alone
     float w;
@@ -369,14 +454,14 @@ __global__ void __launch_bounds__(kScoreWarps * 32) route_scored_kernel(const Sc
         // are exp(l) to fp32) exp(l - the largest chosen logit), which cannot underflow
         // together
         const bool num = lane < a.k && !isnan(ml);
-        const float lc = warp_max(num ? ml : -INFINITY);
+        const float lc = warp_max(num ? ml : none);
         float x = 0.0f;
-        if (num && ml > -INFINITY) {
+        if (num && ml > none) {
             if (sg && lc > -40.0f) x = score_of(ml, nm, true);
             else if (lc == INFINITY) x = ml == lc ? 1.0f : 0.0f;
             else x = expf(__fsub_rn(ml, lc));
         }
-        if (lc == -INFINITY && lane < a.k) x = 1.0f;   // every choice masked: equal weights
+        if (lc == none && lane < a.k) x = 1.0f;   // every choice masked: equal weights
         float s = 0.0f;
         for (int j = 0; j < a.k; ++j) s = __fadd_rn(s, __shfl_sync(0xFFFFFFFFu, x, j));
         w = __fdiv_rn(x, s);
@@ -387,17 +472,192 @@ __global__ void __launch_bounds__(kScoreWarps * 32) route_scored_kernel(const Sc
         a.topk_id[t * a.k + lane] = my;
         a.topk_w[t * a.k + lane] = __fmul_rn(w, a.scale);
     }
+    return lane < a.k ? my : -1;
+}
+
+// exclusive prefix over the block's threads in order, E <= blockDim.x values
+// (threads >= E pass 0); s_warp: 32 ints
+__device__ __forceinline__ int block_exclusive(int v, int *s_warp) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += s_warp[w];
+    return before + x - v;
+}
+
+// Rows of the choices of tokens [t0, t1): s_start[e] = the first row of expert e's
+// choices in this chunk, s_map[e][words] = the bitmap of the chunk's tokens that
+// chose e.
+__device__ __forceinline__ void place_chunk(const int32_t *topk_id, int t0, int t1, int k, int words,
+                                            const int *s_start, const uint32_t *s_map,
+                                            int32_t *row_idx, int32_t *row_of) {
+    const int n = (t1 - t0) * k;
+    for (int c = threadIdx.x; c < n; c += blockDim.x) {
+        const int i = c / k, e = topk_id[static_cast<int64_t>(t0) * k + c];
+        const uint32_t *map = s_map + e * words;
+        int r = s_start[e] + __popc(map[i >> 5] & ((1u << (i & 31)) - 1u));
+        for (int w = 0; w < (i >> 5); ++w) r += __popc(map[w]);
+        row_of[static_cast<int64_t>(t0) * k + c] = r;
+        row_idx[r] = t0 + i;
+    }
+}
+
+// One block of `chunk` tokens: routes them and writes the chunk's counts per
+// expert, counts[chunk][E].
+template <int NPER, bool kLogit>
+__global__ void __launch_bounds__(1024) route_chunk_kernel(const ScoreArgs a, int32_t *counts) {
+    __shared__ int s_count[kMaxE];
+    pdl_wait();
+    pdl_trigger();
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) s_count[e] = 0;
+    __syncthreads();
+    const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
+    for (int t = t0 + (threadIdx.x >> 5); t < t1; t += blockDim.x >> 5) {
+        const int e = route_token<NPER, kLogit>(a, t);
+        if (e >= 0 && counts) atomicAdd(&s_count[e], 1);
+    }
+    if (!counts) return;
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
+        counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = s_count[e];
+}
+
+// The whole call in one block, for few tokens.
+template <int NPER, bool kLogit>
+__global__ void __launch_bounds__(1024) route_solo_kernel(const ScoreArgs a, int32_t *expert_off,
+                                                          int32_t *row_idx, int32_t *row_of) {
+    constexpr int kWords = kSoloTokens / 32;
+    __shared__ uint32_t s_map[kMaxE * kWords];
+    __shared__ int s_start[kMaxE];
+    __shared__ int s_warp[32];
+    pdl_wait();
+    pdl_trigger();
+    for (int e = threadIdx.x; e < a.E * kWords; e += blockDim.x) s_map[e] = 0u;
+    __syncthreads();
+    for (int t = threadIdx.x >> 5; t < a.T; t += blockDim.x >> 5) {
+        const int e = route_token<NPER, kLogit>(a, t);
+        if (e >= 0) atomicOr(&s_map[e * kWords + (t >> 5)], 1u << (t & 31));
+    }
+    __syncthreads();
+    // expert offsets, blockDim.x experts at a time
+    int base = 0;
+    for (int e0 = 0; e0 < a.E; e0 += blockDim.x) {
+        const int e = e0 + threadIdx.x;
+        int n = 0;
+        if (e < a.E)
+            for (int w = 0; w < kWords; ++w) n += __popc(s_map[e * kWords + w]);
+        const int at = base + block_exclusive(n, s_warp);
+        if (e < a.E) {
+            s_start[e] = at;
+            expert_off[e] = at;
+            if (e == a.E - 1) expert_off[a.E] = at + n;
+        }
+        __syncthreads();
+        for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) base += s_warp[w];
+        __syncthreads();
+    }
+    place_chunk(a.topk_id, 0, a.T, a.k, kWords, s_start, s_map, row_idx, row_of);
+}
+
+// One block a chunk: where each expert's rows of the chunk start, then the rows.
+__global__ void __launch_bounds__(kPlaceThreads)
+    route_place_kernel(const int32_t *__restrict__ topk_id, const int32_t *__restrict__ counts, int T,
+                       int E, int k, int chunk, int chunks, int32_t *__restrict__ expert_off,
+                       int32_t *__restrict__ row_idx, int32_t *__restrict__ row_of) {
+    extern __shared__ uint32_t s_map[];   // [E][words]
+    __shared__ int s_before[kMaxE], s_all[kMaxE];
+    __shared__ int s_warp[32];
+    const int words = (chunk + 31) / 32;
+    for (int e = threadIdx.x; e < E; e += kPlaceThreads) s_before[e] = s_all[e] = 0;
+    for (int i = threadIdx.x; i < E * words; i += kPlaceThreads) s_map[i] = 0u;
+    pdl_wait();
+    pdl_trigger();
+    __syncthreads();
+    // counts of earlier chunks and of all, a column (expert) of the table per
+    // thread, the rows shared out over the threads of a column
+    const int cols = min((E + 31) & ~31, kPlaceThreads), segs = kPlaceThreads / cols;
+    const int e = threadIdx.x % cols, seg = threadIdx.x / cols;
+    if (e < E && seg < segs) {
+        int before = 0, all = 0;
+#pragma unroll 8
+        for (int c = seg; c < chunks; c += segs) {
+            const int n = counts[static_cast<int64_t>(c) * E + e];
+            all += n;
+            before += c < static_cast<int>(blockIdx.x) ? n : 0;
+        }
+        atomicAdd(&s_before[e], before);
+        atomicAdd(&s_all[e], all);
+    }
+    const int t0 = blockIdx.x * chunk, t1 = min(T, t0 + chunk), n = (t1 - t0) * k;
+    for (int c = threadIdx.x; c < n; c += kPlaceThreads) {
+        const int i = c / k, x = topk_id[static_cast<int64_t>(t0) * k + c];
+        atomicOr(&s_map[x * words + (i >> 5)], 1u << (i & 31));
+    }
+    __syncthreads();
+    const int x = threadIdx.x;
+    const int tot = x < E ? s_all[x] : 0;
+    const int at = block_exclusive(tot, s_warp);
+    if (x < E) {
+        s_before[x] += at;
+        if (blockIdx.x == 0) {
+            expert_off[x] = at;
+            if (x == E - 1) expert_off[E] = at + tot;
+        }
+    }
+    __syncthreads();
+    place_chunk(topk_id, t0, t1, k, words, s_before, s_map, row_idx, row_of);
+}
+
+// The chunks of a call with a workspace: about as many as the card has SMs, each
+// of at most 512 tokens (the bitmaps' shared memory).
+struct Chunks {
+    int64_t size, count;
+};
+inline Chunks route_chunks(int64_t T) {
+    constexpr int64_t kSms = 152;
+    int64_t size = (T + kSms - 1) / kSms;
+    if (size < 4) size = 4;
+    if (size > 512) size = 512;
+    return Chunks{size, (T + size - 1) / size};
+}
+
+template <int NPER, bool kLogit>
+cudaError_t launch_scored(const ScoreArgs &a, int32_t *counts, int64_t blocks, bool solo,
+                          int32_t *expert_off, int32_t *row_idx, int32_t *row_of, cudaStream_t s) {
+    const int warps = a.chunk < 32 ? a.chunk : 32;
+    if (solo)
+        return launch_pdl(route_solo_kernel<NPER, kLogit>, dim3(1), dim3(warps * 32), 0, s, a,
+                          expert_off, row_idx, row_of);
+    return launch_pdl(route_chunk_kernel<NPER, kLogit>, dim3(static_cast<unsigned>(blocks)),
+                      dim3(warps * 32), 0, s, a, counts);
 }
 
 }  // namespace
 }  // namespace h32
+
+extern "C" h32_status h32_moe_route_scored_workspace_bytes(int64_t T, int32_t E, size_t *bytes) {
+    using namespace h32;
+    if (!bytes) return H32_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (T < 0 || T > 0x7FFFFFFFll || E < 1 || E > kMaxE) return H32_ERR_INVALID_ARG;
+    if (T > kSoloTokens) *bytes = static_cast<size_t>(route_chunks(T).count) * E * 4;
+    return H32_OK;
+}
 
 extern "C" h32_status h32_moe_route_scored(const float *logits, int64_t T, int32_t E, int64_t ldl,
                                            int32_t score, const float *bias, int32_t n_group,
                                            int32_t topk_group, int32_t group_top, int32_t k,
                                            int32_t renormalize, float scale, int32_t *topk_id,
                                            float *topk_w, int32_t *expert_off, int32_t *row_idx,
-                                           int32_t *row_of, void *stream) {
+                                           int32_t *row_of, void *workspace,
+                                           size_t workspace_bytes, void *stream) {
     using namespace h32;
     if (T < 0 || E < 1 || E > kMaxE || k < 1 || k > kMaxK || k > E || ldl < E || !expert_off)
         return H32_ERR_INVALID_ARG;
@@ -413,44 +673,74 @@ extern "C" h32_status h32_moe_route_scored(const float *logits, int64_t T, int32
     if (off4(logits) || off4(bias) || off4(expert_off) || (topk_id && !aligned16(topk_id)) ||
         off4(topk_w) || off4(row_idx) || off4(row_of))
         return H32_ERR_ALIGNMENT;
+    const bool solo = T <= kSoloTokens;
+    const Chunks ch = route_chunks(T);
+    if (workspace && !solo) {
+        if (workspace_bytes < static_cast<size_t>(ch.count) * E * 4) return H32_ERR_INVALID_ARG;
+        if (!aligned16(workspace)) return H32_ERR_ALIGNMENT;
+    }
     H32_TRY(check_device(nullptr));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (T > 0) {
-        ScoreArgs a{};
-        a.logits = logits;
-        a.bias = bias;
-        a.ldl = ldl;
-        a.T = static_cast<int32_t>(T);
-        a.E = E;
-        a.k = k;
-        a.n_group = n_group;
-        a.topk_group = topk_group;
-        a.group_top = group_top;
-        a.per = (E + 31) / 32;
-        a.sigmoid = score == H32_SCORE_SIGMOID;
-        a.renorm = renormalize != 0;
-        a.scale = scale;
-        a.topk_id = topk_id;
-        a.topk_w = topk_w;
-        const dim3 grid(static_cast<unsigned>((T + kScoreWarps - 1) / kScoreWarps));
-        const dim3 block(kScoreWarps * 32);
-        const bool v4 = E % 4 == 0 && ldl % 4 == 0 && aligned16(logits);
-        cudaError_t e1;
-#define H32_SCORED(N)                                                     \
-    do {                                                                  \
-        a.vec = v4 && (N) % 4 == 0 && a.per == (N);                       \
-        e1 = launch_pdl(route_scored_kernel<N>, grid, block, 0, s, a);    \
-    } while (0)
-        if (a.per <= 1) H32_SCORED(1);
-        else if (a.per <= 2) H32_SCORED(2);
-        else if (a.per <= 4) H32_SCORED(4);
-        else if (a.per <= 8) H32_SCORED(8);
-        else if (a.per <= 16) H32_SCORED(16);
-        else H32_SCORED(32);
-#undef H32_SCORED
-        if (e1 != cudaSuccess) return launch_status(e1);
+    const int t32 = static_cast<int>(T);
+    if (T == 0)
+        return launch_status(launch_route_group(topk_id, 0, E, k, expert_off, row_idx, row_of, s));
+    ScoreArgs a{};
+    a.logits = logits;
+    a.bias = bias;
+    a.ldl = ldl;
+    a.T = t32;
+    a.E = E;
+    a.k = k;
+    a.n_group = topk_group == n_group ? 1 : n_group;   // all groups stay: no groups
+    a.topk_group = topk_group;
+    a.group_top = group_top;
+    a.sigmoid = score == H32_SCORE_SIGMOID;
+    a.renorm = renormalize != 0;
+    a.scale = scale;
+    a.topk_id = topk_id;
+    a.topk_w = topk_w;
+    a.chunk = static_cast<int32_t>(solo ? T : workspace ? ch.size : 8);
+    const int64_t blocks = solo ? 1 : workspace ? ch.count : (T + 7) / 8;
+    // experts a lane: the fewest, or the next divisor of a group's size, so that
+    // groups are whole lanes
+    const int fewest = (E + 31) / 32;
+    a.per = fewest;
+    if (a.n_group > 1) {
+        const int size = E / a.n_group;
+        for (int d = fewest; d <= 32 && d <= size; ++d)
+            if (size % d == 0) {
+                a.per = d;
+                a.lanes = size / d;
+                break;
+            }
     }
-    const cudaError_t e2 = launch_route_group(topk_id, static_cast<int>(T), E, k, expert_off, row_idx,
-                                              row_of, s);
-    return launch_status(e2 != cudaSuccess ? e2 : cudaGetLastError());
+    const bool v4 = E % 4 == 0 && ldl % 4 == 0 && aligned16(logits);
+    const bool by_logit = !bias && (a.n_group == 1 || group_top == 1);
+    int32_t *counts = solo ? nullptr : static_cast<int32_t *>(workspace);
+    cudaError_t e;
+#define H32_SCORED(N)                                                                             \
+    do {                                                                                          \
+        a.vec = v4 && (N) % 4 == 0 && a.per == (N);                                               \
+        e = by_logit ? launch_scored<N, true>(a, counts, blocks, solo, expert_off, row_idx, row_of, s) \
+                     : launch_scored<N, false>(a, counts, blocks, solo, expert_off, row_idx, row_of, s); \
+    } while (0)
+    if (a.per <= 1) H32_SCORED(1);
+    else if (a.per <= 2) H32_SCORED(2);
+    else if (a.per <= 4) H32_SCORED(4);
+    else if (a.per <= 8) H32_SCORED(8);
+    else if (a.per <= 16) H32_SCORED(16);
+    else H32_SCORED(32);
+#undef H32_SCORED
+    if (e != cudaSuccess || solo) return launch_status(e != cudaSuccess ? e : cudaGetLastError());
+    if (!workspace)
+        return launch_status(launch_route_group(topk_id, t32, E, k, expert_off, row_idx, row_of, s));
+    const size_t smem = static_cast<size_t>(E) * ((ch.size + 31) / 32) * 4;
+    if (smem > 32768) {   // above what a kernel may use beside its static arrays unasked
+        e = cudaFuncSetAttribute(route_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
+        if (e != cudaSuccess) return launch_status(e);
+    }
+    e = launch_pdl(route_place_kernel, dim3(static_cast<unsigned>(ch.count)), dim3(kPlaceThreads), smem,
+                   s, topk_id, counts, t32, E, k, static_cast<int>(ch.size),
+                   static_cast<int>(ch.count), expert_off, row_idx, row_of);
+    return launch_status(e != cudaSuccess ? e : cudaGetLastError());
 }

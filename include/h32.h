@@ -569,9 +569,10 @@ typedef enum h32_score {
  *     `renormalize` scale * s_j / sum of the k chosen scores, in fp32;
  * then the rows are grouped by expert as by h32_moe_route, with the same outputs
  * topk_id, topk_w, expert_off, row_idx, row_of (and their alignment).
- * Keys and group scores are ordered by their values in double precision, so ids,
- * offsets and row maps do not depend on fp32 rounding; the weights are within a
- * few ulps.  Deterministic.
+ * The order of keys is exact: without a bias, and with groups by their best key,
+ * that of the logits; else that of the keys' (and group scores') values in double
+ * precision.  So ids, offsets and row maps do not depend on fp32 rounding; the
+ * weights are within a few ulps.  Deterministic.
  * Logits that are not finite: a -inf logit masks its expert (score 0, key -inf
  * whatever the bias); a NaN logit or bias ranks below it; +inf logits share the
  * softmax equally.  Masked experts are chosen only when fewer than k others are
@@ -581,13 +582,18 @@ typedef enum h32_score {
  * n_group, 1 <= k <= min(32, topk_group E / n_group), T k < 2^31, a finite scale;
  * logits (row pitch ldl >= E) and bias [E] 4-byte aligned.  T = 0 writes all-zero
  * offsets.
+ *   workspace    nullable, 16-byte aligned device memory of at least
+ *                h32_moe_route_scored_workspace_bytes (0 bytes up to 64 tokens); any
+ *                contents, free again when the call's work is done.  Without it
+ *                more than 64 tokens are grouped as by h32_moe_route (slower).
  */
+h32_status h32_moe_route_scored_workspace_bytes(int64_t T, int32_t E, size_t *bytes);
 h32_status h32_moe_route_scored(const float *logits, int64_t T, int32_t E, int64_t ldl,
                                 int32_t score, const float *bias, int32_t n_group,
                                 int32_t topk_group, int32_t group_top, int32_t k,
                                 int32_t renormalize, float scale, int32_t *topk_id, float *topk_w,
                                 int32_t *expert_off, int32_t *row_idx, int32_t *row_of,
-                                void *stream);
+                                void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * The weighted combine after the expert GEMMs: the k expert outputs of each

@@ -357,12 +357,15 @@ def moe_route_scored(logits: np.ndarray, k: int, score: str = "softmax",
             key = np.where(l == -np.inf, -np.inf, s + b)
             key = np.where(np.isnan(l) | np.isnan(b), np.nan, key)
             gs = []
+            by = l if bias is None and group_top == 1 else key
             for g in range(n_group):
-                kg = key[g * size:(g + 1) * size]
+                kg = by[g * size:(g + 1) * size]
                 kg = np.sort(kg[kg > -np.inf])[::-1][:group_top]
                 gs.append(kg.sum() if kg.size else -np.inf)
             stay = sorted(range(n_group), key=lambda g: (-gs[g], g))[:topk_group]
             cand = [e for e in range(E) if e // size in stay]
+            if bias is None and (group_top == 1 or topk_group == n_group):
+                key = l    # scores grow with their logits: the same order, without ties
             cand.sort(key=lambda e: (np.isnan(key[e]), 0.0 if np.isnan(key[e]) else -key[e], e))
             ids[t] = cand[:k]
             c = s[ids[t]]

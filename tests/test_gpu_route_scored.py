@@ -147,6 +147,55 @@ def test_many_tokens(h32, T, E, k):
            score="sigmoid", n_group=8, topk_group=4, group_top=2, scale=2.5)
 
 
+@pytest.mark.parametrize("T", [63, 64, 65, 153, 609, 700])
+def test_token_counts_around_the_launch_shapes(h32, T):
+    """One block up to 64 tokens, chunks beyond; odd last chunks; every expert count
+    of a lane; a shared row of choices (one expert with every token)."""
+    for E, k, G, tg, gt in ((8, 8, 1, 1, 1), (1024, 2, 1, 1, 1), (72, 6, 8, 3, 2), (640, 9, 5, 2, 2)):
+        l = _logits(T, E, T + E)
+        l[:, 3] = 9.0
+        _check(h32, l, k, None, n_group=G, topk_group=tg, group_top=gt)
+        _check(h32, l, k, np.full(E, 0.25, np.float32), score="sigmoid", n_group=G, topk_group=tg,
+               group_top=gt)
+
+
+def test_long_chunks(h32):
+    """Chunks of 512 tokens (bitmaps of 16 words an expert), more chunks than SMs."""
+    _check_fast(h32, 90001, 1024, 2)
+    _check_fast(h32, 78000, 16, 4)
+
+
+def _check_fast(h32, T, E, k):
+    l = _logits(T, E, 77)
+    ids, w, off, ridx, row_of = (np_of(t) for t in h32.h32_moe_route_scored(torch_of(l), k))
+    assert h32.h32_device_status() == 0
+    rid = np.argsort(-l, axis=1, kind="stable")[:, :k].astype(np.int32)
+    assert np.array_equal(ids, rid)
+    tok = np.repeat(np.arange(T), k)
+    order = np.lexsort((tok, rid.reshape(-1)))
+    assert np.array_equal(ridx, tok[order])
+    back = np.empty(T * k, np.int32)
+    back[order] = np.arange(T * k)
+    assert np.array_equal(row_of.reshape(-1), back)
+    assert np.array_equal(off, np.concatenate(([0], np.cumsum(np.bincount(rid.reshape(-1), minlength=E)))))
+
+
+def test_without_a_workspace(h32):
+    """The library call with a null workspace groups the rows all the same."""
+    import ctypes
+    import torch
+    T, E, k = 300, 96, 5
+    l = torch_of(_logits(T, E, 6))
+    want = h32.h32_moe_route_scored(l, k, score="sigmoid", renormalize=False)
+    got = [torch.full_like(t, -3) for t in want]
+    v = ctypes.c_void_p
+    st = h32.lib().h32_moe_route_scored(
+        v(l.data_ptr()), T, E, E, 1, v(0), 1, 1, 1, k, 0, 1.0, *(v(t.data_ptr()) for t in got), v(0), 0,
+        v(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert st == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_softmax_without_bias_equals_the_plain_router(h32):
     """The same ids, offsets and row maps as h32_moe_route, weights within both bounds."""
     import torch

@@ -39,20 +39,21 @@ def test_library_refusals():
     p = 4096
 
     def call(l=p, T=4, E=16, ldl=16, score=0, bias=None, G=1, tg=1, gt=1, k=2, rn=1, scale=1.0,
-             ids=p, w=p, off=p, ridx=p, rof=p):
+             ids=p, w=p, off=p, ridx=p, rof=p, ws=None, nws=0):
         v = ctypes.c_void_p
         return h32.lib().h32_moe_route_scored(v(l), T, E, ldl, score, v(bias), G, tg, gt, k, rn, scale,
-                                              v(ids), v(w), v(off), v(ridx), v(rof), v(0))
+                                              v(ids), v(w), v(off), v(ridx), v(rof), v(ws), nws,
+                                              v(0))
 
     for kw in (dict(T=-1), dict(E=0), dict(E=1025, ldl=1025), dict(ldl=15), dict(k=0), dict(k=17),
                dict(E=64, ldl=64, k=33), dict(score=2), dict(score=-1), dict(G=0), dict(G=3),
                dict(E=128, ldl=128, G=64), dict(G=4, tg=5), dict(G=4, tg=0), dict(gt=0), dict(gt=3),
                dict(G=8, tg=1, k=3), dict(scale=float("nan")), dict(scale=float("inf")),
                dict(l=None), dict(ids=None), dict(w=None), dict(off=None), dict(ridx=None),
-               dict(rof=None), dict(T=1 << 30)):
+               dict(rof=None), dict(T=1 << 30), dict(T=65, ws=p, nws=100)):
         assert call(**kw) == h32.H32_ERR_INVALID_ARG, kw
     for kw in (dict(l=4098), dict(bias=4097), dict(ids=4104), dict(w=4098), dict(off=4097),
-               dict(ridx=4098), dict(rof=4099)):
+               dict(ridx=4098), dict(rof=4099), dict(T=65, ws=4100, nws=1 << 20)):
         assert call(**kw) == h32.H32_ERR_ALIGNMENT, kw
     if not torch.cuda.is_available():
         assert call() == h32.H32_ERR_UNSUPPORTED
