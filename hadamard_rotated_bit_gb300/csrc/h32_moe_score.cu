@@ -9,8 +9,8 @@
 // The order of keys is exact.  Without a bias (and with groups by their best key)
 // it is the order of the logits.  Else it is that of the keys' values in double:
 // keys are computed in fp32 with a bound on their error, and where two keys whose
-// order matters are nearer than their bounds (about one token in a thousand on
-// random logits) the token is decided again in double.
+// order matters are nearer than their bounds (a few tokens in a thousand on random
+// logits) the keys in question are taken again in double, one a lane.
 //
 // route_token: one warp per token.  Lane i holds `per` consecutive experts, so a
 // lower lane holds lower ids and, with `per` dividing a group's size, a group is a
@@ -127,8 +127,9 @@ __device__ __forceinline__ uint64_t ordered(double key) {
     return (u >> 63) ? ~u : u | 0x8000000000000000ull;
 }
 
-// The token decided in double: lane j returns choice j's expert.  Rare; the
-// card's double rate is low, so every key is computed once and kept.
+// The token decided in double altogether: lane j returns choice j's expert.  For
+// groups whose scores are too near, or more near keys than lanes; rare.  The card's
+// double rate is low, so every key is computed once and kept.
 template <int NPER>
 __device__ __noinline__ int route_exact(const ScoreArgs &a, const float *row) {
     const int lane = threadIdx.x & 31;
@@ -210,6 +211,52 @@ __device__ __noinline__ int route_exact(const ScoreArgs &a, const float *row) {
 #pragma unroll
         for (int i = 0; i < NPER; ++i)
             if (lane == w && i == at) key[i] = 0ull;
+    }
+    return my;
+}
+
+// A token whose nearest keys are among its first c (sorted, c <= 32; lane j holds
+// candidate j's expert and logit): those keys alone in double, one a lane, and
+// their order.  Lane j returns choice j's expert.  Without a bias keys grow with
+// their logits, which then decide by themselves.
+template <int NPER>
+__device__ __noinline__ int route_refine(const ScoreArgs &a, const float *row, int c, int id) {
+    const int lane = threadIdx.x & 31;
+    const bool sg = a.sigmoid != 0, in = lane < c;
+    const double none = -static_cast<double>(INFINITY);
+    const float l = in ? row[id] : -INFINITY;
+    double key = l;
+    if (a.bias) {
+        Norm<double> nm{none, 1.0};
+        if (!sg) {
+            double v[NPER];
+            const int e0 = lane * a.per;
+#pragma unroll
+            for (int i = 0; i < NPER; ++i) {
+                v[i] = (i < a.per && e0 + i < a.E) ? static_cast<double>(row[e0 + i]) : none;
+                if (v[i] > nm.lmax) nm.lmax = v[i];
+            }
+            nm.lmax = warp_max(nm.lmax);
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < NPER; ++i) sum += score_of(v[i], nm, false);
+            sum = warp_sum(sum);
+            nm.inv = sum > 0.0 ? 1.0 / sum : 0.0;
+        }
+        key = key_of<double>(l, score_of(static_cast<double>(l), nm, sg), in ? a.bias[id] : 0.0f);
+    }
+    const uint64_t mine = in ? ordered(key) : 0ull;
+    int rank = 0;
+    for (int j = 0; j < c; ++j) {
+        const uint64_t o = __shfl_sync(0xFFFFFFFFu, mine, j);
+        const int oid = __shfl_sync(0xFFFFFFFFu, id, j);
+        rank += o > mine || (o == mine && oid < id);
+    }
+    int my = -1;
+    for (int j = 0; j < a.k; ++j) {
+        const int from = __ffs(__ballot_sync(0xFFFFFFFFu, in && rank == j)) - 1;
+        const int e = __shfl_sync(0xFFFFFFFFu, id, from);
+        if (lane == j) my = e;
     }
     return my;
 }
@@ -400,7 +447,7 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
     // k rounds; then the best key left out
     int my = -1;
     uint32_t my_u = 0u;
-    for (int j = 0; j < a.k; ++j) {
+    auto take = [&](int j) {   // the best key that is left, to lane j
         const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, k1);
         const int w = __ffs(__ballot_sync(0xFFFFFFFFu, k1 == m)) - 1;
         const int id = __shfl_sync(0xFFFFFFFFu, e0 + i1, w);
@@ -420,7 +467,9 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
                 scan();
             }
         }
-    }
+        return m;
+    };
+    for (int j = 0; j < a.k; ++j) take(j);
     float ml = lane < a.k ? row[my] : 0.0f;
     if constexpr (!kLogit) {
         // choice j against the one after it, the last against the best left out
@@ -437,13 +486,28 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
             ob = (next_u && a.bias) ? a.bias[next] : 0.0f;
         }
         // both finite: above -inf and below +inf as ordered integers
+        bool tie = false;
         if (lane < a.k && ou > 0x007FFFFFu && my_u < 0xFF800000u) {
             const float ka = from_ordered(my_u), kb = from_ordered(ou);
             const bool same = my_u == ou && ml == ol && mb == ob;
-            near = near || (!same && !(ka - kb > err_of(ka) + err_of(kb)));
+            tie = !same && !(ka - kb > err_of(ka) + err_of(kb));
         }
         if (__any_sync(0xFFFFFFFFu, near)) {
             my = route_exact<NPER>(a, row);
+            if (lane < a.k) ml = row[my];
+        } else if (__any_sync(0xFFFFFFFFu, tie)) {
+            // more candidates until one is clearly below the ones before it
+            uint32_t last = __shfl_sync(0xFFFFFFFFu, my_u, a.k - 1);
+            int c = a.k;
+            bool clear = false;
+            for (; c <= 32; ++c) {
+                const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, k1);
+                const float ka = from_ordered(last), kb = from_ordered(m);
+                clear = m <= 0x007FFFFFu || ka - kb > err_of(ka) + err_of(kb);
+                if (clear || c == 32) break;
+                last = take(c);
+            }
+            my = clear ? route_refine<NPER>(a, row, c, my) : route_exact<NPER>(a, row);
             if (lane < a.k) ml = row[my];
         }
     }
@@ -623,7 +687,7 @@ struct Chunks {
 inline Chunks route_chunks(int64_t T) {
     constexpr int64_t kSms = 152;
     int64_t size = (T + kSms - 1) / kSms;
-    if (size < 4) size = 4;
+    if (size < 8) size = 8;
     if (size > 512) size = 512;
     return Chunks{size, (T + size - 1) / size};
 }
@@ -632,9 +696,9 @@ template <int NPER, bool kLogit>
 cudaError_t launch_scored(const ScoreArgs &a, int32_t *counts, int64_t blocks, bool solo,
                           int32_t *expert_off, int32_t *row_idx, int32_t *row_of, cudaStream_t s) {
     const int warps = a.chunk < 32 ? a.chunk : 32;
-    if (solo)
-        return launch_pdl(route_solo_kernel<NPER, kLogit>, dim3(1), dim3(warps * 32), 0, s, a,
-                          expert_off, row_idx, row_of);
+    if (solo)   // (at least 8 warps: they share the offsets of the experts)
+        return launch_pdl(route_solo_kernel<NPER, kLogit>, dim3(1), dim3((warps < 8 ? 8 : warps) * 32),
+                          0, s, a, expert_off, row_idx, row_of);
     return launch_pdl(route_chunk_kernel<NPER, kLogit>, dim3(static_cast<unsigned>(blocks)),
                       dim3(warps * 32), 0, s, a, counts);
 }
