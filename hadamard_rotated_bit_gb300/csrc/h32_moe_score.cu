@@ -49,9 +49,9 @@ struct ScoreArgs {
 // A key as an unsigned integer of the same order: 0 = not a candidate, 1 = NaN,
 // then -inf < ... < +inf (-0 and +0 equal).
 __device__ __forceinline__ uint32_t ordered(float key) {
-    if (isnan(key)) return 1u;
     const uint32_t u = __float_as_uint(__fadd_rn(key, 0.0f));
-    return (u >> 31) ? ~u : u | 0x80000000u;
+    const uint32_t o = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+    return isnan(key) ? 1u : o;
 }
 __device__ __forceinline__ float from_ordered(uint32_t u) {
     return __uint_as_float((u >> 31) ? u & 0x7FFFFFFFu : ~u);
@@ -127,8 +127,12 @@ __device__ __forceinline__ uint64_t ordered(double key) {
     return (u >> 63) ? ~u : u | 0x8000000000000000ull;
 }
 
+__device__ __forceinline__ double from_ordered(uint64_t u) {
+    return __longlong_as_double(static_cast<long long>((u >> 63) ? u & 0x7FFFFFFFFFFFFFFFull : ~u));
+}
+
 // The token decided in double altogether: lane j returns choice j's expert.  For
-// groups whose scores are too near, or more near keys than lanes; rare.  The card's
+// groups that are not whole lanes and too near, or more near keys than lanes; rare.  The card's
 // double rate is low, so every key is computed once and kept.
 template <int NPER>
 __device__ __noinline__ int route_exact(const ScoreArgs &a, const float *row) {
@@ -161,23 +165,29 @@ __device__ __noinline__ int route_exact(const ScoreArgs &a, const float *row) {
     uint32_t groups = 0xFFFFFFFFu;   // the groups chosen, one bit each
     const int size = a.E / a.n_group;
     if (a.n_group > 1) {
-        double mine = none;   // lane g: group g's score
+        // the two best keys of every group, compared as integers of the same order
+        const uint64_t floor = ordered(none);
+        uint64_t g1 = floor, g2 = floor;   // lane g: group g's
         for (int g = 0; g < a.n_group; ++g) {
-            double b1 = none, b2 = none;
+            uint64_t b1 = floor, b2 = floor;
 #pragma unroll
             for (int i = 0; i < NPER; ++i) {
                 const int e = e0 + i;
-                if (i < a.per && e >= g * size && e < (g + 1) * size) insert2(b1, b2, kd[i]);
+                if (i < a.per && e >= g * size && e < (g + 1) * size) insert2(b1, b2, ordered(kd[i]));
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
-                const double c1 = __shfl_xor_sync(0xFFFFFFFFu, b1, o);
-                const double c2 = __shfl_xor_sync(0xFFFFFFFFu, b2, o);
+                const uint64_t c1 = __shfl_xor_sync(0xFFFFFFFFu, b1, o);
+                const uint64_t c2 = __shfl_xor_sync(0xFFFFFFFFu, b2, o);
                 insert2(b1, b2, c1);
                 insert2(b1, b2, c2);
             }
-            if (lane == g) mine = group_score(b1, b2, a.group_top);
+            if (lane == g) {
+                g1 = b1;
+                g2 = b2;
+            }
         }
+        const double mine = group_score(from_ordered(g1), from_ordered(g2), a.group_top);
         int rank = 0;
         for (int g = 0; g < a.n_group; ++g) {
             const double o = __shfl_sync(0xFFFFFFFFu, mine, g);
@@ -215,6 +225,67 @@ __device__ __noinline__ int route_exact(const ScoreArgs &a, const float *row) {
     return my;
 }
 
+// The double normaliser of the token's softmax scores.
+template <int NPER>
+__device__ __forceinline__ Norm<double> exact_norm(const ScoreArgs &a, const float *row) {
+    const int e0 = (threadIdx.x & 31) * a.per;
+    Norm<double> nm{-static_cast<double>(INFINITY), 1.0};
+    double v[NPER];
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+        v[i] = (i < a.per && e0 + i < a.E) ? static_cast<double>(row[e0 + i])
+                                           : -static_cast<double>(INFINITY);
+        if (v[i] > nm.lmax) nm.lmax = v[i];   // false for NaN
+    }
+    nm.lmax = warp_max(nm.lmax);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) sum += score_of(v[i], nm, false);
+    sum = warp_sum(sum);
+    nm.inv = sum > 0.0 ? 1.0 / sum : 0.0;
+    return nm;
+}
+
+// Groups whose scores are too near, a group being whole lanes (ScoreArgs::lanes):
+// bit i of `cand` marks the lane's experts that may be among their group's best,
+// one or two in most lanes; their keys in double, the groups' scores and order.
+// Returns whether the lane's group stays.
+template <int NPER>
+__device__ __noinline__ bool exact_groups(const ScoreArgs &a, const float *row, uint32_t cand) {
+    const int lane = threadIdx.x & 31, e0 = lane * a.per;
+    const bool sg = a.sigmoid != 0;
+    const double none = -static_cast<double>(INFINITY);
+    Norm<double> nm{none, 1.0};
+    if (!sg) nm = exact_norm<NPER>(a, row);
+    uint64_t b1 = ordered(none), b2 = b1;
+    while (__any_sync(0xFFFFFFFFu, cand != 0u)) {
+        if (cand) {
+            const int e = e0 + __ffs(cand) - 1;
+            cand &= cand - 1u;
+            const float l = row[e];
+            insert2(b1, b2, ordered(key_of<double>(l, score_of(static_cast<double>(l), nm, sg),
+                                                   a.bias ? a.bias[e] : 0.0f)));
+        }
+    }
+    const uint64_t m1 = b1, m2 = b2;
+    const int first = lane - lane % a.lanes, me = lane - first;
+    for (int j = 1; j < a.lanes; ++j) {
+        const int from = (first + (me + j >= a.lanes ? me + j - a.lanes : me + j)) & 31;
+        const uint64_t c1 = __shfl_sync(0xFFFFFFFFu, m1, from);
+        const uint64_t c2 = __shfl_sync(0xFFFFFFFFu, m2, from);
+        insert2(b1, b2, c1);
+        insert2(b1, b2, c2);
+    }
+    const double mine = group_score(from_ordered(b1), from_ordered(b2), a.group_top);
+    const int my_group = lane / a.lanes;
+    int rank = 0;
+    for (int g = 0; g < a.n_group; ++g) {
+        const double o = __shfl_sync(0xFFFFFFFFu, mine, g * a.lanes);
+        rank += o > mine || (o == mine && g < my_group);
+    }
+    return my_group < a.n_group && rank < a.topk_group;
+}
+
 // A token whose nearest keys are among its first c (sorted, c <= 32; lane j holds
 // candidate j's expert and logit): those keys alone in double, one a lane, and
 // their order.  Lane j returns choice j's expert.  Without a bias keys grow with
@@ -228,21 +299,7 @@ __device__ __noinline__ int route_refine(const ScoreArgs &a, const float *row, i
     double key = l;
     if (a.bias) {
         Norm<double> nm{none, 1.0};
-        if (!sg) {
-            double v[NPER];
-            const int e0 = lane * a.per;
-#pragma unroll
-            for (int i = 0; i < NPER; ++i) {
-                v[i] = (i < a.per && e0 + i < a.E) ? static_cast<double>(row[e0 + i]) : none;
-                if (v[i] > nm.lmax) nm.lmax = v[i];
-            }
-            nm.lmax = warp_max(nm.lmax);
-            double sum = 0.0;
-#pragma unroll
-            for (int i = 0; i < NPER; ++i) sum += score_of(v[i], nm, false);
-            sum = warp_sum(sum);
-            nm.inv = sum > 0.0 ? 1.0 / sum : 0.0;
-        }
+        if (!sg) nm = exact_norm<NPER>(a, row);
         key = key_of<double>(l, score_of(static_cast<double>(l), nm, sg), in ? a.bias[id] : 0.0f);
     }
     const uint64_t mine = in ? ordered(key) : 0ull;
@@ -261,9 +318,13 @@ __device__ __noinline__ int route_refine(const ScoreArgs &a, const float *row, i
     return my;
 }
 
-// exp(-l) and the reciprocal by the fast units; its error is in the bounds below
+// 1 / (1 + exp(-l)) by the fast units (its error is in the bounds below); results
+// below 2^-126 come out as 0
 __device__ __forceinline__ float fast_sigmoid(float l) {
-    return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-l)));
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(l, -1.4426950408889634f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(__fadd_rn(1.0f, e)));
+    return s;
 }
 
 // Routes the warp's token: writes its choices and weights; lane j returns choice
@@ -302,39 +363,60 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
         nm.inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
     }
     uint32_t key[NPER];
+    float bias[NPER];
+    if (!kLogit && a.bias) {
+        if (NPER % 4 == 0 && a.vec) {
+#pragma unroll
+            for (int i = 0; i + 3 < NPER; i += 4) {
+                float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (e0 + i < a.E) f = *reinterpret_cast<const float4 *>(a.bias + e0 + i);
+                bias[i] = f.x;
+                bias[i + 1] = f.y;
+                bias[i + 2] = f.z;
+                bias[i + 3] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NPER; ++i)
+                bias[i] = (i < a.per && e0 + i < a.E) ? a.bias[e0 + i] : 0.0f;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NPER; ++i) bias[i] = 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < NPER; ++i) {
-        const int e = e0 + i;
-        const bool in = i < a.per && e < a.E;
+        const bool in = i < a.per && e0 + i < a.E;
         float k = l[i];
         if constexpr (!kLogit) {
             // a NaN logit gives a NaN score and key; a -inf logit masks its expert
-            k = sg ? fast_sigmoid(k) : score_of(k, nm, false);
-            if (a.bias && in) k = __fadd_rn(k, a.bias[e]);
+            k = sg ? fast_sigmoid(k) : isnan(k) ? k : score_of(k, nm, false);
+            k = __fadd_rn(k, bias[i]);
             if (l[i] == none && !isnan(k)) k = none;
-            if (isnan(l[i])) k = l[i];
         }
         key[i] = in ? ordered(k) : 0u;
     }
-    // the lane's two largest keys (0: none), the lower id first among equals
+    // the lane's two largest keys after (kl, il) in decreasing order (0: none), the
+    // lower id first among equals
     uint32_t k1 = 0u, k2 = 0u;
     int i1 = 0, i2 = 0;
-    auto scan = [&]() {
+    auto scan = [&](uint32_t kl, int il) {
         k1 = k2 = 0u;
 #pragma unroll
         for (int i = 0; i < NPER; ++i) {
-            if (key[i] > k1) {
+            const uint32_t v = (key[i] < kl || (key[i] == kl && i > il)) ? key[i] : 0u;
+            if (v > k1) {
                 k2 = k1;
                 i2 = i1;
-                k1 = key[i];
+                k1 = v;
                 i1 = i;
-            } else if (key[i] > k2) {
-                k2 = key[i];
+            } else if (v > k2) {
+                k2 = v;
                 i2 = i;
             }
         }
     };
-    scan();
+    scan(0xFFFFFFFFu, -1);
     // Bounds on the fp32 errors of keys, in units of u = 2^-23 (kLogit: none needed).
     // Scores: the fast sigmoid is within (2 + 1.2 |l|) (1 - s) + 2.5 relative, at most
     // 5 absolute; a softmax score within 2.5 + 1.7 d relative (expf, the rounding of
@@ -351,9 +433,11 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
     bool near = false;
     if (a.n_group > 1) {
         const int size = a.E / a.n_group;
-        float mine = none, err = 0.0f;   // group g's score and its bound, in lane `at_g`
+        float mine = none, err = 0.0f;   // the group's score and its bound
+        float f1 = none, f2 = none;      // its two best keys
         auto finish = [&](uint32_t b1, uint32_t b2) {
-            const float f1 = from_ordered(b1), f2 = from_ordered(b2);
+            f1 = from_ordered(b1);
+            f2 = from_ordered(b2);
             mine = group_score(f1, f2, a.group_top);
             if constexpr (!kLogit) {
                 if (f1 > none) err = err_of(f1);
@@ -420,7 +504,7 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
             rank += o > mine || (o == mine && g < my_group);
         }
         const bool have = my_group < a.n_group;
-        const bool stays = have && rank < a.topk_group;
+        bool stays = have && rank < a.topk_group;
         if constexpr (!kLogit) {
             const int in_at = __ffs(__ballot_sync(0xFFFFFFFFu, have && rank == a.topk_group - 1)) - 1;
             const int out_at = __ffs(__ballot_sync(0xFFFFFFFFu, have && rank == a.topk_group)) - 1;
@@ -430,18 +514,27 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
                 __reduce_max_sync(0xFFFFFFFFu, have ? __float_as_uint(err) : 0u));
             // (both -inf: no key in either; they go by id)
             near = out > none && !(in - out > 2.0f * worst);
+            if (a.lanes && near) {
+                // an expert may be among its group's best when its key is within the
+                // errors of the last of them
+                const float last = a.group_top == 2 ? f2 : f1;
+                const float cut = last > none ? last - 4.0f * err_of(last) : none;
+                uint32_t cand = 0u;
+#pragma unroll
+                for (int i = 0; i < NPER; ++i)
+                    if (have && key[i] > 0x007FFFFFu && !(from_ordered(key[i]) < cut)) cand |= 1u << i;
+                stays = exact_groups<NPER>(a, row, cand);
+                near = false;
+            }
         }
         if (a.lanes) {
-            if (!stays) k1 = k2 = 0u;
-            if (!stays)
-#pragma unroll
-                for (int i = 0; i < NPER; ++i) key[i] = 0u;
+            if (!stays) k1 = k2 = 0u;   // never scanned again: it wins no round
         } else {
             const uint32_t groups = __ballot_sync(0xFFFFFFFFu, stays);
 #pragma unroll
             for (int i = 0; i < NPER; ++i)
                 if (!((groups >> min((e0 + i) / size, 31)) & 1u)) key[i] = 0u;
-            scan();
+            scan(0xFFFFFFFFu, -1);
         }
     }
     // k rounds; then the best key left out
@@ -456,15 +549,12 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
             my_u = m;
         }
         if (lane == w) {
-#pragma unroll
-            for (int i = 0; i < NPER; ++i)
-                if (i == i1) key[i] = 0u;
             if (k2) {
                 k1 = k2;
                 i1 = i2;
                 k2 = 0u;
             } else {
-                scan();
+                scan(k1, i1);
             }
         }
         return m;
@@ -778,7 +868,7 @@ extern "C" h32_status h32_moe_route_scored(const float *logits, int64_t T, int32
                 break;
             }
     }
-    const bool v4 = E % 4 == 0 && ldl % 4 == 0 && aligned16(logits);
+    const bool v4 = E % 4 == 0 && ldl % 4 == 0 && aligned16(logits) && (!bias || aligned16(bias));
     const bool by_logit = !bias && (a.n_group == 1 || group_top == 1);
     int32_t *counts = solo ? nullptr : static_cast<int32_t *>(workspace);
     cudaError_t e;
