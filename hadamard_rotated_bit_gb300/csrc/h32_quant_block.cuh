@@ -86,30 +86,36 @@ __device__ __forceinline__ uint32_t pack_low_bytes(uint32_t a, uint32_t b, uint3
 // rounding a block to codes
 // ----------------------------------------------------------------------------
 // d = amax / qmax (IEEE divide); bits[i] holds the code round-half-even(v * fl(1/d))
-// plus 1.5 * 2^23 as a float.  With a finite amax and a finite 1/d every product
-// lies in [-qmax, qmax] up to rounding; when 1/d overflowed (a block of subnormal
-// size) or the rotation itself overflowed to +-inf, the code is the clamped v / d
-// instead.  Returns d.
-template <int kBits>
-__device__ __forceinline__ float quant_block_bits(const float (&v)[32], uint32_t (&bits)[32]) {
+// plus 1.5 * 2^23 as a float, for kN of the block's values.  With a finite amax and
+// a finite 1/d every product lies in [-qmax, qmax] up to rounding; when 1/d
+// overflowed (a block of subnormal size) or the rotation itself overflowed to
+// +-inf, the code is the clamped v / d instead.  Returns d.
+template <int kBits, int kN>
+__device__ __forceinline__ float quant_bits(const float (&v)[kN], float amax, uint32_t (&bits)[kN]) {
     constexpr float kQmax = (kBits == 4) ? 7.0f : 127.0f;
     constexpr float kQmin = (kBits == 4) ? -8.0f : -127.0f;
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
     const float d = __fdiv_rn(amax, kQmax);
     const float id = (d != 0.0f) ? __frcp_rn(d) : 0.0f;
     if (!(amax < INFINITY) || isinf(id)) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < kN; ++i)
             bits[i] = __float_as_uint(__fadd_rn(degenerate_code(v[i], d, kQmin, kQmax),
                                                 kRoundMagic));
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < kN; ++i)
             bits[i] = __float_as_uint(__fadd_rn(__fmul_rn(v[i], id), kRoundMagic));
     }
     return d;
+}
+
+// the whole block of one thread
+template <int kBits>
+__device__ __forceinline__ float quant_block_bits(const float (&v)[32], uint32_t (&bits)[32]) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
+    return quant_bits<kBits>(v, amax, bits);
 }
 
 // 4-bit codes in Q4_0 nibble order: byte j = element j (low) | element j + 16 (high)

@@ -617,11 +617,12 @@ h32_status h32_moe_combine(const float *y, int64_t R, int64_t ldy, const int32_t
  * quantizer ("The rotation": every projection's input is rotated and quantized).
  * Per row:
  *   h = x + residual in fp32, rounded to the residual's type (h = x without one);
- *   S = sum of h^2 in fp32: fma over each 32-block from +0, groups of 32 blocks
- *       by the xor tree of strides 1, 2, 4, 8, 16 (absent blocks 0), then the
- *       groups in order;
- *   r = 1 / sqrt(S / K + eps), every step rounded to fp32; n = (h r) w, two fp32
- *       roundings; where S overflows fp32 the row is scaled by 2^-80 first;
+ *   S = sum of h^2 in fp32: over 16 consecutive values two fma chains from +0, the
+ *       even and the odd places, added; 32 such sums by the xor tree of strides 1,
+ *       2, 4, 8, 16 (absent sums 0); 32 of those the same way; the rest in order;
+ *   r = 1 / sqrt(S fl(1/K) + eps): product, sum and reciprocal root each rounded to
+ *       fp32; n = (h r) w, two fp32 roundings; where S overflows fp32 the row is
+ *       scaled by 2^-80 first;
  *   then n is rotated and quantized exactly as by the quantizer of `form`.
  * Bit-identical to that sequential evaluation.
  *   x            [M][ldx] of type x_dt

@@ -606,32 +606,47 @@ static float round_bf16(float f)
     return f;
 }
 
-/* sum of squares of a row: fma over each 32-block from +0, then groups of 32
- * blocks by the xor tree of strides 1 .. 16 (absent blocks 0), then the groups
- * in order */
+/* the sum of 32 values by the xor tree of strides 1 .. 16 */
+static float tree32(float part[32])
+{
+    for (int o = 1; o < 32; o <<= 1) {
+        float next[32];
+        for (int b = 0; b < 32; ++b) next[b] = part[b] + part[b ^ o];
+        memcpy(part, next, sizeof next);
+    }
+    return part[0];
+}
+
+/* sum of squares of a row: 16 consecutive values in two fma chains from +0 (even
+ * and odd places), added; 32 such sums by the tree (absent ones 0); 32 of those by
+ * the tree; the rest in order */
 static float row_sum_squares(const float *h, int64_t K)
 {
     float total = 0.0f;
-    const int64_t nb = K / 32;
-    for (int64_t g = 0; g < nb; g += 32) {
-        float part[32] = {0.0f};
-        for (int64_t b = 0; b < 32 && g + b < nb; ++b) {
-            float acc = 0.0f;
-            for (int i = 0; i < 32; ++i) {
-                const float v = h[(g + b) * 32 + i];
-                acc = fmaf(v, v, acc);
+    for (int64_t top = 0; top < K; top += 16 * 1024) {
+        float groups[32] = {0.0f};
+        for (int g = 0; g < 32; ++g) {
+            float part[32] = {0.0f};
+            for (int p = 0; p < 32; ++p) {
+                const int64_t at = top + (int64_t)(g * 32 + p) * 16;
+                if (at >= K) break;
+                float even = 0.0f, odd = 0.0f;
+                for (int i = 0; i < 16; i += 2) {
+                    even = fmaf(h[at + i], h[at + i], even);
+                    odd = fmaf(h[at + i + 1], h[at + i + 1], odd);
+                }
+                part[p] = even + odd;
             }
-            part[b] = acc;
+            groups[g] = tree32(part);
         }
-        for (int o = 1; o < 32; o <<= 1) {
-            float next[32];
-            for (int b = 0; b < 32; ++b) next[b] = part[b] + part[b ^ o];
-            memcpy(part, next, sizeof part);
-        }
-        total = g == 0 ? part[0] : total + part[0];
+        const float t = tree32(groups);
+        total = top == 0 ? t : total + t;
     }
     return total;
 }
+
+/* 1 / sqrt(x) rounded once (the double result is far closer than half a step) */
+static float reciprocal_root(float x) { return (float)(1.0 / sqrt((double)x)); }
 
 /* x, res [M][K] fp32 (res may be null), w [K] -> h [M][K] (rounded to bf16
  * where res_bf16 is set and there is a residual), n [M][K] = the normed rows */
@@ -647,11 +662,13 @@ void o_add_rms_norm(const float *x, const float *res, int res_bf16, const float 
         }
         float s = row_sum_squares(nr, K);
         float r;
+        const float inv_k = 1.0f / (float)K;
         if (s < INFINITY) {
-            r = 1.0f / sqrtf(s / (float)K + eps);
+            const float ms = s * inv_k;
+            r = reciprocal_root(ms + eps);
         } else {
             for (int64_t i = 0; i < K; ++i) nr[i] = nr[i] * 0x1p-80f;
-            r = 1.0f / sqrtf(row_sum_squares(nr, K) / (float)K);
+            r = reciprocal_root(row_sum_squares(nr, K) * inv_k);
         }
         for (int64_t i = 0; i < K; ++i) {
             const float t = nr[i] * r;

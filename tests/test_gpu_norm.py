@@ -110,11 +110,13 @@ def test_types(h32, xb, rb, wb):
         _check_codes("q4_tc", xq, xd, n, 32)
 
 
-# rows a warp shares (K <= 1024), one warp to many, more than 768 blocks (an
-# instance of its own) and the longest row; token counts that end inside a block
+# rows a warp shares (K <= 512), one piece a thread (K <= 8192) with fewer and more
+# rows than resident blocks, two pieces (odd halves), the longest row; token counts
+# that end inside a block
 @pytest.mark.parametrize("M,K", [(1, 32), (300, 32), (31, 64), (9, 96), (65, 224), (5, 992),
                                  (3, 1024), (4, 1056), (2, 17408), (3, 24576), (2, 24608),
-                                 (3, 32768), (700, 1280)])
+                                 (3, 32768), (700, 1280), (5, 512), (9, 544), (2, 8192),
+                                 (3, 8224), (2, 16384), (2, 16416), (1100, 4096)])
 def test_sizes(h32, M, K):
     x, res = _rows(M, K, M + K, True), _rows(M, K, M + K + 1, False)
     w = (1 + 0.1 * np.random.default_rng(K).standard_normal(K)).astype(np.float32)

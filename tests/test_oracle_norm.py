@@ -12,10 +12,10 @@ U = 2.0 ** -24   # half a step of fp32
 
 @pytest.mark.parametrize("M,K", [(1, 32), (3, 96), (5, 1024), (2, 1056), (4, 5120), (2, 17408)])
 def test_norm_against_float64(M, K):
-    """n within the forward bound: a 32-term fma chain and the trees above it keep
-    the sum of squares (all positive) within (32 + 5 + K/1024 + 1) half steps, the
-    square root halves that, and divide, add, sqrt, divide and two products add
-    one half step each (the first two halved too)."""
+    """n within the forward bound: an 8-term fma chain, one sum and two 5-level trees
+    (and one more sum above 16384 values) keep the sum of squares (all positive)
+    within 8 + 1 + 10 + 1 half steps, fl(1/K), its product and the sum with eps add
+    3, the root halves them; the reciprocal root and two products add 3."""
     r = np.random.default_rng(M * K)
     x = (r.standard_normal((M, K)) * 3).astype(np.float32)
     res = (r.standard_normal((M, K)) * 2).astype(np.float32)
@@ -24,7 +24,7 @@ def test_norm_against_float64(M, K):
     assert np.array_equal(h, x + res)
     h64 = h.astype(np.float64)
     want = h64 / np.sqrt((h64 ** 2).mean(1, keepdims=True) + np.float64(np.float32(1e-6))) * w
-    bound = ((32 + 5 + K / 1024 + 1 + 2) / 2 + 4) * U * (1 + 1e-4)
+    bound = ((8 + 1 + 10 + 1 + 3) / 2 + 3) * U * (1 + 1e-4)
     assert np.all(np.abs(n - want) <= bound * np.abs(want))
 
 
@@ -55,12 +55,23 @@ def test_closed_forms():
 
 
 def test_sum_order_is_the_stated_one():
-    """1 + 2^-24 terms are lost one by one but kept when their group is summed first."""
+    """Terms of a quarter step are lost one by one but kept when their piece, or
+    their place's chain, is summed first."""
     x = np.zeros((1, 64), np.float32)
     x[0, 0] = 1.0
-    x[0, 1:32] = 2.0 ** -13        # squares 2^-26 (a quarter step): lost in the chain of block 0
-    x[0, 32:64] = 2.0 ** -13       # block 1 sums to 2^-21, then joins
+    x[0, 2:16:2] = 2.0 ** -13      # squares 2^-26 (a quarter step): lost in the chain of 1
+    x[0, 1:16:2] = 2.0 ** -13      # the odd places' chain: 8 * 2^-26 = 2^-23, then joins
+    x[0, 16:32] = 2.0 ** -13       # the next piece: 2^-22
     _, n = oracle.add_rms_norm(x, np.ones(64, np.float32), None, 1e-30)
-    s = np.float32(1.0) + np.float32(2.0 ** -21)
-    r = np.float32(1) / np.sqrt(s / np.float32(64))
-    assert n[0, 0] == r
+    s = np.float32(1.0 + 2.0 ** -23 + 2.0 ** -22)
+    r = np.float32(1 / np.sqrt(np.float64(s / np.float32(64))))
+    assert n[0, 0] == r and s != 1
+    # trees: 32 pieces a group, 32 groups, then in order
+    K = 16384 + 32
+    y = np.zeros((1, K), np.float32)
+    y[0, 0] = 4096.0               # 2^24: a 1 joins a tree neighbour before it
+    y[0, 16384] = y[0, 16384 + 16] = 1.0
+    _, n = oracle.add_rms_norm(y, np.ones(K, np.float32), None, 1e-30)
+    s = np.float32(2.0 ** 24 + 2.0)
+    ms = s * (np.float32(1) / np.float32(K))
+    assert n[0, 16384] == np.float32(1 / np.sqrt(np.float64(ms)))
