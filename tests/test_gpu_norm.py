@@ -116,7 +116,8 @@ def test_types(h32, xb, rb, wb):
 @pytest.mark.parametrize("M,K", [(1, 32), (300, 32), (31, 64), (9, 96), (65, 224), (5, 992),
                                  (3, 1024), (4, 1056), (2, 17408), (3, 24576), (2, 24608),
                                  (3, 32768), (700, 1280), (5, 512), (9, 544), (2, 8192),
-                                 (3, 8224), (2, 16384), (2, 16416), (1100, 4096)])
+                                 (3, 8224), (2, 16384), (2, 16416), (2000, 4096),
+                                 (1900, 1056), (620, 8224), (5000, 96)])
 def test_sizes(h32, M, K):
     x, res = _rows(M, K, M + K, True), _rows(M, K, M + K + 1, False)
     w = (1 + 0.1 * np.random.default_rng(K).standard_normal(K)).astype(np.float32)
@@ -124,6 +125,18 @@ def test_sizes(h32, M, K):
         xq, xd, ro, _ = _run(h32, x, w, res, form, 32)
         h, n = oracle.add_rms_norm(x, w, res)
         assert _same(np_of(ro), h)
+        _check_codes(form, xq, xd, n, 32)
+
+
+def test_rounding_of_the_code_product(h32):
+    """Enough values that some products v * fl(1/d) round onto a tie: the code is that
+    of the rounded product, not of the exact one."""
+    for form, seed in (("q8", 1), ("q8_tc", 2), ("q4_tc", 3), ("q4", 4)):
+        M, K = 220, 4096
+        x = _rows(M, K, seed, False)
+        w = np.ones(K, np.float32)
+        xq, xd, _, _ = _run(h32, x, w, None, form, 32)
+        _, n = oracle.add_rms_norm(x, w, None)
         _check_codes(form, xq, xd, n, 32)
 
 
@@ -220,3 +233,22 @@ def test_empty_stream_and_graph(h32):
         _, n = oracle.add_rms_norm(np_of(x), np_of(w))
         _check_codes("q4_tc", xq, xd, n, 32)
     assert h32.h32_device_status() == 0
+
+
+def test_wait_that_gives_up_is_reported(h32):
+    """A bound of one poll on the wait for a row's copy: the status reads timeout once,
+    and the same context then computes exact results."""
+    import torch
+    M, K = 2000, 1024
+    x, w = _rows(M, K, 21, True), np.ones(K, np.float32)
+    xt, wt = torch_bf16(x), torch_of(w)
+    h32.h32_set_wait_limit(1)
+    try:
+        h32.h32_add_rms_norm_quantize(xt, wt)
+        assert h32.h32_device_status() == h32.H32_ERR_TIMEOUT
+    finally:
+        h32.h32_set_wait_limit(0)
+    assert h32.h32_device_status() == 0
+    xq, xd, _, _ = _run(h32, x, w, None, "q4_tc", 32)
+    _, n = oracle.add_rms_norm(x, w)
+    _check_codes("q4_tc", xq, xd, n, 32)
