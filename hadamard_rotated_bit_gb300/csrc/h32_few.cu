@@ -1,319 +1,512 @@
 // The block-scaled product of a few tokens (sm_103a): one new token of each
 // sequence through a projection, with the epilogue of h32_finish.cuh.
 //
-// Per weight row and token the same definition as the tensor-core GEMM, bit for
-// bit: exact integer sums S of 32-blocks, then acc = fma(fl(d_w d_x), S, acc) in
-// block order.  The tensor-core GEMM runs 128-row tiles over the whole of K one
-// block step after another, which for a few tokens leaves most of the card idle
-// (5120 x 5120, one token: 35 us).  Here the sums and the ordered folds are taken
-// apart: all warps stream weight rows and form sums, any order, as they are exact;
-// one warp a token folds them in order.
+// The definition, the operands and the bits of the tensor-core GEMM
+// (h32_gemm_tc.cu): per 32-block the exact sum S from one tcgen05.mma of K = 32, then
+// acc = fma(fl(d_w d_x), S, acc) in block order.  That kernel's tiles are 128 weight
+// rows wide, and it hands two blocks at a time from the MMA to the epilogue, about
+// 300 clocks each however few the columns are: 35 us for 5120 x 5120 and one token.
+// With at most 16 tokens a block needs only 16 of TMEM's 512 columns, so here
+//   - a hand-off is 8 blocks (128 columns, four buffers: two of 16 blocks
+//     leave the hand-off's latency open);
+//   - a tile is 128, 64 or 32 weight rows, the most that still gives the card one
+//     wave (the MMA always takes 128: the rows beyond the tile's are whatever lies
+//     behind it in shared memory, and their results are not read);
+//   - a stage is two hand-offs' 512 codes (one's 256 for tiles of 128 rows), brought by four
+//     tensor copies: rows and tokens as three-dimensional boxes of 128-byte columns,
+//     swizzled as the MMA reads them, and the blocks' scales of both.
+//   warps 0..3  epilogue, a TMEM lane quarter each (a tile of 32 rows needs one): the
+//               sums of 4 or 8 blocks at a time, the folds on packed pairs of tokens, of
+//               which only those in use are read
+//   warp 4      TMA producer;  warp 5  TMEM allocator and MMA issuer
+// Every wait is bounded.
 //
-// Bound: HBM, 1.125 bytes a weight.  A block takes 8 RW rows (RW a warp), in steps
-// of 1024 codes.  A lane loads 16 codes (16 bytes) of each row, widens them to fp16
-// pairs, and multiplies by the tokens' codes (fp16 in shared memory, widened once a
-// step): |w x| <= 64, so 32 products sum exactly in fp16 (|S| <= 2048).  An 8-bit
-// activation code is 16 h + l, two such sums (16 h: multiples of 16 up to 8192; l:
-// up to 960, a lane), added in fp32.  A register is loaded again for the next step
-// as soon as its codes are widened, so each block keeps 8 KB a row pair in flight.
-// The sums go to shared memory, two buffers, one barrier a step: while warp m folds
-// the step for token m the others form the next one's.
+// Bound: HBM, 1.125 bytes a weight, where the tiles fill the card (34816 x 5120, one
+// token: 35.6 us, 5.6 TB/s, 84% of the measured copy rate); a narrow projection is
+// bound by the pace of one tile's stages, about 0.6 us per 512 codes, most of it the
+// hand-offs (5120 x 5120: 13.3 us; 5120 x 17408: 28.2 us, 53%).  The roles that issue
+// to the tensor core and the copy engine run as whole warps with one elected lane:
+// descriptors in uniform registers, 47 clocks a product less.  (Measured and left:
+// sums on CUDA cores in fp16 pairs, 11.8 us for 5120 x 5120 and one token but 66 us
+// for 34816 x 5120 and five; mma.m16n8k16 on widened codes, 16 rows a warp, 15-17 us
+// and 42-50 us, 47-66 instructions per 512 bytes of weights where this takes about 4.)
+
+// poll without sleeping: the waits here are short and on the critical path
+#ifndef H32_WAIT_SLEEP
+#define H32_WAIT_SLEEP 0
+#endif
+
 #include "h32_few.cuh"
 
-#include <cuda_fp16.h>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "h32_epilogue.cuh"
 
 namespace h32 {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kStep = 1024;           // codes a step
-constexpr int kBlocks = kStep / 32;   // 32-blocks a step
-constexpr int kLoads = kStep / 512;   // 16-byte loads of a row, a lane and step
+__device__ uint32_t g_few_status;   // kStatusTimeout: a bounded wait gave up
+
+constexpr int kGroup = 8;                         // blocks of a hand-off
+constexpr int kBufs = 4;                          // hand-offs in TMEM
+constexpr int kCols = 16;                         // TMEM columns of a block: the tokens
+constexpr int kMaxStages = 12;
+constexpr int kWarps = 6;
+constexpr int kMaxSmem = 225 * 1024;
+constexpr uint64_t kDrainPolls = 1ull << 22;
 
 struct FewArgs {
-    const uint8_t *wp, *xw;
-    const float *wsc, *xdt;
-    int64_t ldws, ldxd;
-    int32_t M, N, K;
+    int32_t M, N, K, rows, tiles, stages;   // rows of a tile
+    uint64_t wait_limit;
     EpiArgs fin;
 };
 
-// two e4m3 bytes -> an fp16 pair, exact
-__device__ __forceinline__ uint32_t half2_of(uint16_t b) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(b));
-    return r;
-}
-__device__ __forceinline__ void widen16(const uint4 &q, uint32_t (&h)[8]) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[2 * i] = half2_of(static_cast<uint16_t>(w[i]));
-        h[2 * i + 1] = half2_of(static_cast<uint16_t>(w[i] >> 16));
-    }
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ float half_sum(uint32_t h) {
-    const __half2 v = *reinterpret_cast<const __half2 *>(&h);
-    return __low2float(v) + __high2float(v);
-}
-
-// Shared memory: sums [2][kBlocks][MT][rows + pad], activations [2][MT][kLoads]
-// [pairs of 16 bytes][32 lanes], weight scales [2][kBlocks][rows + 1], activation
-// scales [2][MT][kBlocks].
-template <int XB, int MT, int RW>
-struct FewCfg {
-    static constexpr int kRows = kWarps * RW;
-    // sums: fp16 (4-bit) with 2 halves of padding, or fp32 with one word
-    static constexpr int kSumStride = XB == 4 ? (kRows + 2) * 2 : (kRows + 1) * 4;
-    static constexpr int kSumBytes = kBlocks * MT * kSumStride;
-    static constexpr int kActVecs = 2 * (XB / 4);                       // uint4 a lane and load
-    static constexpr int kActBytes = MT * kLoads * kActVecs * 512;
-    static constexpr int kDwBytes = kBlocks * (kRows + 1) * 4;
-    static constexpr int kDxBytes = MT * kBlocks * 4;
-    static constexpr int kOffAct = 2 * ((kSumBytes + 15) & ~15);
-    static constexpr int kOffDw = kOffAct + 2 * kActBytes;
-    static constexpr int kOffDx = kOffDw + 2 * kDwBytes;
-    static constexpr int kSmem = kOffDx + 2 * kDxBytes;
+// byte sizes of a stage's parts
+struct Sizes {
+    uint32_t a, b, sa, sb;
+    __host__ __device__ Sizes(int rows, int tokens, int xb, int blocks)
+        : a(rows * blocks * 32), b(tokens * blocks * 32 * (xb / 4)), sa(rows * blocks * 4),
+          sb(blocks * 16 * 4) {}
+    __host__ __device__ uint32_t stage() const { return a + b + sa + sb; }
 };
 
-template <int XB, int MT, int RW>
-__global__ void __launch_bounds__(kWarps * 32, 2) few_kernel(const FewArgs a) {
-    using C = FewCfg<XB, MT, RW>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int n0 = blockIdx.x * C::kRows;
-    const int nb = a.K / 32, steps = (a.K + kStep - 1) / kStep;
-    auto s_sum = [&](int buf) { return smem + buf * (C::kOffAct / 2); };
-    auto s_act = [&](int buf) { return reinterpret_cast<uint4 *>(smem + C::kOffAct + buf * C::kActBytes); };
-    auto s_dw = [&](int buf) { return reinterpret_cast<float *>(smem + C::kOffDw + buf * C::kDwBytes); };
-    auto s_dx = [&](int buf) { return reinterpret_cast<float *>(smem + C::kOffDx + buf * C::kDxBytes); };
+__device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, uint64_t *bar, int32_t x,
+                                            int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// K-major operand in 128B-swizzled 8-row x 128-byte atoms, as TMA writes it
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(1) << 16;            // leading byte offset (unused here)
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;    // 8-row group stride: 1024 bytes
+    d |= static_cast<uint64_t>(1) << 46;            // descriptor version
+    d |= static_cast<uint64_t>(2) << 61;            // swizzle: 128 bytes
+    return d;
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
+// 2 PT consecutive columns of the warp's 32 lanes
+template <int PT>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[2 * PT]) {
+    if constexpr (PT == 1) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];"
+                     : "=r"(r[0]), "=r"(r[1])
+                     : "r"(taddr));
+    } else if constexpr (PT == 4) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                       "=r"(r[7])
+                     : "r"(taddr));
+    } else {
+        tmem_ld_x16(taddr, r);
+    }
+}
+
+// XB: activation bits; PT: pairs of tokens folded (2 PT >= M); kStageBlocks: blocks of a
+// stage, 16 or 8
+template <int XB, int PT, int kStageBlocks>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    few_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+               const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb,
+               const FewArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_sfull[kBufs], s_sempty[kBufs], s_drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr int kStageCodes = 32 * kStageBlocks;
+    constexpr int kCols128 = kStageCodes / 128;   // 128-byte columns of a stage's weights
+    // tokens copied: 8 (the MMA then reads the next column's as tokens 8 .. 15, whose
+    // results nobody reads) or 16
+    constexpr int kTokens = PT <= 4 ? 8 : 16;
+    const Sizes z(a.rows, kTokens, XB, kStageBlocks);
+    const int S = a.stages;
+    uint8_t *s_a = smem, *s_b = s_a + S * z.a, *s_sa = s_b + S * z.b, *s_sb = s_sa + S * z.sa;
+    // (the broadcast tells the compiler that a warp's branch is uniform: the MMA's
+    // descriptors then stay in uniform registers)
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int epi_warps = a.rows / 32;
+    const int nb = a.K / 32, nst = (a.K + kStageCodes - 1) / kStageCodes;
+    const uint64_t lim = a.wait_limit;
+    volatile int *abort = &s_abort;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], epi_warps);
+        }
+        for (int i = 0; i < kBufs; ++i) {
+            mbar_init(&s_sfull[i], 1);
+            mbar_init(&s_sempty[i], epi_warps);
+        }
+        mbar_init(&s_drain, 1);
+        s_abort = 0;
+        fence_barrier_init();
+    }
     pdl_wait();
     pdl_trigger();
-
-    const int row0 = n0 + warp * RW;
-    const uint8_t *wrow = a.wp + static_cast<int64_t>(row0) * a.K + lane * 16;
-    uint4 wq[kLoads][RW];
-    float dw[RW], dx = 0.0f;
-    auto load_w = [&](int st, int i) {
-        const int k = st * kStep + i * 512 + lane * 16;
-#pragma unroll
-        for (int r = 0; r < RW; ++r)
-            wq[i][r] = (k < a.K && row0 + r < a.N)
-                           ? __ldg(reinterpret_cast<const uint4 *>(
-                                 wrow + static_cast<int64_t>(r) * a.K + (st * kStep + i * 512)))
-                           : make_uint4(0u, 0u, 0u, 0u);
-    };
-    auto load_scales = [&](int st) {   // a block of the step a lane; a token a warp
-        const int b = st * kBlocks + lane;
-#pragma unroll
-        for (int r = 0; r < RW; ++r)
-            dw[r] = (b < nb && row0 + r < a.N) ? __ldg(a.wsc + (row0 + r) * a.ldws + b) : 0.0f;
-        if (warp < MT) dx = (warp < a.M && b < nb) ? __ldg(a.xdt + b * a.ldxd + warp) : 0.0f;
-    };
-    // the step's activations, widened into shared memory
-    auto stage_x = [&](int st, int buf) {
-        constexpr int kItems = MT * kLoads * 32;
-#pragma unroll
-        for (int it = 0; it < (kItems + kWarps * 32 - 1) / (kWarps * 32); ++it) {
-            const int item = it * kWarps * 32 + tid;
-            if (kItems % (kWarps * 32) != 0 && item >= kItems) break;
-            const int m = item / (kLoads * 32), i = (item / 32) % kLoads, ln = item & 31;
-            const int k = st * kStep + i * 512 + ln * 16;
-            const bool in = m < a.M && k < a.K;
-            uint4 *dst = s_act(buf) + (m * kLoads + i) * C::kActVecs * 32 + ln;
-#pragma unroll
-            for (int p = 0; p < XB / 4; ++p) {
-                // 4-bit: the codes' bytes; 8-bit: a block's 32 bytes of 16 h, then of l
-                const uint8_t *src =
-                    XB == 4 ? a.xw + static_cast<int64_t>(m) * a.K + k
-                            : a.xw + static_cast<int64_t>(m) * 2 * a.K + (k >> 5) * 64 + p * 32 + (k & 16);
-                uint32_t h[8];
-                widen16(in ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0u, 0u, 0u, 0u), h);
-                dst[(2 * p) * 32] = make_uint4(h[0], h[1], h[2], h[3]);
-                dst[(2 * p + 1) * 32] = make_uint4(h[4], h[5], h[6], h[7]);
-            }
-        }
-    };
-
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) load_w(0, i);
-    load_scales(0);
-    stage_x(0, 0);
+    if (warp == 5) {
+        tmem_alloc(&s_tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    auto give_up = [&]() {
+        s_abort = 1;
+        atomicOr(&g_few_status, kStatusTimeout);
+    };
 
-    float acc = 0.0f;   // of row n0 + lane and token `warp`
-    for (int st = 0; st < steps; ++st) {
-        const int buf = st & 1;
-        uint8_t *sum = s_sum(buf);
-#pragma unroll
-        for (int r = 0; r < RW; ++r) s_dw(buf)[lane * (C::kRows + 1) + warp * RW + r] = dw[r];
-        if (warp < MT) s_dx(buf)[warp * kBlocks + lane] = dx;
-        if (st + 1 < steps) load_scales(st + 1);
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            uint32_t w[RW][8];
-#pragma unroll
-            for (int r = 0; r < RW; ++r) widen16(wq[i][r], w[r]);
-            if (st + 1 < steps) load_w(st + 1, i);
-            const int b = i * 16 + (lane >> 1);   // the lane pair's block within the step
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (m < a.M) {
-                    const uint4 *act = s_act(buf) + (m * kLoads + i) * C::kActVecs * 32 + lane;
-                    if constexpr (XB == 4) {
-                        const uint4 x0 = act[0], x1 = act[32];
-                        const uint32_t x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-                        uint32_t s[RW];
-#pragma unroll
-                        for (int r = 0; r < RW; ++r) {
-                            uint32_t t = 0u;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) t = hfma2(w[r][j], x[j], t);
-                            s[r] = t;
-                        }
-                        __half *to = reinterpret_cast<__half *>(sum + (b * MT + m) * C::kSumStride) + warp * RW;
-                        if constexpr (RW == 1) {
-                            const uint32_t t = hadd2(s[0], s[0] >> 16);   // low half: both
-                            const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, t, 1);
-                            if (!(lane & 1)) {
-                                const uint32_t f = hadd2(t, o);
-                                to[0] = __ushort_as_half(static_cast<uint16_t>(f));
-                            }
-                        } else {
-                            // two rows' sums as one pair
-                            uint32_t f[RW / 2];
-#pragma unroll
-                            for (int q = 0; q < RW / 2; ++q) {
-                                const uint32_t t = hadd2(__byte_perm(s[2 * q], s[2 * q + 1], 0x5410),
-                                                         __byte_perm(s[2 * q], s[2 * q + 1], 0x7632));
-                                f[q] = hadd2(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
-                            }
-                            if constexpr (RW == 2) {
-                                if (!(lane & 1)) *reinterpret_cast<uint32_t *>(to) = f[0];
-                            } else {
-                                *reinterpret_cast<uint32_t *>(to + 2 * (lane & 1)) = (lane & 1) ? f[1] : f[0];
-                            }
-                        }
-                    } else {
-                        float s[RW];
-#pragma unroll
-                        for (int r = 0; r < RW; ++r) s[r] = 0.0f;
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            const uint4 x0 = act[(2 * p) * 32], x1 = act[(2 * p + 1) * 32];
-                            const uint32_t x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-                            for (int r = 0; r < RW; ++r) {
-                                uint32_t t = 0u;
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) t = hfma2(w[r][j], x[j], t);
-                                s[r] += half_sum(t);
-                            }
-                        }
-                        float *to = reinterpret_cast<float *>(sum + (b * MT + m) * C::kSumStride) + warp * RW;
-#pragma unroll
-                        for (int r = 0; r < RW; ++r) {
-                            s[r] += __shfl_xor_sync(0xFFFFFFFFu, s[r], 1);
-                            if ((lane & 1) == (r & 1) || (RW == 1 && !(lane & 1))) to[r] = s[r];
-                        }
-                    }
+    if (warp == 4) {
+        // ------------------------------------------------------------ TMA
+        const bool leader = elect_one();
+        if (leader) {
+            prefetch_tmap(&map_a);
+            prefetch_tmap(&map_b);
+            prefetch_tmap(&map_sa);
+            prefetch_tmap(&map_sb);
+        }
+        int s = 0, fed = 0;   // the stage; stages fed so far, at most S
+        uint32_t ph = 1;      // (the first round's waits pass at once)
+        bool ok = true;
+        for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+            for (int st = 0; st < nst; ++st) {
+                if (!warp_wait(&s_empty[s], ph, lim, abort)) {
+                    ok = false;
+                    break;
+                }
+                if (leader) {
+                    mbar_arrive_expect_tx(&s_full[s], z.stage());
+                    tma_load_3d(s_a + s * z.a, &map_a, &s_full[s], 0, t * a.rows, kCols128 * st);
+                    tma_load_3d(s_b + s * z.b, &map_b, &s_full[s], 0, 0, kCols128 * (XB / 4) * st);
+                    tma_load_2d(s_sa + s * z.sa, &map_sa, &s_full[s], kStageBlocks * st, t * a.rows);
+                    tma_load_2d(s_sb + s * z.sb, &map_sb, &s_full[s], 0, kStageBlocks * st);
+                }
+                __syncwarp();
+                if (fed < S) ++fed;
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
                 }
             }
         }
-        if (st + 1 < steps) stage_x(st + 1, buf ^ 1);
-        __syncthreads();
-        // warp m folds the step for token m, its blocks in order, a row a lane
-        if (warp < MT && warp < a.M && lane < C::kRows) {
-            const int n = min(kBlocks, nb - st * kBlocks);
-            const float *dwp = s_dw(buf) + lane, *dxp = s_dx(buf) + warp * kBlocks;
-            const uint8_t *sp = sum + warp * C::kSumStride;
-#pragma unroll 8
-            for (int b = 0; b < n; ++b) {
-                const uint8_t *at = sp + b * MT * C::kSumStride;
-                const float S = XB == 4 ? __half2float(reinterpret_cast<const __half *>(at)[lane])
-                                        : reinterpret_cast<const float *>(at)[lane];
-                acc = __fmaf_rn(__fmul_rn(dwp[b * (C::kRows + 1)], dxp[b]), S, acc);
+        if (leader) {
+            if (!ok) give_up();
+            // leave only when the copies under way have landed (at once unless a wait
+            // gave up): each fed stage's last phase
+            for (int i = 0; i < fed; ++i) {
+                if (--s < 0) {
+                    s = S - 1;
+                    ph ^= 1;
+                }
+                mbar_wait_bounded(&s_full[s], ph ^ 1, kDrainPolls, nullptr);
             }
         }
+        __syncwarp();
+    } else if (warp == 5) {
+        // ------------------------------------------------------------ MMA
+        {
+            const bool leader = elect_one();
+            const uint32_t idesc = idesc_e4m3_f32(128, kCols);
+            const uint64_t da0 = smem_desc_sw128(smem_u32(s_a)), db0 = smem_desc_sw128(smem_u32(s_b));
+            const uint32_t a_step = z.a >> 4, b_step = z.b >> 4, a_col = a.rows * 128 >> 4;
+            int s = 0, gb = 0;
+            uint32_t ph = 0, gph = 1;
+            bool ok = true;
+            for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+                for (int st = 0; st < nst; ++st) {
+                    if (!warp_wait(&s_full[s], ph, lim, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t da = da0 + s * a_step, db = db0 + s * b_step;
+                    const int n = nb - st * kStageBlocks;   // blocks left: a multiple of 4
+#pragma unroll
+                    for (int j0 = 0; j0 < kStageBlocks; j0 += kGroup) {
+                        if (j0 < n) {
+                            if (!warp_wait(&s_sempty[gb], gph, lim, abort)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+            if (leader) {
+#pragma unroll
+                            for (int i = 0; i < kGroup; ++i) {
+                                const int j = j0 + i;
+                                if ((j & ~3) < n) {
+                                    const uint64_t daj = da + (j >> 2) * a_col + (j & 3) * 2;
+                                    const uint32_t slot = tmem + (gb * kGroup + i) * kCols;
+                                    if constexpr (XB == 4) {
+                                        mma_f8f6f4(slot, daj, db + (((j >> 2) * kTokens * 128 + (j & 3) * 32) >> 4),
+                                                   idesc, 0);
+                                    } else {
+                                        // the 16 h, then the l, into one sum
+                                        const uint64_t dbj = db + (((j >> 1) * kTokens * 128 + (j & 1) * 64) >> 4);
+                                        mma_f8f6f4(slot, daj, dbj, idesc, 0);
+                                        mma_f8f6f4(slot, daj, dbj + (32 >> 4), idesc, 1);
+                                    }
+                                }
+                            }
+                            mma_commit(&s_sfull[gb]);
+            }
+            __syncwarp();
+                            if (++gb == kBufs) {
+                                gb = 0;
+                                gph ^= 1;
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (leader) {
+                if (!ok) give_up();
+                mma_commit(&s_drain);
+                mbar_wait_bounded(&s_drain, 0, kDrainPolls, nullptr);
+            }
+            __syncwarp();
+        }
+    } else if (warp < epi_warps) {
+        // ------------------------------------------------------- epilogue
+        // kBatch blocks' sums a load (measured: loads of the next batch under way while
+        // one is folded made every case 30-80% slower)
+        constexpr int kBatch = PT == 1 ? 8 : 4;
+        static_assert(kGroup % kBatch == 0 && kStageBlocks % kGroup == 0, "batches within hand-offs");
+        const int row = warp * 32 + lane;
+        const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
+        const EpiArgs &f = a.fin;
+        int s = 0, gb = 0;
+        uint32_t sph = 0, gph = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+            uint64_t acc[PT];
+#pragma unroll
+            for (int p = 0; p < PT; ++p) acc[p] = 0ull;
+            for (int st = 0; st < nst && ok; ++st) {
+                if (!warp_wait(&s_full[s], sph, lim, abort)) {
+                    ok = false;
+                    break;
+                }
+                const float *dw = reinterpret_cast<const float *>(s_sa + s * z.sa) + row * kStageBlocks;
+                const float *dx = reinterpret_cast<const float *>(s_sb + s * z.sb);
+                const int n = nb - st * kStageBlocks;   // blocks left: a multiple of 4
+#pragma unroll
+                for (int j0 = 0; j0 < kStageBlocks; j0 += kBatch) {
+                    if (j0 < n) {
+                        if (j0 % kGroup == 0) {
+                            if (!warp_wait(&s_sfull[gb], gph, lim, abort)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                        }
+                        const uint32_t tcol = tmem + lane_addr + (gb * kGroup + j0 % kGroup) * kCols;
+                        uint32_t v[kBatch][2 * PT];
+#pragma unroll
+                        for (int j = 0; j < kBatch; ++j) tmem_ld<PT>(tcol + j * kCols, v[j]);
+                        tmem_ld_wait();
+                        if (j0 % kGroup == kGroup - kBatch || j0 + kBatch >= n) {
+                            // the hand-off's sums are in registers
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&s_sempty[gb]);
+                            if (++gb == kBufs) {
+                                gb = 0;
+                                gph ^= 1;
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < kBatch; q += 4) {
+                            if (q == 0 || j0 + q < n) {
+                                const float4 d = *reinterpret_cast<const float4 *>(dw + j0 + q);
+                                const float ds[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const uint32_t w = __float_as_uint(ds[j]);
+                                    const uint64_t w2 = pair_of(w, w);
+                                    const uint64_t *x = reinterpret_cast<const uint64_t *>(dx + (j0 + q + j) * 16);
+#pragma unroll
+                                    for (int p = 0; p < PT; ++p)
+                                        acc[p] = fma_f32x2(mul_f32x2(w2, x[p]),
+                                                           pair_of(v[q + j][2 * p], v[q + j][2 * p + 1]), acc[p]);
+                                }
+                            }
+                        }
+                    }
+                }
+                // (the products that read the stage are done: their sums were waited for)
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[s]);
+                if (++s == S) {
+                    s = 0;
+                    sph ^= 1;
+                }
+            }
+            if (!ok) break;
+            // bias, activation, residual
+            const int n = t * a.rows + row;
+            const bool in = n < a.N;
+            const float bias = (f.bias && in) ? __ldg(f.bias + n) : 0.0f;
+            float y[2 * PT];
+#pragma unroll
+            for (int p = 0; p < PT; ++p) {
+                y[2 * p] = __uint_as_float(static_cast<uint32_t>(acc[p]));
+                y[2 * p + 1] = __uint_as_float(static_cast<uint32_t>(acc[p] >> 32));
+            }
+            if (f.bias) {
+#pragma unroll
+                for (int m = 0; m < 2 * PT; ++m) y[m] = __fadd_rn(y[m], bias);
+            }
+            if (f.act == H32_EPI_SWIGLU) {
+                // gate and up rows are adjacent lanes
+#pragma unroll
+                for (int m = 0; m < 2 * PT; ++m) y[m] = swiglu(y[m], __shfl_xor_sync(0xFFFFFFFFu, y[m], 1));
+                if (in && !(lane & 1)) finish_columns<2 * PT>(f, y, 0, 0, a.M, n >> 1);
+            } else {
+#pragma unroll
+                for (int m = 0; m < 2 * PT; ++m) y[m] = activate(y[m], f.act);
+                if (in) finish_columns<2 * PT>(f, y, 0, 0, a.M, n);
+            }
+        }
+        if (!ok && lane == 0) give_up();
     }
-    if (warp >= MT || warp >= a.M) return;
-    // bias, activation, residual: gate and up rows sit in adjacent lanes
-    const EpiArgs &f = a.fin;
-    const int n = n0 + lane;
-    const bool in = lane < C::kRows && n < a.N;
-    float z = acc;
-    if (f.bias && in) z = __fadd_rn(z, __ldg(f.bias + n));
-    int j = n;
-    bool out = in;
-    if (f.act == H32_EPI_SWIGLU) {
-        const float up = __shfl_xor_sync(0xFFFFFFFFu, z, 1);
-        z = swiglu(z, up);
-        j = n >> 1;
-        out = in && !(lane & 1);
-    } else {
-        z = activate(z, f.act);
-    }
-    if (out) {
-        if (f.res) z = __fadd_rn(z, load_value(f.res, warp * f.ldr + j, f.res_bf16));
-        store_value(f.y, warp * f.ldy + j, f.y_bf16, z);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
 }
 
-template <int XB, int MT, int RW>
-cudaError_t launch_few_rows(const FewArgs &a, cudaStream_t s) {
-    using C = FewCfg<XB, MT, RW>;
-    if (C::kSmem > 49152) {
-        const cudaError_t e = cudaFuncSetAttribute(few_kernel<XB, MT, RW>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(few_kernel<XB, MT, RW>, dim3((a.N + C::kRows - 1) / C::kRows), dim3(kWarps * 32),
-                      C::kSmem, s, a);
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
 }
 
-// rows a warp: 4 where the blocks still fill the card
-template <int XB, int MT>
-cudaError_t launch_few_tokens(const FewArgs &a, int sms, cudaStream_t s) {
-    if (a.N >= 32 * sms) return launch_few_rows<XB, MT, 4>(a, s);
-    if (a.N >= 16 * sms) return launch_few_rows<XB, MT, 2>(a, s);
-    return launch_few_rows<XB, MT, 1>(a, s);
+// rows of `row_bytes` as [row_bytes / 128][rows][128 bytes], boxes of `box_rows` rows
+// and `box_cols` 128-byte columns, 128B-swizzled
+bool code_map(CUtensorMap *map, const void *base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows,
+              uint32_t box_cols) {
+    const cuuint64_t dims[3] = {128, rows, row_bytes / 128}, strides[2] = {row_bytes, 128};
+    const cuuint32_t box[3] = {128, box_rows, box_cols}, estr[3] = {1, 1, 1};
+    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
+                     estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool scale_map(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer, uint32_t box_inner,
+               uint32_t box_outer) {
+    const cuuint64_t dims[2] = {inner, outer}, strides[1] = {inner * 4};
+    const cuuint32_t box[2] = {box_inner, box_outer}, estr[2] = {1, 1};
+    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base), dims, strides, box,
+                     estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int XB>
-cudaError_t launch_few_bits(const FewArgs &a, int sms, cudaStream_t s) {
-    if (a.M == 1) return launch_few_tokens<XB, 1>(a, sms, s);
-    if (a.M == 2) return launch_few_tokens<XB, 2>(a, sms, s);
-    if (a.M <= 4) return launch_few_tokens<XB, 4>(a, sms, s);
-    return launch_few_tokens<XB, 8>(a, sms, s);
+template <int XB, int PT, int kStageBlocks>
+h32_status launch_few_kernel(const CUtensorMap *maps, const FewArgs &a, int grid, int smem,
+                             cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(few_kernel<XB, PT, kStageBlocks>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess)
+        e = launch_pdl(few_kernel<XB, PT, kStageBlocks>, dim3(grid), dim3(kWarps * 32), smem, s, maps[0],
+                       maps[1], maps[2], maps[3], a);
+    return launch_status(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+template <int XB, int PT>
+h32_status launch_few_pairs(const CUtensorMap *maps, const FewArgs &a, int blocks, int grid, int smem,
+                            cudaStream_t s) {
+    return blocks == 16 ? launch_few_kernel<XB, PT, 16>(maps, a, grid, smem, s)
+                        : launch_few_kernel<XB, PT, 8>(maps, a, grid, smem, s);
 }
 
 }  // namespace
 
-cudaError_t launch_few(int xbits, const uint8_t *wp, const float *wsc, int64_t ldws,
-                       const uint8_t *xw, const float *xdt, int64_t ldxd, int64_t M, int64_t N,
-                       int64_t K, const EpiArgs &fin, int sms, cudaStream_t s) {
+h32_status launch_few(int xbits, const uint8_t *wp, const float *wsc, int64_t ldws,
+                      const uint8_t *xw, const float *xdt, int64_t ldxd, int64_t M, int64_t N,
+                      int64_t K, const EpiArgs &fin, int sms, cudaStream_t s) {
     FewArgs a{};
-    a.wp = wp;
-    a.wsc = wsc;
-    a.ldws = ldws;
-    a.xw = xw;
-    a.xdt = xdt;
-    a.ldxd = ldxd;
     a.M = static_cast<int32_t>(M);
     a.N = static_cast<int32_t>(N);
     a.K = static_cast<int32_t>(K);
+    // the widest tile that still is one wave of at least half the SMs
+    a.rows = N > 128 * sms / 2 ? 128 : N > 64 * sms / 2 ? 64 : 32;
+    a.tiles = static_cast<int32_t>((N + a.rows - 1) / a.rows);
+    a.wait_limit = wait_limit();
     a.fin = fin;
-    return xbits == 4 ? launch_few_bits<4>(a, sms, s) : launch_few_bits<8>(a, sms, s);
+    // longer stages for the narrow tiles, whose pace the barriers between the warps set;
+    // of 128 rows more short ones fit
+    const int blocks = a.rows == 128 ? 8 : 16;
+    const uint32_t tokens = M <= 8 ? 8 : 16;
+    const Sizes z(a.rows, tokens, xbits, blocks);
+    // (the MMA reads 128 rows from every column of a stage's weights: what lies behind
+    // the last one, at most 12 KB, is the tokens' and the scales' stages)
+    const int fit = (kMaxSmem - 1024) / static_cast<int>(z.stage());
+    a.stages = fit < kMaxStages ? fit : kMaxStages;
+    const int smem = a.stages * static_cast<int>(z.stage()) + 1024;
+    if (!encoder()) {
+        note_error("cuTensorMapEncodeTiled is not available from the driver");
+        return H32_ERR_CUDA;
+    }
+    const uint64_t xrow = K * (xbits / 4);
+    CUtensorMap maps[4];
+    if (!code_map(&maps[0], wp, K, N, a.rows, blocks / 4) ||
+        !code_map(&maps[1], xw, xrow, M, tokens, blocks / 4 * (xbits / 4)) ||
+        !scale_map(&maps[2], wsc, ldws, N, blocks, a.rows) ||
+        !scale_map(&maps[3], xdt, ldxd, K / 32, 16, blocks)) {
+        note_error("cuTensorMapEncodeTiled rejected a tensor map of the few-token product");
+        return H32_ERR_CUDA;
+    }
+    const int grid = a.tiles < sms ? a.tiles : sms;
+    if (xbits == 4) {
+        if (M <= 2) return launch_few_pairs<4, 1>(maps, a, blocks, grid, smem, s);
+        if (M <= 8) return launch_few_pairs<4, 4>(maps, a, blocks, grid, smem, s);
+        return launch_few_pairs<4, 8>(maps, a, blocks, grid, smem, s);
+    }
+    if (M <= 2) return launch_few_pairs<8, 1>(maps, a, blocks, grid, smem, s);
+    if (M <= 8) return launch_few_pairs<8, 4>(maps, a, blocks, grid, smem, s);
+    return launch_few_pairs<8, 8>(maps, a, blocks, grid, smem, s);
+}
+
+__device__ uint32_t g_few_status_taken;
+__global__ void take_g_few_status() { g_few_status_taken = atomicExch(&g_few_status, 0u); }
+
+h32_status few_read_and_clear_status(cudaStream_t s) {
+    bool ok = false;
+    const uint32_t v = take_status(take_g_few_status, g_few_status_taken, s, &ok);
+    if (!ok) return H32_ERR_CUDA;
+    return (v & kStatusTimeout) ? H32_ERR_TIMEOUT : H32_OK;
 }
 
 }  // namespace h32

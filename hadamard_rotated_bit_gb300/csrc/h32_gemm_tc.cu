@@ -1481,11 +1481,9 @@ h32_status run_gemm_tc(int xbits, const uint8_t *wp, const float *wsc, int64_t l
     if (M > 0x7FFFFFFFll || E * N > 0x7FFFFFFFll || K > 0x7FFFFFFFll) return H32_ERR_INVALID_ARG;
     int sms = 0;
     H32_TRY(check_device(&sms));
-    if (fin && !expert_off && M <= kFewTokens) {
-        const cudaError_t e = launch_few(xbits, wp, wsc, ldws, xw, xdt, ldxd, M, N, K, *fin, sms,
-                                         reinterpret_cast<cudaStream_t>(stream));
-        return launch_status(e != cudaSuccess ? e : cudaGetLastError());
-    }
+    if (fin && !expert_off && M <= kFewTokens)
+        return launch_few(xbits, wp, wsc, ldws, xw, xdt, ldxd, M, N, K, *fin, sms,
+                          reinterpret_cast<cudaStream_t>(stream));
     // dense: the tile width and the cut of the last wave from the schedule
     // simulation; groups: full 128-row chunks, nothing cut
     TcPlan plan{kBNMax, 1, 0, 0, sms};
