@@ -356,44 +356,55 @@ __device__ __forceinline__ void stage_dw(const float *s_sa, int s, int row, int 
 // feature) and 16 token columns per chunk, so for each column the warp's 32 lanes
 // read and write 32 consecutive features.  For the gated activation the lanes of
 // a pair hold a gate row and its up row: they exchange halves of the chunk (8
-// shuffles), the even lane finishes columns 0..7, the odd lane 8..15.
-template <int kMaxChunks>
-__device__ __forceinline__ void finish_tile(const TcArgs &a, const TcTile &ti, int row, int lane,
-                                            int c0, int nch, const uint64_t *acc) {
+// shuffles), the even lane finishes columns 0..7, the odd lane 8..15.  The
+// accumulators pass through local memory into loops of eight columns that are not
+// unrolled, and the tile is looked up again, so that the block loop holds as little
+// as it can for this code: gate/up, 512 x 34816 x 5120, to bf16 with SwiGLU 358 us
+// (unrolled on the accumulators 395; the bare product 311: the block loop still takes
+// 7% more instructions than the plain instance's).
+template <int EPQ, int kMaxChunks, int kProdWarps, bool kTail>
+__device__ __forceinline__ void finish_tile(const TcArgs &a, int t, const int *s_off, const int *s_tpre,
+                                            const uint64_t *acc) {
     const EpiArgs &f = a.fin;
-    const int n = ti.n0 + row;
-    const bool in = n < a.N;
-    const float bias = (f.bias && in) ? __ldg(f.bias + ti.wrow + row) : 0.0f;
-    const bool gated = f.act == H32_EPI_SWIGLU;
+    uint64_t z[8 * kMaxChunks];
 #pragma unroll
-    for (int c = 0; c < kMaxChunks; ++c) {
-        if (c < nch) {
-            float z[16];
+    for (int q = 0; q < 8 * kMaxChunks; ++q) z[q] = acc[q];
+    // the tile is looked up again, so that the block loop holds nothing for this code
+    int tid = threadIdx.x;
+    asm volatile("" : "+r"(t), "+r"(tid) : : "memory");
+    const TcTile ti = tc_tile<kTail>(t, a, s_off, s_tpre);
+    const int warp = tid >> 5, part = (warp - kProdWarps) >> 2, row = (warp & 3) * 32 + (tid & 31);
+    const int base = (ti.ncols >> 4) / EPQ, rem = (ti.ncols >> 4) % EPQ;
+    const int nch = base + (part < rem ? 1 : 0), c0 = 16 * (part * base + min(part, rem));
+    const int n = ti.n0 + row, wrow = ti.wrow + row, g0 = ti.g0, clo = ti.clo, chi = ti.chi;
+    const bool in = n < a.N;
+    const float bias = (f.bias && in) ? __ldg(f.bias + wrow) : 0.0f;
+    const bool odd = n & 1;   // (tiles start at even rows)
+    auto value = [&](int q) {
+        const float v = __uint_as_float(static_cast<uint32_t>(z[q >> 1] >> (32 * (q & 1))));
+        return f.bias ? __fadd_rn(v, bias) : v;
+    };
+    if (f.act == H32_EPI_SWIGLU) {
+#pragma unroll 1
+        for (int c = 0; c < nch; ++c) {
+            float v[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const uint64_t pr = acc[8 * c + q];
-                z[2 * q] = __uint_as_float(static_cast<uint32_t>(pr));
-                z[2 * q + 1] = __uint_as_float(static_cast<uint32_t>(pr >> 32));
+                const float lo = value(16 * c + q), hi = value(16 * c + 8 + q);
+                const float u = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo : hi, 1);
+                v[q] = odd ? swiglu(u, hi) : swiglu(lo, u);
             }
-            if (f.bias) {
+            const int first = c0 + 16 * c + (odd ? 8 : 0);
+            if (in) finish_columns<8>(f, v, static_cast<int64_t>(g0) + first, clo - first, chi - first, n >> 1);
+        }
+    } else {
+#pragma unroll 1
+        for (int h = 0; h < 2 * nch; ++h) {
+            float v[8];
 #pragma unroll
-                for (int q = 0; q < 16; ++q) z[q] = __fadd_rn(z[q], bias);
-            }
-            const int col = c0 + 16 * c;
-            if (gated) {
-                const bool odd = lane & 1;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float v = __shfl_xor_sync(0xFFFFFFFFu, odd ? z[q] : z[8 + q], 1);
-                    z[q] = odd ? swiglu(v, z[8 + q]) : swiglu(z[q], v);
-                }
-                const int first = col + (odd ? 8 : 0);
-                if (in) finish_columns<8>(f, z, ti.g0 + first, ti.clo - first, ti.chi - first, n >> 1);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 16; ++q) z[q] = activate(z[q], f.act);
-                if (in) finish_columns<16>(f, z, ti.g0 + col, ti.clo - col, ti.chi - col, n);
-            }
+            for (int q = 0; q < 8; ++q) v[q] = activate(value(8 * h + q), f.act);
+            const int first = c0 + 8 * h;
+            if (in) finish_columns<8>(f, v, static_cast<int64_t>(g0) + first, clo - first, chi - first, n);
         }
     }
 }
@@ -527,7 +538,7 @@ __device__ __forceinline__ bool epi_item(const TcArgs &a, int t, int st0, int ns
     }
     const int64_t n = ti.n0 + row;
     if constexpr (kFin) {
-        finish_tile<C::kMaxChunks>(a, ti, row, lane, c0, nch, acc);
+        finish_tile<EPQ, C::kMaxChunks, C::kProdWarps, kTail>(a, t, s_off, s_tpre, acc);
     } else if (n < a.N && (!kQN || a.y)) {
 #pragma unroll
         for (int c = 0; c < C::kMaxChunks; ++c) {
@@ -710,7 +721,7 @@ __device__ __forceinline__ bool epilogue_tiles_plain(const TcArgs &a, int total,
         }
         const int64_t n = ti.n0 + row;
         if constexpr (kFin) {
-            finish_tile<C::kMaxChunks>(a, ti, row, lane, c0, nch, acc);
+            finish_tile<EPQ, C::kMaxChunks, C::kProdWarps, kTail>(a, t, s_off, s_tpre, acc);
         } else if (n < a.N && (!kQN || a.y)) {
 #pragma unroll
             for (int c = 0; c < C::kMaxChunks; ++c) {
