@@ -273,23 +273,33 @@ def _same_gpu(*named):
             raise ValueError(f"{name} is on {t.device}, the call's other tensors on {dev}")
 
 
-def _on_stream(dev, stream, body):
-    """body(stream handle) with `dev` current and torch allocating for `stream` (None:
-    the device's current stream; a torch stream, or a raw handle), so that outputs
-    allocated inside belong to the stream the kernels run on."""
+def _enter_stream(dev, stream):
+    """(stream handle, guard): `dev` current and torch allocating for `stream` (None: the
+    device's current stream; a torch stream, or a raw handle) until guard.__exit__, so
+    that outputs allocated meanwhile belong to the stream the kernels run on.  The guard
+    is None where nothing has to change."""
     torch = _torch()
+    index = dev.index
     if stream is None:
-        if torch.cuda.current_device() == dev.index:
-            return body(_current_raw_stream(dev.index))
-        with torch.cuda.device(dev):
-            return body(_current_raw_stream(dev.index))
+        if _current_device() == index:
+            return _current_raw_stream(index), None
+        guard = torch.cuda.device(dev)
+        guard.__enter__()
+        return _current_raw_stream(index), guard
     if not hasattr(stream, "cuda_stream"):
         stream = (torch.cuda.ExternalStream(int(stream), device=dev) if int(stream)
                   else torch.cuda.default_stream(dev))
     elif stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the call's tensors on {dev}")
-    with torch.cuda.stream(stream):
-        return body(stream.cuda_stream)
+    guard = torch.cuda.stream(stream)
+    guard.__enter__()
+    return stream.cuda_stream, guard
+
+
+def _current_device():
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getDevice", None)   # (CUDA tensors exist: initialised)
+    return get() if get else torch.cuda.current_device()
 
 
 def _act_dtype(x, name="x"):
@@ -915,6 +925,7 @@ def h32_moe_combine(y, row_of, topk_w, out=None, stream=None):
     return out
 
 
+EPILOGUE_FEW_TOKENS = 16   # up to here the products with an epilogue need no workspace
 EPI_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu_tanh": 3, "gelu_erf": 4, "swiglu": 5}
 
 
@@ -966,21 +977,26 @@ def _gemm_epilogue(fn, wp, wsc, xw, xdt, M, bias, act, residual, y, y_dtype, str
               ("residual", residual), ("y", y), ("workspace", workspace if explicit_ws else None))
     dev = wp.device
 
-    def body(raw, y=y):
+    raw, guard = _enter_stream(dev, stream)
+    try:
         if y is None:
             y = torch.empty((M, n_out), dtype=y_dtype or f32, device=dev)
         ws = workspace if explicit_ws else None
-        if workspace is None and M > 0:
+        if workspace is None and M > EPILOGUE_FEW_TOKENS:
             ws = _workspace_for(M, N, K, dev, raw)
+        rp, rb, ldr = None, False, 0
+        if residual is not None:
+            rp, rb, ldr = residual.data_ptr(), residual.dtype == bf16, _pitch(residual)
         st = getattr(lib(), fn)(
             wp.data_ptr(), wsc.data_ptr(), wsc.shape[1], xw.data_ptr(), xdt.data_ptr(), xdt.shape[1],
-            M, N, K, _raw(bias), EPI_ACTS[act], _raw(residual),
-            residual is not None and residual.dtype == bf16, _pitch(residual), y.data_ptr(),
-            y.dtype == bf16, _pitch(y), _raw(ws), 0 if ws is None else ws.numel(), raw)
+            M, N, K, None if bias is None else bias.data_ptr(), EPI_ACTS[act], rp, rb, ldr,
+            y.data_ptr(), y.dtype == bf16, _pitch(y), _raw(ws), 0 if ws is None else ws.numel(), raw)
+    finally:
+        if guard is not None:
+            guard.__exit__(None, None, None)
+    if st:
         _check(fn, st)
-        return y
-
-    return _on_stream(dev, stream, body)
+    return y
 
 
 ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
@@ -1031,8 +1047,8 @@ def h32_moe_route_scored(logits, k, score="softmax", bias=None, n_group=1, topk_
               ("expert_off", expert_off), ("row_idx", row_idx), ("row_of", row_of))
     dev = logits.device
 
-    def body(raw, topk_id=topk_id, topk_w=topk_w, expert_off=expert_off, row_idx=row_idx,
-             row_of=row_of):
+    raw, guard = _enter_stream(dev, stream)
+    try:
         if topk_id is None:
             topk_id = torch.empty((T, k), dtype=torch.int32, device=dev)
         if topk_w is None:
@@ -1043,20 +1059,23 @@ def h32_moe_route_scored(logits, k, score="softmax", bias=None, n_group=1, topk_
             row_idx = torch.empty(T * k, dtype=torch.int32, device=dev)
         if row_of is None:
             row_of = torch.empty((T, k), dtype=torch.int32, device=dev)
-        ws, ws_bytes = None, 0
+        wp, ws_bytes = None, 0
         if T > ROUTE_SOLO_TOKENS:
             # the call's own: freed with it, reused only by later work of the stream
             ws_bytes = h32_moe_route_scored_workspace_bytes(T, E)
             ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+            wp = ws.data_ptr()
         st = lib().h32_moe_route_scored(
-            logits.data_ptr(), T, E, _pitch(logits) if T > 0 else E, ROUTE_SCORES[score],
-            _raw(bias), n_group, topk_group, group_top, k, bool(renormalize), scale,
-            topk_id.data_ptr(), topk_w.data_ptr(), expert_off.data_ptr(), row_idx.data_ptr(),
-            row_of.data_ptr(), _raw(ws), ws_bytes, raw)
+            logits.data_ptr(), T, E, logits.stride(0) if T > 1 else E, ROUTE_SCORES[score],
+            None if bias is None else bias.data_ptr(), n_group, topk_group, group_top, k,
+            bool(renormalize), scale, topk_id.data_ptr(), topk_w.data_ptr(), expert_off.data_ptr(),
+            row_idx.data_ptr(), row_of.data_ptr(), wp, ws_bytes, raw)
+    finally:
+        if guard is not None:
+            guard.__exit__(None, None, None)
+    if st:
         _check("h32_moe_route_scored", st)
-        return topk_id, topk_w, expert_off, row_idx, row_of
-
-    return _on_stream(dev, stream, body)
+    return topk_id, topk_w, expert_off, row_idx, row_of
 
 
 ACT_FORMS = {"q4": 0, "q8": 1, "q4_tc": 2, "q8_tc": 3, "q4_tc_e5m2": 4}
@@ -1092,11 +1111,14 @@ def h32_add_rms_norm_quantize(x, weight, residual=None, eps=1e-6, form="q4_tc", 
         raise ValueError("form=None needs norm_out")
     if residual_out is not None and residual_out is not False:
         _need(residual_out, "residual_out", (residual.dtype,), (_ge(M), _ge(K)), pitched=True)
-    if isinstance(norm_out, torch.dtype):
-        if norm_out not in either:
-            raise ValueError("norm_out must be bf16 or fp32")
-    elif norm_out is not None:
-        _need(norm_out, "norm_out", either, (_ge(M), _ge(K)), pitched=True)
+    want = None   # the type of a norm_out to allocate
+    if norm_out is not None:
+        if isinstance(norm_out, torch.dtype):
+            if norm_out not in either:
+                raise ValueError("norm_out must be bf16 or fp32")
+            want = norm_out
+        else:
+            _need(norm_out, "norm_out", either, (_ge(M), _ge(K)), pitched=True)
     tc = form is not None and form.endswith(("_tc", "_e5m2"))
     qshape = None
     if form is None:
@@ -1109,35 +1131,48 @@ def h32_add_rms_norm_quantize(x, weight, residual=None, eps=1e-6, form="q4_tc", 
                   (_ge(M), qshape[1]))
         if xd is not None:
             _need(xd, "xd", (f32,), (_ge(K // 32), _ge(M)) if tc else (_ge(M), K // 32))
-    keep = residual_out if isinstance(residual_out, torch.Tensor) else None
-    nrm = norm_out if isinstance(norm_out, torch.Tensor) else None
+    keep = None if residual_out is False else residual_out
+    nrm = None if want is not None else norm_out
     _same_gpu(("x", x), ("weight", weight), ("residual", residual), ("residual_out", keep),
               ("norm_out", nrm), ("xq", xq), ("xd", xd))
     dev = x.device
-
-    def body(raw, res_out=keep, nrm=nrm, xq=xq, xd=xd):
-        if residual is not None and residual_out is None:
-            res_out = torch.empty((M, K), dtype=residual.dtype, device=dev)
-        if nrm is None and norm_out is not None:
-            nrm = torch.empty((M, K), dtype=norm_out, device=dev)
+    raw, guard = _enter_stream(dev, stream)
+    try:
+        rp = op = np_ = None
+        rb = nb16 = False
+        ldr = ldo = ldn = 0
+        if residual is not None:
+            rb, rp = residual.dtype == bf16, residual.data_ptr()
+            ldr = residual.stride(0) if M > 1 else K
+            if residual_out is None:
+                keep = torch.empty((M, K), dtype=residual.dtype, device=dev)
+            if keep is not None:
+                op, ldo = keep.data_ptr(), keep.stride(0) if keep.shape[0] > 1 else keep.shape[1]
+        if want is not None:
+            nrm = torch.empty((M, K), dtype=want, device=dev)
+        if nrm is not None:
+            nb16, np_ = nrm.dtype == bf16, nrm.data_ptr()
+            ldn = nrm.stride(0) if nrm.shape[0] > 1 else nrm.shape[1]
+        qp = dp = None
+        ldxd = 0
         if form is not None:
             if xq is None:
                 xq = torch.empty(qshape, dtype=torch.int8 if form == "q8" else torch.uint8,
                                  device=dev)
             if xd is None:
-                xd = torch.empty((K // 32, _round4(M)) if tc else (M, K // 32), dtype=f32,
+                xd = torch.empty((K // 32, (M + 3) // 4 * 4) if tc else (M, K // 32), dtype=f32,
                                  device=dev)
+            qp, dp, ldxd = xq.data_ptr(), xd.data_ptr(), xd.shape[1] if tc else 0
         st = lib().h32_add_rms_norm_quantize(
-            x.data_ptr(), x.dtype == bf16, _rows(x, "x"),
-            _raw(residual), residual is not None and residual.dtype == bf16, _pitch(residual),
-            weight.data_ptr(), weight.dtype == bf16, eps, M, K,
-            _raw(res_out), _pitch(res_out), _raw(nrm), nrm is not None and nrm.dtype == bf16,
-            _pitch(nrm), ACT_FORMS.get(form, 0), _rot_arg(rotate), _raw(xq), _raw(xd),
-            xd.shape[1] if tc else 0, raw)
+            x.data_ptr(), x.dtype == bf16, x.stride(0) if M > 1 else K, rp, rb, ldr,
+            weight.data_ptr(), weight.dtype == bf16, eps, M, K, op, ldo, np_, nb16, ldn,
+            0 if form is None else ACT_FORMS[form], _rot_arg(rotate), qp, dp, ldxd, raw)
+    finally:
+        if guard is not None:
+            guard.__exit__(None, None, None)
+    if st:
         _check("h32_add_rms_norm_quantize", st)
-        return xq, xd, res_out, nrm
-
-    return _on_stream(dev, stream, body)
+    return xq, xd, keep, nrm
 
 
 # --------------------------------------------------------------------------
