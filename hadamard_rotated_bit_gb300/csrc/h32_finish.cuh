@@ -35,7 +35,7 @@ __device__ __forceinline__ float swiglu(float gate, float up) {
 // at negative z.
 __device__ __forceinline__ float activate(float z, int act) {
     switch (act) {
-        case H32_EPI_RELU: return z > 0.0f ? z : 0.0f;
+        case H32_EPI_RELU: return z < 0.0f ? 0.0f : z;   // NaN stays
         case H32_EPI_SILU: return sigmoid_times(z, z);
         case H32_EPI_GELU_TANH: {
             const float c = 1.5957691216057308f;   // 2 sqrt(2 / pi)

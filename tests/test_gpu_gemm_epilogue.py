@@ -123,6 +123,22 @@ def test_every_activation(h32, bits, act, M):
                 _check(h32, z, ops, bits, bias=b, act=act, res=rs, y_bf16=yb)
 
 
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M", [2, 40])
+def test_nan_stays_where_it_is(h32, act, M):
+    """A NaN of the bias comes out of its own outputs, and of no others."""
+    import torch
+    N, K = 64, 128
+    z, ops = _operands(h32, M, N, K, 4, 3)
+    bias = np.zeros(N, np.float32)
+    bias[[5, 32]] = np.nan
+    y = h32.q4_0_x_q4_gemm_tc_epilogue(*ops, M=M, bias=torch_of(bias), act=act)
+    torch.cuda.synchronize()
+    want = np.zeros(N // 2 if act == "swiglu" else N, bool)
+    want[[2, 16] if act == "swiglu" else [5, 32]] = True
+    assert np.array_equal(np.isnan(np_of(y)), np.broadcast_to(want, y.shape))
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh", "gelu_erf", "swiglu"])
 def test_activation_range(h32, bits, act):
