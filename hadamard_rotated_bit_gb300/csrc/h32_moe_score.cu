@@ -34,6 +34,8 @@ namespace {
 
 constexpr int kSoloTokens = 64;       // tokens one block routes and groups in one launch
 constexpr int kPlaceThreads = 1024;
+static_assert(kPlaceThreads >= kMaxE, "a thread an expert");
+constexpr int kPassTokens = 512;      // tokens whose bitmaps are in shared memory at once
 
 struct ScoreArgs {
     const float *logits, *bias;
@@ -672,9 +674,9 @@ __global__ void __launch_bounds__(1024) route_chunk_kernel(const ScoreArgs a, in
     pdl_trigger();
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) s_count[e] = 0;
     __syncthreads();
-    const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
-    for (int t = t0 + (threadIdx.x >> 5); t < t1; t += blockDim.x >> 5) {
-        const int e = route_token<NPER, kLogit>(a, t);
+    const int t0 = blockIdx.x * a.chunk, n = min(a.T - t0, a.chunk);
+    for (int i = threadIdx.x >> 5; i < n; i += blockDim.x >> 5) {
+        const int e = route_token<NPER, kLogit>(a, static_cast<int64_t>(t0) + i);
         if (e >= 0 && counts) atomicAdd(&s_count[e], 1);
     }
     if (!counts) return;
@@ -720,7 +722,8 @@ __global__ void __launch_bounds__(1024) route_solo_kernel(const ScoreArgs a, int
     place_chunk(a.topk_id, 0, a.T, a.k, kWords, s_start, s_map, row_idx, row_of);
 }
 
-// One block a chunk: where each expert's rows of the chunk start, then the rows.
+// One block a chunk: where each expert's rows of the chunk start, then the rows, the
+// bitmaps of up to kPassTokens tokens at a time.
 __global__ void __launch_bounds__(kPlaceThreads)
     route_place_kernel(const int32_t *__restrict__ topk_id, const int32_t *__restrict__ counts, int T,
                        int E, int k, int chunk, int chunks, int32_t *__restrict__ expert_off,
@@ -728,7 +731,7 @@ __global__ void __launch_bounds__(kPlaceThreads)
     extern __shared__ uint32_t s_map[];   // [E][words]
     __shared__ int s_before[kMaxE], s_all[kMaxE];
     __shared__ int s_warp[32];
-    const int words = (chunk + 31) / 32;
+    const int words = (min(chunk, kPassTokens) + 31) / 32;
     for (int e = threadIdx.x; e < E; e += kPlaceThreads) s_before[e] = s_all[e] = 0;
     for (int i = threadIdx.x; i < E * words; i += kPlaceThreads) s_map[i] = 0u;
     pdl_wait();
@@ -749,11 +752,15 @@ __global__ void __launch_bounds__(kPlaceThreads)
         atomicAdd(&s_before[e], before);
         atomicAdd(&s_all[e], all);
     }
-    const int t0 = blockIdx.x * chunk, t1 = min(T, t0 + chunk), n = (t1 - t0) * k;
-    for (int c = threadIdx.x; c < n; c += kPlaceThreads) {
-        const int i = c / k, x = topk_id[static_cast<int64_t>(t0) * k + c];
-        atomicOr(&s_map[x * words + (i >> 5)], 1u << (i & 31));
-    }
+    const int t0 = blockIdx.x * chunk, t1 = t0 + min(T - t0, chunk);
+    auto fill = [&](int p0, int p1) {
+        for (int c = threadIdx.x; c < (p1 - p0) * k; c += kPlaceThreads) {
+            const int i = c / k, x = topk_id[static_cast<int64_t>(p0) * k + c];
+            atomicOr(&s_map[x * words + (i >> 5)], 1u << (i & 31));
+        }
+    };
+    int p0 = t0, p1 = t0 + min(t1 - t0, kPassTokens);
+    fill(p0, p1);
     __syncthreads();
     const int x = threadIdx.x;
     const int tot = x < E ? s_all[x] : 0;
@@ -766,11 +773,26 @@ __global__ void __launch_bounds__(kPlaceThreads)
         }
     }
     __syncthreads();
-    place_chunk(topk_id, t0, t1, k, words, s_before, s_map, row_idx, row_of);
+    for (;;) {
+        place_chunk(topk_id, p0, p1, k, words, s_before, s_map, row_idx, row_of);
+        if (p1 == t1) break;
+        __syncthreads();
+        if (x < E) {   // past this pass's rows
+            for (int w = 0; w < words; ++w) {
+                s_before[x] += __popc(s_map[x * words + w]);
+                s_map[x * words + w] = 0u;
+            }
+        }
+        __syncthreads();
+        p0 = p1;
+        p1 += min(t1 - p1, kPassTokens);
+        fill(p0, p1);
+        __syncthreads();
+    }
 }
 
-// The chunks of a call with a workspace: about as many as the card has SMs, each
-// of at most 512 tokens (the bitmaps' shared memory).
+// The chunks of a call with a workspace: as many as the card has SMs, twice that where
+// they are longer than a pass (their table of counts stays small for any T).
 struct Chunks {
     int64_t size, count;
 };
@@ -778,7 +800,7 @@ inline Chunks route_chunks(int64_t T) {
     constexpr int64_t kSms = 152;
     int64_t size = (T + kSms - 1) / kSms;
     if (size < 8) size = 8;
-    if (size > 512) size = 512;
+    if (size > kPassTokens) size = (T + 2 * kSms - 1) / (2 * kSms);
     return Chunks{size, (T + size - 1) / size};
 }
 
@@ -888,7 +910,8 @@ extern "C" h32_status h32_moe_route_scored(const float *logits, int64_t T, int32
     if (e != cudaSuccess || solo) return launch_status(e != cudaSuccess ? e : cudaGetLastError());
     if (!workspace)
         return launch_status(launch_route_group(topk_id, t32, E, k, expert_off, row_idx, row_of, s));
-    const size_t smem = static_cast<size_t>(E) * ((ch.size + 31) / 32) * 4;
+    const int64_t pass = ch.size < kPassTokens ? ch.size : kPassTokens;
+    const size_t smem = static_cast<size_t>(E) * ((pass + 31) / 32) * 4;
     if (smem > 32768) {   // above what a kernel may use beside its static arrays unasked
         e = cudaFuncSetAttribute(route_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
         if (e != cudaSuccess) return launch_status(e);

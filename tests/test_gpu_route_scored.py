@@ -76,6 +76,12 @@ def test_matches_the_rule(h32, score, renorm, T, E, k, G, tg, gt):
                renormalize=renorm, scale=2.5)
 
 
+@pytest.mark.parametrize("T,E,k,G,tg", [(77824, 33, 3, 1, 1), (77825, 40, 4, 8, 3), (190001, 20, 2, 1, 1)])
+def test_long_batches(h32, T, E, k, G, tg):
+    """Chunks of exactly one pass of tokens, and of more than one."""
+    _check(h32, _logits(T, E, T), k, score="sigmoid", n_group=G, topk_group=tg)
+
+
 def test_row_pitch(h32):
     l = _logits(19, 64, 3)
     for pad in (1, 4, 64):
