@@ -244,27 +244,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                                 break;
                             }
                             tc_fence_after();
-            if (leader) {
+                            if (leader) {
 #pragma unroll
-                            for (int i = 0; i < kGroup; ++i) {
-                                const int j = j0 + i;
-                                if ((j & ~3) < n) {
-                                    const uint64_t daj = da + (j >> 2) * a_col + (j & 3) * 2;
-                                    const uint32_t slot = tmem + (gb * kGroup + i) * kCols;
-                                    if constexpr (XB == 4) {
-                                        mma_f8f6f4(slot, daj, db + (((j >> 2) * kTokens * 128 + (j & 3) * 32) >> 4),
-                                                   idesc, 0);
-                                    } else {
-                                        // the 16 h, then the l, into one sum
-                                        const uint64_t dbj = db + (((j >> 1) * kTokens * 128 + (j & 1) * 64) >> 4);
-                                        mma_f8f6f4(slot, daj, dbj, idesc, 0);
-                                        mma_f8f6f4(slot, daj, dbj + (32 >> 4), idesc, 1);
+                                for (int i = 0; i < kGroup; ++i) {
+                                    const int j = j0 + i;
+                                    if ((j & ~3) < n) {
+                                        const uint64_t daj = da + (j >> 2) * a_col + (j & 3) * 2;
+                                        const uint32_t slot = tmem + (gb * kGroup + i) * kCols;
+                                        if constexpr (XB == 4) {
+                                            mma_f8f6f4(slot, daj, db + (((j >> 2) * kTokens * 128 + (j & 3) * 32) >> 4),
+                                                       idesc, 0);
+                                        } else {
+                                            // the 16 h, then the l, into one sum
+                                            const uint64_t dbj = db + (((j >> 1) * kTokens * 128 + (j & 1) * 64) >> 4);
+                                            mma_f8f6f4(slot, daj, dbj, idesc, 0);
+                                            mma_f8f6f4(slot, daj, dbj + (32 >> 4), idesc, 1);
+                                        }
                                     }
                                 }
+                                mma_commit(&s_sfull[gb]);
                             }
-                            mma_commit(&s_sfull[gb]);
-            }
-            __syncwarp();
+                            __syncwarp();
                             if (++gb == kBufs) {
                                 gb = 0;
                                 gph ^= 1;
