@@ -240,9 +240,15 @@ __device__ __forceinline__ Norm<double> exact_norm(const ScoreArgs &a, const flo
         if (v[i] > nm.lmax) nm.lmax = v[i];   // false for NaN
     }
     nm.lmax = warp_max(nm.lmax);
+    const bool inf = isinf(nm.lmax);
     double sum = 0.0;
+    // (no branches: the exps run side by side; terms below exp(-700) add nothing)
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) sum += score_of(v[i], nm, false);
+    for (int i = 0; i < NPER; ++i) {
+        const double e = exp(fmax(v[i] - nm.lmax, -700.0));
+        const bool none = !(v[i] > -static_cast<double>(INFINITY));   // or NaN
+        sum += none ? 0.0 : inf ? (v[i] == nm.lmax ? 1.0 : 0.0) : e;
+    }
     sum = warp_sum(sum);
     nm.inv = sum > 0.0 ? 1.0 / sum : 0.0;
     return nm;
@@ -582,7 +588,15 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
         if (lane < a.k && ou > 0x007FFFFFu && my_u < 0xFF800000u) {
             const float ka = from_ordered(my_u), kb = from_ordered(ou);
             const bool same = my_u == ou && ml == ol && mb == ob;
-            tie = !same && !(ka - kb > err_of(ka) + err_of(kb));
+            float err = err_of(ka) + err_of(kb);
+            if (a.bias && !sg) {
+                // what the softmax's scores share weighs only by their difference, the
+                // rest by its own d
+                const float sa = score_of(ml, nm, false), sb = score_of(ol, nm, false);
+                err = fminf(err, u * (40.0f * fabsf(sa - sb) + sa * (3.0f + 1.7f * (nm.lmax - ml)) +
+                                      sb * (3.0f + 1.7f * (nm.lmax - ol)) + fabsf(ka) + fabsf(kb)) + tiny);
+            }
+            tie = !same && !(ka - kb > err);
         }
         if (__any_sync(0xFFFFFFFFu, near)) {
             my = route_exact<NPER>(a, row);
@@ -665,14 +679,18 @@ __device__ __forceinline__ void place_chunk(const int32_t *topk_id, int t0, int 
     }
 }
 
+// pitch of a row of counts: whole 16-byte groups
+__host__ __device__ constexpr int count_pitch(int E) { return (E + 3) & ~3; }
+
 // One block of `chunk` tokens: routes them and writes the chunk's counts per
-// expert, counts[chunk][E].
+// expert, counts[chunk][count_pitch(E)].
 template <int NPER, bool kLogit>
 __global__ void __launch_bounds__(1024) route_chunk_kernel(const ScoreArgs a, int32_t *counts) {
     __shared__ int s_count[kMaxE];
     pdl_wait();
     pdl_trigger();
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) s_count[e] = 0;
+    const int pitch = count_pitch(a.E);
+    for (int e = threadIdx.x; e < pitch; e += blockDim.x) s_count[e] = 0;
     __syncthreads();
     const int t0 = blockIdx.x * a.chunk, n = min(a.T - t0, a.chunk);
     for (int i = threadIdx.x >> 5; i < n; i += blockDim.x >> 5) {
@@ -681,8 +699,8 @@ __global__ void __launch_bounds__(1024) route_chunk_kernel(const ScoreArgs a, in
     }
     if (!counts) return;
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-        counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = s_count[e];
+    for (int e = threadIdx.x; e < pitch; e += blockDim.x)
+        counts[static_cast<int64_t>(blockIdx.x) * pitch + e] = s_count[e];
 }
 
 // The whole call in one block, for few tokens.
@@ -737,30 +755,44 @@ __global__ void __launch_bounds__(kPlaceThreads)
     pdl_wait();
     pdl_trigger();
     __syncthreads();
-    // counts of earlier chunks and of all, a column (expert) of the table per
-    // thread, the rows shared out over the threads of a column
-    const int cols = min((E + 31) & ~31, kPlaceThreads), segs = kPlaceThreads / cols;
-    const int e = threadIdx.x % cols, seg = threadIdx.x / cols;
-    if (e < E && seg < segs) {
-        int before = 0, all = 0;
-#pragma unroll 8
-        for (int c = seg; c < chunks; c += segs) {
-            const int n = counts[static_cast<int64_t>(c) * E + e];
-            all += n;
-            before += c < static_cast<int>(blockIdx.x) ? n : 0;
-        }
-        atomicAdd(&s_before[e], before);
-        atomicAdd(&s_all[e], all);
-    }
     const int t0 = blockIdx.x * chunk, t1 = t0 + min(T - t0, chunk);
-    auto fill = [&](int p0, int p1) {
-        for (int c = threadIdx.x; c < (p1 - p0) * k; c += kPlaceThreads) {
-            const int i = c / k, x = topk_id[static_cast<int64_t>(p0) * k + c];
+    int p0 = t0, p1 = t0 + min(t1 - t0, kPassTokens);
+    const int32_t *ids = topk_id + static_cast<int64_t>(t0) * k;
+    const int n0 = (p1 - p0) * k;
+    const int x0 = threadIdx.x < n0 ? ids[threadIdx.x] : 0;   // on its way during the counts
+    // counts of earlier chunks and of all: four columns (experts) of the table per
+    // thread, the rows shared out over the threads of a column
+    const int quads = count_pitch(E) / 4, cols = min((quads + 31) & ~31, kPlaceThreads);
+    const int segs = kPlaceThreads / cols, q = threadIdx.x % cols, seg = threadIdx.x / cols;
+    if (q < quads && seg < segs) {
+        int4 before = make_int4(0, 0, 0, 0), all = before;
+        const int4 *table = reinterpret_cast<const int4 *>(counts) + q;
+#pragma unroll 10
+        for (int c = seg; c < chunks; c += segs) {
+            const int4 n = table[static_cast<int64_t>(c) * quads];
+            const int m = c < static_cast<int>(blockIdx.x) ? -1 : 0;
+            all = make_int4(all.x + n.x, all.y + n.y, all.z + n.z, all.w + n.w);
+            before = make_int4(before.x + (n.x & m), before.y + (n.y & m), before.z + (n.z & m),
+                               before.w + (n.w & m));
+        }
+        auto add = [&](int i, int b, int t) {
+            if (t) {   // (columns past E are 0)
+                atomicAdd(&s_before[4 * q + i], b);
+                atomicAdd(&s_all[4 * q + i], t);
+            }
+        };
+        add(0, before.x, all.x);
+        add(1, before.y, all.y);
+        add(2, before.z, all.z);
+        add(3, before.w, all.w);
+    }
+    auto fill = [&](const int32_t *id, int n, int first) {
+        for (int c = threadIdx.x; c < n; c += kPlaceThreads) {
+            const int i = c / k, x = c == static_cast<int>(threadIdx.x) ? first : id[c];
             atomicOr(&s_map[x * words + (i >> 5)], 1u << (i & 31));
         }
     };
-    int p0 = t0, p1 = t0 + min(t1 - t0, kPassTokens);
-    fill(p0, p1);
+    fill(ids, n0, x0);
     __syncthreads();
     const int x = threadIdx.x;
     const int tot = x < E ? s_all[x] : 0;
@@ -786,7 +818,8 @@ __global__ void __launch_bounds__(kPlaceThreads)
         __syncthreads();
         p0 = p1;
         p1 += min(t1 - p1, kPassTokens);
-        fill(p0, p1);
+        ids = topk_id + static_cast<int64_t>(p0) * k;
+        fill(ids, (p1 - p0) * k, threadIdx.x < (p1 - p0) * k ? ids[threadIdx.x] : 0);
         __syncthreads();
     }
 }
@@ -823,7 +856,7 @@ extern "C" h32_status h32_moe_route_scored_workspace_bytes(int64_t T, int32_t E,
     if (!bytes) return H32_ERR_INVALID_ARG;
     *bytes = 0;
     if (T < 0 || T > 0x7FFFFFFFll || E < 1 || E > kMaxE) return H32_ERR_INVALID_ARG;
-    if (T > kSoloTokens) *bytes = static_cast<size_t>(route_chunks(T).count) * E * 4;
+    if (T > kSoloTokens) *bytes = static_cast<size_t>(route_chunks(T).count) * count_pitch(E) * 4;
     return H32_OK;
 }
 
@@ -852,7 +885,7 @@ extern "C" h32_status h32_moe_route_scored(const float *logits, int64_t T, int32
     const bool solo = T <= kSoloTokens;
     const Chunks ch = route_chunks(T);
     if (workspace && !solo) {
-        if (workspace_bytes < static_cast<size_t>(ch.count) * E * 4) return H32_ERR_INVALID_ARG;
+        if (workspace_bytes < static_cast<size_t>(ch.count) * count_pitch(E) * 4) return H32_ERR_INVALID_ARG;
         if (!aligned16(workspace)) return H32_ERR_ALIGNMENT;
     }
     H32_TRY(check_device(nullptr));
