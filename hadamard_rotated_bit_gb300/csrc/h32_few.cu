@@ -24,7 +24,7 @@
 // Bound: HBM, 1.125 bytes a weight, where the tiles fill the card (34816 x 5120, one
 // token: 35.6 us, 5.6 TB/s, 84% of the measured copy rate); a narrow projection is
 // bound by the pace of one tile's stages, about 0.6 us per 512 codes, most of it the
-// hand-offs (5120 x 5120: 13.3 us; 5120 x 17408: 28.2 us, 53%).  The roles that issue
+// hand-offs (5120 x 5120: 12.4 us; 5120 x 17408: 28.2 us, 53%).  The roles that issue
 // to the tensor core and the copy engine run as whole warps with one elected lane:
 // descriptors in uniform registers, 47 clocks a product less.  (Measured and left:
 // sums on CUDA cores in fp16 pairs, 11.8 us for 5120 x 5120 and one token but 66 us

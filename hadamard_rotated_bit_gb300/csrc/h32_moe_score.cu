@@ -10,7 +10,8 @@
 // it is the order of the logits.  Else it is that of the keys' values in double:
 // keys are computed in fp32 with a bound on their error, and where two keys whose
 // order matters are nearer than their bounds (a few tokens in a thousand on random
-// logits) the keys in question are taken again in double, one a lane.
+// sigmoid keys, fewer with the softmax) the keys in question are taken again in
+// double, one a lane.
 //
 // route_token: one warp per token.  Lane i holds `per` consecutive experts, so a
 // lower lane holds lower ids and, with `per` dividing a group's size, a group is a
@@ -25,7 +26,10 @@
 // Up to 64 tokens one block does both, in one launch.
 //
 // Bound: instruction issue.  The data are 4 bytes a logit (16.8 MB for 16384 tokens
-// x 256 experts, 2.5 us at the copy rate).
+// x 256 experts, 2.5 us at the copy rate); measured, sigmoid with a bias, 8 groups by
+// their two best, top 8: routing 28.8 us (22 without groups), grouping 9.7.  1024 x
+// 128, softmax with a bias: 7.2 and 6.3 us.  One token: 6.3 us, one launch (grouping
+// by a block an expert, as h32_moe_route: 16384 x 256 290 us altogether).
 #include "h32_common.cuh"
 #include "h32_moe.cuh"
 
