@@ -83,6 +83,7 @@ constexpr int kMaxStages = 5;        // 128-element K stages in flight (at most)
 constexpr int kTileBytes = 16384;    // 128 rows x 128 bytes
 constexpr int kNibBytes = 8192;      // widening instance: 128 rows x 64 bytes of Q4_0 nibbles
 constexpr int kWidenWarps = 2;       // widening instance: warps 2 and 3
+constexpr int kFinWarps = 2;         // finished output: warps 2 and 3
 constexpr int kScaleBytes = 2048;    // 4 blocks x 128 fp32
 #ifndef H32_TC_GROUP
 #define H32_TC_GROUP 2
@@ -99,23 +100,27 @@ constexpr int kSplitMaxP = 128;      // pieces of a K split (flags in the worksp
 // 128-element stage carries two activation tiles.
 // QN: the instance that also quantizes its output for the next projection; it
 // gives up a stage for a 4 KB staging tile per epilogue warp.
+// FIN: the instance that finishes its output; a stage for the 64 KB tile between the
+// epilogue warps and the finishing warps (2 and 3), which take 64 registers.
 // WQ: the widening instance (Q4_0 nibbles and fp16 scales in, widened in
 // shared memory); a stage also holds the nibble tile, and a constant tile of
 // -8 * 2^-9 follows the stages.
-template <int EPQ, int XB, bool QN = false, bool WQ = false>
+template <int EPQ, int XB, bool QN = false, bool WQ = false, bool FIN = false>
 struct TcCfg {
     static_assert(!WQ || (EPQ == 4 && XB == 4 && !QN), "widening: 4-bit route, 16 epilogue warps");
-    static constexpr int kStages = (XB == 8 || QN || WQ) ? 4 : 5;
+    static_assert(!FIN || (!QN && !WQ), "one output");
+    static constexpr int kStages = (FIN && XB == 8) ? 3 : (XB == 8 || QN || WQ || FIN) ? 4 : 5;
     static constexpr int kBTile = XB == 8 ? 2 * kTileBytes : kTileBytes;   // activations per stage
     static constexpr int kEpiWarps = 4 * EPQ;
     // With 16 epilogue warps the producers form a warpgroup of their own (TMA,
     // MMA and two idle warps) that hands registers to the epilogue
     // (setmaxnreg): 96 a thread at launch, then 32 for the producer warpgroup
-    // and 112 for the epilogue, 4 x 32 x 32 + 16 x 32 x 112 = 640 x 96.
+    // and 112 for the epilogue, 4 x 32 x 32 + 16 x 32 x 112 = 640 x 96 (FIN: 64 and
+    // 104, the same sum).
     static constexpr bool kRegSplit = EPQ == 4;
-    static constexpr int kProdWarps = kRegSplit ? 4 : 2;
+    static constexpr int kProdWarps = (kRegSplit || FIN) ? 4 : 2;
     static constexpr int kThreads = (kProdWarps + kEpiWarps) * 32;
-    static constexpr int kLaunchRegs = 96, kProdRegs = 32, kEpiRegs = 112;
+    static constexpr int kLaunchRegs = 96, kProdRegs = FIN ? 64 : 32, kEpiRegs = FIN ? 104 : 112;
     static_assert(!kRegSplit || (kProdWarps * kProdRegs + kEpiWarps * kEpiRegs) * 32 <=
                                     kThreads * kLaunchRegs,
                   "register split above the launch's registers");
@@ -129,8 +134,9 @@ struct TcCfg {
     static constexpr int kOffBar = kOffSB + kStages * kScaleBytes;
     static constexpr int kOffMisc = kOffBar + 32 * 8;
     static constexpr int kOffGrp = kOffMisc + 16 * 4;            // row offsets, tile prefix
-    static constexpr int kOffQ = (kOffGrp + 2 * (kMaxExperts + 1) * 4 + 127) & ~127;
-    static constexpr int kBytes = kOffQ + (QN ? kEpiWarps * 4096 : 0);
+    static constexpr int kGroups = FIN ? 1 : kMaxExperts;        // FIN: dense
+    static constexpr int kOffQ = (kOffGrp + 2 * (kGroups + 1) * 4 + 127) & ~127;
+    static constexpr int kBytes = kOffQ + (QN ? kEpiWarps * 4096 : FIN ? kBM * kBNMax * 4 : 0);
     static constexpr int kSmem = kBytes + 1024;
     static_assert(kSmem <= 232448, "shared memory above the per-block limit");
 };
@@ -141,9 +147,12 @@ enum {
     kBarSFull = kBarEmpty + kMaxStages,
     kBarSEmpty = kBarSFull + kBufs,
     kBarDrain = kBarSEmpty + kBufs,
-    kBarWide = kBarDrain + 1    // widening instance: a stage's e4m3 weight tile is written
+    kBarWide = kBarDrain + 1,   // widening instance: a stage's e4m3 weight tile is written
+    kBarFinFull = kBarWide + kMaxStages,   // finished output: a tile's sums are staged, are
+    kBarFinEmpty,                          // taken
+    kBarSelf                               // the same where the epilogue warps finish a tile
 };
-static_assert(kBarWide + kMaxStages <= 32, "barriers above their shared-memory slots");
+static_assert(kBarSelf < 32, "barriers above their shared-memory slots");
 enum { kMiscTmem = 0, kMiscAbort = 1, kMiscBad = 2, kMiscTotal = 3 };
 
 struct TcArgs {
@@ -167,6 +176,7 @@ struct TcArgs {
     int32_t split_p, split_kh, ws_ld;
     uint64_t wait_limit;
     EpiArgs fin;                 // the finished output (kEpi == 3); y is unused then
+    int32_t fin_self;            // the epilogue warps finish every tile, not only the last
 };
 
 __device__ __forceinline__ void record(uint32_t bits) { atomicOr(&g_tc_status, bits); }
@@ -351,68 +361,183 @@ __device__ __forceinline__ void stage_dw(const float *s_sa, int s, int row, int 
     }
 }
 
-// The finished output of a warp's share of a tile (kEpi == 3): bias, activation,
-// residual, one rounding to y's type.  A lane holds one weight row (output
-// feature) and 16 token columns per chunk, so for each column the warp's 32 lanes
-// read and write 32 consecutive features.  For the gated activation the lanes of
-// a pair hold a gate row and its up row: they exchange halves of the chunk (8
-// shuffles), the even lane finishes columns 0..7, the odd lane 8..15.  The
-// accumulators pass through local memory into loops of eight columns that are not
-// unrolled, and the tile is looked up again, so that the block loop holds as little
-// as it can for this code: gate/up, 512 x 34816 x 5120, to bf16 with SwiGLU 358 us
-// (unrolled on the accumulators 395; the bare product 311: the block loop still takes
-// 7% more instructions than the plain instance's).
-template <int EPQ, int kMaxChunks, int kProdWarps, bool kTail>
-__device__ __forceinline__ void finish_tile(const TcArgs &a, int t, const int *s_off, const int *s_tpre,
-                                            const uint64_t *acc) {
-    const EpiArgs &f = a.fin;
-    uint64_t z[8 * kMaxChunks];
+// The finished output (kEpi == 3): bias, activation, residual, one rounding to y's type.
+// The epilogue warps leave a tile's sums in shared memory, [column][128 rows] fp32, and
+// go on with the next tile; the producer warpgroup's other two warps finish and store
+// them meanwhile, so the block loop holds nothing for it.  A CTA's last tile, and every
+// tile where two warps would not keep up (finish_in_epilogue), the epilogue warps finish, 8
+// columns each.  512 x 34816 x 5120 to bf16 with SwiGLU 332 us, the bare product 314
+// (finished in the epilogue warps' registers 395, from local memory 357); 333 x 5120 x
+// 17408, 8-bit, with bias and residual 138, bare 134 (142 from local memory).  The 64 KB
+// of a tile cost one K stage, the finishing warps 8 registers of each epilogue thread.
+template <int kMaxChunks>
+__device__ __forceinline__ void stage_tile(float *s_q, int row, int c0, int nch, const uint64_t *acc) {
 #pragma unroll
-    for (int q = 0; q < 8 * kMaxChunks; ++q) z[q] = acc[q];
+    for (int c = 0; c < kMaxChunks; ++c) {
+        if (c < nch) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                float *p = s_q + (c0 + 16 * c + 2 * q) * kBM + row;
+                p[0] = __uint_as_float(static_cast<uint32_t>(acc[8 * c + q]));
+                p[kBM] = __uint_as_float(static_cast<uint32_t>(acc[8 * c + q] >> 32));
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float2 load_pair(const void *p, int64_t i, bool bf16) {
+    if (!bf16) return *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + i);
+    const uint32_t u = *reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p) + i);
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store_pair(void *p, int64_t i, bool bf16, float2 v) {
+    if (bf16)
+        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p) + i) =
+            __floats2bfloat162_rn(v.x, v.y);
+    else
+        *reinterpret_cast<float2 *>(static_cast<float *>(p) + i) = v;
+}
+
+// One warp's share of the staged tile: columns c0 .. c0 + 7, then every `step`; a lane
+// takes two adjacent rows (output features, or a gate row and its up row).
+template <int kAct>
+__device__ __forceinline__ void finish_share(const EpiArgs &f, const float *s_q, int n0, int N, int64_t g0,
+                                             int ncol, int c0, int step, int lane) {
+    constexpr int kC = 8;
+    constexpr bool kGate = kAct == H32_EPI_SWIGLU;
+    for (int h = 2 * lane; h < kBM + 2 * lane; h += 64) {
+        const int n = n0 + h, j = kGate ? n >> 1 : n;
+        if (n >= N) break;   // (N and n are even)
+        const float b0 = f.bias ? __ldg(f.bias + n) : 0.0f, b1 = f.bias ? __ldg(f.bias + n + 1) : 0.0f;
+        for (int c = c0; c < ncol; c += step) {
+            const int nc = ncol - c;   // columns left
+            const float *src = s_q + c * kBM + h;
+            float2 r[kC], v[kC];
+            if (f.res) {
+                int64_t i = (g0 + c) * f.ldr + j;
+#pragma unroll
+                for (int q = 0; q < kC; ++q, i += f.ldr) {
+                    r[q] = make_float2(0.0f, 0.0f);
+                    if (q < nc) {
+                        if constexpr (kGate) r[q].x = load_value(f.res, i, f.res_bf16);
+                        else r[q] = load_pair(f.res, i, f.res_bf16);
+                    }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kC; ++q) {
+                float2 z = *reinterpret_cast<const float2 *>(src + q * kBM);
+                if (f.bias) z = make_float2(__fadd_rn(z.x, b0), __fadd_rn(z.y, b1));
+                v[q] = kGate ? make_float2(swiglu(z.x, z.y), 0.0f)
+                             : make_float2(activate(z.x, kAct), activate(z.y, kAct));
+            }
+            if (f.res) {
+#pragma unroll
+                for (int q = 0; q < kC; ++q)
+                    v[q] = make_float2(__fadd_rn(v[q].x, r[q].x), __fadd_rn(v[q].y, r[q].y));
+            }
+            int64_t i = (g0 + c) * f.ldy + j;
+            if (f.y_bf16) {
+#pragma unroll
+                for (int q = 0; q < kC; ++q, i += f.ldy)
+                    if (q < nc) {
+                        if constexpr (kGate) store_value(f.y, i, true, v[q].x);
+                        else store_pair(f.y, i, true, v[q]);
+                    }
+            } else {
+#pragma unroll
+                for (int q = 0; q < kC; ++q, i += f.ldy)
+                    if (q < nc) {
+                        if constexpr (kGate) store_value(f.y, i, false, v[q].x);
+                        else store_pair(f.y, i, false, v[q]);
+                    }
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void finish_tile(const EpiArgs &f, const float *s_q, const TcTile &ti, int N,
+                                            int c0, int step, int lane) {
+    switch (f.act) {
+        case H32_EPI_RELU: finish_share<H32_EPI_RELU>(f, s_q, ti.n0, N, ti.g0, ti.chi, c0, step, lane); break;
+        case H32_EPI_SILU: finish_share<H32_EPI_SILU>(f, s_q, ti.n0, N, ti.g0, ti.chi, c0, step, lane); break;
+        case H32_EPI_GELU_TANH:
+            finish_share<H32_EPI_GELU_TANH>(f, s_q, ti.n0, N, ti.g0, ti.chi, c0, step, lane);
+            break;
+        case H32_EPI_GELU_ERF:
+            finish_share<H32_EPI_GELU_ERF>(f, s_q, ti.n0, N, ti.g0, ti.chi, c0, step, lane);
+            break;
+        case H32_EPI_SWIGLU:
+            finish_share<H32_EPI_SWIGLU>(f, s_q, ti.n0, N, ti.g0, ti.chi, c0, step, lane);
+            break;
+        default: finish_share<H32_EPI_NONE>(f, s_q, ti.n0, N, ti.g0, ti.chi, c0, step, lane);
+    }
+}
+
+// The finishing warps' loop over the CTA's tiles, in the epilogue warps' order; false
+// when a wait gave up.
+template <bool kTail, bool kSplit>
+__device__ __forceinline__ bool finish_tiles(const TcArgs &a, int total, const int *s_off,
+                                             const int *s_tpre, uint64_t *bars, const float *s_q, int fw,
+                                             int lane, volatile int *abort_flag) {
+    const int nit = a.fin_self ? 0 : tc_item_count<kSplit>(a, total) - 1;   // (not the last)
+    uint32_t ph = 0;
+    for (int k = 0; k < nit; ++k) {
+        const TcItem it = tc_item<kSplit>(a, k, a.nb / 4);
+        if (it.mode == 1) continue;   // a first part: its sums go to the second
+        const TcTile ti = tc_tile<kTail>(it.t, a, s_off, s_tpre);
+        if (kTail && ti.ncols == 0) continue;
+        if (!warp_wait(&bars[kBarFinFull], ph, a.wait_limit, abort_flag)) return false;
+        finish_tile(a.fin, s_q, ti, a.N, 8 * fw, 8 * kFinWarps, lane);
+        __syncwarp();
+        elect_arrive(&bars[kBarFinEmpty]);
+        ph ^= 1;
+    }
+    return true;
+}
+
+constexpr int kFinNone = 0, kFinHand = 1, kFinSelf = 2;   // how an epilogue warp ends a tile
+
+// A tile's sums handed to the finishing warps by an epilogue warp ...
+template <int kMaxChunks>
+__device__ __forceinline__ bool hand_over(const TcArgs &a, uint64_t *bars, float *s_q, int row, int c0,
+                                          int nch, const uint64_t *acc, uint32_t &fph,
+                                          volatile int *abort_flag) {
+    if (!warp_wait(&bars[kBarFinEmpty], fph, a.wait_limit, abort_flag)) return false;
+    stage_tile<kMaxChunks>(s_q, row, c0, nch, acc);
+    __syncwarp();
+    elect_arrive(&bars[kBarFinFull]);
+    fph ^= 1;
+    return true;
+}
+// ... or finished by the epilogue warps themselves, 8 columns a warp.  kBarSelf: the
+// even phases end when a tile is staged, the odd ones when it is taken.
+template <int EPQ, int kMaxChunks, int kProdWarps, bool kTail>
+__device__ __forceinline__ bool finish_self(const TcArgs &a, int t, const int *s_off, const int *s_tpre,
+                                            uint64_t *bars, float *s_q, int row, int c0, int nch,
+                                            const uint64_t *acc, uint32_t fph, volatile int *abort_flag) {
+    if (!warp_wait(&bars[kBarFinEmpty], fph, a.wait_limit, abort_flag) ||
+        !warp_wait(&bars[kBarSelf], 1, a.wait_limit, abort_flag))
+        return false;
+    stage_tile<kMaxChunks>(s_q, row, c0, nch, acc);
+    __syncwarp();
+    elect_arrive(&bars[kBarSelf]);
+    if (!warp_wait(&bars[kBarSelf], 0, a.wait_limit, abort_flag)) return false;
     // the tile is looked up again, so that the block loop holds nothing for this code
     int tid = threadIdx.x;
     asm volatile("" : "+r"(t), "+r"(tid) : : "memory");
-    const TcTile ti = tc_tile<kTail>(t, a, s_off, s_tpre);
-    const int warp = tid >> 5, part = (warp - kProdWarps) >> 2, row = (warp & 3) * 32 + (tid & 31);
-    const int base = (ti.ncols >> 4) / EPQ, rem = (ti.ncols >> 4) % EPQ;
-    const int nch = base + (part < rem ? 1 : 0), c0 = 16 * (part * base + min(part, rem));
-    const int n = ti.n0 + row, wrow = ti.wrow + row, g0 = ti.g0, clo = ti.clo, chi = ti.chi;
-    const bool in = n < a.N;
-    const float bias = (f.bias && in) ? __ldg(f.bias + wrow) : 0.0f;
-    const bool odd = n & 1;   // (tiles start at even rows)
-    auto value = [&](int q) {
-        const float v = __uint_as_float(static_cast<uint32_t>(z[q >> 1] >> (32 * (q & 1))));
-        return f.bias ? __fadd_rn(v, bias) : v;
-    };
-    if (f.act == H32_EPI_SWIGLU) {
-#pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
-            float v[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float lo = value(16 * c + q), hi = value(16 * c + 8 + q);
-                const float u = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo : hi, 1);
-                v[q] = odd ? swiglu(u, hi) : swiglu(lo, u);
-            }
-            const int first = c0 + 16 * c + (odd ? 8 : 0);
-            if (in) finish_columns<8>(f, v, static_cast<int64_t>(g0) + first, clo - first, chi - first, n >> 1);
-        }
-    } else {
-#pragma unroll 1
-        for (int h = 0; h < 2 * nch; ++h) {
-            float v[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = activate(value(8 * h + q), f.act);
-            const int first = c0 + 8 * h;
-            if (in) finish_columns<8>(f, v, static_cast<int64_t>(g0) + first, clo - first, chi - first, n);
-        }
-    }
+    finish_tile(a.fin, s_q, tc_tile<kTail>(t, a, s_off, s_tpre), a.N, 8 * ((tid >> 5) - kProdWarps),
+                8 * 4 * EPQ, tid & 31);
+    __syncwarp();
+    elect_arrive(&bars[kBarSelf]);
+    return true;
 }
 
 // The ring positions of an epilogue warp: shared-memory stage and TMEM buffer,
 // each a counter and a phase bit.
 struct EpiRing {
     uint32_t s, sph, gb, gph;
+    uint32_t fph;   // finished output: the parity at which the staged tile is taken
 };
 
 // One work item of an epilogue warp, without block sums: tile (or piece) t,
@@ -422,13 +547,13 @@ struct EpiRing {
 // come from one elected lane.  Returns false when a wait gave up.  A warp holds
 // its lane quarter's 32 weight rows (one a thread, the 32x32b TMEM fragment)
 // times its share of the tile's columns.
-template <int EPQ, int XB, bool kQN, bool kTail, bool kWQ, int kMode, bool kFin>
+template <int EPQ, int XB, bool kQN, bool kTail, bool kWQ, int kMode, int kFin>
 __device__ __forceinline__ bool epi_item(const TcArgs &a, int t, int st0, int nstage,
                                          const int *s_off, const int *s_tpre, uint64_t *bars,
                                          const float *s_sa, const float *s_sb, float *s_q,
                                          uint32_t tmem, int warp, int lane,
                                          volatile int *abort_flag, EpiRing &r) {
-    using C = TcCfg<EPQ, XB, kQN, kWQ>;
+    using C = TcCfg<EPQ, XB, kQN, kWQ, kFin != kFinNone>;
     const int ew = warp - C::kProdWarps;
     const int quad = warp & 3;                 // TMEM lanes 32 quad .. 32 quad + 31
     const int part = ew >> 2;                  // share of the columns
@@ -537,8 +662,11 @@ __device__ __forceinline__ bool epi_item(const TcArgs &a, int t, int st0, int ns
         return true;
     }
     const int64_t n = ti.n0 + row;
-    if constexpr (kFin) {
-        finish_tile<EPQ, C::kMaxChunks, C::kProdWarps, kTail>(a, t, s_off, s_tpre, acc);
+    if constexpr (kFin == kFinHand) {
+        return hand_over<C::kMaxChunks>(a, bars, s_q, row, c0, nch, acc, r.fph, abort_flag);
+    } else if constexpr (kFin == kFinSelf) {
+        return finish_self<EPQ, C::kMaxChunks, C::kProdWarps, kTail>(a, t, s_off, s_tpre, bars, s_q, row,
+                                                                     c0, nch, acc, r.fph, abort_flag);
     } else if (n < a.N && (!kQN || a.y)) {
 #pragma unroll
         for (int c = 0; c < C::kMaxChunks; ++c) {
@@ -617,28 +745,46 @@ __device__ __forceinline__ bool epilogue_tiles(const TcArgs &a, int total, const
                                                int warp, int lane, volatile int *abort_flag) {
     const int b = blockIdx.x, g = gridDim.x;
     const int nst = a.nb / 4;
-    EpiRing r{0u, 0u, 0u, 0u};
+    EpiRing r{0u, 0u, 0u, 0u, 1u};
     int main_end = total;
     if constexpr (kSplit) {
         if (a.split_p > 0) {
             main_end = a.tail_first;
             if (b < a.split_p &&
-                !epi_item<EPQ, XB, kQN, kTail, kWQ, 1, kFin>(a, a.tail_first + b, 0, a.split_kh, s_off,
-                                                        s_tpre, bars, s_sa, s_sb, s_q, tmem, warp,
-                                                        lane, abort_flag, r))
+                !epi_item<EPQ, XB, kQN, kTail, kWQ, 1, kFin ? kFinHand : kFinNone>(
+                    a, a.tail_first + b, 0, a.split_kh, s_off, s_tpre, bars, s_sa, s_sb, s_q, tmem, warp,
+                    lane, abort_flag, r))
                 return false;
         }
     }
     const int nit = b < main_end ? (main_end - 1 - b) / g + 1 : 0;
-    for (int k = 0; k < nit; ++k)
-        if (!epi_item<EPQ, XB, kQN, kTail, kWQ, 0, kFin>(a, b + k * g, 0, nst, s_off, s_tpre, bars, s_sa,
-                                                    s_sb, s_q, tmem, warp, lane, abort_flag, r))
-            return false;
+    if constexpr (kFin) {
+        // the tile loop hands its tiles to the finishing warps; the last one, and every
+        // one where they would not keep up, the epilogue warps finish
+        const bool second = kSplit && a.split_p > 0 && b >= a.split_p && b < 2 * a.split_p;
+        const int hand = a.fin_self ? 0 : second ? nit : nit - 1;
+        for (int k = 0; k < hand; ++k)
+            if (!epi_item<EPQ, XB, kQN, kTail, kWQ, 0, kFinHand>(a, b + k * g, 0, nst, s_off, s_tpre, bars,
+                                                                 s_sa, s_sb, s_q, tmem, warp, lane,
+                                                                 abort_flag, r))
+                return false;
+        for (int k = max(hand, 0); k < nit; ++k)
+            if (!epi_item<EPQ, XB, kQN, kTail, kWQ, 0, kFinSelf>(a, b + k * g, 0, nst, s_off, s_tpre, bars,
+                                                                 s_sa, s_sb, s_q, tmem, warp, lane,
+                                                                 abort_flag, r))
+                return false;
+    } else {
+        for (int k = 0; k < nit; ++k)
+            if (!epi_item<EPQ, XB, kQN, kTail, kWQ, 0, kFinNone>(a, b + k * g, 0, nst, s_off, s_tpre, bars,
+                                                                 s_sa, s_sb, s_q, tmem, warp, lane,
+                                                                 abort_flag, r))
+                return false;
+    }
     if constexpr (kSplit) {
         if (a.split_p > 0 && b >= a.split_p && b < 2 * a.split_p &&
-            !epi_item<EPQ, XB, kQN, kTail, kWQ, 2, kFin>(a, a.tail_first + b - a.split_p, a.split_kh,
-                                                    nst - a.split_kh, s_off, s_tpre, bars, s_sa,
-                                                    s_sb, s_q, tmem, warp, lane, abort_flag, r))
+            !epi_item<EPQ, XB, kQN, kTail, kWQ, 2, kFin ? kFinSelf : kFinNone>(
+                a, a.tail_first + b - a.split_p, a.split_kh, nst - a.split_kh, s_off, s_tpre, bars, s_sa,
+                s_sb, s_q, tmem, warp, lane, abort_flag, r))
             return false;
     }
     return true;
@@ -653,7 +799,7 @@ __device__ __forceinline__ bool epilogue_tiles(const TcArgs &a, int total, const
 // counters and phase bits, arrivals come from one elected lane.  Returns false
 // when a wait gave up.  A warp holds its lane quarter's 32 weight rows (one a
 // thread, the 32x32b TMEM fragment) times its share of the tile's columns.
-template <int EPQ, int XB, bool kQN, bool kTail, bool kWQ, bool kFin>
+template <int EPQ, int XB, bool kQN, bool kTail, bool kWQ>
 __device__ __forceinline__ bool epilogue_tiles_plain(const TcArgs &a, int total, const int *s_off,
                                                const int *s_tpre, uint64_t *bars, const float *s_sa,
                                                const float *s_sb, float *s_q, uint32_t tmem,
@@ -720,9 +866,7 @@ __device__ __forceinline__ bool epilogue_tiles_plain(const TcArgs &a, int total,
             }
         }
         const int64_t n = ti.n0 + row;
-        if constexpr (kFin) {
-            finish_tile<EPQ, C::kMaxChunks, C::kProdWarps, kTail>(a, t, s_off, s_tpre, acc);
-        } else if (n < a.N && (!kQN || a.y)) {
+        if (n < a.N && (!kQN || a.y)) {
 #pragma unroll
             for (int c = 0; c < C::kMaxChunks; ++c) {
                 if (c < nch) {
@@ -841,18 +985,18 @@ __device__ __forceinline__ bool widen_tiles(const TcArgs &a, int total, const in
 
 // kEpi: 0 = y only, 1 = y and the block sums, 2 = y (optional) and the output
 // quantized for the next projection, 3 = the finished output (TcArgs::fin).
-// kTail: the last partial wave's tiles are cut into pieces (TcArgs::tail_first, tail_k).  kWQ: the widening instance
-// (map_a over the Q4_0 nibbles, map_sa over the fp16 scales).  kSplit: the cut
+// kTail: the last partial wave's tiles are cut into pieces (TcArgs::tail_first,
+// tail_k).  kWQ: the widening instance (map_a over the Q4_0 nibbles, map_sa over the fp16 scales).  kSplit: the cut
 // pieces also run in two parts along K (TcArgs::split_p, TcItem); an instance
 // of its own, as the cut instance without that code measured about 4% faster
 // on GB300.
 template <int EPQ, int XB, int kEpi, bool kTail = false, bool kWQ = false, bool kSplit = false>
-__global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ>::kThreads, 1)
+__global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ, kEpi == 3>::kThreads, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ CUtensorMap map_sa,
                    const __grid_constant__ CUtensorMap map_sb, const TcArgs a) {
     static_assert(!kSplit || (kTail && kEpi != 1 && !kWQ), "the K split: no block sums, cut tail");
-    using C = TcCfg<EPQ, XB, kEpi == 2, kWQ>;
+    using C = TcCfg<EPQ, XB, kEpi == 2, kWQ, kEpi == 3>;
     constexpr int kStages = C::kStages;
     constexpr bool kSums = kEpi == 1;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -864,8 +1008,8 @@ __global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ>::kThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     volatile int *misc = reinterpret_cast<volatile int *>(smem + C::kOffMisc);
     int *s_off = reinterpret_cast<int *>(smem + C::kOffGrp);
-    int *s_tpre = s_off + kMaxExperts + 1;
-    float *s_q = reinterpret_cast<float *>(smem + C::kOffQ);   // kEpi == 2: staging tiles
+    int *s_tpre = s_off + C::kGroups + 1;
+    float *s_q = reinterpret_cast<float *>(smem + C::kOffQ);   // kEpi >= 2: staging tiles
     uint8_t *s_n = smem + C::kOffN;                             // kWQ: Q4_0 nibble tiles
     uint8_t *s_c = smem + C::kOffC;                             // kWQ: the constant tile
 
@@ -889,6 +1033,11 @@ __global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ>::kThreads, 1)
         mbar_init(&bars[kBarDrain], 1);
         if constexpr (kWQ)
             for (int i = 0; i < kStages; ++i) mbar_init(&bars[kBarWide + i], kWidenWarps);
+        if constexpr (kEpi == 3) {
+            mbar_init(&bars[kBarFinFull], C::kEpiWarps);
+            mbar_init(&bars[kBarFinEmpty], kFinWarps);
+            mbar_init(&bars[kBarSelf], C::kEpiWarps);
+        }
         misc[kMiscAbort] = 0;
         misc[kMiscBad] = 0;
         fence_barrier_init();
@@ -1080,19 +1229,23 @@ __global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ>::kThreads, 1)
             mbar_wait_bounded(&bars[kBarDrain], 0, kDrainPolls, nullptr);
         }
     } else if (warp < C::kProdWarps) {
-        // the producer warpgroup's other two warps: idle, or the widening warps
+        // the producer warpgroup's other two warps: idle, widening or finishing
         if constexpr (C::kRegSplit) reg_dealloc<C::kProdRegs>();
         if constexpr (kWQ) {
             if (!widen_tiles<kTail>(a, total, s_off, s_tpre, bars, s_n, s_a, (warp - 2) * 32 + lane,
                                     abort_flag))
                 set_abort(misc);
         }
+        if constexpr (kEpi == 3) {
+            if (!finish_tiles<kTail, kSplit>(a, total, s_off, s_tpre, bars, s_q, warp - 2, lane, abort_flag))
+                set_abort(misc);
+        }
     } else if constexpr (!kSums) {
         // ------------------------------------------------------- epilogue
         if constexpr (C::kRegSplit) reg_alloc<C::kEpiRegs>();
         bool eok;
-        if constexpr (!kTail)
-            eok = epilogue_tiles_plain<EPQ, XB, kEpi == 2, kTail, kWQ, kEpi == 3>(
+        if constexpr (!kTail && kEpi != 3)
+            eok = epilogue_tiles_plain<EPQ, XB, kEpi == 2, kTail, kWQ>(
                 a, total, s_off, s_tpre, bars, s_sa, s_sb, s_q, tmem, warp, lane, abort_flag);
         else
             eok = epilogue_tiles<EPQ, XB, kEpi == 2, kTail, kWQ, kSplit, kEpi == 3>(
@@ -1264,6 +1417,23 @@ h32_status make_map(CUtensorMap *map, CUtensorMapDataType type, int esize, const
     return H32_OK;
 }
 
+// K stages that a tile must have for two warps to finish the tile before it meanwhile.
+// Measured on 512 x 34816 x K, handed over / finished by the epilogue warps: nothing to
+// do, 8 stages 85 / 95 us; SwiGLU, 8 stages 128 / 101, 40 stages 332 / 345; SiLU, 8 185 /
+// 111, 40 339 / 355; GELU, 40 369 / 361; a bf16 residual and a bias, 8 167 / 109, 40 330 /
+// 353: a stage is 1 us, and two warps take 18 us for a tile's SwiGLU, 26 for its SiLU, 50
+// for its GELU and 23 for its residual.  (A CTA with one whole tile and a piece waits for
+// what the tile's finishing takes beyond the piece: 512 x 5120 x 5120, SiLU 79 / 72 us,
+// SwiGLU 68 / 70.)
+inline bool finish_in_epilogue(const EpiArgs &f, int64_t stages, bool one_tile) {
+    int act = 8;
+    if (f.act == H32_EPI_SWIGLU) act = 15;
+    if (f.act == H32_EPI_SILU) act = 23;
+    if (f.act == H32_EPI_GELU_TANH || f.act == H32_EPI_GELU_ERF) act = 48;
+    const int need = act + (f.res ? 12 : 0);
+    return stages < need || (one_tile && need > 20);
+}
+
 // The dense schedule: tokens per tile (bn), and how many pieces each tile of
 // the last partial wave is cut into along the tokens (tail_k), chosen by
 // simulating the kernel's static round-robin assignment of tiles to CTAs.
@@ -1413,7 +1583,7 @@ inline size_t split_ws_bytes(const TcPlan &p) {
 
 template <int EPQ, int XB, int kEpi, bool kTail = false, bool kWQ = false, bool kSplit = false>
 h32_status launch_tc(const CUtensorMap *maps, const TcArgs &a, int grid, cudaStream_t s) {
-    using C = TcCfg<EPQ, XB, kEpi == 2, kWQ>;
+    using C = TcCfg<EPQ, XB, kEpi == 2, kWQ, kEpi == 3>;
     constexpr int kSmem = C::kSmem;
     const cudaError_t e = cudaFuncSetAttribute(gemm_tc_kernel<EPQ, XB, kEpi, kTail, kWQ, kSplit>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -1557,7 +1727,10 @@ h32_status run_gemm_tc(int xbits, const uint8_t *wp, const float *wsc, int64_t l
         a.ws_ld = static_cast<int32_t>(plan.ws_ld);
     }
     a.wait_limit = wait_limit();
-    if (fin) a.fin = *fin;
+    if (fin) {
+        a.fin = *fin;
+        a.fin_self = finish_in_epilogue(*fin, K / 128, a.tail_first <= grid);
+    }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int g = static_cast<int>(grid);
     if (wd16) {

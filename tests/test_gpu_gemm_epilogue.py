@@ -170,6 +170,31 @@ def test_sizes(h32, bits, M, N, K):
            res=torch_of(r.standard_normal((M, N // 2)).astype(np.float32)).bfloat16())
 
 
+@pytest.mark.parametrize("bits,M,N,K,act,res", [
+    (4, 130, 20480, 1024, "none", False), (4, 130, 20480, 896, "none", False),
+    (8, 130, 20480, 1024, "relu", False), (4, 90, 40960, 1024, "relu", False),
+    (4, 70, 40960, 2688, "none", True), (4, 257, 10256, 1920, "swiglu", False),
+    (8, 200, 20480, 3456, "swiglu", True), (4, 130, 20496, 2944, "silu", False),
+    (4, 130, 20480, 6144, "gelu_erf", False), (4, 512, 34816, 1024, "none", False)])
+def test_several_tiles_a_block(h32, bits, M, N, K, act, res):
+    """More tiles than SMs, long and short of K: finished while the next one runs, the
+    last one (whole, cut or split along K) and the short ones by the warps that summed
+    them.  Held to the formula on the bare product's own bits."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(N + K)
+    w = 0.05 * torch.randn((N, K), device="cuda", generator=g)
+    ws = h32.h32_prepack_weights_q4_0_tc(*h32.h32_rotate_quantize_weights_q4_0(w))
+    del w
+    x = torch.randn((M, K), device="cuda", generator=g) / 4
+    ops = ws + (h32.h32_quantize_act_q4_tc if bits == 4 else h32.h32_quantize_act_q8_tc)(x)
+    z = np_of((h32.q4_0_x_q4_gemm_tc if bits == 4 else h32.q4_0_x_q8_gemm_tc)(*ops, M=M))
+    n_out = N // 2 if act == "swiglu" else N
+    r = torch.randn((M, n_out), device="cuda", generator=g).bfloat16() if res else None
+    bias = np_of(torch.randn(N, device="cuda", generator=g))
+    for b, yb in ((None, False), (bias, True)):
+        _check(h32, z, ops, bits, M=M, bias=b, act=act, res=r, y_bf16=yb)
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("M", [1, 6, 70])
 def test_rows_do_not_depend_on_the_batch(h32, bits, M):
@@ -286,3 +311,22 @@ def test_waits_that_give_up_are_reported(h32, bits, M):
         h32.h32_set_wait_limit(0)
     assert h32.h32_device_status() == 0
     _check(h32, z, ops, bits)
+
+
+def test_waits_between_tiles_that_give_up_are_reported(h32):
+    """The same where tiles are handed from warps to warps: a timeout, then exact results."""
+    import torch
+    w = 0.05 * torch.randn((20480, 1024), device="cuda")
+    x = torch.randn((130, 1024), device="cuda")
+    ops = h32.h32_prepack_weights_q4_0_tc(*h32.h32_rotate_quantize_weights_q4_0(w)) + \
+        h32.h32_quantize_act_q4_tc(x)
+    z = np_of(h32.q4_0_x_q4_gemm_tc(*ops))
+    assert h32.h32_device_status() == 0
+    h32.h32_set_wait_limit(1)
+    try:
+        h32.q4_0_x_q4_gemm_tc_epilogue(*ops)
+        assert h32.h32_device_status() == h32.H32_ERR_TIMEOUT
+    finally:
+        h32.h32_set_wait_limit(0)
+    assert h32.h32_device_status() == 0
+    _check(h32, z, ops, 4)
