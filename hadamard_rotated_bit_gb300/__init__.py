@@ -13,6 +13,7 @@ Build the library with ``python -m hadamard_rotated_bit_gb300._build`` (or
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -1011,6 +1012,9 @@ def h32_moe_route_scored_workspace_bytes(T: int, E: int) -> int:
     return int(n.value)
 
 
+_route_workspace_bytes = functools.lru_cache(maxsize=1024)(h32_moe_route_scored_workspace_bytes)
+
+
 def h32_moe_route_scored(logits, k, score="softmax", bias=None, n_group=1, topk_group=1,
                          group_top=1, renormalize=True, scale=1.0, topk_id=None, topk_w=None,
                          expert_off=None, row_idx=None, row_of=None, stream=None):
@@ -1062,7 +1066,7 @@ def h32_moe_route_scored(logits, k, score="softmax", bias=None, n_group=1, topk_
         wp, ws_bytes = None, 0
         if T > ROUTE_SOLO_TOKENS:
             # the call's own: freed with it, reused only by later work of the stream
-            ws_bytes = h32_moe_route_scored_workspace_bytes(T, E)
+            ws_bytes = _route_workspace_bytes(T, E)
             ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
             wp = ws.data_ptr()
         st = lib().h32_moe_route_scored(
