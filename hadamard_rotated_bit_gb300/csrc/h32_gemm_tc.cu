@@ -366,10 +366,10 @@ __device__ __forceinline__ void stage_dw(const float *s_sa, int s, int row, int 
 // go on with the next tile; the producer warpgroup's other two warps finish and store
 // them meanwhile, so the block loop holds nothing for it.  A CTA's last tile, and every
 // tile where two warps would not keep up (finish_in_epilogue), the epilogue warps finish, 8
-// columns each.  512 x 34816 x 5120 to bf16 with SwiGLU 332 us, the bare product 314
+// columns each.  512 x 34816 x 5120 to bf16 with SwiGLU 322 us, the bare product 314
 // (finished in the epilogue warps' registers 395, from local memory 357); 333 x 5120 x
 // 17408, 8-bit, with bias and residual 138, bare 134 (142 from local memory).  The 64 KB
-// of a tile cost one K stage, the finishing warps 8 registers of each epilogue thread.
+// of a tile cost one K stage.
 template <int kMaxChunks>
 __device__ __forceinline__ void stage_tile(float *s_q, int row, int c0, int nch, const uint64_t *acc) {
 #pragma unroll
@@ -999,6 +999,13 @@ __global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ, kEpi == 3>::kTh
     using C = TcCfg<EPQ, XB, kEpi == 2, kWQ, kEpi == 3>;
     constexpr int kStages = C::kStages;
     constexpr bool kSums = kEpi == 1;
+    // the finished output of many whole tiles a CTA (4-bit, a cut tail): the epilogue
+    // keeps its 112 registers, the finishing warps spill but have the time.  512 x 34816 x
+    // 5120, 112 / 104: SwiGLU 322 / 332 us, SiLU 330 / 339, nothing to do 320 / 328 (GELU
+    // 376 / 361; K = 1024, SwiGLU, 105 / 101).  The other instances are 3-4% slower with
+    // 112: 512 x 5120 x 5120 with a residual 70 / 68, 333 x 5120 x 17408 in 8 bits 144 / 138.
+    constexpr bool kLong = kEpi == 3 && kTail && !kSplit && XB == 4;
+    constexpr int kProdRegs = kLong ? 32 : C::kProdRegs, kEpiRegs = kLong ? 112 : C::kEpiRegs;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *s_a = smem + C::kOffA;
@@ -1117,7 +1124,7 @@ __global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ, kEpi == 3>::kTh
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA
-        if constexpr (C::kRegSplit) reg_dealloc<C::kProdRegs>();
+        if constexpr (C::kRegSplit) reg_dealloc<kProdRegs>();
         if (lane == 0) {
             prefetch_tmap(&map_a);
             prefetch_tmap(&map_b);
@@ -1163,7 +1170,7 @@ __global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ, kEpi == 3>::kTh
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
-        if constexpr (C::kRegSplit) reg_dealloc<C::kProdRegs>();
+        if constexpr (C::kRegSplit) reg_dealloc<kProdRegs>();
         if (lane == 0) {
             uint32_t ks = 0, kg = 0;
             bool ok = true;
@@ -1230,7 +1237,7 @@ __global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ, kEpi == 3>::kTh
         }
     } else if (warp < C::kProdWarps) {
         // the producer warpgroup's other two warps: idle, widening or finishing
-        if constexpr (C::kRegSplit) reg_dealloc<C::kProdRegs>();
+        if constexpr (C::kRegSplit) reg_dealloc<kProdRegs>();
         if constexpr (kWQ) {
             if (!widen_tiles<kTail>(a, total, s_off, s_tpre, bars, s_n, s_a, (warp - 2) * 32 + lane,
                                     abort_flag))
@@ -1242,7 +1249,7 @@ __global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ, kEpi == 3>::kTh
         }
     } else if constexpr (!kSums) {
         // ------------------------------------------------------- epilogue
-        if constexpr (C::kRegSplit) reg_alloc<C::kEpiRegs>();
+        if constexpr (C::kRegSplit) reg_alloc<kEpiRegs>();
         bool eok;
         if constexpr (!kTail && kEpi != 3)
             eok = epilogue_tiles_plain<EPQ, XB, kEpi == 2, kTail, kWQ>(
@@ -1253,7 +1260,7 @@ __global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ, kEpi == 3>::kTh
         if (!eok) set_abort(misc);
     } else {
         // ------------------------------------ epilogue with block sums
-        if constexpr (C::kRegSplit) reg_alloc<C::kEpiRegs>();
+        if constexpr (C::kRegSplit) reg_alloc<kEpiRegs>();
         const int ew = warp - C::kProdWarps;
         const int quad = warp & 3;                 // TMEM lanes 32*quad .. +31
         const int part = ew >> 2;                  // share of the columns
@@ -1418,7 +1425,8 @@ h32_status make_map(CUtensorMap *map, CUtensorMapDataType type, int esize, const
 }
 
 // K stages that a tile must have for two warps to finish the tile before it meanwhile.
-// Measured on 512 x 34816 x K, handed over / finished by the epilogue warps: nothing to
+// Measured on 512 x 34816 x K (epilogue warps of 104 registers), handed over / finished
+// by the epilogue warps: nothing to
 // do, 8 stages 85 / 95 us; SwiGLU, 8 stages 128 / 101, 40 stages 332 / 345; SiLU, 8 185 /
 // 111, 40 339 / 355; GELU, 40 369 / 361; a bf16 residual and a bias, 8 167 / 109, 40 330 /
 // 353: a stage is 1 us, and two warps take 18 us for a tile's SwiGLU, 26 for its SiLU, 50
