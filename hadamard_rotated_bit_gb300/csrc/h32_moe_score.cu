@@ -442,7 +442,7 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
         const float d = k > 0.0f ? fmaxf(0.0f, -__logf(sg ? k : __fdividef(k, nm.inv))) : 104.0f;
         return fabsf(k) * (8.0f + 2.0f * d) * u + tiny;
     };
-    bool near = false;
+    bool near = false, alive = true;   // alive: the lane's experts may be chosen
     if (a.n_group > 1) {
         const int size = a.E / a.n_group;
         float mine = none, err = 0.0f;   // the group's score and its bound
@@ -540,6 +540,7 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
             }
         }
         if (a.lanes) {
+            alive = stays;
             if (!stays) k1 = k2 = 0u;   // never scanned again: it wins no round
         } else {
             const uint32_t groups = __ballot_sync(0xFFFFFFFFu, stays);
@@ -574,6 +575,19 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
     for (int j = 0; j < a.k; ++j) take(j);
     float ml = lane < a.k ? row[my] : 0.0f;
     if constexpr (!kLogit) {
+        // whether key ka (logit la, bias ba) is at least kb for certain: they are the same
+        // key, or further apart than their errors
+        auto apart = [&](float ka, float la, float ba, float kb, float lb, float bb) {
+            float err = err_of(ka) + err_of(kb);
+            if (a.bias && !sg) {
+                // what the softmax's scores share weighs only by their difference, the
+                // rest by its own d
+                const float sa = score_of(la, nm, false), sb = score_of(lb, nm, false);
+                err = fminf(err, u * (40.0f * fabsf(sa - sb) + sa * (3.0f + 1.7f * (nm.lmax - la)) +
+                                      sb * (3.0f + 1.7f * (nm.lmax - lb)) + fabsf(ka) + fabsf(kb)) + tiny);
+            }
+            return (ka == kb && la == lb && ba == bb) || ka - kb > err;
+        };
         // choice j against the one after it, the last against the best left out
         const uint32_t next_u = __reduce_max_sync(0xFFFFFFFFu, k1);
         const int w = __ffs(__ballot_sync(0xFFFFFFFFu, k1 == next_u)) - 1;
@@ -589,18 +603,33 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
         }
         // both finite: above -inf and below +inf as ordered integers
         bool tie = false;
-        if (lane < a.k && ou > 0x007FFFFFu && my_u < 0xFF800000u) {
-            const float ka = from_ordered(my_u), kb = from_ordered(ou);
-            const bool same = my_u == ou && ml == ol && mb == ob;
-            float err = err_of(ka) + err_of(kb);
-            if (a.bias && !sg) {
-                // what the softmax's scores share weighs only by their difference, the
-                // rest by its own d
-                const float sa = score_of(ml, nm, false), sb = score_of(ol, nm, false);
-                err = fminf(err, u * (40.0f * fabsf(sa - sb) + sa * (3.0f + 1.7f * (nm.lmax - ml)) +
-                                      sb * (3.0f + 1.7f * (nm.lmax - ol)) + fabsf(ka) + fabsf(kb)) + tiny);
+        if (lane < a.k && ou > 0x007FFFFFu && my_u < 0xFF800000u)
+            tie = !apart(from_ordered(my_u), ml, mb, from_ordered(ou), ol, ob);
+        // The best left out may be the last choice's very key (duplicates): it then says
+        // nothing of the keys after it, and every key left out within the errors of the
+        // last choice is held against that by itself.
+        const uint32_t last_u = __shfl_sync(0xFFFFFFFFu, my_u, a.k - 1);
+        if (next_u == last_u && last_u > 0x007FFFFFu && last_u < 0xFF800000u) {
+            const float last = from_ordered(last_u), cut = last - 4.0f * err_of(last);
+            const int last_id = __shfl_sync(0xFFFFFFFFu, my, a.k - 1);
+            const float last_l = __shfl_sync(0xFFFFFFFFu, ml, a.k - 1);
+            const float last_b = __shfl_sync(0xFFFFFFFFu, mb, a.k - 1);
+            uint32_t cand = 0u;   // the lane's keys left out that are not below `cut`
+#pragma unroll
+            for (int i = 0; i < NPER; ++i)
+                if (alive && key[i] > 0x007FFFFFu && !(from_ordered(key[i]) < cut) &&
+                    (key[i] < last_u || (key[i] == last_u && e0 + i > last_id)))
+                    cand |= 1u << i;
+            while (cand) {
+                const int at = __ffs(cand) - 1;
+                cand &= cand - 1u;
+                uint32_t v = 0u;
+#pragma unroll
+                for (int i = 0; i < NPER; ++i)
+                    if (i == at) v = key[i];
+                tie |= !apart(last, last_l, last_b, from_ordered(v), row[e0 + at],
+                              a.bias ? a.bias[e0 + at] : 0.0f);
             }
-            tie = !same && !(ka - kb > err);
         }
         if (__any_sync(0xFFFFFFFFu, near)) {
             my = route_exact<NPER>(a, row);

@@ -245,3 +245,35 @@ def test_empty_given_outputs_stream_and_graph(h32):
         rid, rw, roff, rridx, rrow = oracle.moe_route_scored(np_of(l), k, score="sigmoid")
         assert np.array_equal(np_of(out[0]), rid) and np.array_equal(np_of(out[3]), rridx)
         assert np.array_equal(np_of(out[2]), roff) and np.array_equal(np_of(out[4]), rrow)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,G,tg", [(3, 1, 1, 1), (16, 3, 1, 1), (256, 8, 1, 1), (1024, 5, 1, 1), (64, 2, 4, 2)])
+def test_duplicates_on_the_border_of_the_choice(h32, score, E, k, G, tg):
+    """Two experts of the same logit and bias share the k-th key, and one of a higher id
+    has a key one step above theirs, within fp32's errors: it is chosen, the duplicates
+    go without (or the lower one takes the last place)."""
+    r = np.random.default_rng(E + k)
+    T = 200
+    for bias in (np.zeros(E, np.float32), np.full(E, 0.125, np.float32)):
+        l = (r.standard_normal((T, E)) * 0.5 - 8).astype(np.float32)
+        for t in range(T):
+            at = np.sort(r.permutation(E)[:3])
+            top = np.float32(r.standard_normal() * 0.5)
+            l[t, at[:2]] = top
+            l[t, at[2]] = np.nextafter(top, np.float32(9))
+            others = np.setdiff1d(r.permutation(E), at)[:k - 1]
+            l[t, others] = top + 2 + 0.5 * np.arange(k - 1)
+        _check(h32, l, k, bias, score=score, n_group=G, topk_group=tg, group_top=1)
+        _check(h32, l, min(k + 1, E), bias, score=score, n_group=G, topk_group=tg, group_top=1)
+
+
+def test_duplicates_and_a_bias_that_undoes_a_score(h32):
+    """The duplicates' key is 0.5, a third key is 0.5 and a little in double but at most
+    0.5 in fp32."""
+    l = np.array([[0, 0, 0.1]], np.float32)
+    bias = np.array([0, 0, 0.5 - 1 / (1 + np.exp(-np.float64(l[0, 2]))) + 6.7e-10], np.float32)
+    assert bias[2] + 1 / (1 + np.exp(-np.float64(l[0, 2]))) > 0.5
+    _check(h32, l, 1, bias, score="sigmoid")
+    _check(h32, np.zeros((70, 200), np.float32), 9, np.zeros(200, np.float32), score="softmax")
+    _check(h32, np.zeros((70, 200), np.float32), 9, np.full(200, -0.5, np.float32), score="sigmoid")
