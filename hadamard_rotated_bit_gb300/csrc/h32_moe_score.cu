@@ -588,29 +588,24 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
             }
             return (ka == kb && la == lb && ba == bb) || ka - kb > err;
         };
-        // choice j against the one after it, the last against the best left out
-        const uint32_t next_u = __reduce_max_sync(0xFFFFFFFFu, k1);
-        const int w = __ffs(__ballot_sync(0xFFFFFFFFu, k1 == next_u)) - 1;
-        const int next = __shfl_sync(0xFFFFFFFFu, e0 + i1, w);
+        // choice j against the one after it, both finite: above -inf and below +inf as
+        // ordered integers
         const float mb = (lane < a.k && a.bias) ? a.bias[my] : 0.0f;
-        uint32_t ou = __shfl_down_sync(0xFFFFFFFFu, my_u, 1);
-        float ol = __shfl_down_sync(0xFFFFFFFFu, ml, 1);
-        float ob = __shfl_down_sync(0xFFFFFFFFu, mb, 1);
-        if (lane == a.k - 1) {
-            ou = next_u;
-            ol = next_u ? row[next] : 0.0f;
-            ob = (next_u && a.bias) ? a.bias[next] : 0.0f;
-        }
-        // both finite: above -inf and below +inf as ordered integers
+        const uint32_t ou = __shfl_down_sync(0xFFFFFFFFu, my_u, 1);
+        const float ol = __shfl_down_sync(0xFFFFFFFFu, ml, 1);
+        const float ob = __shfl_down_sync(0xFFFFFFFFu, mb, 1);
         bool tie = false;
-        if (lane < a.k && ou > 0x007FFFFFu && my_u < 0xFF800000u)
+        if (lane < a.k - 1 && ou > 0x007FFFFFu && my_u < 0xFF800000u)
             tie = !apart(from_ordered(my_u), ml, mb, from_ordered(ou), ol, ob);
-        // The best left out may be the last choice's very key (duplicates): it then says
-        // nothing of the keys after it, and every key left out within the errors of the
-        // last choice is held against that by itself.
+        // The last choice: below it by err_of's bounds, which do not depend on the pair, the
+        // best key left out speaks for all of them.  Else every key left out within the
+        // errors is held against the last choice by itself: one that is apart (its scores
+        // share what they err by, or it is the very same key) says nothing of the others.
         const uint32_t last_u = __shfl_sync(0xFFFFFFFFu, my_u, a.k - 1);
-        if (next_u == last_u && last_u > 0x007FFFFFu && last_u < 0xFF800000u) {
-            const float last = from_ordered(last_u), cut = last - 4.0f * err_of(last);
+        const uint32_t next_u = __reduce_max_sync(0xFFFFFFFFu, k1);
+        const float last = from_ordered(last_u), next = from_ordered(next_u);
+        if (next_u > 0x007FFFFFu && last_u < 0xFF800000u && !(last - next > err_of(last) + err_of(next))) {
+            const float cut = last - 4.0f * err_of(last);
             const int last_id = __shfl_sync(0xFFFFFFFFu, my, a.k - 1);
             const float last_l = __shfl_sync(0xFFFFFFFFu, ml, a.k - 1);
             const float last_b = __shfl_sync(0xFFFFFFFFu, mb, a.k - 1);

@@ -277,3 +277,35 @@ def test_duplicates_and_a_bias_that_undoes_a_score(h32):
     _check(h32, l, 1, bias, score="sigmoid")
     _check(h32, np.zeros((70, 200), np.float32), 9, np.zeros(200, np.float32), score="softmax")
     _check(h32, np.zeros((70, 200), np.float32), 9, np.full(200, -0.5, np.float32), score="sigmoid")
+
+
+@pytest.mark.parametrize("E,k", [(5, 1), (40, 4), (256, 8)])
+def test_small_scores_beside_a_large_one_that_the_bias_undoes(h32, E, k):
+    """Softmax: two experts of negligible scores and biases 2e-8 and 1.9e-8 on the border,
+    and one of a score near 0.4 whose bias leaves a little more than 2e-8 of it: in fp32
+    its key may come out below both, and it is chosen all the same."""
+    r = np.random.default_rng(E)
+    T = 300
+    bias = np.full(E, -1.0, np.float32)
+    a, b, c = k - 1, k, E - 1
+    bias[a], bias[b] = 2e-8, 1.9e-8
+    bias[:k - 1] = 0.5                      # clear choices
+    l = (r.standard_normal((T, E)) - 3).astype(np.float32)
+    l[:, [a, b]] = -60 + r.standard_normal((T, 2))
+    target = np.float64(3e-8)
+    bias[c] = np.float32(-0.4)
+
+    def key(row):
+        e = np.exp(row.astype(np.float64) - row.max())
+        return e[c] / e.sum() + np.float64(bias[c])
+
+    for t in range(T):
+        others = np.exp(np.delete(l[t].astype(np.float64), c)).sum()
+        l[t, c] = np.log(others * (target - bias[c]) / (1 - target + bias[c]))
+        while key(l[t]) < 2.2e-8:
+            l[t, c] = np.nextafter(l[t, c], np.float32(9))
+        assert 2.2e-8 <= key(l[t]) < 2e-7
+    _check(h32, l, k, bias)
+    assert (oracle.moe_route_scored(l, k, bias=bias)[0][:, -1] == c).all()
+    for renorm in (True, False):
+        _check(h32, l, k + 1, bias, renormalize=renorm)
