@@ -300,20 +300,17 @@ __device__ __noinline__ bool exact_groups(const ScoreArgs &a, const float *row, 
 
 // A token whose nearest keys are among its first c (sorted, c <= 32; lane j holds
 // candidate j's expert and logit): those keys alone in double, one a lane, and
-// their order.  Lane j returns choice j's expert.  Without a bias keys grow with
-// their logits, which then decide by themselves.
+// their order.  Lane j returns choice j's expert.  (Without a bias too: logits that
+// differ may have one score, and then the lower id is first.)
 template <int NPER>
 __device__ __noinline__ int route_refine(const ScoreArgs &a, const float *row, int c, int id) {
     const int lane = threadIdx.x & 31;
     const bool sg = a.sigmoid != 0, in = lane < c;
-    const double none = -static_cast<double>(INFINITY);
     const float l = in ? row[id] : -INFINITY;
-    double key = l;
-    if (a.bias) {
-        Norm<double> nm{none, 1.0};
-        if (!sg) nm = exact_norm<NPER>(a, row);
-        key = key_of<double>(l, score_of(static_cast<double>(l), nm, sg), in ? a.bias[id] : 0.0f);
-    }
+    Norm<double> nm{-static_cast<double>(INFINITY), 1.0};
+    if (!sg) nm = exact_norm<NPER>(a, row);
+    const double key = key_of<double>(l, score_of(static_cast<double>(l), nm, sg),
+                                      (in && a.bias) ? a.bias[id] : 0.0f);
     const uint64_t mine = in ? ordered(key) : 0ull;
     int rank = 0;
     for (int j = 0; j < c; ++j) {

@@ -569,10 +569,11 @@ typedef enum h32_score {
  *     `renormalize` scale * s_j / sum of the k chosen scores, in fp32;
  * then the rows are grouped by expert as by h32_moe_route, with the same outputs
  * topk_id, topk_w, expert_off, row_idx, row_of (and their alignment).
- * The order of keys is exact: without a bias, and with groups by their best key,
- * that of the logits; else that of the keys' (and group scores') values in double
- * precision.  So ids, offsets and row maps do not depend on fp32 rounding; the
- * weights are within a few ulps.  Deterministic.
+ * The order of keys is exact: without a bias, where every group stays or groups go
+ * by their best key, that of the logits; else that of the keys' (and group scores')
+ * values in double precision, equal values (saturated scores) by id.  So ids,
+ * offsets and row maps do not depend on fp32 rounding; the weights are within a few
+ * ulps.  Deterministic.
  * Logits that are not finite: a -inf logit masks its expert (score 0, key -inf
  * whatever the bias); a NaN logit or bias ranks below it; +inf logits share the
  * softmax equally.  Masked experts are chosen only when fewer than k others are

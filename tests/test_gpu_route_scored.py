@@ -309,3 +309,25 @@ def test_small_scores_beside_a_large_one_that_the_bias_undoes(h32, E, k):
     assert (oracle.moe_route_scored(l, k, bias=bias)[0][:, -1] == c).all()
     for renorm in (True, False):
         _check(h32, l, k + 1, bias, renormalize=renorm)
+
+
+@pytest.mark.parametrize("E,G,tg,k", [(16, 4, 2, 2), (16, 4, 2, 4), (36, 4, 3, 6), (256, 8, 4, 8), (12, 2, 1, 3)])
+def test_scores_that_saturate_without_a_bias(h32, E, G, tg, k):
+    """Groups by their two best keys, no bias: sigmoids of different large logits are all 1
+    in double, softmax scores of different very low ones all 0, and the lower id is
+    first; few such experts (decided one a lane) and many (decided altogether)."""
+    r = np.random.default_rng(E + k)
+    T = 60
+    for many in (2, min(k + 1, E), E):
+        l = (r.standard_normal((T, E)) * 0.5 - 3).astype(np.float32)
+        for t in range(T):
+            at = r.permutation(E)[:many]
+            l[t, at] = 39 + 10 * r.random(many)
+        _check(h32, l, k, None, score="sigmoid", n_group=G, topk_group=tg, group_top=2)
+    l = np.full((1, E), -3, np.float32)
+    l[0, 2], l[0, 3] = 39, 40
+    assert oracle.moe_route_scored(l, 2, "sigmoid", n_group=G, topk_group=tg, group_top=2)[0].tolist() == [[2, 3]]
+    _check(h32, l, 2, None, score="sigmoid", n_group=G, topk_group=tg, group_top=2)
+    l = (-1000 * r.random((T, E)) - 1000).astype(np.float32)
+    l[:, E // 2] = 0.0
+    _check(h32, l, k, None, score="softmax", n_group=G, topk_group=tg, group_top=2)
