@@ -30,6 +30,8 @@
 // their two best, top 8: routing 28.8 us (22 without groups), grouping 9.7.  1024 x
 // 128, softmax with a bias: 7.2 and 6.3 us.  One token: 6.3 us, one launch (grouping
 // by a block an expert, as h32_moe_route: 16384 x 256 290 us altogether).
+#include <float.h>
+
 #include "h32_common.cuh"
 #include "h32_moe.cuh"
 
@@ -449,6 +451,8 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
             f2 = from_ordered(b2);
             mine = group_score(f1, f2, a.group_top);
             if constexpr (!kLogit) {
+                // (a sum below fp32's range is a score all the same, unlike no key at all)
+                if (f1 > none) mine = fmaxf(mine, -FLT_MAX);
                 if (f1 > none) err = err_of(f1);
                 if (a.group_top == 2 && f2 > none) err += err_of(f2) + fabsf(mine) * u;
             }

@@ -331,3 +331,29 @@ def test_scores_that_saturate_without_a_bias(h32, E, G, tg, k):
     l = (-1000 * r.random((T, E)) - 1000).astype(np.float32)
     l[:, E // 2] = 0.0
     _check(h32, l, k, None, score="softmax", n_group=G, topk_group=tg, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_near_the_lowest_value(h32, score):
+    """Experts switched off by biases near fp32's lowest value: sums of two such keys leave
+    fp32's range, and still order their groups; groups of one key and of none beside."""
+    low = np.finfo(np.float32).min
+    r = np.random.default_rng(12)
+    for E, G in ((4, 2), (48, 4), (40, 8), (64, 32)):
+        size = E // G
+        l = _logits(30, E, E)
+        some = np.zeros(E, np.float32)
+        some[::2] = low
+        some[: size] = low
+        scaled = (low * (0.8 + 0.2 * r.random(E))).astype(np.float32)
+        high = (-low * (0.8 + 0.2 * r.random(E))).astype(np.float32)
+        sums = np.array([np.sort(scaled[g * size:(g + 1) * size].astype(np.float64))[-2:].sum()
+                         for g in range(G)])
+        assert (sums < low).all() and np.unique(sums).size == G
+        masked = l.copy()
+        masked[:, size:2 * size] = -np.inf          # a group of no key
+        masked[:, 1:size] = -np.inf                 # and one of a single key
+        for b in (np.full(E, low, np.float32), some, scaled, high):
+            for x in (l, masked):
+                for tg in (1, G // 2, G - 1):
+                    _check(h32, x, min(size, 4), b, score=score, n_group=G, topk_group=tg, group_top=2)
