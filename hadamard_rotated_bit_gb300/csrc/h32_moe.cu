@@ -263,7 +263,7 @@ extern "C" h32_status h32_moe_route(const float *logits, int64_t T, int32_t E, i
     using namespace h32;
     if (T < 0 || E < 1 || E > kMaxE || k < 1 || k > kMaxK || k > E || ldl < E || !expert_off)
         return H32_ERR_INVALID_ARG;
-    if (T * k > 0x7FFFFFFFll) return H32_ERR_INVALID_ARG;
+    if (T > 0x7FFFFFFFll || T * k > 0x7FFFFFFFll) return H32_ERR_INVALID_ARG;
     if (T > 0 && (!logits || !topk_id || !topk_w || !row_idx || !row_of))
         return H32_ERR_INVALID_ARG;
     if ((logits && (reinterpret_cast<uintptr_t>(logits) & 3u)) ||

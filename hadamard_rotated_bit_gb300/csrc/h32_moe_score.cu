@@ -904,7 +904,7 @@ extern "C" h32_status h32_moe_route_scored(const float *logits, int64_t T, int32
         group_top < 1 || group_top > 2 || k > topk_group * (E / n_group) || !(scale > -INFINITY) ||
         !(scale < INFINITY))
         return H32_ERR_INVALID_ARG;
-    if (T * k > 0x7FFFFFFFll) return H32_ERR_INVALID_ARG;
+    if (T > 0x7FFFFFFFll || T * k > 0x7FFFFFFFll) return H32_ERR_INVALID_ARG;
     if (T > 0 && (!logits || !topk_id || !topk_w || !row_idx || !row_of))
         return H32_ERR_INVALID_ARG;
     auto off4 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };

@@ -93,3 +93,14 @@ def test_rule_closed_forms():
     b = np.zeros(8, np.float32)
     b[0] = 5.0
     assert 0 not in oracle.moe_route_scored(l, 7, "sigmoid", bias=b)[0]
+
+
+def test_token_counts_whose_row_count_wraps():
+    """T k above 2^63: refused, not taken modulo 2^64 (by both routers)."""
+    _build.build()
+    v = ctypes.c_void_p
+    p, E, k = v(4096), 64, 32
+    for T in (1 << 59, (1 << 59) + 5, 1 << 62, (1 << 63) - 1):
+        assert h32.lib().h32_moe_route_scored(p, T, E, E, 0, v(0), 1, 1, 1, k, 1, 1.0, p, p, p, p, p, v(0), 0,
+                                              v(0)) == h32.H32_ERR_INVALID_ARG
+        assert h32.lib().h32_moe_route(p, T, E, E, k, p, p, p, p, p, v(0)) == h32.H32_ERR_INVALID_ARG
