@@ -415,11 +415,12 @@ __global__ void __launch_bounds__(kThreads, kPieces == 1 ? 2 : 1) norm_quant_ker
         const float s = row_sum(v, a, s_part[turn][0]);
         // (the block has met in row_sum: every thread has read its part of the slot)
         if (kAhead && threadIdx.x == 0) copy_row(row + kSlots * stride, turn);
-        float r = __frsqrt_rn(__fadd_rn(__fmul_rn(s, a.inv_k), a.eps));
-        // a sum of squares above fp32's range: the row times 2^-80 (exact but for
-        // values too small to matter), whose norm is the same; eps is nothing there
-        // (a warp that holds several rows goes along where one of them overflows)
-        const bool over = !(s < INFINITY);
+        const float ms = __fadd_rn(__fmul_rn(s, a.inv_k), a.eps);
+        float r = __frsqrt_rn(ms);
+        // a mean square above fp32's range: the row times 2^-80 (exact but for values too
+        // small to matter) and eps times 2^-160 (nothing unless eps is huge), whose norm is
+        // the same (a warp that holds several rows goes along where one of them overflows)
+        const bool over = !(ms < INFINITY);
         if (shared_warp ? __any_sync(0xFFFFFFFFu, over) : over) {
             const uint64_t down = pair_f(over ? 0x1p-80f : 1.0f, over ? 0x1p-80f : 1.0f);
 #pragma unroll
@@ -427,7 +428,9 @@ __global__ void __launch_bounds__(kThreads, kPieces == 1 ? 2 : 1) norm_quant_ker
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = mul_f32x2(v[i][j], down);
             const float s2 = row_sum(v, a, s_part[turn][1]);
-            if (over) r = __frsqrt_rn(__fmul_rn(s2, a.inv_k));
+            if (over)
+                r = __frsqrt_rn(__fadd_rn(__fmul_rn(s2, a.inv_k),
+                                          __fmul_rn(__fmul_rn(a.eps, 0x1p-80f), 0x1p-80f)));
         }
         const uint64_t rr = pair_f(r, r);
 #pragma unroll

@@ -622,8 +622,8 @@ h32_status h32_moe_combine(const float *y, int64_t R, int64_t ldy, const int32_t
  *       even and the odd places, added; 32 such sums by the xor tree of strides 1,
  *       2, 4, 8, 16 (absent sums 0); 32 of those the same way; the rest in order;
  *   r = 1 / sqrt(S fl(1/K) + eps): product, sum and reciprocal root each rounded to
- *       fp32; n = (h r) w, two fp32 roundings; where S overflows fp32 the row is
- *       scaled by 2^-80 first;
+ *       fp32; n = (h r) w, two fp32 roundings; where S or the sum with eps overflows
+ *       fp32, the row is scaled by 2^-80 and eps by 2^-160 first;
  *   then n is rotated and quantized exactly as by the quantizer of `form`.
  * Bit-identical to that sequential evaluation.
  *   x            [M][ldx] of type x_dt

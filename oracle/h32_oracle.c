@@ -660,16 +660,16 @@ void o_add_rms_norm(const float *x, const float *res, int res_bf16, const float 
             if (res && res_bf16) hr[i] = round_bf16(hr[i]);
             nr[i] = hr[i];
         }
-        float s = row_sum_squares(nr, K);
-        float r;
         const float inv_k = 1.0f / (float)K;
-        if (s < INFINITY) {
-            const float ms = s * inv_k;
-            r = reciprocal_root(ms + eps);
-        } else {
+        float ms = row_sum_squares(nr, K) * inv_k;
+        ms = ms + eps;
+        if (!(ms < INFINITY)) {   /* the row times 2^-80, eps times 2^-160 */
+            const float e = eps * 0x1p-80f * 0x1p-80f;
             for (int64_t i = 0; i < K; ++i) nr[i] = nr[i] * 0x1p-80f;
-            r = reciprocal_root(row_sum_squares(nr, K) * inv_k);
+            ms = row_sum_squares(nr, K) * inv_k;
+            ms = ms + e;
         }
+        const float r = reciprocal_root(ms);
         for (int64_t i = 0; i < K; ++i) {
             const float t = nr[i] * r;
             nr[i] = t * w[i];

@@ -253,3 +253,20 @@ def test_wait_that_gives_up_is_reported(h32):
     xq, xd, _, _ = _run(h32, x, w, None, "q4_tc", 32)
     _, n = oracle.add_rms_norm(x, w)
     _check_codes("q4_tc", xq, xd, n, 32)
+
+
+@pytest.mark.parametrize("K", [96, 512, 5120, 12288])
+def test_huge_eps(h32, K):
+    """eps beside rows whose sum of squares leaves fp32's range, and beside small ones."""
+    import torch
+    for M in (5, 40):
+        x = _rows(M, K, K, False)
+        x[1] *= np.float32(2.0 ** 60)
+        x[2] *= np.float32(2.0 ** 66)
+        x[3] *= np.float32(2.0 ** 90)
+        w = np.ones(K, np.float32)
+        for eps in (1e30, 1e36, 1e38, 3.4028234e38):
+            xq, xd, _, nrm = _run(h32, x, w, None, "q8", 32, torch.float32, eps=eps)
+            _, n = oracle.add_rms_norm(x, w, None, eps)
+            assert np.isfinite(n).all() and _same(np_of(nrm), n)
+            _check_codes("q8", xq, xd, n, 32)

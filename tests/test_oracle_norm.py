@@ -75,3 +75,21 @@ def test_sum_order_is_the_stated_one():
     s = np.float32(2.0 ** 24 + 2.0)
     ms = s * (np.float32(1) / np.float32(K))
     assert n[0, 16384] == np.float32(1 / np.sqrt(np.float64(ms)))
+
+
+@pytest.mark.parametrize("K", [32, 512, 5120, 17408])
+def test_overflowing_rows_keep_their_eps(K):
+    """Rows whose sum of squares leaves fp32's range, and rows whose mean square does with
+    eps: the formula in float64, eps included, within the same bound."""
+    r = np.random.default_rng(K)
+    x = (r.choice((-1.0, 1.0), (4, K)) * (1 + r.random((4, K)))).astype(np.float32)
+    x *= (2.0 ** np.array([57, 62, 64, 70]))[:, None].astype(np.float32)
+    w = np.ones(K, np.float32)
+    with np.errstate(over="ignore"):
+        assert np.isinf((x.astype(np.float32) ** 2).sum(1)[2:]).all()
+    for eps in (1e-6, 1.0, 1e30, 1e36, 1e38, 3.4028234e38):
+        _, n = oracle.add_rms_norm(x, w, None, eps)
+        x64 = x.astype(np.float64)
+        want = x64 / np.sqrt((x64 ** 2).mean(1, keepdims=True) + np.float64(np.float32(eps)))
+        bound = ((8 + 1 + 10 + 1 + 3) / 2 + 3) * U * (1 + 1e-4)
+        assert np.all(np.abs(n - want) <= bound * np.abs(want))
