@@ -188,6 +188,24 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64
     return __all_sync(0xFFFFFFFFu, ok);
 }
 
+// The same, but a bound of one poll is one look at the barrier that never suspends the
+// warp.  try_wait may, for longer than a copy takes, so a wait for a copy would never run
+// out, whatever the bound; with one look, a copy issued just before is not there yet.
+__device__ __forceinline__ bool warp_wait_or_look(uint64_t *bar, uint32_t parity, uint64_t limit,
+                                                  volatile int *abort) {
+    uint32_t all;
+    asm volatile(
+        "{\n.reg .pred p, q;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "vote.sync.all.pred q, p, 0xffffffff;\nselp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(all)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (all) return true;
+    if (limit == 1) return false;
+    const bool ok = mbar_wait_bounded(bar, parity, limit, abort);
+    return __all_sync(0xFFFFFFFFu, ok);
+}
+
 __device__ __forceinline__ void fence_barrier_init() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }

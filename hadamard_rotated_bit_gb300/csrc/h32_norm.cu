@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, kPieces == 1 ? 2 : 1) norm_quant_ker
     for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows; row0 < a.M; row0 += stride) {
         const int64_t row = row0 + my_row;
         uint64_t v[kPieces][8];
-        if (kAhead && !warp_wait(&s_full[turn], phase, a.wait_limit, nullptr)) {
+        if (kAhead && !warp_wait_or_look(&s_full[turn], phase, a.wait_limit, nullptr)) {
             // gave up: the block's rows from this one on are undefined; the thread that
             // copies leaves when its copies under way have landed, or after as long again
             if ((threadIdx.x & 31) == 0) atomicOr(&g_norm_status, kStatusTimeout);

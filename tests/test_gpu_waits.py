@@ -143,3 +143,39 @@ def test_tc_gemm_one_poll_wait_bound(h32, kind):
     _exact_small_case(h32)
     if kind.endswith("_split"):
         _exact_split_case(h32)
+
+
+@pytest.mark.parametrize("K,xb,rb", [(640, True, None), (1024, True, None), (5120, False, True), (8192, True, True),
+                                     (13312, True, None)])
+def test_norm_one_poll_wait_bound(h32, K, xb, rb):
+    """The norm that copies rows ahead, under a one-poll wait bound: a look at a copy issued
+    just before finds it under way, so the status reads H32_ERR_TIMEOUT, once; the copies
+    land before the blocks leave, and the same context then computes exact results."""
+    import torch
+    from tests.test_gpu_norm import _check_codes, _f32, _rows, _run, _same
+    M = 20000
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn((M, K), device="cuda", generator=g).to(torch.bfloat16 if xb else torch.float32)
+    res = None if rb is None else torch.randn((M, K), device="cuda", generator=g).bfloat16()
+    w = torch.ones(K, device="cuda")
+    assert h32.h32_device_status() == 0
+    h32.h32_set_wait_limit(1)
+    try:
+        for _ in range(3):
+            h32.h32_add_rms_norm_quantize(x, w, residual=res)
+            assert h32.h32_device_status() == h32.H32_ERR_TIMEOUT
+            assert h32.h32_device_status() == 0
+        # a row a block waits for nothing
+        h32.h32_add_rms_norm_quantize(x[:7], w, residual=None if res is None else res[:7])
+        assert h32.h32_device_status() == 0
+    finally:
+        h32.h32_set_wait_limit(0)
+    sample = [0, 1, 151, 4321, M - 1]
+    xq, xd, ro, nrm = h32.h32_add_rms_norm_quantize(x, w, residual=res, norm_out=torch.float32)
+    assert h32.h32_device_status() == 0
+    at = torch.tensor(sample, device="cuda")
+    xs = np_of(x[at].float())
+    rs = None if res is None else wl.f32_to_bf16_bits(np_of(res[at].float()))
+    h, n = oracle.add_rms_norm(xs, np.ones(K, np.float32), rs)
+    assert _same(np_of(nrm[at]), n) and (res is None or _same(_f32(ro[at]), h))
+    _check_codes("q4_tc", xq[at], xd[:, at], n, True)
