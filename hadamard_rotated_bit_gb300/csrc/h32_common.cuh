@@ -191,6 +191,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64
 // The same, but a bound of one poll is one look at the barrier that never suspends the
 // warp.  try_wait may, for longer than a copy takes, so a wait for a copy would never run
 // out, whatever the bound; with one look, a copy issued just before is not there yet.
+// (The bound is compared only where the look failed: compared first, it cost the
+// few-token product 2-6%.)
 __device__ __forceinline__ bool warp_wait_or_look(uint64_t *bar, uint32_t parity, uint64_t limit,
                                                   volatile int *abort) {
     uint32_t all;

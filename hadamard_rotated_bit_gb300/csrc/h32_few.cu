@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         bool ok = true;
         for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
             for (int st = 0; st < nst; ++st) {
-                if (!warp_wait(&s_empty[s], ph, lim, abort)) {
+                if (!warp_wait_or_look(&s_empty[s], ph, lim, abort)) {
                     ok = false;
                     break;
                 }
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             bool ok = true;
             for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
                 for (int st = 0; st < nst; ++st) {
-                    if (!warp_wait(&s_full[s], ph, lim, abort)) {
+                    if (!warp_wait_or_look(&s_full[s], ph, lim, abort)) {
                         ok = false;
                         break;
                     }
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
                     for (int j0 = 0; j0 < kStageBlocks; j0 += kGroup) {
                         if (j0 < n) {
-                            if (!warp_wait(&s_sempty[gb], gph, lim, abort)) {
+                            if (!warp_wait_or_look(&s_sempty[gb], gph, lim, abort)) {
                                 ok = false;
                                 break;
                             }
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
             for (int p = 0; p < PT; ++p) acc[p] = 0ull;
             for (int st = 0; st < nst && ok; ++st) {
-                if (!warp_wait(&s_full[s], sph, lim, abort)) {
+                if (!warp_wait_or_look(&s_full[s], sph, lim, abort)) {
                     ok = false;
                     break;
                 }
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 for (int j0 = 0; j0 < kStageBlocks; j0 += kBatch) {
                     if (j0 < n) {
                         if (j0 % kGroup == 0) {
-                            if (!warp_wait(&s_sfull[gb], gph, lim, abort)) {
+                            if (!warp_wait_or_look(&s_sfull[gb], gph, lim, abort)) {
                                 ok = false;
                                 break;
                             }

@@ -179,3 +179,33 @@ def test_norm_one_poll_wait_bound(h32, K, xb, rb):
     h, n = oracle.add_rms_norm(xs, np.ones(K, np.float32), rs)
     assert _same(np_of(nrm[at]), n) and (res is None or _same(_f32(ro[at]), h))
     _check_codes("q4_tc", xq[at], xd[:, at], n, True)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("M", [1, 8, 16])
+@pytest.mark.parametrize("N,K", [(1024, 2048), (5120, 640), (20480, 4096), (32, 128)])
+def test_few_token_product_one_poll_wait_bound(h32, bits, M, N, K):
+    """The product of a few tokens under a one-poll wait bound, in tiles of 32, 64 and 128
+    rows: looks at copies and products just issued find them under way, so the status
+    reads H32_ERR_TIMEOUT, once; the block's copies and products end before it leaves,
+    and the same context then computes exact results."""
+    import torch
+    from tests.test_gpu_gemm_epilogue import _check, _operands
+    wp, wsc = _tc_ones(h32, N, K, 0.0625)
+    xw = torch.full((M, K * bits // 4), 0x38, dtype=torch.uint8, device="cuda")
+    xdt = torch.ones((K // 32, 16), dtype=torch.float32, device="cuda")
+    call = h32.q4_0_x_q4_gemm_tc_epilogue if bits == 4 else h32.q4_0_x_q8_gemm_tc_epilogue
+    assert h32.h32_device_status() == 0
+    h32.h32_set_wait_limit(1)
+    try:
+        for _ in range(3):
+            call(wp, wsc, xw, xdt, M=M)
+            assert h32.h32_device_status() == h32.H32_ERR_TIMEOUT
+            assert h32.h32_device_status() == 0
+    finally:
+        h32.h32_set_wait_limit(0)
+    y = call(wp, wsc, xw, xdt, M=M)
+    assert h32.h32_device_status() == 0
+    assert torch.all(y == K * bits // 4 * 0.0625)
+    z, ops = _operands(h32, M, 160, 256, bits, 6)
+    _check(h32, z, ops, bits)
