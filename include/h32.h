@@ -460,7 +460,11 @@ typedef enum h32_epi_act {
  *                   y itself (same type and pitch)
  *   y               [M][ldy] out of type y_dt, ldy >= outputs
  *   workspace       as for q4_0_x_q4_gemm_tc_ws (null: no split)
- * z is bit-exact; v is within a few ulps of the formula (the CUDA expf, erfcf).
+ * z is bit-exact.  v is off from act of the fp32 sum z + bias by at most, relative,
+ * in half steps of fp32 (2^-24): none, ReLU 0; SiLU 6; SwiGLU 7; GELU_TANH 6 + 6 |2 u|;
+ * GELU_ERF 10 + 2 (z^2 + 2) (the rounded argument of exp and erfc, which weighs more
+ * the nearer v is to 0).  Where exp leaves fp32's range (arguments beyond 88.7) v
+ * comes out 0, off by less than 2^-121 (SwiGLU: 2^-121 |z_up|).
  * Other arguments and conditions as for q4_0_x_q4_gemm_tc.
  */
 h32_status q4_0_x_q4_gemm_tc_epilogue(const uint8_t *wp, const float *wsc, int64_t ldws,
@@ -572,8 +576,11 @@ typedef enum h32_score {
  * The order of keys is exact: without a bias, where every group stays or groups go
  * by their best key, that of the logits; else that of the keys' (and group scores')
  * values in double precision, equal values (saturated scores) by id.  So ids,
- * offsets and row maps do not depend on fp32 rounding; the weights are within a few
- * ulps.  Deterministic.
+ * offsets and row maps do not depend on fp32 rounding.  The weights are fp32
+ * evaluations, relatively within 260 half steps (2^-24) at any E and any spread of the
+ * logits: |l - the largest| of them come from the exponential's rounded argument, 37
+ * from the softmax's sum, a dozen from all else; below 2^-126 they may vanish.
+ * Deterministic.
  * Logits that are not finite: a -inf logit masks its expert (score 0, key -inf
  * whatever the bias); a NaN logit or bias ranks below it; +inf logits share the
  * softmax equally.  Masked experts are chosen only when fewer than k others are

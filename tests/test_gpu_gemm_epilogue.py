@@ -330,3 +330,24 @@ def test_waits_between_tiles_that_give_up_are_reported(h32):
         h32.h32_set_wait_limit(0)
     assert h32.h32_device_status() == 0
     _check(h32, z, ops, 4)
+
+
+@pytest.mark.parametrize("M", [2, 40])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "gelu_erf", "swiglu"])
+def test_stated_bounds_of_the_activations(h32, act, M):
+    """Dense arguments where the results cancel, vanish and leave fp32's range: within the
+    relative bounds stated with the entry points, and within 2^-121 (SwiGLU: times |up|)
+    where the exponential's range ends."""
+    import torch
+    K = 128
+    for lo, hi, N in ((-14.0, 8.0, 4096), (-110.0, -80.0, 2048), (-13.5, -8.0, 2048)):
+        z, ops = _operands(h32, M, N, K, 4, 11)
+        bias = np.linspace(lo, hi, N).astype(np.float32)
+        if act == "swiglu":
+            bias[1::2] = 1000 * np.cos(np.arange(N // 2)).astype(np.float32)
+        y = h32.q4_0_x_q4_gemm_tc_epilogue(*ops, M=M, bias=torch_of(bias), act=act)
+        torch.cuda.synchronize()
+        zb = z + bias
+        v, steps = _formula(zb, act)
+        floor = 2.0 ** -121 * (np.maximum(1.0, np.abs(zb[:, 1::2].astype(np.float64))) if act == "swiglu" else 1.0)
+        assert np.all(np.abs(np_of(y) - v) <= steps * H * np.abs(v) * (1 + 2.0 ** -10) + floor)
