@@ -1426,20 +1426,22 @@ h32_status make_map(CUtensorMap *map, CUtensorMapDataType type, int esize, const
 
 // K stages that a tile must have for two warps to finish the tile before it meanwhile.
 // Measured on 512 x 34816 x K (epilogue warps of 104 registers), handed over / finished
-// by the epilogue warps: nothing to
-// do, 8 stages 85 / 95 us; SwiGLU, 8 stages 128 / 101, 40 stages 332 / 345; SiLU, 8 185 /
-// 111, 40 339 / 355; GELU, 40 369 / 361; a bf16 residual and a bias, 8 167 / 109, 40 330 /
-// 353: a stage is 1 us, and two warps take 18 us for a tile's SwiGLU, 26 for its SiLU, 50
-// for its GELU and 23 for its residual.  (A CTA with one whole tile and a piece waits for
-// what the tile's finishing takes beyond the piece: 512 x 5120 x 5120, SiLU 79 / 72 us,
-// SwiGLU 68 / 70.)
+// by the epilogue warps: nothing to do, 8 stages 85 / 95 us; SwiGLU, 8 stages 128 / 101,
+// 40 stages 332 / 345; SiLU, 8 185 / 111, 40 339 / 355; GELU, 40 369 / 361; a bf16
+// residual and a bias, 8 167 / 109, 40 330 / 353: a stage is 1 us, and two warps take 18
+// us for a tile's SwiGLU, 26 for its SiLU, 50 for its GELU and 23 for its residual.
+// A CTA with one whole tile has only a piece to hide the tile's finishing behind, and
+// that takes as long only from about 70 stages on: 512 x 5120 x K, SiLU, 40 stages 75 /
+// 69 us, 64 101 / 100, 80 118 / 121, 136 190 / 194; SwiGLU with a residual, 40 80 / 70,
+// 80 123 / 122, 136 190 / 195; GELU, 136 193 / 200; 512 x 6144 x K turns at 55 stages,
+// 8-bit activations at 60.
 inline bool finish_in_epilogue(const EpiArgs &f, int64_t stages, bool one_tile) {
     int act = 8;
     if (f.act == H32_EPI_SWIGLU) act = 15;
     if (f.act == H32_EPI_SILU) act = 23;
     if (f.act == H32_EPI_GELU_TANH || f.act == H32_EPI_GELU_ERF) act = 48;
     const int need = act + (f.res ? 12 : 0);
-    return stages < need || (one_tile && need > 20);
+    return stages < need || (one_tile && need > 20 && stages < 72);
 }
 
 // The dense schedule: tokens per tile (bn), and how many pieces each tile of

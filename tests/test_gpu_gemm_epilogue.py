@@ -351,3 +351,13 @@ def test_stated_bounds_of_the_activations(h32, act, M):
         v, steps = _formula(zb, act)
         floor = 2.0 ** -121 * (np.maximum(1.0, np.abs(zb[:, 1::2].astype(np.float64))) if act == "swiglu" else 1.0)
         assert np.all(np.abs(np_of(y) - v) <= steps * H * np.abs(v) * (1 + 2.0 ** -10) + floor)
+
+
+@pytest.mark.parametrize("bits,M,N,K,act,res", [
+    (4, 512, 5120, 9088, "silu", False), (4, 512, 5120, 9216, "silu", False),
+    (4, 512, 6144, 9216, "swiglu", True), (8, 512, 5120, 9216, "gelu_erf", False),
+    (8, 512, 5120, 9088, "swiglu", True)])
+def test_one_tile_a_block_and_a_piece(h32, bits, M, N, K, act, res):
+    """One whole tile a block and pieces of the last wave, K on both sides of the length
+    from which the tile is finished while the piece runs."""
+    test_several_tiles_a_block(h32, bits, M, N, K, act, res)
