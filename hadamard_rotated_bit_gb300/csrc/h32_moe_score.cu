@@ -651,14 +651,22 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
     if (a.renorm) {
         // ratios of scores: for the softmax (and for sigmoids so far below 1 that they
         // are exp(l) to fp32) exp(l - the largest chosen logit), which cannot underflow
-        // together
+        // together; else the sigmoids times 2^64, those far below 1 as (exp(l / 2) 2^32)^2,
+        // so that none vanishes before its ratio does
         const bool num = lane < a.k && !isnan(ml);
         const float lc = warp_max(num ? ml : none);
         float x = 0.0f;
         if (num && ml > none) {
-            if (sg && lc > -40.0f) x = score_of(ml, nm, true);
-            else if (lc == INFINITY) x = ml == lc ? 1.0f : 0.0f;
-            else x = expf(__fsub_rn(ml, lc));
+            if (sg && lc > -40.0f) {
+                const bool far = ml <= -40.0f;
+                const float e = expf(far ? 0.5f * ml : -ml);
+                const float r = far ? __fmul_rn(e, 0x1p32f) : __fdiv_rn(1.0f, __fadd_rn(1.0f, e));
+                x = __fmul_rn(r, far ? r : 0x1p64f);
+            } else if (lc == INFINITY) {
+                x = ml == lc ? 1.0f : 0.0f;
+            } else {
+                x = expf(__fsub_rn(ml, lc));
+            }
         }
         if (lc == none && lane < a.k) x = 1.0f;   // every choice masked: equal weights
         float s = 0.0f;

@@ -579,7 +579,8 @@ typedef enum h32_score {
  * offsets and row maps do not depend on fp32 rounding.  The weights are fp32
  * evaluations, relatively within 260 half steps (2^-24) at any E and any spread of the
  * logits: |l - the largest| of them come from the exponential's rounded argument, 37
- * from the softmax's sum, a dozen from all else; below 2^-126 they may vanish.
+ * from the softmax's sum, a dozen from all else; scores and ratios below 2^-126 may
+ * vanish.
  * Deterministic.
  * Logits that are not finite: a -inf logit masks its expert (score 0, key -inf
  * whatever the bias); a NaN logit or bias ranks below it; +inf logits share the

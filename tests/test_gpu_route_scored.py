@@ -357,3 +357,18 @@ def test_biases_near_the_lowest_value(h32, score):
             for x in (l, masked):
                 for tg in (1, G // 2, G - 1):
                     _check(h32, x, min(size, 4), b, score=score, n_group=G, topk_group=tg, group_top=2)
+
+
+def test_ratios_of_sigmoids_far_apart(h32):
+    """Renormalised weights of choices whose sigmoids are far below the others', down to
+    where the weight itself leaves fp32's range: sigmoids that leave it sooner than
+    their ratio to a small largest one, on both sides of where the evaluation turns."""
+    r = np.random.default_rng(3)
+    T, E = 400, 6
+    for top in (60.0, 5.0, 0.0, -20.0, -39.9, -40.1, -70.0, -110.0):
+        l = (top - 100 * r.random((T, E))).astype(np.float32)
+        l[:, 2] = top
+        l[0, 3:] = (-39.99, -40.0, -40.01)
+        for bias in (None, (0.1 * r.standard_normal(E)).astype(np.float32)):
+            _check(h32, l, E, bias, score="sigmoid", scale=2.5)
+            _check(h32, l, 3, bias, score="sigmoid", n_group=3, topk_group=2, group_top=2)
