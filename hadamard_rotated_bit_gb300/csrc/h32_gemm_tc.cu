@@ -999,11 +999,13 @@ __global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ, kEpi == 3>::kTh
     using C = TcCfg<EPQ, XB, kEpi == 2, kWQ, kEpi == 3>;
     constexpr int kStages = C::kStages;
     constexpr bool kSums = kEpi == 1;
-    // the finished output of many whole tiles a CTA (4-bit, a cut tail): the epilogue
-    // keeps its 112 registers, the finishing warps spill but have the time.  512 x 34816 x
-    // 5120, 112 / 104: SwiGLU 322 / 332 us, SiLU 330 / 339, nothing to do 320 / 328 (GELU
-    // 376 / 361; K = 1024, SwiGLU, 105 / 101).  The other instances are 3-4% slower with
-    // 112: 512 x 5120 x 5120 with a residual 70 / 68, 333 x 5120 x 17408 in 8 bits 144 / 138.
+    // the finished output with 4-bit activations, a cut tail and no split: the epilogue
+    // keeps its 112 registers, the finishing warps spill but have the time where a CTA has
+    // several long tiles.  512 x 34816 x 5120, 112 / 104: SwiGLU 317 / 326 us, SiLU 325 /
+    // 333, a residual 316 / 325.  The instance serves every call of that kind, also those
+    // that lose: GELU 372 / 359, K = 1024 with SwiGLU 100 / 97, one tile or less a CTA (64 x
+    // 5120 x 5120) 29.2 / 28.4.  The other instances are 3-4% slower with 112: 512 x 5120 x
+    // 5120 with a residual 70 / 68, 333 x 5120 x 17408 in 8 bits 144 / 138.
     constexpr bool kLong = kEpi == 3 && kTail && !kSplit && XB == 4;
     constexpr int kProdRegs = kLong ? 32 : C::kProdRegs, kEpiRegs = kLong ? 112 : C::kEpiRegs;
     extern __shared__ __align__(1024) uint8_t smem_raw[];

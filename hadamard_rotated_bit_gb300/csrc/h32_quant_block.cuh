@@ -1,6 +1,8 @@
-// One 32-block of activations in registers, shared by the kernels that
-// quantize (the activation quantizers, and the norm that quantizes its output):
-// loading, rotating, rounding to integer codes and packing them (sm_103a).
+// One 32-block of activations in a thread's registers (sm_103a): loading, rotating,
+// rounding to integer codes and packing them, as the activation quantizers do it.  The
+// norm that quantizes its output holds half a block a lane and has its own forms of
+// these steps, with the same bits; it shares the rotate argument, the codes of
+// degenerate blocks and the byte packing.
 #pragma once
 
 #include <stdint.h>

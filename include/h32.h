@@ -575,13 +575,13 @@ typedef enum h32_score {
  * topk_id, topk_w, expert_off, row_idx, row_of (and their alignment).
  * The order of keys is exact: without a bias, where every group stays or groups go
  * by their best key, that of the logits; else that of the keys' (and group scores')
- * values in double precision, equal values (saturated scores) by id.  So ids,
- * offsets and row maps do not depend on fp32 rounding.  The weights are fp32
+ * values as evaluated in double precision, equal values (saturated scores) by id; what
+ * differs by less than double's roundings is in the order of its rounded values.  So
+ * ids, offsets and row maps do not depend on fp32 rounding.  The weights are fp32
  * evaluations, relatively within 260 half steps (2^-24) at any E and any spread of the
  * logits: |l - the largest| of them come from the exponential's rounded argument, 37
  * from the softmax's sum, a dozen from all else; scores and ratios below 2^-126 may
- * vanish.
- * Deterministic.
+ * vanish.  Deterministic.
  * Logits that are not finite: a -inf logit masks its expert (score 0, key -inf
  * whatever the bias); a NaN logit or bias ranks below it; +inf logits share the
  * softmax equally.  Masked experts are chosen only when fewer than k others are
