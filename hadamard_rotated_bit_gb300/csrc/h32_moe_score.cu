@@ -576,55 +576,63 @@ __device__ __forceinline__ int route_token(const ScoreArgs &a, int64_t t) {
     for (int j = 0; j < a.k; ++j) take(j);
     float ml = lane < a.k ? row[my] : 0.0f;
     if constexpr (!kLogit) {
-        // whether key ka (logit la, bias ba) is at least kb for certain: they are the same
-        // key, or further apart than their errors
-        auto apart = [&](float ka, float la, float ba, float kb, float lb, float bb) {
-            float err = err_of(ka) + err_of(kb);
-            if (a.bias && !sg) {
-                // what the softmax's scores share weighs only by their difference, the
-                // rest by its own d
-                const float sa = score_of(la, nm, false), sb = score_of(lb, nm, false);
-                err = fminf(err, u * (40.0f * fabsf(sa - sb) + sa * (3.0f + 1.7f * (nm.lmax - la)) +
-                                      sb * (3.0f + 1.7f * (nm.lmax - lb)) + fabsf(ka) + fabsf(kb)) + tiny);
-            }
-            return (ka == kb && la == lb && ba == bb) || ka - kb > err;
-        };
-        // choice j against the one after it, both finite: above -inf and below +inf as
-        // ordered integers
-        const float mb = (lane < a.k && a.bias) ? a.bias[my] : 0.0f;
-        const uint32_t ou = __shfl_down_sync(0xFFFFFFFFu, my_u, 1);
-        const float ol = __shfl_down_sync(0xFFFFFFFFu, ml, 1);
-        const float ob = __shfl_down_sync(0xFFFFFFFFu, mb, 1);
-        bool tie = false;
-        if (lane < a.k - 1 && ou > 0x007FFFFFu && my_u < 0xFF800000u)
-            tie = !apart(from_ordered(my_u), ml, mb, from_ordered(ou), ol, ob);
-        // The last choice: below it by err_of's bounds, which do not depend on the pair, the
-        // best key left out speaks for all of them.  Else every key left out within the
-        // errors is held against the last choice by itself: one that is apart (its scores
-        // share what they err by, or it is the very same key) says nothing of the others.
-        const uint32_t last_u = __shfl_sync(0xFFFFFFFFu, my_u, a.k - 1);
+        // choice j against the one after it, the last against the best left out; both
+        // finite: above -inf and below +inf as ordered integers
         const uint32_t next_u = __reduce_max_sync(0xFFFFFFFFu, k1);
-        const float last = from_ordered(last_u), next = from_ordered(next_u);
-        if (next_u > 0x007FFFFFu && last_u < 0xFF800000u && !(last - next > err_of(last) + err_of(next))) {
-            const float cut = last - 4.0f * err_of(last);
-            const int last_id = __shfl_sync(0xFFFFFFFFu, my, a.k - 1);
-            const float last_l = __shfl_sync(0xFFFFFFFFu, ml, a.k - 1);
-            const float last_b = __shfl_sync(0xFFFFFFFFu, mb, a.k - 1);
-            uint32_t cand = 0u;   // the lane's keys left out that are not below `cut`
-#pragma unroll
-            for (int i = 0; i < NPER; ++i)
-                if (alive && key[i] > 0x007FFFFFu && !(from_ordered(key[i]) < cut) &&
-                    (key[i] < last_u || (key[i] == last_u && e0 + i > last_id)))
-                    cand |= 1u << i;
-            while (cand) {
-                const int at = __ffs(cand) - 1;
-                cand &= cand - 1u;
-                uint32_t v = 0u;
+        uint32_t ou = __shfl_down_sync(0xFFFFFFFFu, my_u, 1);
+        if (lane == a.k - 1) ou = next_u;
+        bool unclear = false;
+        if (lane < a.k && ou > 0x007FFFFFu && my_u < 0xFF800000u) {
+            const float ka = from_ordered(my_u), kb = from_ordered(ou);
+            unclear = !(ka - kb > err_of(ka) + err_of(kb));
+        }
+        const uint32_t unclears = __ballot_sync(0xFFFFFFFFu, unclear);
+        bool tie = false;
+        if (unclears) {
+            // whether key ka (logit la, bias ba) is at least kb for certain: they are the
+            // same key, or further apart than their errors
+            auto apart = [&](float ka, float la, float ba, float kb, float lb, float bb) {
+                float err = err_of(ka) + err_of(kb);
+                if (a.bias && !sg) {
+                    // what the softmax's scores share weighs only by their difference, the
+                    // rest by its own d
+                    const float sa = score_of(la, nm, false), sb = score_of(lb, nm, false);
+                    err = fminf(err, u * (40.0f * fabsf(sa - sb) + sa * (3.0f + 1.7f * (nm.lmax - la)) +
+                                          sb * (3.0f + 1.7f * (nm.lmax - lb)) + fabsf(ka) + fabsf(kb)) + tiny);
+                }
+                return (ka == kb && la == lb && ba == bb) || ka - kb > err;
+            };
+            const float mb = (lane < a.k && a.bias) ? a.bias[my] : 0.0f;
+            const float ol = __shfl_down_sync(0xFFFFFFFFu, ml, 1);
+            const float ob = __shfl_down_sync(0xFFFFFFFFu, mb, 1);
+            if (unclear && lane < a.k - 1) tie = !apart(from_ordered(my_u), ml, mb, from_ordered(ou), ol, ob);
+            // The last choice: below it by err_of's bounds, which do not depend on the pair,
+            // the best key left out speaks for all of them.  Else every key left out within
+            // the errors is held against the last choice by itself: one that is apart (its
+            // scores share what they err by, or it is the very same key) says nothing of the
+            // others.
+            if ((unclears >> (a.k - 1)) & 1u) {
+                const uint32_t last_u = __shfl_sync(0xFFFFFFFFu, my_u, a.k - 1);
+                const float last = from_ordered(last_u), cut = last - 4.0f * err_of(last);
+                const int last_id = __shfl_sync(0xFFFFFFFFu, my, a.k - 1);
+                const float last_l = __shfl_sync(0xFFFFFFFFu, ml, a.k - 1);
+                const float last_b = __shfl_sync(0xFFFFFFFFu, mb, a.k - 1);
+                uint32_t cand = 0u;   // the lane's keys left out that are not below `cut`
 #pragma unroll
                 for (int i = 0; i < NPER; ++i)
-                    if (i == at) v = key[i];
-                tie |= !apart(last, last_l, last_b, from_ordered(v), row[e0 + at],
-                              a.bias ? a.bias[e0 + at] : 0.0f);
+                    if (alive && key[i] > 0x007FFFFFu && !(from_ordered(key[i]) < cut) &&
+                        (key[i] < last_u || (key[i] == last_u && e0 + i > last_id)))
+                        cand |= 1u << i;
+                while (cand) {
+                    const int at = __ffs(cand) - 1;
+                    cand &= cand - 1u;
+                    uint32_t v = 0u;
+#pragma unroll
+                    for (int i = 0; i < NPER; ++i)
+                        if (i == at) v = key[i];
+                    tie |= !apart(last, last_l, last_b, from_ordered(v), row[e0 + at],
+                                  a.bias ? a.bias[e0 + at] : 0.0f);
+                }
             }
         }
         if (__any_sync(0xFFFFFFFFu, near)) {
