@@ -33,6 +33,8 @@ __all__ = [
     "q4_0_x_q4_gemm_tc_noalloc", "q4_0_x_q8_gemm_tc_noalloc",
     "h32_add_rms_norm_quantize", "h32_moe_route_scored",
     "h32_moe_route_scored_workspace_bytes", "q4_0_x_q4_gemm_tc_epilogue", "q4_0_x_q8_gemm_tc_epilogue",
+    "h32_quantize_act_f8", "h32_quantize_weights_f8", "h32_f8_gemm", "h32_f8_gemm_experts",
+    "h32_token_logprobs",
 ]
 
 
@@ -105,6 +107,12 @@ _SIGS = {
     "h32_add_rms_norm_quantize": (_INT, [_P, _INT, _I64, _P, _INT, _I64, _P, _INT, ctypes.c_float,
                                          _I64, _I64, _P, _I64, _P, _INT, _I64, _I32, _INT, _P, _P,
                                          _I64, _P]),
+    "h32_quantize_act_f8": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _INT, _P]),
+    "h32_quantize_weights_f8": (_INT, [_P, _INT, _I64, _I64, _I64, _INT, _P, _P, _P]),
+    "h32_f8_gemm": (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _INT, _I64, _P]),
+    "h32_f8_gemm_experts": (_INT, [_P, _P, _I32, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _INT,
+                                   _I64, _P]),
+    "h32_token_logprobs": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I32, _I32, _P, _P, _P, _P, _P]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGS)
 
@@ -1180,6 +1188,198 @@ def h32_add_rms_norm_quantize(x, weight, residual=None, eps=1e-6, form="q4_tc", 
 
 
 # --------------------------------------------------------------------------
+# 8-bit floating-point products with a scale for each block of 128, and the log
+# probabilities behind the output head
+# --------------------------------------------------------------------------
+def _blocks128(n) -> int:
+    return (int(n) + 127) // 128
+
+
+def h32_quantize_act_f8(x, rotate=False, row_idx=None, xq=None, xd=None, stream=None):
+    """x [T][K] bf16/fp32 -> (xq [R][K] uint8 e4m3 codes, xd [ceil(K/128)][ldxd] fp32):
+    one scale amax / 448 for each 128 values of a row, group-major.
+
+    row_idx [R] int32: output row r is x[row_idx[r]] (the grouped order of an expert
+    product); None: R = T.  rotate as for the other quantizers, here off by default
+    (weights quantized elsewhere are not rotated)."""
+    torch = _torch()
+    f32 = (torch.float32,)
+    _need(x, "x", (torch.bfloat16, torch.float32), (_ge(0), _ge(0)), pitched=True)
+    T, K = x.shape
+    R = T
+    if row_idx is not None:
+        _need(row_idx, "row_idx", (torch.int32,), (_ge(0),))
+        R = row_idx.shape[0]
+    if xq is not None:
+        _need(xq, "xq", (torch.uint8,), (_ge(R), K))
+    if xd is not None:
+        _need(xd, "xd", f32, (_ge(_blocks128(K)), _ge(R)))
+    _same_gpu(("x", x), ("row_idx", row_idx), ("xq", xq), ("xd", xd))
+    dev = x.device
+    raw, guard = _enter_stream(dev, stream)
+    try:
+        if xq is None:
+            xq = torch.empty((R, K), dtype=torch.uint8, device=dev)
+        if xd is None:
+            xd = torch.empty((_blocks128(K), (R + 3) // 4 * 4), dtype=torch.float32, device=dev)
+        st = lib().h32_quantize_act_f8(x.data_ptr(), x.dtype == torch.bfloat16, T, K, _pitch(x),
+                                       _raw(row_idx), R, xq.data_ptr(), xd.data_ptr(), xd.shape[1],
+                                       _rot_arg(rotate), raw)
+    finally:
+        if guard is not None:
+            guard.__exit__(None, None, None)
+    if st:
+        _check("h32_quantize_act_f8", st)
+    return xq, xd
+
+
+def h32_quantize_weights_f8(w, rotate=False, wq=None, wd=None, stream=None):
+    """w [N][K] bf16/fp32 -> (wq [N][K] uint8 e4m3 codes, wd [ceil(N/128)][ceil(K/128)] fp32):
+    one scale amax / 448 for each block of 128 x 128."""
+    torch = _torch()
+    _need(w, "w", (torch.bfloat16, torch.float32), (_ge(0), _ge(0)), pitched=True)
+    N, K = w.shape
+    if wq is not None:
+        _need(wq, "wq", (torch.uint8,), (_ge(N), K))
+    if wd is not None:
+        _need(wd, "wd", (torch.float32,), (_ge(_blocks128(N)), _blocks128(K)))
+    _same_gpu(("w", w), ("wq", wq), ("wd", wd))
+    dev = w.device
+    raw, guard = _enter_stream(dev, stream)
+    try:
+        if wq is None:
+            wq = torch.empty((N, K), dtype=torch.uint8, device=dev)
+        if wd is None:
+            wd = torch.empty((_blocks128(N), _blocks128(K)), dtype=torch.float32, device=dev)
+        st = lib().h32_quantize_weights_f8(w.data_ptr(), w.dtype == torch.bfloat16, N, K, _pitch(w),
+                                           _rot_arg(rotate), wq.data_ptr(), wd.data_ptr(), raw)
+    finally:
+        if guard is not None:
+            guard.__exit__(None, None, None)
+    if st:
+        _check("h32_quantize_weights_f8", st)
+    return wq, wd
+
+
+def h32_f8_gemm(wq, wd, xq, xd, M=None, y=None, y_dtype=None, stream=None):
+    """y [M][N] = the product of e4m3 codes wq [N][K] and xq [M][K] with their scales
+    wd [ceil(N/128)][ceil(K/128)] and xd [ceil(K/128)][ldxd]; y bf16/fp32, by default
+    allocated as y_dtype (fp32).  Any number of tokens from one on."""
+    return _f8_gemm("h32_f8_gemm", wq, wd, xq, xd, None, None, M, y, y_dtype, stream)
+
+
+def h32_f8_gemm_experts(wq, wd, xq, xd, expert_off, N, R=None, y=None, y_dtype=None, stream=None):
+    """The expert-batched product: wq [E*N][K], wd [E*ceil(N/128)][ceil(K/128)] (the experts'
+    planes stacked), xq / xd in grouped order, expert_off [E+1] int32 -> y [R][N]."""
+    return _f8_gemm("h32_f8_gemm_experts", wq, wd, xq, xd, expert_off, N, R, y, y_dtype, stream)
+
+
+def _f8_gemm(fn, wq, wd, xq, xd, off, N, M, y, y_dtype, stream):
+    torch = _torch()
+    bf16, f32, u8 = torch.bfloat16, torch.float32, (torch.uint8,)
+    _need(wq, "wq", u8, (_ge(0), _ge(0)))
+    rows, K = wq.shape
+    _need(xq, "xq", u8, (_ge(0 if M is None else M), K))
+    if M is None:
+        M = xq.shape[0]
+    E = 1
+    if off is None:
+        N = rows
+    else:
+        N = int(N)
+        if N <= 0 or rows % N != 0:
+            raise ValueError("wq must have E * N rows")
+        E = rows // N
+        _need(off, "expert_off", (torch.int32,), (_ge(E + 1),))
+    _need(wd, "wd", (f32,), (E * _blocks128(N), _blocks128(K)))
+    _need(xd, "xd", (f32,), (_ge(_blocks128(K)), _ge(M)))
+    if y is not None:
+        _need(y, "y", (bf16, f32), (_ge(M), _ge(N)), pitched=True)
+        if y_dtype is not None and y_dtype != y.dtype:
+            raise ValueError(f"y is {y.dtype}, y_dtype {y_dtype}")
+    elif y_dtype is not None and y_dtype not in (bf16, f32):
+        raise ValueError("y_dtype must be bf16 or fp32")
+    _same_gpu(("wq", wq), ("wd", wd), ("xq", xq), ("xd", xd), ("expert_off", off), ("y", y))
+    dev = wq.device
+    raw, guard = _enter_stream(dev, stream)
+    try:
+        if y is None:
+            y = torch.empty((M, N), dtype=y_dtype or f32, device=dev)
+        if off is None:
+            st = lib().h32_f8_gemm(wq.data_ptr(), wd.data_ptr(), xq.data_ptr(), xd.data_ptr(),
+                                   xd.shape[1], M, N, K, y.data_ptr(), y.dtype == bf16, _pitch(y), raw)
+        else:
+            st = lib().h32_f8_gemm_experts(
+                wq.data_ptr(), wd.data_ptr(), E, xq.data_ptr(), xd.data_ptr(), xd.shape[1],
+                off.data_ptr(), M, N, K, y.data_ptr(), y.dtype == bf16, _pitch(y), raw)
+    finally:
+        if guard is not None:
+            guard.__exit__(None, None, None)
+    if st:
+        _check(fn, st)
+    return y
+
+
+LOGPROBS_MAX_TOP = 32
+
+
+def h32_token_logprobs(logits, targets=None, top=0, logprob=None, entropy=None, top_id=None,
+                       top_logprob=None, stream=None):
+    """Log probabilities of given tokens, entropy and the most probable tokens of each row.
+
+    logits [T][V] bf16/fp32 (rows of any pitch), targets int32 [T] or [T][n] or None
+    (negative: no token given, its result 0; V or more: NaN) -> (logprob, shaped as
+    targets, or None; entropy [T] fp32; top_id [T][top] int32 and top_logprob [T][top]
+    fp32, by decreasing logit, ties to the lower id, or None with top = 0)."""
+    torch = _torch()
+    i32, f32 = (torch.int32,), (torch.float32,)
+    _need(logits, "logits", (torch.bfloat16, torch.float32), (_ge(0), _ge(1)), pitched=True)
+    T, V = logits.shape
+    top = int(top)
+    if not 0 <= top <= min(LOGPROBS_MAX_TOP, V):
+        raise ValueError(f"top must be between 0 and {min(LOGPROBS_MAX_TOP, V)}")
+    n = 0
+    if targets is not None:
+        _need(targets, "targets", i32, (T,) if targets.dim() == 1 else (T, _ge(0)))
+        n = 1 if targets.dim() == 1 else targets.shape[1]
+        if logprob is not None:
+            _need(logprob, "logprob", f32, tuple(targets.shape))
+    elif logprob is not None:
+        raise ValueError("logprob needs targets")
+    if entropy is not None:
+        _need(entropy, "entropy", f32, (_ge(T),))
+    if top == 0 and (top_id is not None or top_logprob is not None):
+        raise ValueError("top_id and top_logprob need top")
+    if top_id is not None:
+        _need(top_id, "top_id", i32, (_ge(T), top))
+    if top_logprob is not None:
+        _need(top_logprob, "top_logprob", f32, (_ge(T), top))
+    _same_gpu(("logits", logits), ("targets", targets), ("logprob", logprob), ("entropy", entropy),
+              ("top_id", top_id), ("top_logprob", top_logprob))
+    dev = logits.device
+    raw, guard = _enter_stream(dev, stream)
+    try:
+        if targets is not None and logprob is None:
+            logprob = torch.empty(targets.shape, dtype=torch.float32, device=dev)
+        if entropy is None:
+            entropy = torch.empty(T, dtype=torch.float32, device=dev)
+        if top > 0:
+            if top_id is None:
+                top_id = torch.empty((T, top), dtype=torch.int32, device=dev)
+            if top_logprob is None:
+                top_logprob = torch.empty((T, top), dtype=torch.float32, device=dev)
+        st = lib().h32_token_logprobs(
+            logits.data_ptr(), logits.dtype == torch.bfloat16, T, V, _pitch(logits), _raw(targets), n, top,
+            _raw(logprob), entropy.data_ptr(), _raw(top_id), _raw(top_logprob), raw)
+    finally:
+        if guard is not None:
+            guard.__exit__(None, None, None)
+    if st:
+        _check("h32_token_logprobs", st)
+    return logprob, entropy, top_id, top_logprob
+
+
+# --------------------------------------------------------------------------
 # optional per-call tracing (H32_TRACE=1: device time per call; H32_TRACE=hash:
 # also a hash of every output), off by default; see trace.py
 # --------------------------------------------------------------------------
@@ -1196,6 +1396,8 @@ _COMPUTE_CALLS = (
     "h32_q4_0_blocks_to_planes", "h32_q4_0_planes_to_blocks",
     "q4_0_x_q4_gemm_tc_noalloc", "q4_0_x_q8_gemm_tc_noalloc", "h32_add_rms_norm_quantize",
     "h32_moe_route_scored", "q4_0_x_q4_gemm_tc_epilogue", "q4_0_x_q8_gemm_tc_epilogue",
+    "h32_quantize_act_f8", "h32_quantize_weights_f8", "h32_f8_gemm", "h32_f8_gemm_experts",
+    "h32_token_logprobs",
 )
 for _name in _COMPUTE_CALLS:
     globals()[_name] = _trace.traced(_name)(globals()[_name])

@@ -6,10 +6,13 @@
 
 namespace h32 {
 // the status words of the router and combine kernels (h32_moe.cu), of the norm
-// (h32_norm.cu) and of the few-token product (h32_few.cu)
+// (h32_norm.cu), of the few-token product (h32_few.cu) and of the 8-bit products and
+// their quantizers (h32_f8_gemm.cu, h32_f8_quant.cu)
 h32_status moe_read_and_clear_status(cudaStream_t s);
 h32_status norm_read_and_clear_status(cudaStream_t s);
 h32_status few_read_and_clear_status(cudaStream_t s);
+h32_status f8_read_and_clear_status(cudaStream_t s);
+h32_status f8q_read_and_clear_status(cudaStream_t s);
 
 namespace {
 
@@ -75,12 +78,14 @@ extern "C" h32_status h32_device_status(void *stream) {
     // one caller at a time: each status word is taken through one device word
     static std::mutex mu;
     std::lock_guard<std::mutex> lock(mu);
-    const h32_status st[6] = {h32::quant_read_and_clear_status(s),
+    const h32_status st[8] = {h32::quant_read_and_clear_status(s),
                               h32::gemm_read_and_clear_status(s),
                               h32::tc_read_and_clear_status(s),
                               h32::moe_read_and_clear_status(s),
                               h32::norm_read_and_clear_status(s),
-                              h32::few_read_and_clear_status(s)};
+                              h32::few_read_and_clear_status(s),
+                              h32::f8_read_and_clear_status(s),
+                              h32::f8q_read_and_clear_status(s)};
     for (h32_status v : st)
         if (v == H32_ERR_CUDA) return H32_ERR_CUDA;
     for (h32_status v : st)

@@ -1,0 +1,436 @@
+// Products of e4m3 codes with a scale for each block of 128 (sm_103a):
+//   y[m][n] = sum over b of fl(dx[b][m] dw[n / 128][b]) S_b,
+//   S_b = the sum over block b's 128 codes of xq[m][k] wq[n][k], in fp32 by the tensor core,
+// folded in block order by one fp32 fma each, and rounded once to y's type.
+//
+// One block is one 128-byte K step: four tcgen05.mma (kind::f8f6f4, K = 32) give S for a
+// tile in TMEM, the epilogue warps read it back and fold it into registers while the
+// tensor core does the next one.
+//
+// rows_kernel: weight rows on the TMEM lanes, NC tokens as its columns.
+//   A tile is 128 weight rows (one block of scales: d_w is uniform) x NC tokens.
+//   warps 0..3  epilogue, a lane quarter each
+//   warp 4      TMA producer: per K step the rows' and the tokens' codes and the tokens' scales
+//   warp 5      TMEM allocator and MMA issuer
+// Every wait is bounded.
+#include "h32_f8.cuh"
+
+#include "h32_epilogue.cuh"
+
+namespace h32 {
+namespace {
+
+__device__ uint32_t g_f8_status;   // kStatusTimeout, kStatusGuard
+
+constexpr int kMaxStages = 12;
+constexpr int kRowsWarps = 6;
+constexpr int kMaxSmem = 225 * 1024;
+constexpr uint64_t kDrainPolls = 1ull << 22;
+
+struct F8Args {
+    int32_t M, N, K;         // token rows, weight rows (of an expert), reduction length
+    int32_t E;               // experts; 1 and off null: all rows
+    int32_t stages;
+    const int32_t *off;      // [E + 1] or null
+    const float *wd;         // [E][ceil(N / 128)][ceil(K / 128)]
+    void *y;
+    int64_t ldy;
+    int32_t y_bf16;
+    uint64_t wait_limit;
+};
+
+// The groups of token rows: their offsets and the first tile of each, tiles numbered
+// group-major, then by weight tile, then by chunk of tokens.  A group's chunks start at
+// its first row rounded down to a multiple of 4 (the scales' copies start on 16 bytes);
+// the rows of a chunk outside the group are computed and not stored.
+struct Groups {
+    int *off, *first;   // [E + 1] each
+    static __host__ __device__ size_t bytes(int E) { return (2 * size_t(E + 1) * 4 + 1023) / 1024 * 1024; }
+    __device__ int chunks(int e, int cols) const {
+        const int lo = off[e], hi = off[e + 1];
+        return hi > lo ? (hi - (lo & ~3) + cols - 1) / cols : 0;
+    }
+};
+
+struct Tile {
+    int e, n0, g0, clo, chi;   // expert, first weight row in it, first token row, its columns in use
+};
+
+__device__ __forceinline__ Tile tile_of(int t, const Groups &g, int E, int cols, int rows) {
+    int lo = 0, hi = E;   // the last group whose first tile is <= t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (g.first[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    Tile r;
+    r.e = lo;
+    const int local = t - g.first[lo], chunks = g.chunks(lo, cols), wt = local / chunks;
+    r.n0 = wt * rows;
+    r.g0 = (g.off[lo] & ~3) + (local - wt * chunks) * cols;
+    r.clo = max(0, g.off[lo] - r.g0);
+    r.chi = min(cols, g.off[lo + 1] - r.g0);
+    return r;
+}
+
+// Reads and checks the offsets (0 = off[0] <= ... <= off[E] = M) and numbers the tiles.
+// Every thread of the CTA calls it; returns the number of tiles, -1 where the offsets
+// are none.
+__device__ int load_groups(const Groups &g, const F8Args &a, int cols, int weight_tiles, int *s_word) {
+    const int tid = threadIdx.x, E = a.E;
+    if (tid == 0) *s_word = 0;
+    for (int i = tid; i <= E; i += blockDim.x) g.off[i] = a.off ? a.off[i] : i * a.M;
+    __syncthreads();
+    for (int i = tid; i <= E; i += blockDim.x) {
+        const int v = g.off[i];
+        if ((i == 0 && v != 0) || (i == E && v != a.M) || (i < E && g.off[i + 1] < v)) *s_word = 1;
+    }
+    __syncthreads();
+    const bool bad = *s_word != 0;
+    if (tid < 32 && !bad) {
+        const int per = (E + 31) / 32, e0 = tid * per;
+        int sum = 0;
+        for (int i = e0; i < min(e0 + per, E); ++i) sum += weight_tiles * g.chunks(i, cols);
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (tid >= o) incl += v;
+        }
+        int run = incl - sum;
+        for (int i = e0; i < min(e0 + per, E); ++i) {
+            g.first[i] = run;
+            run += weight_tiles * g.chunks(i, cols);
+        }
+        if (tid == 31) g.first[E] = incl;
+    }
+    __syncthreads();
+    return bad ? -1 : g.first[E];
+}
+
+__device__ __forceinline__ void store_y(const F8Args &a, int64_t m, int n, float v) {
+    if (a.y_bf16) static_cast<__nv_bfloat16 *>(a.y)[m * a.ldy + n] = __float2bfloat16_rn(v);
+    else static_cast<float *>(a.y)[m * a.ldy + n] = v;
+}
+
+// ----------------------------------------------------------------------------
+// weight rows on the lanes
+// ----------------------------------------------------------------------------
+template <int NC>
+struct Rows {
+    static constexpr int kBufs = NC <= 32 ? 4 : 2;            // sums in TMEM
+    static constexpr uint32_t kTmem = kBufs * NC < 32 ? 32 : kBufs * NC;
+    static constexpr uint32_t kA = 128 * 128, kB = NC * 128;  // bytes of a stage's parts
+    static constexpr uint32_t kS = NC * 4 < 128 ? 128 : NC * 4;
+    static constexpr uint32_t kStage = kA + kB + kS;
+};
+
+template <int NC>
+__global__ void __launch_bounds__(kRowsWarps * 32, 1)
+    rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                const __grid_constant__ CUtensorMap map_s, const F8Args a) {
+    using C = Rows<NC>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_sum[C::kBufs], s_free[C::kBufs], s_drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_word;
+    __shared__ volatile int s_abort;
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int S = a.stages;
+    uint8_t *s_a = smem, *s_b = s_a + S * C::kA, *s_s = s_b + S * C::kB;
+    int *s_table = reinterpret_cast<int *>(s_s + S * C::kS);
+    const Groups g{s_table, s_table + a.E + 1};
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int nb = (a.K + 127) / 128, nt = (a.N + 127) / 128;
+    const uint64_t lim = a.wait_limit;
+    volatile int *abort = &s_abort;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], 4);
+        }
+        for (int i = 0; i < C::kBufs; ++i) {
+            mbar_init(&s_sum[i], 1);
+            mbar_init(&s_free[i], 4);
+        }
+        mbar_init(&s_drain, 1);
+        s_abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 5) {
+        tmem_alloc(&s_tmem, C::kTmem);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_trigger();
+    tc_fence_before();
+    int total = load_groups(g, a, NC, nt, &s_word);
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    if (total < 0) {
+        if (threadIdx.x == 0) atomicOr(&g_f8_status, kStatusGuard);
+        total = 0;
+    }
+    auto give_up = [&]() {
+        s_abort = 1;
+        atomicOr(&g_f8_status, kStatusTimeout);
+    };
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ TMA
+        const bool leader = elect_one();
+        if (leader) {
+            prefetch_tmap(&map_w);
+            prefetch_tmap(&map_x);
+            prefetch_tmap(&map_s);
+        }
+        int s = 0, fed = 0;
+        uint32_t ph = 1;   // (the first round's waits pass at once)
+        bool ok = true;
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            const Tile ti = tile_of(t, g, a.E, NC, 128);
+            for (int kb = 0; kb < nb; ++kb) {
+                if (!warp_wait_or_look(&s_empty[s], ph, lim, abort)) {
+                    ok = false;
+                    break;
+                }
+                if (leader) {
+                    mbar_arrive_expect_tx(&s_full[s], C::kA + C::kB + NC * 4);
+                    tma_load_2d(s_a + s * C::kA, &map_w, &s_full[s], kb * 128, ti.e * a.N + ti.n0);
+                    tma_load_2d(s_b + s * C::kB, &map_x, &s_full[s], kb * 128, ti.g0);
+                    tma_load_2d(s_s + s * C::kS, &map_s, &s_full[s], ti.g0, kb);
+                }
+                __syncwarp();
+                if (fed < S) ++fed;
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        if (leader) {
+            if (!ok) give_up();
+            // leave only when the copies under way have landed (at once unless a wait
+            // gave up): each fed stage's last phase
+            for (int i = 0; i < fed; ++i) {
+                if (--s < 0) {
+                    s = S - 1;
+                    ph ^= 1;
+                }
+                mbar_wait_bounded(&s_full[s], ph ^ 1, kDrainPolls, nullptr);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        // ------------------------------------------------------------ MMA
+        const bool leader = elect_one();
+        const uint32_t idesc = idesc_e4m3_f32(128, NC);
+        const uint64_t da0 = smem_desc_sw128(smem_u32(s_a)), db0 = smem_desc_sw128(smem_u32(s_b));
+        int s = 0, buf = 0;
+        uint32_t ph = 0, bph = 1;
+        bool ok = true;
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int kb = 0; kb < nb; ++kb) {
+                if (!warp_wait_or_look(&s_full[s], ph, lim, abort) ||
+                    !warp_wait_or_look(&s_free[buf], bph, lim, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (leader) {
+                    // (columns behind K are zeros in both operands)
+                    const uint64_t da = da0 + s * (C::kA >> 4), db = db0 + s * (C::kB >> 4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_f8f6f4(tmem + buf * NC, da + 2 * j, db + 2 * j, idesc, j > 0);
+                    mma_commit(&s_sum[buf]);
+                }
+                __syncwarp();
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
+                }
+                if (++buf == C::kBufs) {
+                    buf = 0;
+                    bph ^= 1;
+                }
+            }
+        }
+        if (leader) {
+            if (!ok) give_up();
+            mma_commit(&s_drain);
+            mbar_wait_bounded(&s_drain, 0, kDrainPolls, nullptr);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------- epilogue
+        const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
+        int s = 0, buf = 0;
+        uint32_t ph = 0, bph = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            const Tile ti = tile_of(t, g, a.E, NC, 128);
+            uint64_t acc[NC / 2];
+#pragma unroll
+            for (int i = 0; i < NC / 2; ++i) acc[i] = 0ull;
+            // the tile's weight scales, a lane's share of 32 blocks ahead
+            const float *wd = a.wd + (int64_t(ti.e) * nt + ti.n0 / 128) * nb;
+            float dw_next = lane < nb ? __ldg(wd + lane) : 0.0f, dw_lane = 0.0f;
+            for (int kb = 0; kb < nb; ++kb) {
+                if ((kb & 31) == 0) {
+                    dw_lane = dw_next;
+                    dw_next = kb + 32 + lane < nb ? __ldg(wd + kb + 32 + lane) : 0.0f;
+                }
+                const float dw = __shfl_sync(0xFFFFFFFFu, dw_lane, kb & 31);
+                // (the stage's scales; its codes' sums follow)
+                if (!warp_wait_or_look(&s_full[s], ph, lim, abort) ||
+                    !warp_wait_or_look(&s_sum[buf], bph, lim, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float *dx = reinterpret_cast<const float *>(s_s + s * C::kS);
+                const uint32_t col = tmem + lane_addr + buf * NC;
+                if constexpr (NC == 16) {
+                    uint32_t v[16];
+                    tmem_ld_x16(col, v);
+                    tmem_ld_wait();
+                    fold16(acc, dw, dx, v);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < NC; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld_x32(col + c, v);
+                        tmem_ld_wait();
+                        fold16(acc + c / 2, dw, dx + c, reinterpret_cast<const uint32_t(&)[16]>(v[0]));
+                        fold16(acc + c / 2 + 8, dw, dx + c + 16, reinterpret_cast<const uint32_t(&)[16]>(v[16]));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&s_free[buf]);
+                    mbar_arrive(&s_empty[s]);
+                }
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
+                }
+                if (++buf == C::kBufs) {
+                    buf = 0;
+                    bph ^= 1;
+                }
+            }
+            if (!ok) break;
+            const int n = ti.n0 + warp * 32 + lane;
+            if (n < a.N) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const uint32_t bits = static_cast<uint32_t>(c & 1 ? acc[c / 2] >> 32 : acc[c / 2]);
+                    if (c >= ti.clo && c < ti.chi) store_y(a, ti.g0 + c, n, __uint_as_float(bits));
+                }
+            }
+        }
+        if (!ok && lane == 0) give_up();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmem);
+    }
+}
+
+template <int NC>
+h32_status launch_rows(const uint8_t *wq, const uint8_t *xq, const float *xd, int64_t ldxd, F8Args a, int64_t tiles,
+                       int sms, cudaStream_t s) {
+    using C = Rows<NC>;
+    const size_t table = Groups::bytes(a.E) + 1024;
+    const int fit = static_cast<int>((kMaxSmem - table) / C::kStage);
+    a.stages = fit < kMaxStages ? fit : kMaxStages;
+    CUtensorMap maps[3];
+    if (!code_map(&maps[0], wq, a.K, int64_t(a.E) * a.N, 128) || !code_map(&maps[1], xq, a.K, a.M, NC) ||
+        !scale_map(&maps[2], xd, ldxd, (a.K + 127) / 128, NC)) {
+        note_error("cuTensorMapEncodeTiled rejected a tensor map of the 8-bit product");
+        return H32_ERR_CUDA;
+    }
+    const int grid = static_cast<int>(tiles < sms ? tiles : sms);
+    cudaError_t e = cudaFuncSetAttribute(rows_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess)
+        e = launch_pdl(rows_kernel<NC>, dim3(grid), dim3(kRowsWarps * 32), a.stages * C::kStage + table, s, maps[0],
+                       maps[1], maps[2], a);
+    return launch_status(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint8_t *xq, const float *xd,
+                       int64_t ldxd, const int32_t *off, int64_t M, int64_t N, int64_t K, void *y,
+                       h32_in_dtype y_dt, int64_t ldy, void *stream) {
+    if (M < 0 || N <= 0 || K <= 0 || K % 32 != 0 || E < 1 || E > kMaxExperts || ldxd < M || ldxd % 4 != 0 ||
+        ldy < N || (y_dt != H32_IN_F32 && y_dt != H32_IN_BF16))
+        return H32_ERR_INVALID_ARG;
+    if (M == 0) return H32_OK;
+    if (!wq || !wd || !xq || !xd || !y) return H32_ERR_INVALID_ARG;
+    if (!aligned16(wq) || !aligned16(wd) || !aligned16(xq) || !aligned16(xd) || !aligned16(y) ||
+        (off && reinterpret_cast<uintptr_t>(off) % 4 != 0))
+        return H32_ERR_ALIGNMENT;
+    // the kernels number rows and tiles in int (a group starts up to 3 rows early: at most
+    // two chunks more than its rows fill)
+    const int64_t nt = (N + 127) / 128, tiles = nt * (M / 16 + 2 * int64_t(E));
+    if (M > 0x7FFFFFFFll - 256 || K > 0x7FFFFFFFll - 256 || int64_t(E) * N > 0x7FFFFFFFll - 256 ||
+        ldxd > 0xFFFFFFFFll || tiles > 0x7FFFFFFFll)
+        return H32_ERR_INVALID_ARG;
+    int sms = 0;
+    H32_TRY(check_device(&sms));
+    if (!encoder()) {
+        note_error("cuTensorMapEncodeTiled is not available from the driver");
+        return H32_ERR_CUDA;
+    }
+    F8Args a{};
+    a.M = static_cast<int32_t>(M);
+    a.N = static_cast<int32_t>(N);
+    a.K = static_cast<int32_t>(K);
+    a.E = E;
+    a.off = off;
+    a.wd = wd;
+    a.y = y;
+    a.ldy = ldy;
+    a.y_bf16 = y_dt == H32_IN_BF16;
+    a.wait_limit = wait_limit();
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // columns for the tokens of one group, as far as the host knows them
+    const int64_t per = (M + E - 1) / E;
+    if (per <= 16) return launch_rows<16>(wq, xq, xd, ldxd, a, nt * (off ? E : (M + 15) / 16), sms, s);
+    if (per <= 32) return launch_rows<32>(wq, xq, xd, ldxd, a, nt * (off ? E : (M + 31) / 32), sms, s);
+    if (per <= 64) return launch_rows<64>(wq, xq, xd, ldxd, a, nt * (off ? E : (M + 63) / 64), sms, s);
+    return launch_rows<128>(wq, xq, xd, ldxd, a, nt * (off ? E : (M + 127) / 128), sms, s);
+}
+
+}  // namespace
+
+__device__ uint32_t g_f8_status_taken;
+__global__ void take_g_f8_status() { g_f8_status_taken = atomicExch(&g_f8_status, 0u); }
+
+h32_status f8_read_and_clear_status(cudaStream_t s) {
+    bool ok = false;
+    const uint32_t v = take_status(take_g_f8_status, g_f8_status_taken, s, &ok);
+    if (!ok) return H32_ERR_CUDA;
+    if (v & kStatusTimeout) return H32_ERR_TIMEOUT;
+    return (v & kStatusGuard) ? H32_ERR_DEVICE_GUARD : H32_OK;
+}
+
+}  // namespace h32
+
+extern "C" h32_status h32_f8_gemm(const uint8_t *wq, const float *wd, const uint8_t *xq, const float *xd,
+                                  int64_t ldxd, int64_t M, int64_t N, int64_t K, void *y, h32_in_dtype y_dt,
+                                  int64_t ldy, void *stream) {
+    return h32::run_f8_gemm(wq, wd, 1, xq, xd, ldxd, nullptr, M, N, K, y, y_dt, ldy, stream);
+}
+
+extern "C" h32_status h32_f8_gemm_experts(const uint8_t *wq, const float *wd, int32_t E, const uint8_t *xq,
+                                          const float *xd, int64_t ldxd, const int32_t *expert_off, int64_t R,
+                                          int64_t N, int64_t K, void *y, h32_in_dtype y_dt, int64_t ldy,
+                                          void *stream) {
+    if (!expert_off) return H32_ERR_INVALID_ARG;
+    return h32::run_f8_gemm(wq, wd, E, xq, xd, ldxd, expert_off, R, N, K, y, y_dt, ldy, stream);
+}

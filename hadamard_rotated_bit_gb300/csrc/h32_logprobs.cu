@@ -1,0 +1,432 @@
+// Log probabilities behind the output head (sm_103a): per row of logits the log softmax at
+// given tokens, the entropy, and the k most probable tokens.
+//
+//   m = max l,  S = sum e^(l - m),  W = sum e^(l - m) (l - m)
+//   log p(i) = (l_i - m) - log S,   H = log S - W / S
+//
+// One pass over the logits.  Each thread keeps m, S and W of what it has read (all fp32,
+// rescaled when m grows).  For the k largest, a warp keeps its best 32 as one sorted
+// 64-bit key a lane (the value as an ordered integer, then the lower index first); a value
+// above the warp's k-th goes to a short buffer, and each 32 of those are sorted and merged
+// by shuffles.  Before the first merge the k-th largest of the lanes' first maxima is
+// the bound, and the warps of a CTA share their bounds, so after the first few thousand
+// values hardly any gets that far.
+//
+// A row is one CTA's, or with few rows a cluster's: its CTAs take consecutive parts and
+// leave their results in the first one's shared memory.
+// Bound: HBM, one read of the logits.
+#include "h32_common.cuh"
+
+#include <float.h>
+
+namespace h32 {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxTop = 32, kMaxCluster = 8;
+constexpr int kVecs = 4;             // 16-byte loads of a thread's step
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kFar = -200.0f;      // e^kFar is 0 in fp32
+
+struct LogprobArgs {
+    const void *logits;
+    int64_t V, ldl;
+    const int32_t *targets;   // [T][n]
+    int32_t n, top;
+    float *logprob, *entropy, *top_logprob;
+    int32_t *top_id;
+};
+
+// what a part of a row leaves: the running maximum, sums and best keys
+struct Part {
+    float m, S, W;
+    uint64_t best[kMaxTop];
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// the larger one; NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// floats as integers of the same order (-0 as +0)
+__device__ __forceinline__ uint32_t ordered(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+// the number below (none of the keys is ordered(-0) as it stands)
+__device__ __forceinline__ float below(uint32_t o) { return value_of(o == 0x80000000u ? o - 2 : o - 1); }
+// 0 is no key: the numbers above -inf have ordered() > 0
+__device__ __forceinline__ uint64_t key_of(float v, uint32_t i) {
+    return static_cast<uint64_t>(ordered(v)) << 32 | (0xFFFFFFFFu - i);
+}
+__device__ __forceinline__ uint32_t index_of(uint64_t key) { return 0xFFFFFFFFu - static_cast<uint32_t>(key); }
+
+// one compare-exchange with the lane `o` apart; `large`: this lane keeps the larger
+template <typename T>
+__device__ __forceinline__ T exchange(T v, int o, bool large) {
+    const T w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return (v > w) == large ? v : w;
+}
+// the warp's 32 values, largest in lane 0
+template <typename T>
+__device__ __forceinline__ T sort_warp(T v, int lane) {
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int o = size >> 1; o > 0; o >>= 1) v = exchange(v, o, ((lane & o) == 0) == ((lane & size) == 0));
+    return v;
+}
+// the 32 largest of two sorted lists, sorted
+__device__ __forceinline__ uint64_t merge_sorted(uint64_t a, uint64_t b, int lane) {
+    b = __shfl_xor_sync(0xFFFFFFFFu, b, 31);
+    uint64_t v = a > b ? a : b;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = exchange(v, o, (lane & o) == 0);
+    return v;
+}
+
+// (m, S, W) joined with another part's
+__device__ __forceinline__ void join(float &m, float &S, float &W, float m2, float S2, float W2) {
+    const float top = fmaxf(m, m2);
+    const float da = fmaxf(m - top, kFar), db = fmaxf(m2 - top, kFar);
+    const float fa = exp2_fast(da * kLog2e), fb = exp2_fast(db * kLog2e);
+    W = fa * fmaf(S, da, W) + fb * fmaf(S2, db, W2);
+    S = fa * S + fb * S2;
+    m = top;
+}
+
+template <bool kBf16>
+struct Vec {
+    static constexpr int kN = kBf16 ? 8 : 4;
+    uint4 u;
+    __device__ __forceinline__ float operator[](int i) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        if constexpr (kBf16) return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        else return __uint_as_float(w[i]);
+    }
+};
+
+template <bool kBf16>
+__device__ __forceinline__ float load_logit(const void *p, int64_t i) {
+    if constexpr (kBf16) return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << 16);
+    else return static_cast<const float *>(p)[i];
+}
+
+// A warp's k best.
+struct Best {
+    uint64_t key = 0;      // the lane's of the sorted list
+    float bound = -INFINITY;   // values at or below it are not among the k
+    int pending = 0;
+    uint64_t *buf;         // [64], the warp's
+    int32_t *shared;       // the CTA's bound: the largest k-th of its warps, as ordered() - 2^31
+    int k, lane;
+
+    // values equal to another warp's k-th may still be among the k by their index
+    __device__ __forceinline__ void look() {
+        const uint32_t o = static_cast<uint32_t>(*static_cast<volatile int32_t *>(shared)) ^ 0x80000000u;
+        bound = fmaxf(bound, below(o));   // (below -inf: NaN, which fmaxf passes over)
+    }
+    __device__ __forceinline__ void share(uint32_t o) {
+        if (lane == 0) atomicMax(shared, static_cast<int32_t>(o ^ 0x80000000u));
+    }
+    // from the first maxima of the lanes
+    __device__ __forceinline__ void first(float cm) {
+        const uint32_t o = __shfl_sync(0xFFFFFFFFu, sort_warp(ordered(cm), lane), k - 1);
+        if (value_of(o) > -INFINITY) {
+            bound = fmaxf(bound, below(o));
+            share(o);
+        }
+    }
+    __device__ __forceinline__ void push(bool p, float v, uint32_t i) {
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, p);
+        if (mask == 0) return;
+        if (p) buf[pending + __popc(mask & ((1u << lane) - 1))] = key_of(v, i);
+        pending += __popc(mask);
+        __syncwarp();
+        if (pending >= 32) {
+            key = merge_sorted(key, sort_warp(buf[lane], lane), lane);
+            const uint64_t rest = buf[32 + lane];
+            __syncwarp();
+            buf[lane] = rest;
+            pending -= 32;
+            __syncwarp();
+        }
+    }
+    // once a step's values are pushed: the k-th of the list is a bound
+    __device__ __forceinline__ void raise() {
+        const uint64_t kth = __shfl_sync(0xFFFFFFFFu, key, k - 1);
+        if (kth == 0) return;
+        const float v = value_of(static_cast<uint32_t>(kth >> 32));
+        if (v > bound) {
+            bound = v;
+            share(static_cast<uint32_t>(kth >> 32));
+        }
+    }
+    __device__ __forceinline__ void finish() {
+        const uint64_t last = lane < pending ? buf[lane] : 0;
+        key = merge_sorted(key, sort_warp(last, lane), lane);
+    }
+};
+
+__device__ __forceinline__ uint32_t rank_in_cluster() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void sync_cluster() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// `n` bytes (a multiple of 8) of this CTA's shared memory to the first CTA's
+__device__ __forceinline__ void to_first(void *dst, const void *src, int bytes) {
+    uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst)), r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(d));
+    for (int i = threadIdx.x; i < bytes / 8; i += kThreads)
+        asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(r + 8 * i), "l"(static_cast<const uint64_t *>(src)[i])
+                     : "memory");
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a) {
+    using V4 = Vec<kBf16>;
+    constexpr int kN = V4::kN;
+    __shared__ uint64_t s_buf[kWarps][64];
+    __shared__ Part s_part[kMaxCluster];
+    __shared__ float s_m[kWarps], s_S[kWarps], s_W[kWarps];
+    __shared__ int32_t s_bound;
+    __shared__ int s_count[2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t c = cluster_size(), rank = rank_in_cluster();
+    const int64_t row = blockIdx.x / c;
+    if (threadIdx.x == 0) s_bound = static_cast<int32_t>(ordered(-INFINITY) ^ 0x80000000u);
+    pdl_wait();
+    pdl_trigger();
+    __syncthreads();
+
+    constexpr int kSize = kBf16 ? 2 : 4;
+    const uint8_t *l = static_cast<const uint8_t *>(a.logits) + row * a.ldl * kSize;
+    // the row as values up to its first 16-byte boundary, whole 16-byte vectors, the rest
+    const int64_t skew = (16 - (reinterpret_cast<uintptr_t>(l) & 15)) & 15;
+    const int64_t head = min(a.V, skew / kSize), nvec = (a.V - head) / kN, tail = head + nvec * kN;
+    const uint4 *body = reinterpret_cast<const uint4 *>(l + head * kSize);
+    // this CTA's vectors: steps of kThreads x kVecs, dealt to the cluster in order
+    const int64_t steps = (nvec + kThreads * kVecs - 1) / (kThreads * kVecs);
+    const int64_t step0 = steps * rank / c, step1 = steps * (rank + 1) / c;
+
+    float m = -FLT_MAX, S = 0.0f, W = 0.0f;
+    Best best;
+    best.buf = s_buf[warp];
+    best.shared = &s_bound;
+    best.k = a.top;
+    best.lane = lane;
+
+    // values read as what changes nothing: -inf
+    constexpr uint32_t kNone = kBf16 ? 0xFF80FF80u : 0xFF800000u;
+    auto load = [&](int64_t step, V4 (&v)[kVecs]) {
+        const int64_t at = (step * kWarps + warp) * (32 * kVecs) + lane;
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u)
+            v[u].u = step < step1 && at + 32 * u < nvec ? __ldcs(body + at + 32 * u)
+                                                        : make_uint4(kNone, kNone, kNone, kNone);
+    };
+    V4 next[kVecs];
+    load(step0, next);
+    for (int64_t step = step0; step < step1; ++step) {
+        V4 v[kVecs];
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) v[u] = next[u];
+        load(step + 1, next);
+        float cm = v[0][0];
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+            for (int i = 0; i < kN; ++i) cm = fmaxf(cm, v[u][i]);
+        // (what was summed so far, under the new maximum)
+        const float top = fmaxf(m, cm);
+        const float dm = fmaxf(m - top, kFar), f = exp2_fast(dm * kLog2e);
+        W = f * fmaf(S, dm, W);
+        S *= f;
+        m = top;
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                // (-inf and far values: e = 0, and 0 times a finite d)
+                const float d = max_nan(v[u][i] - m, kFar), e = exp2_fast(d * kLog2e);
+                S += e;
+                W = fmaf(e, d, W);
+            }
+        if (a.top > 0) {
+            if (step == step0) best.first(cm);
+            best.look();
+            if (__any_sync(0xFFFFFFFFu, cm > best.bound)) {
+                const uint32_t i0 = static_cast<uint32_t>(head + ((step * kWarps + warp) * (32 * kVecs) + lane) * kN);
+#pragma unroll
+                for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+                    for (int i = 0; i < kN; ++i)
+                        best.push(v[u][i] > best.bound, v[u][i], i0 + u * 32 * kN + i);
+                best.raise();
+            }
+        }
+    }
+    // the values before and behind the vectors: fewer than 16, a lane each, last (their
+    // indices are out of order: equal values pass the bound, and the keys decide)
+    if (rank == 0 && warp == 0) {
+        const int64_t at = lane < 16 ? lane : tail + (lane - 16);
+        const bool in = lane < 16 ? lane < head : at < a.V;
+        const float v = in ? load_logit<kBf16>(l, at) : -INFINITY;
+        join(m, S, W, fmaxf(v, -FLT_MAX), v > -INFINITY ? 1.0f : v == v ? 0.0f : v, 0.0f);
+        if (a.top > 0) best.push(v >= best.bound && v > -INFINITY, v, static_cast<uint32_t>(at));
+    }
+    if (a.top > 0) best.finish();
+
+    // the warp's, then the CTA's
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        join(m, S, W, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, S, o),
+             __shfl_xor_sync(0xFFFFFFFFu, W, o));
+    __syncwarp();
+    s_buf[warp][lane] = best.key;
+    if (lane == 0) {
+        s_m[warp] = m;
+        s_S[warp] = S;
+        s_W[warp] = W;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        m = s_m[0], S = s_S[0], W = s_W[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) join(m, S, W, s_m[w], s_S[w], s_W[w]);
+        if (a.top > 0)
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) best.key = merge_sorted(best.key, s_buf[w][lane], lane);
+        s_part[rank].best[lane] = best.key;
+        if (lane == 0) {
+            s_part[rank].m = m;
+            s_part[rank].S = S;
+            s_part[rank].W = W;
+        }
+    }
+    if (c > 1) {
+        sync_cluster();   // (every CTA of the cluster runs, and its part is in its shared memory)
+        if (rank != 0) to_first(&s_part[rank], &s_part[rank], sizeof(Part));
+        sync_cluster();
+        if (rank != 0) return;
+    } else {
+        __syncthreads();
+    }
+    // the row's
+    m = s_part[0].m, S = s_part[0].S, W = s_part[0].W;
+    for (uint32_t r = 1; r < c; ++r) join(m, S, W, s_part[r].m, s_part[r].S, s_part[r].W);
+    if (m == INFINITY) {
+        // +inf logits share the probability (the limit of the softmax): count them
+        if (threadIdx.x < 2) s_count[threadIdx.x] = 0;
+        __syncthreads();
+        int inf = 0, nan = 0;
+        for (int64_t i = threadIdx.x; i < a.V; i += kThreads) {
+            const float v = load_logit<kBf16>(l, i);
+            inf += v == INFINITY;
+            nan |= v != v;
+        }
+        atomicAdd(&s_count[0], inf);
+        atomicOr(&s_count[1], nan);
+        __syncthreads();
+        S = s_count[1] ? NAN : static_cast<float>(s_count[0]);
+        W = 0.0f;
+    }
+    // log S by log1p: exact near a certain token.  An empty row (S = 0): log S is not used
+    const float log_s = log1pf(S - 1.0f);
+    auto logprob_of = [&](float v) {
+        if (S != S) return S;
+        if (v == -INFINITY || S == 0.0f) return -INFINITY;
+        if (m == INFINITY) return v == INFINITY ? -log_s : -INFINITY;
+        return v == v ? (v - m) - log_s : v;
+    };
+    if (threadIdx.x == 0 && a.entropy) a.entropy[row] = S != S ? S : S == 0.0f ? 0.0f : log_s - W / S;
+    for (int i = threadIdx.x; i < a.n; i += kThreads) {
+        const int32_t t = a.targets[row * a.n + i];
+        a.logprob[row * a.n + i] = t < 0 ? 0.0f : t >= a.V ? NAN : logprob_of(load_logit<kBf16>(l, t));
+    }
+    if (warp == 0 && a.top > 0) {
+        uint64_t key = s_part[0].best[lane];
+        for (uint32_t r = 1; r < c; ++r) key = merge_sorted(key, s_part[r].best[lane], lane);
+        const int found = min(a.top, __popc(__ballot_sync(0xFFFFFFFFu, key != 0)));
+        int32_t *ids = a.top_id + row * a.top;
+        float *lps = a.top_logprob + row * a.top;
+        if (lane < found) {
+            ids[lane] = static_cast<int32_t>(index_of(key));
+            lps[lane] = logprob_of(value_of(static_cast<uint32_t>(key >> 32)));
+        }
+        // fewer numbers above -inf than asked for: the first -inf, then the first NaN
+        int have = found;
+        for (int pass = 0; pass < 2 && have < a.top; ++pass)
+            for (int64_t i0 = 0; i0 < a.V && have < a.top; i0 += 32) {
+                const float v = i0 + lane < a.V ? load_logit<kBf16>(l, i0 + lane) : 0.0f;
+                const bool p = pass == 0 ? v == -INFINITY : v != v;
+                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, p);
+                const int at = have + __popc(mask & ((1u << lane) - 1));
+                if (p && at < a.top) {
+                    ids[at] = static_cast<int32_t>(i0 + lane);
+                    lps[at] = logprob_of(v);
+                }
+                have += __popc(mask);
+            }
+    }
+}
+
+}  // namespace
+}  // namespace h32
+
+extern "C" h32_status h32_token_logprobs(const void *logits, h32_in_dtype dt, int64_t T, int64_t V, int64_t ldl,
+                                         const int32_t *targets, int32_t n, int32_t top, float *logprob,
+                                         float *entropy, int32_t *top_id, float *top_logprob, void *stream) {
+    using namespace h32;
+    if (T < 0 || V <= 0 || V > 0x7FFFFFFFll || ldl < V || (dt != H32_IN_F32 && dt != H32_IN_BF16) || n < 0 ||
+        top < 0 || top > kMaxTop || top > V || T > 0x7FFFFFFFll / kMaxCluster)
+        return H32_ERR_INVALID_ARG;
+    if (T == 0) return H32_OK;
+    if (!logits || (n > 0 && (!targets || !logprob)) || (top > 0 && (!top_id || !top_logprob)))
+        return H32_ERR_INVALID_ARG;
+    const auto off4 = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 4 != 0; };
+    if (reinterpret_cast<uintptr_t>(logits) % (dt == H32_IN_BF16 ? 2 : 4) != 0 || off4(targets) || off4(logprob) ||
+        off4(entropy) || off4(top_id) || off4(top_logprob))
+        return H32_ERR_ALIGNMENT;
+    int sms = 0;
+    H32_TRY(check_device(&sms));
+    // CTAs of a row: as many as leave each at least one whole step, while the grid
+    // stays within one wave of 4 CTAs an SM
+    const int64_t steps = V / (kThreads * kVecs * (dt == H32_IN_BF16 ? 8 : 4));
+    int c = 1;
+    while (c < kMaxCluster && 2 * c <= steps && T * 2 * c <= 4 * int64_t(sms)) c *= 2;
+    const LogprobArgs a{logits, V, ldl, targets, n, top, logprob, entropy, top_logprob, top_id};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(T * c));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(c);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = dt == H32_IN_BF16 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<true>, a)
+                                            : cudaLaunchKernelEx(&cfg, logprobs_kernel<false>, a);
+    return launch_status(e != cudaSuccess ? e : cudaGetLastError());
+}

@@ -658,6 +658,81 @@ h32_status h32_add_rms_norm_quantize(const void *x, h32_in_dtype x_dt, int64_t l
                                      void *xq, float *xd, int64_t ldxd, void *stream);
 
 /*
+ * Quantizers of the 8-bit floating-point products below (the tensors that do not go to
+ * 4 bits, an output head among them, and checkpoints that hold such codes): e4m3 codes,
+ * one fp32 scale d for a block of values,
+ *   d = fl(amax |v| / 448),  code = the e4m3 number nearest to fl(v * fl(1/d)), ties to even
+ * (all codes 0 when d = 0), v the rotated values (`rotate` as for h32_quantize_act_q4).
+ * 448 is the largest e4m3 number.  Where 1/d is not finite (d below 2^-128) v / d by an
+ * IEEE divide replaces v * (1/d).  A NaN gets the code 0x7F (NaN); a block that holds an
+ * infinity gets d = inf, 0x7F for the infinities and 0 for the rest: products with it are
+ * NaN.
+ * Activations: a block is 128 consecutive values of a row (the last one what is left).
+ *   x        [T][ldx] of type dt, ldx >= K
+ *   row_idx  nullable int32 [R] device, 4-byte aligned: output row r is x[row_idx[r]]
+ *            (grouped order of an expert product; an index outside [0, T) records
+ *            H32_ERR_DEVICE_GUARD and gives zero codes and scales).  Null: R must be T
+ *   xq       [R][K] out: codes;  xd [ceil(K/128)][ldxd] out: scales, ldxd >= R, a multiple
+ *            of 4; entries r >= R are left untouched
+ * Weights: a block is 128 rows x 128 values (at the edges what is left).
+ *   w        [N][ldw] of type dt;  wq [N][K] out;  wd [ceil(N/128)][ceil(K/128)] out
+ */
+h32_status h32_quantize_act_f8(const void *x, h32_in_dtype dt, int64_t T, int64_t K, int64_t ldx,
+                               const int32_t *row_idx, int64_t R, uint8_t *xq, float *xd,
+                               int64_t ldxd, int rotate, void *stream);
+h32_status h32_quantize_weights_f8(const void *w, h32_in_dtype dt, int64_t N, int64_t K, int64_t ldw,
+                                   int rotate, uint8_t *wq, float *wd, void *stream);
+
+/*
+ * Products of e4m3 codes with a scale for each block of 128:
+ *   y[m][n] = acc after acc = fma(fl(xd[b][m] * wd[n/128][b]), S_b, acc), b = 0 .. K/128,
+ *   S_b = the fp32 sum of block b's products xq[m][k] * wq[n][k] (exact products; the sum's
+ *   order and rounding are the tensor core's), rounded once to y's type.
+ * For any M: one new token to long prompts (few tokens share one read of the weights).
+ *   wq   [N][K] codes, wd [ceil(N/128)][ceil(K/128)] (h32_quantize_weights_f8)
+ *   xq   [M][K] codes, xd [ceil(K/128)][ldxd], ldxd >= M a multiple of 4 (h32_quantize_act_f8)
+ *   y    [M][ldy] out of type y_dt, any ldy >= N
+ * Any N >= 1; K a multiple of 32.
+ * The expert form multiplies rows r in [expert_off[e], expert_off[e+1]) by expert e's
+ * weights: wq [E][N][K], wd [E][ceil(N/128)][ceil(K/128)], expert_off [E+1] int32 device,
+ * 4-byte aligned, 0 = off[0] <= ... <= off[E] = R (else H32_ERR_DEVICE_GUARD is recorded
+ * and nothing is computed), 1 <= E <= 1024.
+ */
+h32_status h32_f8_gemm(const uint8_t *wq, const float *wd, const uint8_t *xq, const float *xd,
+                       int64_t ldxd, int64_t M, int64_t N, int64_t K, void *y, h32_in_dtype y_dt,
+                       int64_t ldy, void *stream);
+h32_status h32_f8_gemm_experts(const uint8_t *wq, const float *wd, int32_t E, const uint8_t *xq,
+                               const float *xd, int64_t ldxd, const int32_t *expert_off, int64_t R,
+                               int64_t N, int64_t K, void *y, h32_in_dtype y_dt, int64_t ldy,
+                               void *stream);
+
+/*
+ * Log probabilities behind the output head: what scoring a prompt takes from its logits
+ * (perplexity, the divergence of two routes, the alternatives of a token).  Per row, in
+ * one pass, with p the softmax of its V logits:
+ *   logprob[t][j]     = log p of token targets[t][j]; 0 where the target is negative (no
+ *                       token given), NaN where it is V or more
+ *   entropy[t]        = -sum p log p
+ *   top_id, top_logprob [t][j] = the `top` most probable tokens, by decreasing logit,
+ *                       ties to the lower id, and their log p
+ * Statistics are held in fp32; a log p is off by at most a few 2^-24 of |l - max l| +
+ * log(sum), plus the rounding of the sum.  The ids are exact.
+ * Masked tokens (-inf) have log p = -inf and count for nothing; a row whose every logit is
+ * -inf has log p = -inf throughout and entropy 0; +inf logits share the probability
+ * equally; a NaN makes the row's log p (of given tokens and alternatives) and entropy NaN.
+ * Among the alternatives NaN ranks below -inf, both by id.
+ *   logits   [T][ldl] of type dt, any ldl >= V and any alignment of its type
+ *   targets  [T][n] int32, n >= 0;  logprob [T][n] out (both null with n = 0)
+ *   entropy  nullable [T] out
+ *   top_id, top_logprob  [T][top] out, 0 <= top <= min(32, V) (both null with top = 0)
+ * Other pointers 4-byte aligned.  Requires 1 <= V < 2^31, T < 2^28.
+ */
+h32_status h32_token_logprobs(const void *logits, h32_in_dtype dt, int64_t T, int64_t V,
+                              int64_t ldl, const int32_t *targets, int32_t n, int32_t top,
+                              float *logprob, float *entropy, int32_t *top_id,
+                              float *top_logprob, void *stream);
+
+/*
  * Synchronize `stream`, then report and clear the device status words that
  * this library's kernels on the current device write: H32_OK, H32_ERR_TIMEOUT
  * or H32_ERR_DEVICE_GUARD (or H32_ERR_CUDA when the synchronization, or a

@@ -445,3 +445,107 @@ def q4_0_blocks_from_planes(wq: np.ndarray, wd: np.ndarray) -> np.ndarray:
     out[:, :, 1] = (wd >> 8).astype(np.uint8)
     out[:, :, 2:] = wq.reshape(N, nb, 16)
     return out
+
+
+# --------------------------------------------------------------------------
+# 8-bit floating-point codes with a scale for each block of 128
+# --------------------------------------------------------------------------
+def e4m3_values() -> np.ndarray:
+    """The number each of the 256 e4m3 bytes stands for: sign, 4 exponent bits (bias 7),
+    3 mantissa bits; no infinities, 0x7F and 0xFF are NaN."""
+    b = np.arange(256)
+    e, m = (b >> 3) & 15, b & 7
+    v = np.where(e == 0, m * 2.0 ** -9, (8 + m) * 2.0 ** (e - 10.0))
+    v[(b & 127) == 127] = np.nan
+    return np.where(b & 128, -v, v)
+
+
+def e4m3_round(q: np.ndarray) -> np.ndarray:
+    """Bytes of the e4m3 numbers nearest to q (ties to the even byte), at most 448; NaN 0x7F."""
+    q = np.asarray(q, np.float64)
+    pos = e4m3_values()[:127]                      # ascending, 0 .. 448
+    a = np.minimum(np.abs(q), 448.0)
+    hi = np.clip(np.searchsorted(pos, a), 0, 126)  # the first number >= a
+    lo = np.maximum(hi - 1, 0)
+    up, down = pos[hi] - a, a - pos[lo]
+    code = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    code = np.where(np.isnan(q), 127, code | np.where(np.signbit(q), 128, 0))
+    return code.astype(np.uint8)
+
+
+def _f8_codes(v, amax):
+    """(codes, d) of fp32 values v and their block's largest magnitude (broadcast)."""
+    with np.errstate(all="ignore"):
+        d = (amax / np.float32(448)).astype(np.float32)
+        inv = np.where(d != 0, np.float32(1) / d, np.float32(0)).astype(np.float32)
+        q = np.where(np.isinf(inv), v / d, v * inv).astype(np.float32)
+    return e4m3_round(q), d
+
+
+def _rotated(x, rotate):
+    x = _widen(x)
+    n = rot_points(rotate)
+    return fwht_n(x, n) if n else x
+
+
+def quantize_act_f8(x, rotate=False):
+    """x [M][K] fp32 (or bf16 bits) -> (codes [M][K] u8, scales [M][ceil(K/128)] f32)."""
+    v = _rotated(x, rotate)
+    M, K = v.shape
+    g = np.pad(v, ((0, 0), (0, -K % 128))).reshape(M, -1, 128)
+    codes, d = _f8_codes(g, np.fmax.reduce(np.abs(g), axis=2, keepdims=True, initial=0))
+    return np.ascontiguousarray(codes.reshape(M, -1)[:, :K]), d[:, :, 0]
+
+
+def quantize_weights_f8(w, rotate=False):
+    """w [N][K] -> (codes [N][K] u8, scales [ceil(N/128)][ceil(K/128)] f32)."""
+    v = _rotated(w, rotate)
+    N, K = v.shape
+    g = np.pad(v, ((0, -N % 128), (0, -K % 128)))
+    g = g.reshape(g.shape[0] // 128, 128, g.shape[1] // 128, 128)
+    codes, d = _f8_codes(g, np.fmax.reduce(np.abs(g), axis=(1, 3), keepdims=True, initial=0))
+    return np.ascontiguousarray(codes.reshape(g.shape[0] * 128, -1)[:N, :K]), d[:, 0, :, 0]
+
+
+def f8_gemm(wq, wd, xq, xd):
+    """(y, t) [M][N] in fp64 of codes wq [N][K], xq [M][K] and scales wd [ceil(N/128)][nb],
+    xd [M][nb]: y the product, t the same with every term's magnitude."""
+    val = e4m3_values()
+    N, K = wq.shape
+    w = val[wq] * np.repeat(np.repeat(wd.astype(np.float64), 128, 0)[:N], 128, 1)[:, :K]
+    x = val[xq] * np.repeat(xd.astype(np.float64), 128, 1)[:, :K]
+    return x @ w.T, np.abs(x) @ np.abs(w).T
+
+
+def token_logprobs(logits, targets=None, top=0):
+    """fp64 evaluation of (logprob, entropy, top_id, top_logprob) by the rule of
+    h32_token_logprobs; logits [T][V] fp32, targets [T][n]."""
+    l = np.asarray(logits, np.float64)
+    T, V = l.shape
+    lp = np.empty((T, V))
+    ent = np.empty(T)
+    for t in range(T):
+        r = l[t]
+        if np.isnan(r).any():
+            lp[t], ent[t] = np.nan, np.nan
+        elif (r == np.inf).any():
+            n = np.count_nonzero(r == np.inf)
+            lp[t], ent[t] = np.where(r == np.inf, -np.log(n), -np.inf), np.log(n)
+        elif (r == -np.inf).all():
+            lp[t], ent[t] = -np.inf, 0.0
+        else:
+            e = np.exp(r - r.max())
+            S = e.sum()
+            # log S from what the largest logit's own term leaves: exact near certainty
+            rest = S - 1.0 if S > 1.5 else np.delete(e, int(r.argmax())).sum()
+            lp[t] = r - r.max() - np.log1p(rest)
+            p = np.exp(lp[t])
+            ent[t] = -(p[p > 0] * lp[t][p > 0]).sum()
+    # by decreasing logit, ties by id, NaN last
+    key = np.where(np.isnan(l), -np.inf, l)
+    ids = np.lexsort((np.broadcast_to(np.arange(V), l.shape), np.isnan(l), -key), axis=1)[:, :top]
+    given = None
+    if targets is not None:
+        given = np.take_along_axis(lp, np.clip(targets, 0, V - 1), 1)
+        given = np.where(targets < 0, 0.0, np.where(targets >= V, np.nan, given))
+    return given, ent, ids.astype(np.int32), np.take_along_axis(lp, ids, 1)

@@ -1,0 +1,322 @@
+"""GPU parity of the 8-bit floating-point quantizers and products: codes and scales bit
+for bit against the oracle; products exactly where the arithmetic is exact (small integer
+codes, power-of-two scales), else within a bound derived from the roundings."""
+import numpy as np
+import pytest
+
+import oracle
+from hadamard_rotated_bit_gb300 import workloads as wl
+from tests._gpu import np_of, torch_bf16, torch_of
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24   # half a step of fp32, relative
+
+
+@pytest.fixture(scope="module")
+def h32():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import hadamard_rotated_bit_gb300 as m
+    from hadamard_rotated_bit_gb300 import _build
+    _build.build()
+    return m
+
+
+def _ok(h32):
+    import torch
+    torch.cuda.synchronize()
+    assert h32.h32_device_status() == 0
+
+
+def _rows(M, K, seed, bf16, scale=1.0):
+    x = wl.act_normal_outliers(M, K, 0.01, 30.0, seed, wl.CFG_TEST, 5000) * np.float32(scale)
+    return wl.f32_to_bf16_bits(x) if bf16 else x
+
+
+def _dev(a):
+    return torch_bf16(a) if a.dtype == np.uint16 else torch_of(a)
+
+
+def _check_act(xq, xd, x, rotate):
+    q, d = oracle.quantize_act_f8(x, rotate)
+    R = q.shape[0]
+    assert np.array_equal(np_of(xq)[:R], q), "codes"
+    assert np.array_equal(np_of(xd)[:, :R].T, d), "scales"
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("M,K,rotate", [(1, 32, 0), (1, 5120, 128), (3, 96, 32), (5, 160, 0), (4, 192, 64),
+                                        (7, 1152, 128), (33, 256, 64), (130, 4128, 32)])
+def test_quantize_act(h32, M, K, rotate, bf16):
+    x = _rows(M, K, M + K, bf16)
+    x[M // 2, :min(K, 128)] = 0      # an all-zero group
+    xq, xd = h32.h32_quantize_act_f8(_dev(x), rotate=rotate)
+    _ok(h32)
+    assert xd.shape == ((K + 127) // 128, (M + 3) // 4 * 4)
+    _check_act(xq, xd, x, rotate)
+
+
+@pytest.mark.parametrize("scale", [1e-38, 2.0 ** -130, 1e-41, 1e30, 3e36])
+def test_quantize_act_extreme_scales(h32, scale):
+    """Groups whose 1/d overflows (an IEEE divide takes its place), and large ones."""
+    x = _rows(6, 256, 3, False, scale)
+    xq, xd = h32.h32_quantize_act_f8(_dev(x))
+    wq, wd = h32.h32_quantize_weights_f8(_dev(x))
+    _ok(h32)
+    _check_act(xq, xd, x, 0)
+    q, d = oracle.quantize_weights_f8(x)
+    assert np.array_equal(np_of(wq), q) and np.array_equal(np_of(wd), d)
+
+
+def test_quantize_act_non_finite(h32):
+    x = _rows(4, 256, 5, False)
+    x[0, 7], x[1, 130], x[2, :128] = np.nan, -np.inf, np.nan
+    xq, xd = h32.h32_quantize_act_f8(_dev(x))
+    _ok(h32)
+    q, d = np_of(xq), np_of(xd)[:, :4].T
+    rq, rd = oracle.quantize_act_f8(x)
+    assert np.array_equal(d, rd) and d[1, 1] == np.inf
+    nan = (rq & 127) == 127
+    assert np.array_equal((q & 127) == 127, nan) and np.array_equal(q[~nan], rq[~nan])
+    assert nan[0, 7] and nan[1, 130] and not nan[1, 129] and nan[2, :128].all() and nan.sum() == 130
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_quantize_act_pitched_gathered_into(h32, bf16):
+    """Rows of a wider array, gathered, into buffers larger than needed: what lies behind
+    the rows stays; an index outside the rows is reported and gives zeros."""
+    import torch
+    x = _rows(40, 352, 9, bf16)
+    t = _dev(x)[:, 32:352]
+    idx = np.random.default_rng(0).integers(0, 40, 101).astype(np.int32)
+    big = np.concatenate([[0], idx]).astype(np.int32)
+    xq = torch.full((110, 320), 77, dtype=torch.uint8, device="cuda")
+    xd = torch.full((4, 112), -5.0, device="cuda")
+    r = h32.h32_quantize_act_f8(t, rotate=64, row_idx=torch_of(big)[1:], xq=xq, xd=xd)
+    _ok(h32)
+    assert r[0] is xq and r[1] is xd
+    _check_act(xq, xd[:3], x[idx, 32:], 64)
+    assert (np_of(xq)[101:] == 77).all() and (np_of(xd)[:3, 101:] == -5).all() and (np_of(xd)[3] == -5).all()
+    idx[[3, 50]] = 40, -1
+    xq, xd = h32.h32_quantize_act_f8(t, row_idx=torch_of(idx))
+    torch.cuda.synchronize()
+    assert h32.h32_device_status() == h32.H32_ERR_DEVICE_GUARD
+    good = np.setdiff1d(np.arange(101), [3, 50])
+    q, d = oracle.quantize_act_f8(x[idx[good], 32:])
+    assert np.array_equal(np_of(xq)[good], q) and not np_of(xq)[[3, 50]].any()
+    assert np.array_equal(np_of(xd).T[good], d) and not np_of(xd).T[[3, 50]].any()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("N,K,rotate", [(1, 32, 0), (127, 160, 32), (128, 128, 128), (129, 192, 64), (300, 1024, 128),
+                                        (260, 4128, 0)])
+def test_quantize_weights(h32, N, K, rotate, bf16):
+    w = _rows(N, K, N + K, bf16, 0.02)
+    wide = np.concatenate([w, w], 1)
+    wq, wd = h32.h32_quantize_weights_f8(_dev(wide)[:, :K], rotate=rotate)
+    _ok(h32)
+    q, d = oracle.quantize_weights_f8(w, rotate)
+    assert np.array_equal(np_of(wq), q) and np.array_equal(np_of(wd), d)
+
+
+# --------------------------------------------------------------------------
+# products
+# --------------------------------------------------------------------------
+def _exact_operands(M, N, K, seed, E=1):
+    """Integer codes of at most 8 and scales of 1/2, 1 and 2: every sum is a multiple of
+    1/4 below 64 * K * 4, exact in fp32 for K < 16384."""
+    r = np.random.default_rng(seed)
+    byte = oracle.e4m3_round(np.arange(-8, 9))
+    wq, xq = byte[r.integers(0, 17, (E * N, K))], byte[r.integers(0, 17, (M, K))]
+    nb, nt = (K + 127) // 128, (N + 127) // 128
+    wd = (2.0 ** r.integers(-1, 2, (E * nt, nb))).astype(np.float32)
+    xd = (2.0 ** r.integers(-1, 2, (M, nb))).astype(np.float32)
+    return wq, wd, xq, xd
+
+
+def _xd(xd, pad=0.0):
+    import torch
+    M, nb = xd.shape
+    t = torch.full((nb, (M + 3) // 4 * 4), pad, device="cuda")
+    t[:, :M] = torch_of(xd.T.copy())
+    return t
+
+
+SHAPES = [(1, 1, 32), (1, 5120, 5120), (2, 129, 96), (7, 384, 4224), (15, 100, 160), (16, 128, 128), (17, 500, 640),
+          (31, 1000, 2048), (33, 77, 1056), (64, 640, 512), (65, 2000, 384), (128, 257, 1024), (129, 128, 4096),
+          (200, 1537, 96), (255, 4096, 320), (256, 256, 256), (257, 700, 5120), (333, 5120, 1024), (511, 96, 736),
+          (1030, 1300, 288), (2048, 8192, 128)]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product_exact(h32, M, N, K, bf16):
+    import torch
+    wq, wd, xq, xd = _exact_operands(M, N, K, M * 7 + N * 3 + K)
+    y = h32.h32_f8_gemm(torch_of(wq), torch_of(wd), torch_of(xq), _xd(xd, np.nan),
+                        y_dtype=torch.bfloat16 if bf16 else None)
+    _ok(h32)
+    ref = torch.from_numpy(oracle.f8_gemm(wq, wd, xq, xd)[0]).float()
+    assert torch.equal(y.cpu(), ref.bfloat16() if bf16 else ref)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 640, 5120), (5, 300, 17408), (40, 256, 2080), (100, 130, 4096), (300, 520, 5120)])
+def test_product_random_codes(h32, M, N, K):
+    """Every finite code, scales over several octaves.  Per block the tensor core adds 128
+    products: 128 additions off by at most 2 U each of the magnitudes' sum; then the
+    scales' product, the fold and nb additions, U each."""
+    r = np.random.default_rng(M + N)
+    fin = np.setdiff1d(np.arange(256), [127, 255]).astype(np.uint8)
+    wq, xq = fin[r.integers(0, 254, (N, K))], fin[r.integers(0, 254, (M, K))]
+    nb = (K + 127) // 128
+    wd = (10.0 ** r.uniform(-4, 0, ((N + 127) // 128, nb))).astype(np.float32)
+    xd = (10.0 ** r.uniform(-4, 0, (M, nb))).astype(np.float32)
+    y = h32.h32_f8_gemm(torch_of(wq), torch_of(wd), torch_of(xq), _xd(xd))
+    _ok(h32)
+    ref, mag = oracle.f8_gemm(wq, wd, xq, xd)
+    err = np.abs(np_of(y).astype(np.float64) - ref)
+    print("largest error in U of the magnitudes:", (err / mag).max() / U)
+    assert (err <= (256 + nb + 2) * U * mag).all()
+
+
+def test_product_nan_stays_in_its_row_and_column(h32):
+    wq, wd, xq, xd = _exact_operands(40, 300, 256, 1)
+    wq[7, 3], xq[5, 200] = 0x7F, 0xFF
+    for M in (6, 40):
+        y = h32.h32_f8_gemm(torch_of(wq), torch_of(wd), torch_of(xq[:M]), _xd(xd[:M]))
+        _ok(h32)
+        want = np.zeros((M, 300), bool)
+        want[:, 7] = want[5] = True
+        assert np.array_equal(np.isnan(np_of(y)), want)
+
+
+def test_product_into_pitched_rows_and_larger_buffers(h32):
+    """Outputs into the middle of wider, longer arrays of odd pitch; M below the operands' rows."""
+    import torch
+    for M, N, dt in ((3, 133, torch.float32), (3, 133, torch.bfloat16), (150, 301, torch.bfloat16), (290, 700, torch.float32)):
+        wq, wd, xq, xd = _exact_operands(M + 5, N, 384, M)
+        full = torch.full((M + 2, N + 3), 9.0, dtype=dt, device="cuda")
+        y = h32.h32_f8_gemm(torch_of(wq), torch_of(wd), torch_of(xq), _xd(xd), M=M, y=full)
+        _ok(h32)
+        assert y is full
+        ref = torch.from_numpy(oracle.f8_gemm(wq, wd, xq[:M], xd[:M])[0]).float().to(dt)
+        assert torch.equal(full[:M, :N].cpu(), ref)
+        assert bool((full[M:] == 9).all()) and bool((full[:, N:] == 9).all())
+
+
+def test_empty_calls(h32):
+    import torch
+    wq, wd, xq, xd = _exact_operands(1, 40, 128, 0)
+    y = h32.h32_f8_gemm(torch_of(wq), torch_of(wd), torch_of(xq)[:0], torch.zeros((1, 0), device="cuda"))
+    assert y.shape == (0, 40)
+    q, d = h32.h32_quantize_act_f8(torch.zeros((0, 128), device="cuda"))
+    assert q.shape == (0, 128) and d.shape == (1, 0)
+    q, d = h32.h32_quantize_weights_f8(torch.zeros((0, 128), device="cuda"))
+    assert q.shape == (0, 128) and d.shape == (0, 1)
+    _ok(h32)
+
+
+# --------------------------------------------------------------------------
+# expert products
+# --------------------------------------------------------------------------
+def _experts_ref(wq, wd, xq, xd, off, N):
+    E, nt = len(off) - 1, (N + 127) // 128
+    return np.concatenate([oracle.f8_gemm(wq[e * N:(e + 1) * N], wd[e * nt:(e + 1) * nt], xq[off[e]:off[e + 1]],
+                                          xd[off[e]:off[e + 1]])[0] for e in range(E)])
+
+
+@pytest.mark.parametrize("counts,N,K", [([1], 128, 128), ([0, 5, 0, 1, 16], 130, 288), ([3, 17, 29, 0, 2, 15], 300, 512),
+                                        ([40, 61, 0, 64, 65, 3], 384, 256), ([100, 7, 131, 128, 129], 96, 640),
+                                        ([300, 0, 1, 513, 255], 520, 384), ([0, 0, 900], 257, 160), ([2] * 160, 64, 96)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_experts_exact(h32, counts, N, K, bf16):
+    import torch
+    E, R = len(counts), sum(counts)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    wq, wd, xq, xd = _exact_operands(R, N, K, R + N, E)
+    y = torch.full((R + 1, N), 9.0, dtype=torch.bfloat16 if bf16 else torch.float32, device="cuda")
+    h32.h32_f8_gemm_experts(torch_of(wq), torch_of(wd), torch_of(xq), _xd(xd, np.nan), torch_of(off), N, y=y)
+    _ok(h32)
+    ref = torch.from_numpy(_experts_ref(wq, wd, xq, xd, off, N)).float()
+    assert torch.equal(y[:R].cpu(), ref.to(y.dtype)) and bool((y[R] == 9).all())
+
+
+def test_experts_bad_offsets_are_reported(h32):
+    import torch
+    for R, bad in ((24, [0, 10, 9, 24]), (24, [1, 2, 3, 24]), (24, [0, 4, 8, 23]), (600, [0, 4, 2000000000, 600]),
+                   (24, [0, -5, 3, 24])):
+        wq, wd, xq, xd = _exact_operands(R, 140, 128, 1, 3)
+        y = torch.full((R, 140), 9.0, device="cuda")
+        h32.h32_f8_gemm_experts(torch_of(wq), torch_of(wd), torch_of(xq), _xd(xd),
+                                torch_of(np.array(bad, np.int32)), 140, y=y)
+        torch.cuda.synchronize()
+        assert h32.h32_device_status() == h32.H32_ERR_DEVICE_GUARD and h32.h32_device_status() == 0
+        assert bool((y == 9).all())
+
+
+# --------------------------------------------------------------------------
+# streams, graphs
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("M,N,K", [(2, 640, 5120), (40, 300, 512), (300, 1000, 640)])
+def test_streams_and_graphs(h32, M, N, K):
+    """On a stream of its own, two at once, and captured; every run gives the same bits."""
+    import torch
+    x = _rows(M, K, 11, True)
+    w = _rows(N, K, 12, False, 0.02)
+    tx, (wq, wd) = torch_bf16(x), h32.h32_quantize_weights_f8(torch_of(w), rotate=32)
+
+    def path(stream=None):
+        q, d = h32.h32_quantize_act_f8(tx, rotate=32, stream=stream)
+        return h32.h32_f8_gemm(wq, wd, q, d, stream=stream)
+
+    torch.cuda.synchronize()
+    first = path()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    a, b = [], []
+    for _ in range(4):
+        a.append(path(s1))
+        b.append(path(s2))
+    torch.cuda.synchronize()
+    for y in a + b:
+        assert torch.equal(y, first)
+    graphs = []
+    for s in (s1, s2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            y = path()
+        graphs.append((g, y, s))
+    x2 = _rows(M, K, 13, True)
+    tx.copy_(torch_bf16(x2))
+    torch.cuda.synchronize()
+    for g, _, s in graphs:
+        with torch.cuda.stream(s):
+            g.replay()
+    torch.cuda.synchronize()
+    want = path()
+    _ok(h32)
+    for _, y, _ in graphs:
+        assert torch.equal(y, want)
+    assert not torch.equal(want, first)
+
+
+@pytest.mark.parametrize("M", [2, 24, 60, 120, 700])
+def test_one_poll_wait_bound(h32, M):
+    """A bound of one poll: waits give up, the status says so once, and the same context
+    then computes exactly."""
+    wq, wd, xq, xd = _exact_operands(M, 4096, 4096, M)
+    t = torch_of(wq), torch_of(wd), torch_of(xq), _xd(xd)
+    ref = oracle.f8_gemm(wq[:256], wd[:2], xq, xd)[0].astype(np.float32)
+    assert h32.h32_device_status() == 0
+    h32.h32_set_wait_limit(1)
+    try:
+        for _ in range(3):
+            h32.h32_f8_gemm(*t)
+        st = h32.h32_device_status()
+    finally:
+        h32.h32_set_wait_limit(0)
+    assert st == h32.H32_ERR_TIMEOUT and h32.h32_device_status() == 0
+    y = h32.h32_f8_gemm(*t)
+    _ok(h32)
+    assert np.array_equal(np_of(y)[:, :256], ref)
