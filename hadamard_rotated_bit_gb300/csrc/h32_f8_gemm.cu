@@ -24,6 +24,11 @@ __device__ uint32_t g_f8_status;   // kStatusTimeout, kStatusGuard
 
 constexpr int kMaxStages = 12;
 constexpr int kRowsWarps = 6;
+constexpr int kPairWarps = 12;
+// registers of pair_kernel: 12 warps of 168 at launch; the epilogue's two warpgroups take
+// over what the third, of the roles that issue, does not need
+constexpr int kPairIssueRegs = 72, kPairEpiRegs = 216;
+static_assert(128 * kPairIssueRegs + 256 * kPairEpiRegs <= 384 * 168, "registers handed over");
 constexpr int kMaxSmem = 225 * 1024;
 constexpr uint64_t kDrainPolls = 1ull << 22;
 
@@ -31,11 +36,12 @@ struct F8Args {
     int32_t M, N, K;         // token rows, weight rows (of an expert), reduction length
     int32_t E;               // experts; 1 and off null: all rows
     int32_t stages;
+    int32_t bn;              // pair_kernel: weight rows of a tile
     const int32_t *off;      // [E + 1] or null
     const float *wd;         // [E][ceil(N / 128)][ceil(K / 128)]
     void *y;
     int64_t ldy;
-    int32_t y_bf16;
+    uint8_t y_bf16, y_vec;   // y_vec: every row of y starts on 16 bytes
     uint64_t wait_limit;
 };
 
@@ -111,6 +117,37 @@ __device__ int load_groups(const Groups &g, const F8Args &a, int cols, int weigh
 __device__ __forceinline__ void store_y(const F8Args &a, int64_t m, int n, float v) {
     if (a.y_bf16) static_cast<__nv_bfloat16 *>(a.y)[m * a.ldy + n] = __float2bfloat16_rn(v);
     else static_cast<float *>(a.y)[m * a.ldy + n] = v;
+}
+
+// 32 consecutive outputs of a token: 16 bytes a store where y's rows are so aligned
+__device__ __forceinline__ void store_row(const F8Args &a, int64_t m, int n, const uint64_t (&acc)[16]) {
+    const auto value = [&](int i) {
+        return __uint_as_float(static_cast<uint32_t>(i & 1 ? acc[i / 2] >> 32 : acc[i / 2]));
+    };
+    if (a.y_vec && n + 32 <= a.N) {
+        if (a.y_bf16) {
+            uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + m * a.ldy + n);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(value(8 * q + 2 * i), value(8 * q + 2 * i + 1));
+                    w[i] = reinterpret_cast<const uint32_t &>(b);
+                }
+                p[q] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.y) + m * a.ldy + n);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                p[q] = make_float4(value(4 * q), value(4 * q + 1), value(4 * q + 2), value(4 * q + 3));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (n + i < a.N) store_y(a, m, n + i, value(i));
+    }
 }
 
 // ----------------------------------------------------------------------------
@@ -342,6 +379,280 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1)
     }
 }
 
+// ----------------------------------------------------------------------------
+// token rows on the lanes, two CTAs a tile
+// ----------------------------------------------------------------------------
+struct Pair {
+    static constexpr uint32_t kA = 128 * 128;          // codes of a CTA's tokens, a stage
+    static constexpr uint32_t kSlots = kMaxStages + 2; // scales of a K step each
+    static __host__ __device__ uint32_t b_bytes(int bn) { return bn / 2 * 128; }
+};
+
+// (the scale barrier's phases and the ring positions of the three rings a role walks)
+struct Ring {
+    int i = 0;
+    uint32_t ph;
+    __device__ explicit Ring(uint32_t phase) : ph(phase) {}
+    __device__ __forceinline__ void next(int n) {
+        if (++i == n) {
+            i = 0;
+            ph ^= 1;
+        }
+    }
+};
+
+__global__ void __launch_bounds__(kPairWarps * 32, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                const __grid_constant__ CUtensorMap map_s, const F8Args a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    // s_full: this CTA's copies of a stage; s_peer (used in CTA 0): the other's are there too;
+    // s_empty: the products have read the stage; s_sum: a K step's sums are in TMEM;
+    // s_free (in CTA 0): both CTAs' epilogues have them in registers; s_scale: a slot's scales
+    __shared__ uint64_t s_full[kMaxStages], s_peer[kMaxStages], s_empty[kMaxStages], s_scale[Pair::kSlots], s_sum[2],
+        s_free[2], s_drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_word;
+    __shared__ volatile int s_abort;
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int S = a.stages, slots = S + 2;
+    const uint32_t b_bytes = Pair::b_bytes(a.bn);
+    uint8_t *s_a = smem, *s_b = s_a + S * Pair::kA, *s_s = s_b + S * b_bytes;
+    int *s_table = reinterpret_cast<int *>(s_s + slots * 512);
+    const Groups g{s_table, s_table + a.E + 1};
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int nb = (a.K + 127) / 128, nt = (a.N + a.bn - 1) / a.bn;
+    const int first = blockIdx.x / 2, step = gridDim.x / 2;
+    const uint64_t lim = a.wait_limit;
+    volatile int *abort = &s_abort;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_peer[i], 1);
+            mbar_init(&s_empty[i], 1);
+        }
+        for (int i = 0; i < slots; ++i) mbar_init(&s_scale[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_sum[i], 1);
+            mbar_init(&s_free[i], 16);
+        }
+        mbar_init(&s_drain, 1);
+        s_abort = 0;
+        fence_barrier_init();
+    }
+    cluster_sync();   // both CTAs run, and their barriers are there
+    if (warp == 9) tmem_alloc_pair(&s_tmem, 512);
+    pdl_wait();
+    pdl_trigger();
+    tc_fence_before();
+    int total = load_groups(g, a, 256, nt, &s_word);
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    if (total < 0) {
+        if (threadIdx.x == 0) atomicOr(&g_f8_status, kStatusGuard);
+        total = 0;
+    }
+    auto give_up = [&]() {
+        s_abort = 1;
+        atomicOr(&g_f8_status, kStatusTimeout);
+    };
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairIssueRegs));
+        if (warp == 8) {
+            // ------------------------------------------------------------ TMA
+            const bool leader = elect_one();
+            if (leader) {
+                prefetch_tmap(&map_w);
+                prefetch_tmap(&map_x);
+                prefetch_tmap(&map_s);
+            }
+            Ring st(1), sl(0);   // (the first round's waits pass at once)
+            int fed = 0;
+            bool ok = true;
+            for (int t = first; t < total && ok; t += step) {
+                const Tile ti = tile_of(t, g, a.E, 256, a.bn);
+                const int x_row = ti.g0 + 128 * rank, w_row = ti.e * a.N + ti.n0 + a.bn / 2 * rank;
+                for (int kb = 0; kb < nb; ++kb) {
+                    if (!warp_wait_or_look(&s_empty[st.i], st.ph, lim, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) {
+                        mbar_arrive_expect_tx(&s_full[st.i], Pair::kA + b_bytes);
+                        tma_load_2d(s_a + st.i * Pair::kA, &map_x, &s_full[st.i], kb * 128, x_row);
+                        tma_load_2d(s_b + st.i * b_bytes, &map_w, &s_full[st.i], kb * 128, w_row);
+                        // the slot's last scales were read before the sums two steps later
+                        // were waited for, and those before this stage was free
+                        mbar_arrive_expect_tx(&s_scale[sl.i], 512);
+                        tma_load_2d(s_s + sl.i * 512, &map_s, &s_scale[sl.i], x_row, kb);
+                    }
+                    __syncwarp();
+                    if (fed < slots) ++fed;
+                    st.next(S);
+                    sl.next(slots);
+                }
+            }
+            if (leader) {
+                if (!ok) give_up();
+                // leave only when the last products have read the stages (in a whole run: their
+                // arrivals come from CTA 0) and the copies under way have landed
+                for (int i = 0; i < S && ok; ++i) {
+                    mbar_wait_bounded(&s_empty[st.i], st.ph, kDrainPolls, nullptr);
+                    st.next(S);
+                }
+                if (ok) st.ph ^= 1;   // (once around the ring)
+                for (int i = 0; i < fed; ++i) {
+                    if (i < S) {
+                        if (--st.i < 0) {
+                            st.i = S - 1;
+                            st.ph ^= 1;
+                        }
+                        mbar_wait_bounded(&s_full[st.i], st.ph ^ 1, kDrainPolls, nullptr);
+                    }
+                    if (--sl.i < 0) {
+                        sl.i = slots - 1;
+                        sl.ph ^= 1;
+                    }
+                    mbar_wait_bounded(&s_scale[sl.i], sl.ph, kDrainPolls, nullptr);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 9 && rank == 0) {
+            // ------------------------------------------------------------ MMA
+            const bool leader = elect_one();
+            const uint32_t idesc = idesc_e4m3_f32(256, a.bn);
+            const uint64_t da0 = smem_desc_sw128(smem_u32(s_a)), db0 = smem_desc_sw128(smem_u32(s_b));
+            Ring st(0), bf(1);
+            bool ok = true;
+            for (int t = first; t < total && ok; t += step) {
+                for (int kb = 0; kb < nb; ++kb) {
+                    if (!warp_wait_or_look(&s_full[st.i], st.ph, lim, abort) ||
+                        !warp_wait_cluster(&s_peer[st.i], st.ph, lim, abort) ||
+                        !warp_wait_cluster(&s_free[bf.i], bf.ph, lim, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (leader) {
+                        // (columns behind K are zeros in both operands)
+                        const uint64_t da = da0 + st.i * (Pair::kA >> 4), db = db0 + st.i * (b_bytes >> 4);
+    #pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_pair_f8f6f4(tmem + bf.i * 256, da + 2 * j, db + 2 * j, idesc, j > 0);
+                        mma_commit_pair(&s_empty[st.i]);
+                        mma_commit_pair(&s_sum[bf.i]);
+                    }
+                    __syncwarp();
+                    st.next(S);
+                    bf.next(2);
+                }
+            }
+            if (leader) {
+                if (!ok) give_up();
+                mma_commit_pair(&s_drain);
+                mbar_wait_bounded(&s_drain, 0, kDrainPolls, nullptr);
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            // ------------------------------ CTA 1: its copies' arrival, passed on to CTA 0
+            Ring st(0);
+            bool ok = true;
+            for (int t = first; t < total && ok; t += step) {
+                for (int kb = 0; kb < nb; ++kb) {
+                    if (!warp_wait_or_look(&s_full[st.i], st.ph, lim, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) peer_arrive(peer_smem(&s_peer[st.i], 0));
+                    __syncwarp();
+                    st.next(S);
+                }
+            }
+            if (!ok && lane == 0) give_up();
+            if (lane == 0) mbar_wait_bounded(&s_drain, 0, kDrainPolls, nullptr);   // CTA 0's last arrival
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairEpiRegs));
+        // ------------------------------------------------------- epilogue
+        // warp w: lanes of its quarter, the 32-column chunks w / 4, w / 4 + 2, ..
+        const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int chunks = a.bn / 32;
+        const uint32_t free0 = peer_smem(&s_free[0], 0), free1 = peer_smem(&s_free[1], 0);
+        Ring bf(0), sl(0);
+        bool ok = true;
+        for (int t = first; t < total && ok; t += step) {
+            const Tile ti = tile_of(t, g, a.E, 256, a.bn);
+            uint64_t acc[4][16];
+            const float *wd[4];
+            float dw[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[j][i] = 0ull;
+                // the chunk's row of weight scales (a chunk lies in one block of 128)
+                const int n = min(ti.n0 + 32 * (half + 2 * j), a.N - 1);
+                wd[j] = a.wd + (int64_t(ti.e) * ((a.N + 127) / 128) + n / 128) * nb;
+                dw[j] = __ldg(wd[j]);
+            }
+            for (int kb = 0; kb < nb; ++kb) {
+                if (!warp_wait_or_look(&s_scale[sl.i], sl.ph, lim, abort)) {
+                    ok = false;
+                    break;
+                }
+                const float dx = *reinterpret_cast<const float *>(s_s + sl.i * 512 + row * 4);
+                uint64_t s2[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t s = __float_as_uint(__fmul_rn(dx, dw[j]));
+                    s2[j] = pair_of(s, s);
+                    if (kb + 1 < nb) dw[j] = __ldg(wd[j] + kb + 1);
+                }
+                if (!warp_wait_or_look(&s_sum[bf.i], bf.ph, lim, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t col = tmem + lane_addr + bf.i * 256 + 32 * half;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (half + 2 * j < chunks) {
+                        uint32_t v[32];
+                        tmem_ld_x32(col + 64 * j, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            acc[j][i] = fma_f32x2(s2[j], pair_of(v[2 * i], v[2 * i + 1]), acc[j][i]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) peer_arrive(bf.i ? free1 : free0);
+                bf.next(2);
+                sl.next(slots);
+            }
+            if (!ok) break;
+            const int c = 128 * rank + row;   // the token's place in the tile
+            if (c >= ti.clo && c < ti.chi) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int n = ti.n0 + 32 * (half + 2 * j);
+                    if (half + 2 * j < chunks && n < a.N) store_row(a, ti.g0 + c, n, acc[j]);
+                }
+            }
+        }
+        if (!ok && lane == 0) give_up();
+    }
+    tc_fence_before();
+    cluster_sync();   // nothing of either CTA reaches into the other any more
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
 template <int NC>
 h32_status launch_rows(const uint8_t *wq, const uint8_t *xq, const float *xd, int64_t ldxd, F8Args a, int64_t tiles,
                        int sms, cudaStream_t s) {
@@ -360,6 +671,47 @@ h32_status launch_rows(const uint8_t *wq, const uint8_t *xq, const float *xd, in
     if (e == cudaSuccess)
         e = launch_pdl(rows_kernel<NC>, dim3(grid), dim3(kRowsWarps * 32), a.stages * C::kStage + table, s, maps[0],
                        maps[1], maps[2], a);
+    return launch_status(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+h32_status launch_pair(const uint8_t *wq, const uint8_t *xq, const float *xd, int64_t ldxd, F8Args a, int64_t tiles,
+                       int sms, cudaStream_t s) {
+    const uint32_t stage = Pair::kA + Pair::b_bytes(a.bn) + 512;
+    const size_t rest = Groups::bytes(a.E) + 1024 + 2 * 512;
+    const int fit = static_cast<int>((kMaxSmem - rest) / stage);
+    a.stages = fit < kMaxStages ? fit : kMaxStages;
+    CUtensorMap maps[3];
+    if (!code_map(&maps[0], wq, a.K, int64_t(a.E) * a.N, a.bn / 2) || !code_map(&maps[1], xq, a.K, a.M, 128) ||
+        !scale_map(&maps[2], xd, ldxd, (a.K + 127) / 128, 128)) {
+        note_error("cuTensorMapEncodeTiled rejected a tensor map of the 8-bit product");
+        return H32_ERR_CUDA;
+    }
+    const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kPairWarps * 32);
+    cfg.dynamicSmemBytes = a.stages * stage + rest;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    // the epilogue's setmaxnreg.inc waits until the pool holds its registers: never launch
+    // with fewer registers a thread than the hand-over assumes
+    static const int regs = [] {
+        cudaFuncAttributes fa{};
+        return cudaFuncGetAttributes(&fa, pair_kernel) == cudaSuccess ? fa.numRegs : -1;
+    }();
+    if (regs < 168) {
+        note_error("8-bit product compiled with fewer registers than its warpgroups hand over");
+        return H32_ERR_CUDA;
+    }
+    cudaError_t e = cudaFuncSetAttribute(pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, pair_kernel, maps[0], maps[1], maps[2], a);
     return launch_status(e != cudaSuccess ? e : cudaGetLastError());
 }
 
@@ -396,6 +748,7 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
     a.y = y;
     a.ldy = ldy;
     a.y_bf16 = y_dt == H32_IN_BF16;
+    a.y_vec = ldy * (a.y_bf16 ? 2 : 4) % 16 == 0;
     a.wait_limit = wait_limit();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // columns for the tokens of one group, as far as the host knows them
@@ -403,6 +756,10 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
     if (per <= 16) return launch_rows<16>(wq, xq, xd, ldxd, a, nt * (off ? E : (M + 15) / 16), sms, s);
     if (per <= 32) return launch_rows<32>(wq, xq, xd, ldxd, a, nt * (off ? E : (M + 31) / 32), sms, s);
     if (per <= 64) return launch_rows<64>(wq, xq, xd, ldxd, a, nt * (off ? E : (M + 63) / 64), sms, s);
+    if (per > 128) {
+        a.bn = 256;
+        return launch_pair(wq, xq, xd, ldxd, a, (N + 255) / 256 * (off ? E + M / 256 : (M + 255) / 256), sms, s);
+    }
     return launch_rows<128>(wq, xq, xd, ldxd, a, nt * (off ? E : (M + 127) / 128), sms, s);
 }
 
