@@ -51,6 +51,19 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr));
 }
 
+// wait for the loads issued; `r`, one of them, is read after it
+__device__ __forceinline__ void tmem_wait_for(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29])
+                 :);
+    asm volatile("" : "+r"(r[30]), "+r"(r[31]));
+}
+
+
 // clusters -------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -67,28 +80,12 @@ __device__ __forceinline__ uint32_t peer_smem(const void *p, uint32_t q) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(q));
     return r;
 }
-__device__ __forceinline__ void peer_store(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
+// Arrive on another CTA's barrier.  Nothing this thread wrote is handed over by it (the
+// copy engine's writes and the tensor-core loads it stands for were waited for), so it
+// carries no release: that would wait for the thread's loads under way, too (a K step of
+// the pair kernel took twice the time).
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// wait (bounded, warp-uniform outcome) for arrivals that release other CTAs' writes
-__device__ __forceinline__ bool warp_wait_cluster(uint64_t *bar, uint32_t parity, uint64_t limit,
-                                                  volatile int *abort) {
-    bool ok = false;
-    for (uint64_t i = 0; i < limit && !ok; ++i) {
-        uint32_t r;
-        asm volatile(
-            "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-            "selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(r)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-        ok = r != 0;
-        if (!ok && *abort) break;
-    }
-    return __all_sync(0xFFFFFFFFu, ok);
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // CTA pairs: tensor memory and products of both CTAs (cta_group::2) ------------

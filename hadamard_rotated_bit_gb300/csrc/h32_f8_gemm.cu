@@ -528,8 +528,8 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
             for (int t = first; t < total && ok; t += step) {
                 for (int kb = 0; kb < nb; ++kb) {
                     if (!warp_wait_or_look(&s_full[st.i], st.ph, lim, abort) ||
-                        !warp_wait_cluster(&s_peer[st.i], st.ph, lim, abort) ||
-                        !warp_wait_cluster(&s_free[bf.i], bf.ph, lim, abort)) {
+                        !warp_wait_or_look(&s_peer[st.i], st.ph, lim, abort) ||
+                        !warp_wait_or_look(&s_free[bf.i], bf.ph, lim, abort)) {
                         ok = false;
                         break;
                     }
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                     if (half + 2 * j < chunks) {
                         uint32_t v[32];
                         tmem_ld_x32(col + 64 * j, v);
-                        tmem_ld_wait();
+                        tmem_wait_for(v);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             acc[j][i] = fma_f32x2(s2[j], pair_of(v[2 * i], v[2 * i + 1]), acc[j][i]);
