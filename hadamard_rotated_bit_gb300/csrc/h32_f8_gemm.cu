@@ -119,34 +119,57 @@ __device__ __forceinline__ void store_y(const F8Args &a, int64_t m, int n, float
     else static_cast<float *>(a.y)[m * a.ldy + n] = v;
 }
 
-// 32 consecutive outputs of a token: 16 bytes a store where y's rows are so aligned
-__device__ __forceinline__ void store_row(const F8Args &a, int64_t m, int n, const uint64_t (&acc)[16]) {
+// A warp's 32 x 32 outputs (lane = token row m0 + lane, columns n ..), turned around in its
+// 4 KB of shared memory so that each store covers whole 128-byte lines: a lane's own row
+// a store made the tile's end twice as long.  16-byte pieces, piece p of row r at
+// p ^ (r & 7): no bank conflicts either way.  Rows outside [lo, hi) of the tile (r0: the
+// warp's first) and columns behind N are left out.  bf16: `fill` 0 stages the left half
+// of a line, 1 the right one and stores (`last`: stores what there is).
+__device__ __forceinline__ void stage_row(uint8_t *buf, int lane, bool bf16, int fill, const uint64_t (&acc)[16]) {
     const auto value = [&](int i) {
         return __uint_as_float(static_cast<uint32_t>(i & 1 ? acc[i / 2] >> 32 : acc[i / 2]));
     };
-    if (a.y_vec && n + 32 <= a.N) {
-        if (a.y_bf16) {
-            uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + m * a.ldy + n);
+    uint4 *row = reinterpret_cast<uint4 *>(buf + lane * 128);
+    if (bf16) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t w[4];
+        for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(value(8 * q + 2 * i), value(8 * q + 2 * i + 1));
-                    w[i] = reinterpret_cast<const uint32_t &>(b);
-                }
-                p[q] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(value(8 * q + 2 * i), value(8 * q + 2 * i + 1));
+                w[i] = reinterpret_cast<const uint32_t &>(b);
             }
-        } else {
-            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.y) + m * a.ldy + n);
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                p[q] = make_float4(value(4 * q), value(4 * q + 1), value(4 * q + 2), value(4 * q + 3));
+            row[(4 * fill + q) ^ (lane & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (n + i < a.N) store_y(a, m, n + i, value(i));
+        for (int q = 0; q < 8; ++q)
+            row[q ^ (lane & 7)] = make_uint4(__float_as_uint(value(4 * q)), __float_as_uint(value(4 * q + 1)),
+                                             __float_as_uint(value(4 * q + 2)), __float_as_uint(value(4 * q + 3)));
+    }
+}
+// the staged lines: `bytes` of each (64 or 128), from column n on
+__device__ __forceinline__ void store_lines(const F8Args &a, const uint8_t *buf, int lane, int64_t m0, int r0, int lo,
+                                            int hi, int n, int bytes) {
+    const int es = a.y_bf16 ? 2 : 4;
+    uint8_t *y = static_cast<uint8_t *>(a.y) + (m0 * a.ldy + n) * es;
+    if (a.y_vec && n + bytes / es <= a.N) {
+        const int p = lane & 7;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            if (r0 + r >= lo && r0 + r < hi && 16 * p < bytes)
+                *reinterpret_cast<uint4 *>(y + r * a.ldy * es + 16 * p) =
+                    *reinterpret_cast<const uint4 *>(buf + r * 128 + ((p ^ (r & 7)) << 4));
+        }
+    } else {
+        const int cols = min(bytes / es, a.N - n);
+        for (int r = max(0, lo - r0); r < min(32, hi - r0); ++r)
+            for (int c = lane; c < cols; c += 32) {
+                const uint8_t *v = buf + r * 128 + (((c * es >> 4) ^ (r & 7)) << 4) + (c * es & 15);
+                if (es == 2) reinterpret_cast<uint16_t *>(y + r * a.ldy * 2)[c] = *reinterpret_cast<const uint16_t *>(v);
+                else reinterpret_cast<uint32_t *>(y + r * a.ldy * 4)[c] = *reinterpret_cast<const uint32_t *>(v);
+            }
     }
 }
 
@@ -417,7 +440,8 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
     const int S = a.stages, slots = S + 2;
     const uint32_t b_bytes = Pair::b_bytes(a.bn);
     uint8_t *s_a = smem, *s_b = s_a + S * Pair::kA, *s_s = s_b + S * b_bytes;
-    int *s_table = reinterpret_cast<int *>(s_s + slots * 512);
+    uint8_t *s_y = s_s + (slots * 512 + 1023) / 1024 * 1024;   // 4 KB an epilogue warp
+    int *s_table = reinterpret_cast<int *>(s_y + 8 * 4096);
     const Groups g{s_table, s_table + a.E + 1};
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -576,10 +600,11 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairEpiRegs));
         // ------------------------------------------------------- epilogue
-        // warp w: lanes of its quarter, the 32-column chunks w / 4, w / 4 + 2, ..
+        // warp w: lanes of its quarter, half w / 4 of the columns in chunks of 32
         const int half = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const int chunks = a.bn / 32;
+        const int chunks = a.bn / 64;
+        uint8_t *buf = s_y + warp * 4096;
         const uint32_t free0 = peer_smem(&s_free[0], 0), free1 = peer_smem(&s_free[1], 0);
         Ring bf(0), sl(0);
         bool ok = true;
@@ -593,7 +618,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[j][i] = 0ull;
                 // the chunk's row of weight scales (a chunk lies in one block of 128)
-                const int n = min(ti.n0 + 32 * (half + 2 * j), a.N - 1);
+                const int n = min(ti.n0 + 32 * (half * chunks + j), a.N - 1);
                 wd[j] = a.wd + (int64_t(ti.e) * ((a.N + 127) / 128) + n / 128) * nb;
                 dw[j] = __ldg(wd[j]);
             }
@@ -615,12 +640,12 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t col = tmem + lane_addr + bf.i * 256 + 32 * half;
+                const uint32_t col = tmem + lane_addr + bf.i * 256 + 32 * chunks * half;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (half + 2 * j < chunks) {
+                    if (j < chunks) {
                         uint32_t v[32];
-                        tmem_ld_x32(col + 64 * j, v);
+                        tmem_ld_x32(col + 32 * j, v);
                         tmem_wait_for(v);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -634,12 +659,19 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                 sl.next(slots);
             }
             if (!ok) break;
-            const int c = 128 * rank + row;   // the token's place in the tile
-            if (c >= ti.clo && c < ti.chi) {
+            const int r0 = 128 * rank + (warp & 3) * 32;   // the warp's first row of the tile
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int n = ti.n0 + 32 * (half + 2 * j);
-                    if (half + 2 * j < chunks && n < a.N) store_row(a, ti.g0 + c, n, acc[j]);
+            for (int j = 0; j < 4; ++j) {
+                const int n = ti.n0 + 32 * (half * chunks + j);
+                if (j < chunks && n < a.N) {
+                    const bool right = a.y_bf16 && (j & 1);
+                    __syncwarp();   // (the lines before are read)
+                    stage_row(buf, lane, a.y_bf16, right, acc[j]);
+                    if (!a.y_bf16 || right || j + 1 == chunks || n + 32 >= a.N) {
+                        __syncwarp();
+                        store_lines(a, buf, lane, ti.g0 + r0, r0, ti.clo, ti.chi, right ? n - 32 : n,
+                                    a.y_bf16 && !right ? 64 : 128);
+                    }
                 }
             }
         }
@@ -677,7 +709,7 @@ h32_status launch_rows(const uint8_t *wq, const uint8_t *xq, const float *xd, in
 h32_status launch_pair(const uint8_t *wq, const uint8_t *xq, const float *xd, int64_t ldxd, F8Args a, int64_t tiles,
                        int sms, cudaStream_t s) {
     const uint32_t stage = Pair::kA + Pair::b_bytes(a.bn) + 512;
-    const size_t rest = Groups::bytes(a.E) + 1024 + 2 * 512;
+    const size_t rest = Groups::bytes(a.E) + 2 * 1024 + 2 * 512 + 8 * 4096;
     const int fit = static_cast<int>((kMaxSmem - rest) / stage);
     a.stages = fit < kMaxStages ? fit : kMaxStages;
     CUtensorMap maps[3];
