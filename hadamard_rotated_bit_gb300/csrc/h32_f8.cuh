@@ -80,6 +80,30 @@ __device__ __forceinline__ uint32_t peer_smem(const void *p, uint32_t q) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(q));
     return r;
 }
+__device__ __forceinline__ void peer_store(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+// arrive on another CTA's barrier, handing over what the warp stored
+__device__ __forceinline__ void peer_arrive_release(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// wait (bounded, warp-uniform outcome) for arrivals that release other CTAs' writes
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t *bar, uint32_t parity, uint64_t limit,
+                                                  volatile int *abort) {
+    bool ok = false;
+    for (uint64_t i = 0; i < limit && !ok; ++i) {
+        uint32_t r;
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(r)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        ok = r != 0;
+        if (!ok && *abort) break;
+    }
+    return __all_sync(0xFFFFFFFFu, ok);
+}
 // Arrive on another CTA's barrier.  Nothing this thread wrote is handed over by it (the
 // copy engine's writes and the tensor-core loads it stands for were waited for), so it
 // carries no release: that would wait for the thread's loads under way, too (a K step of

@@ -37,6 +37,7 @@ struct F8Args {
     int32_t E;               // experts; 1 and off null: all rows
     int32_t stages;
     int32_t bn;              // pair_kernel: weight rows of a tile
+    int32_t cluster;         // rows_kernel: CTAs of a tile
     const int32_t *off;      // [E + 1] or null
     const float *wd;         // [E][ceil(N / 128)][ceil(K / 128)]
     void *y;
@@ -176,32 +177,60 @@ __device__ __forceinline__ void store_lines(const F8Args &a, const uint8_t *buf,
 // ----------------------------------------------------------------------------
 // weight rows on the lanes
 // ----------------------------------------------------------------------------
+// the position and phase of a role that walks a ring of barriers
+struct Ring {
+    int i = 0;
+    uint32_t ph;
+    __device__ explicit Ring(uint32_t phase) : ph(phase) {}
+    __device__ __forceinline__ void next(int n) {
+        if (++i == n) {
+            i = 0;
+            ph ^= 1;
+        }
+    }
+};
+
+// With fewer tiles than SMs the K steps of a tile are dealt to the CTAs of a cluster
+// (consecutive shares), and each CTA takes a slice of its columns at the end: the others'
+// partial sums come to its shared memory and are added in the order of the shares.
 template <int NC>
 struct Rows {
-    static constexpr int kBufs = NC <= 32 ? 4 : 2;            // sums in TMEM
-    static constexpr uint32_t kTmem = kBufs * NC < 32 ? 32 : kBufs * NC;
+    static constexpr int kBufs = 8;                           // sums in TMEM
+    static constexpr uint32_t kTmem = kBufs * NC;
     static constexpr uint32_t kA = 128 * 128, kB = NC * 128;  // bytes of a stage's parts
     static constexpr uint32_t kS = NC * 4 < 128 ? 128 : NC * 4;
     static constexpr uint32_t kStage = kA + kB + kS;
+    static constexpr int kMaxCluster = 8, kPerSm = 2;         // CTAs of a tile, of an SM
+    // the partial sums that a CTA gets: [share][column][row]
+    static __host__ __device__ uint32_t parts(int cluster) { return (cluster - 1) * (NC / cluster) * 512; }
 };
 
 template <int NC>
-__global__ void __launch_bounds__(kRowsWarps * 32, 1)
+__global__ void __launch_bounds__(kRowsWarps * 32, Rows<NC>::kPerSm)
     rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                 const __grid_constant__ CUtensorMap map_s, const F8Args a) {
     using C = Rows<NC>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_sum[C::kBufs], s_free[C::kBufs], s_drain;
+    // s_full: a stage's copies; s_empty: its products are done and its scales read; s_sum: a K
+    // step's sums are in TMEM; s_free: they are in registers; s_part: the other CTAs' partial
+    // sums are here
+    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_sum[C::kBufs], s_free[C::kBufs], s_part, s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_word;
     __shared__ volatile int s_abort;
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const int S = a.stages;
+    const int S = a.stages, cluster = a.cluster;
+    const int slice = NC / cluster, slice_bits = 31 - __clz(slice);   // columns of a CTA: a power of 2
+    const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
     uint8_t *s_a = smem, *s_b = s_a + S * C::kA, *s_s = s_b + S * C::kB;
-    int *s_table = reinterpret_cast<int *>(s_s + S * C::kS);
+    float *s_parts = reinterpret_cast<float *>(s_s + S * C::kS);
+    int *s_table = reinterpret_cast<int *>(s_s + S * C::kS + C::parts(cluster));
     const Groups g{s_table, s_table + a.E + 1};
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int nb = (a.K + 127) / 128, nt = (a.N + 127) / 128;
+    // this CTA's K steps
+    const int kb0 = nb * static_cast<int>(rank) / cluster, steps = nb * (static_cast<int>(rank) + 1) / cluster - kb0;
+    const int first = blockIdx.x / cluster, stride = gridDim.x / cluster;
     const uint64_t lim = a.wait_limit;
     volatile int *abort = &s_abort;
     if (threadIdx.x == 0) {
@@ -213,6 +242,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1)
             mbar_init(&s_sum[i], 1);
             mbar_init(&s_free[i], 4);
         }
+        mbar_init(&s_part, cluster > 1 ? 4 * (cluster - 1) : 1);
         mbar_init(&s_drain, 1);
         s_abort = 0;
         fence_barrier_init();
@@ -221,6 +251,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1)
         tmem_alloc(&s_tmem, C::kTmem);
         tmem_relinquish();
     }
+    if (cluster > 1) cluster_sync();   // every CTA runs, and its barriers are there
     pdl_wait();
     pdl_trigger();
     tc_fence_before();
@@ -244,28 +275,26 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1)
             prefetch_tmap(&map_x);
             prefetch_tmap(&map_s);
         }
-        int s = 0, fed = 0;
-        uint32_t ph = 1;   // (the first round's waits pass at once)
+        Ring st(1);   // (the first round's waits pass at once)
+        int fed = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        for (int t = first; t < total && ok; t += stride) {
             const Tile ti = tile_of(t, g, a.E, NC, 128);
-            for (int kb = 0; kb < nb; ++kb) {
-                if (!warp_wait_or_look(&s_empty[s], ph, lim, abort)) {
+            for (int i = 0; i < steps; ++i) {
+                if (!warp_wait_or_look(&s_empty[st.i], st.ph, lim, abort)) {
                     ok = false;
                     break;
                 }
                 if (leader) {
-                    mbar_arrive_expect_tx(&s_full[s], C::kA + C::kB + NC * 4);
-                    tma_load_2d(s_a + s * C::kA, &map_w, &s_full[s], kb * 128, ti.e * a.N + ti.n0);
-                    tma_load_2d(s_b + s * C::kB, &map_x, &s_full[s], kb * 128, ti.g0);
-                    tma_load_2d(s_s + s * C::kS, &map_s, &s_full[s], ti.g0, kb);
+                    const int kb = kb0 + i;
+                    mbar_arrive_expect_tx(&s_full[st.i], C::kA + C::kB + NC * 4);
+                    tma_load_2d(s_a + st.i * C::kA, &map_w, &s_full[st.i], kb * 128, ti.e * a.N + ti.n0);
+                    tma_load_2d(s_b + st.i * C::kB, &map_x, &s_full[st.i], kb * 128, ti.g0);
+                    tma_load_2d(s_s + st.i * C::kS, &map_s, &s_full[st.i], ti.g0, kb);
                 }
                 __syncwarp();
                 if (fed < S) ++fed;
-                if (++s == S) {
-                    s = 0;
-                    ph ^= 1;
-                }
+                st.next(S);
             }
         }
         if (leader) {
@@ -273,11 +302,11 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1)
             // leave only when the copies under way have landed (at once unless a wait
             // gave up): each fed stage's last phase
             for (int i = 0; i < fed; ++i) {
-                if (--s < 0) {
-                    s = S - 1;
-                    ph ^= 1;
+                if (--st.i < 0) {
+                    st.i = S - 1;
+                    st.ph ^= 1;
                 }
-                mbar_wait_bounded(&s_full[s], ph ^ 1, kDrainPolls, nullptr);
+                mbar_wait_bounded(&s_full[st.i], st.ph ^ 1, kDrainPolls, nullptr);
             }
         }
         __syncwarp();
@@ -286,34 +315,27 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1)
         const bool leader = elect_one();
         const uint32_t idesc = idesc_e4m3_f32(128, NC);
         const uint64_t da0 = smem_desc_sw128(smem_u32(s_a)), db0 = smem_desc_sw128(smem_u32(s_b));
-        int s = 0, buf = 0;
-        uint32_t ph = 0, bph = 1;
+        Ring st(0), bf(1);
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            for (int kb = 0; kb < nb; ++kb) {
-                if (!warp_wait_or_look(&s_full[s], ph, lim, abort) ||
-                    !warp_wait_or_look(&s_free[buf], bph, lim, abort)) {
+        for (int t = first; t < total && ok; t += stride) {
+            for (int i = 0; i < steps; ++i) {
+                if (!warp_wait_or_look(&s_full[st.i], st.ph, lim, abort) ||
+                    !warp_wait_or_look(&s_free[bf.i], bf.ph, lim, abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (leader) {
                     // (columns behind K are zeros in both operands)
-                    const uint64_t da = da0 + s * (C::kA >> 4), db = db0 + s * (C::kB >> 4);
+                    const uint64_t da = da0 + st.i * (C::kA >> 4), db = db0 + st.i * (C::kB >> 4);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        mma_f8f6f4(tmem + buf * NC, da + 2 * j, db + 2 * j, idesc, j > 0);
-                    mma_commit(&s_sum[buf]);
+                        mma_f8f6f4(tmem + bf.i * NC, da + 2 * j, db + 2 * j, idesc, j > 0);
+                    mma_commit(&s_sum[bf.i]);
                 }
                 __syncwarp();
-                if (++s == S) {
-                    s = 0;
-                    ph ^= 1;
-                }
-                if (++buf == C::kBufs) {
-                    buf = 0;
-                    bph ^= 1;
-                }
+                st.next(S);
+                bf.next(C::kBufs);
             }
         }
         if (leader) {
@@ -324,77 +346,98 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------- epilogue
+        const int row = warp * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
-        int s = 0, buf = 0;
-        uint32_t ph = 0, bph = 0;
+        Ring st(0), bf(0);
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        for (int t = first; t < total && ok; t += stride) {
             const Tile ti = tile_of(t, g, a.E, NC, 128);
             uint64_t acc[NC / 2];
 #pragma unroll
             for (int i = 0; i < NC / 2; ++i) acc[i] = 0ull;
-            // the tile's weight scales, a lane's share of 32 blocks ahead
-            const float *wd = a.wd + (int64_t(ti.e) * nt + ti.n0 / 128) * nb;
-            float dw_next = lane < nb ? __ldg(wd + lane) : 0.0f, dw_lane = 0.0f;
-            for (int kb = 0; kb < nb; ++kb) {
-                if ((kb & 31) == 0) {
+            // the tile's weight scales, a lane's share of 32 steps ahead
+            const float *wd = a.wd + (int64_t(ti.e) * nt + ti.n0 / 128) * nb + kb0;
+            float dw_next = lane < steps ? __ldg(wd + lane) : 0.0f, dw_lane = 0.0f;
+            for (int i = 0; i < steps; ++i) {
+                if ((i & 31) == 0) {
                     dw_lane = dw_next;
-                    dw_next = kb + 32 + lane < nb ? __ldg(wd + kb + 32 + lane) : 0.0f;
+                    dw_next = i + 32 + lane < steps ? __ldg(wd + i + 32 + lane) : 0.0f;
                 }
-                const float dw = __shfl_sync(0xFFFFFFFFu, dw_lane, kb & 31);
+                const float dw = __shfl_sync(0xFFFFFFFFu, dw_lane, i & 31);
                 // (the stage's scales; its codes' sums follow)
-                if (!warp_wait_or_look(&s_full[s], ph, lim, abort) ||
-                    !warp_wait_or_look(&s_sum[buf], bph, lim, abort)) {
+                if (!warp_wait_or_look(&s_full[st.i], st.ph, lim, abort) ||
+                    !warp_wait_or_look(&s_sum[bf.i], bf.ph, lim, abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const float *dx = reinterpret_cast<const float *>(s_s + s * C::kS);
-                const uint32_t col = tmem + lane_addr + buf * NC;
+                const float *dx = reinterpret_cast<const float *>(s_s + st.i * C::kS);
+                const uint32_t col = tmem + lane_addr + bf.i * NC;
                 if constexpr (NC == 16) {
                     uint32_t v[16];
                     tmem_ld_x16(col, v);
                     tmem_ld_wait();
                     fold16(acc, dw, dx, v);
                 } else {
-#pragma unroll
-                    for (int c = 0; c < NC; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld_x32(col + c, v);
-                        tmem_ld_wait();
-                        fold16(acc + c / 2, dw, dx + c, reinterpret_cast<const uint32_t(&)[16]>(v[0]));
-                        fold16(acc + c / 2 + 8, dw, dx + c + 16, reinterpret_cast<const uint32_t(&)[16]>(v[16]));
-                    }
+                    uint32_t v[32];
+                    tmem_ld_x32(col, v);
+                    tmem_wait_for(v);
+                    fold16(acc, dw, dx, reinterpret_cast<const uint32_t(&)[16]>(v[0]));
+                    fold16(acc + 8, dw, dx + 16, reinterpret_cast<const uint32_t(&)[16]>(v[16]));
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&s_free[buf]);
-                    mbar_arrive(&s_empty[s]);
+                    mbar_arrive(&s_free[bf.i]);
+                    mbar_arrive(&s_empty[st.i]);
                 }
-                if (++s == S) {
-                    s = 0;
-                    ph ^= 1;
-                }
-                if (++buf == C::kBufs) {
-                    buf = 0;
-                    bph ^= 1;
-                }
+                st.next(S);
+                bf.next(C::kBufs);
             }
             if (!ok) break;
-            const int n = ti.n0 + warp * 32 + lane;
-            if (n < a.N) {
+            const int n = ti.n0 + row;
+            const auto value = [&](int c) {
+                return __uint_as_float(static_cast<uint32_t>(c & 1 ? acc[c / 2] >> 32 : acc[c / 2]));
+            };
+            if (cluster == 1) {
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const uint32_t bits = static_cast<uint32_t>(c & 1 ? acc[c / 2] >> 32 : acc[c / 2]);
-                    if (c >= ti.clo && c < ti.chi) store_y(a, ti.g0 + c, n, __uint_as_float(bits));
+                for (int c = 0; c < NC; ++c)
+                    if (n < a.N && c >= ti.clo && c < ti.chi) store_y(a, ti.g0 + c, n, value(c));
+                continue;
+            }
+            // (one tile a cluster.)  The other slices over, share p's sums of slice q to slot p
+            // (p < q) or p - 1 (p > q) of CTA q; then this CTA's added up
+            int share = static_cast<int>(rank);
+            asm volatile("" : "+r"(share));   // (the addresses are made here, not kept over the steps)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int q = c >> slice_bits;
+                if (q != share)
+                    peer_store(peer_smem(s_parts + ((share < q ? share : share - 1) * slice + (c & (slice - 1))) * 128 + row, q),
+                               value(c));
+            }
+            __syncwarp();
+            if (lane < cluster && lane != share) peer_arrive_release(peer_smem(&s_part, lane));
+            if (!warp_wait_cluster(&s_part, 0, lim, abort)) {
+                ok = false;
+                break;
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                if (c >> slice_bits == share) {
+                    const float *slot = s_parts + (c & (slice - 1)) * 128 + row;
+                    float y = share == 0 ? value(c) : slot[0];
+                    for (int p = 1; p < cluster; ++p)
+                        y = __fadd_rn(y, p == share ? value(c) : slot[(p < share ? p : p - 1) * slice * 128]);
+                    if (n < a.N && c >= ti.clo && c < ti.chi) store_y(a, ti.g0 + c, n, y);
                 }
             }
         }
         if (!ok && lane == 0) give_up();
     }
     tc_fence_before();
-    __syncthreads();
+    if (cluster > 1) cluster_sync();   // nothing of any CTA reaches into another any more
+    else __syncthreads();
     if (warp == 5) {
         __syncwarp();
         tc_fence_after();
@@ -411,19 +454,9 @@ struct Pair {
     static __host__ __device__ uint32_t b_bytes(int bn) { return bn / 2 * 128; }
 };
 
-// (the scale barrier's phases and the ring positions of the three rings a role walks)
-struct Ring {
-    int i = 0;
-    uint32_t ph;
-    __device__ explicit Ring(uint32_t phase) : ph(phase) {}
-    __device__ __forceinline__ void next(int n) {
-        if (++i == n) {
-            i = 0;
-            ph ^= 1;
-        }
-    }
-};
-
+// kChunks: 32-column chunks of an epilogue warp, a.bn = 64 kChunks.  (Compiled in, as every
+// branch taken in the loop over the K steps costs about as much as a wait.)
+template <int kChunks>
 __global__ void __launch_bounds__(kPairWarps * 32, 1)
     pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                 const __grid_constant__ CUtensorMap map_s, const F8Args a) {
@@ -603,34 +636,34 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
         // warp w: lanes of its quarter, half w / 4 of the columns in chunks of 32
         const int half = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const int chunks = a.bn / 64;
         uint8_t *buf = s_y + warp * 4096;
         const uint32_t free0 = peer_smem(&s_free[0], 0), free1 = peer_smem(&s_free[1], 0);
         Ring bf(0), sl(0);
         bool ok = true;
         for (int t = first; t < total && ok; t += step) {
             const Tile ti = tile_of(t, g, a.E, 256, a.bn);
-            uint64_t acc[4][16];
-            const float *wd[4];
-            float dw[4];
+            uint64_t acc[kChunks][16];
+            const float *wd[kChunks];
+            float dw[kChunks];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kChunks; ++j) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[j][i] = 0ull;
                 // the chunk's row of weight scales (a chunk lies in one block of 128)
-                const int n = min(ti.n0 + 32 * (half * chunks + j), a.N - 1);
+                const int n = min(ti.n0 + 32 * (half * kChunks + j), a.N - 1);
                 wd[j] = a.wd + (int64_t(ti.e) * ((a.N + 127) / 128) + n / 128) * nb;
                 dw[j] = __ldg(wd[j]);
             }
+#pragma unroll 4
             for (int kb = 0; kb < nb; ++kb) {
                 if (!warp_wait_or_look(&s_scale[sl.i], sl.ph, lim, abort)) {
                     ok = false;
                     break;
                 }
                 const float dx = *reinterpret_cast<const float *>(s_s + sl.i * 512 + row * 4);
-                uint64_t s2[4];
+                uint64_t s2[kChunks];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < kChunks; ++j) {
                     const uint32_t s = __float_as_uint(__fmul_rn(dx, dw[j]));
                     s2[j] = pair_of(s, s);
                     if (kb + 1 < nb) dw[j] = __ldg(wd[j] + kb + 1);
@@ -640,17 +673,15 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t col = tmem + lane_addr + bf.i * 256 + 32 * chunks * half;
+                const uint32_t col = tmem + lane_addr + bf.i * 256 + 32 * kChunks * half;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j < chunks) {
-                        uint32_t v[32];
-                        tmem_ld_x32(col + 32 * j, v);
-                        tmem_wait_for(v);
+                for (int j = 0; j < kChunks; ++j) {
+                    uint32_t v[32];
+                    tmem_ld_x32(col + 32 * j, v);
+                    tmem_wait_for(v);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            acc[j][i] = fma_f32x2(s2[j], pair_of(v[2 * i], v[2 * i + 1]), acc[j][i]);
-                    }
+                    for (int i = 0; i < 16; ++i)
+                        acc[j][i] = fma_f32x2(s2[j], pair_of(v[2 * i], v[2 * i + 1]), acc[j][i]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -661,13 +692,13 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
             if (!ok) break;
             const int r0 = 128 * rank + (warp & 3) * 32;   // the warp's first row of the tile
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = ti.n0 + 32 * (half * chunks + j);
-                if (j < chunks && n < a.N) {
+            for (int j = 0; j < kChunks; ++j) {
+                const int n = ti.n0 + 32 * (half * kChunks + j);
+                if (n < a.N) {
                     const bool right = a.y_bf16 && (j & 1);
                     __syncwarp();   // (the lines before are read)
                     stage_row(buf, lane, a.y_bf16, right, acc[j]);
-                    if (!a.y_bf16 || right || j + 1 == chunks || n + 32 >= a.N) {
+                    if (!a.y_bf16 || right || j + 1 == kChunks || n + 32 >= a.N) {
                         __syncwarp();
                         store_lines(a, buf, lane, ti.g0 + r0, r0, ti.clo, ti.chi, right ? n - 32 : n,
                                     a.y_bf16 && !right ? 64 : 128);
@@ -685,29 +716,58 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
     }
 }
 
+// one launch in clusters of `cluster` CTAs, overlapping the tail of the stream's last kernel
+template <typename K>
+h32_status launch_clusters(K kernel, int grid, int threads, size_t smem, int cluster, cudaStream_t s,
+                           const CUtensorMap *maps, const F8Args &a) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], a);
+    return launch_status(e != cudaSuccess ? e : cudaGetLastError());
+}
+
 template <int NC>
 h32_status launch_rows(const uint8_t *wq, const uint8_t *xq, const float *xd, int64_t ldxd, F8Args a, int64_t tiles,
                        int sms, cudaStream_t s) {
     using C = Rows<NC>;
-    const size_t table = Groups::bytes(a.E) + 1024;
-    const int fit = static_cast<int>((kMaxSmem - table) / C::kStage);
+    const int nb = (a.K + 127) / 128;
+    // Fewer tiles than SMs: a tile to the CTAs of a cluster, each a share of the K steps of at
+    // least 4, as long as all of them run at once.  (5120 x 5120 and 7 tokens:
+    // one CTA a tile 12.6 us, 4 7.2.)
+    a.cluster = 1;
+    if (!a.off)
+        while (2 * a.cluster <= C::kMaxCluster && tiles * 2 * a.cluster <= C::kPerSm * int64_t(sms) && nb >= 8 * a.cluster)
+            a.cluster *= 2;
+    const bool two = tiles * a.cluster > sms && a.cluster > 1;
+    const size_t rest = Groups::bytes(a.E) + 1024 + C::parts(a.cluster);
+    const int fit = static_cast<int>(((two ? kMaxSmem / 2 : kMaxSmem) - rest) / C::kStage);
     a.stages = fit < kMaxStages ? fit : kMaxStages;
     CUtensorMap maps[3];
     if (!code_map(&maps[0], wq, a.K, int64_t(a.E) * a.N, 128) || !code_map(&maps[1], xq, a.K, a.M, NC) ||
-        !scale_map(&maps[2], xd, ldxd, (a.K + 127) / 128, NC)) {
+        !scale_map(&maps[2], xd, ldxd, nb, NC)) {
         note_error("cuTensorMapEncodeTiled rejected a tensor map of the 8-bit product");
         return H32_ERR_CUDA;
     }
-    const int grid = static_cast<int>(tiles < sms ? tiles : sms);
-    cudaError_t e = cudaFuncSetAttribute(rows_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e == cudaSuccess)
-        e = launch_pdl(rows_kernel<NC>, dim3(grid), dim3(kRowsWarps * 32), a.stages * C::kStage + table, s, maps[0],
-                       maps[1], maps[2], a);
-    return launch_status(e != cudaSuccess ? e : cudaGetLastError());
+    const int grid = a.cluster > 1 ? static_cast<int>(tiles * a.cluster) : static_cast<int>(tiles < sms ? tiles : sms);
+    return launch_clusters(rows_kernel<NC>, grid, kRowsWarps * 32, a.stages * C::kStage + rest, a.cluster, s, maps, a);
 }
 
+template <int kChunks>
 h32_status launch_pair(const uint8_t *wq, const uint8_t *xq, const float *xd, int64_t ldxd, F8Args a, int64_t tiles,
                        int sms, cudaStream_t s) {
+    a.bn = 64 * kChunks;
     const uint32_t stage = Pair::kA + Pair::b_bytes(a.bn) + 512;
     const size_t rest = Groups::bytes(a.E) + 2 * 1024 + 2 * 512 + 8 * 4096;
     const int fit = static_cast<int>((kMaxSmem - rest) / stage);
@@ -719,32 +779,17 @@ h32_status launch_pair(const uint8_t *wq, const uint8_t *xq, const float *xd, in
         return H32_ERR_CUDA;
     }
     const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(kPairWarps * 32);
-    cfg.dynamicSmemBytes = a.stages * stage + rest;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
     // the epilogue's setmaxnreg.inc waits until the pool holds its registers: never launch
     // with fewer registers a thread than the hand-over assumes
     static const int regs = [] {
         cudaFuncAttributes fa{};
-        return cudaFuncGetAttributes(&fa, pair_kernel) == cudaSuccess ? fa.numRegs : -1;
+        return cudaFuncGetAttributes(&fa, pair_kernel<kChunks>) == cudaSuccess ? fa.numRegs : -1;
     }();
     if (regs < 168) {
         note_error("8-bit product compiled with fewer registers than its warpgroups hand over");
         return H32_ERR_CUDA;
     }
-    cudaError_t e = cudaFuncSetAttribute(pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, pair_kernel, maps[0], maps[1], maps[2], a);
-    return launch_status(e != cudaSuccess ? e : cudaGetLastError());
+    return launch_clusters(pair_kernel<kChunks>, 2 * pairs, kPairWarps * 32, a.stages * stage + rest, 2, s, maps, a);
 }
 
 h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint8_t *xq, const float *xd,
@@ -783,16 +828,27 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
     a.y_vec = ldy * (a.y_bf16 ? 2 : 4) % 16 == 0;
     a.wait_limit = wait_limit();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // columns for the tokens of one group, as far as the host knows them
+    // Tokens of a group, as far as the host knows them, decide the kernel.  Dense, 34816 x
+    // 5120: 32 tokens as columns 39 us, on the lanes 44; 50 tokens 42 (as 64 columns) and
+    // 44, but 5120 x 5120 27 and 21.  Experts (128 of 1536 x 2048) with 4, 16 and 32 tokens on
+    // average: 16 columns 67, 101 and 151 us, 32 columns 75, 85 and 129, lanes 100, 102 and 103
+    // (groups differ, and a second chunk reads the weights again).
     const int64_t per = (M + E - 1) / E;
-    if (per <= 16) return launch_rows<16>(wq, xq, xd, ldxd, a, nt * (off ? E : (M + 15) / 16), sms, s);
-    if (per <= 32) return launch_rows<32>(wq, xq, xd, ldxd, a, nt * (off ? E : (M + 31) / 32), sms, s);
-    if (per <= 64) return launch_rows<64>(wq, xq, xd, ldxd, a, nt * (off ? E : (M + 63) / 64), sms, s);
-    if (per > 128) {
-        a.bn = 256;
-        return launch_pair(wq, xq, xd, ldxd, a, (N + 255) / 256 * (off ? E + M / 256 : (M + 255) / 256), sms, s);
-    }
-    return launch_rows<128>(wq, xq, xd, ldxd, a, nt * (off ? E : (M + 127) / 128), sms, s);
+    if (per <= (off ? 8 : 16)) return launch_rows<16>(wq, xq, xd, ldxd, a, nt * E, sms, s);
+    if (per <= (off ? 20 : 32)) return launch_rows<32>(wq, xq, xd, ldxd, a, nt * E, sms, s);
+    // The width of a tile: a K step of 64, 128 and 256 weight rows takes 332, 355 and
+    // 406 ns (256 x 5120 against 5120 rows; 192 rows 444, so never), a tile's end about 3 us
+    // for 256 rows; the narrow ones pay where they fill pairs that were idle (256 tokens x
+    // 8192 x 5120: 128 rows 29.5 us, 256 rows 33.6).
+    const int64_t chunks = off ? E + M / 256 : (M + 255) / 256, nb = (K + 127) / 128;
+    const auto cost = [&](int64_t bn, int64_t step) {
+        const int64_t tiles = (N + bn - 1) / bn * chunks;
+        return (tiles + sms / 2 - 1) / (sms / 2) * (nb * step + 12 * bn);
+    };
+    const int64_t c64 = cost(64, 332), c128 = cost(128, 355), c256 = cost(256, 406);
+    if (c256 <= c128 && c256 <= c64) return launch_pair<4>(wq, xq, xd, ldxd, a, (N + 255) / 256 * chunks, sms, s);
+    if (c128 <= c64) return launch_pair<2>(wq, xq, xd, ldxd, a, (N + 127) / 128 * chunks, sms, s);
+    return launch_pair<1>(wq, xq, xd, ldxd, a, (N + 63) / 64 * chunks, sms, s);
 }
 
 }  // namespace
