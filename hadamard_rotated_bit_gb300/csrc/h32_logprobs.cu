@@ -10,7 +10,8 @@
 // above the warp's k-th goes to a short buffer, and each 32 of those are sorted and merged
 // by shuffles.  Before the first merge the k-th largest of the lanes' first maxima is
 // the bound, and the warps of a CTA share their bounds, so after the first few thousand
-// values hardly any gets that far.
+// values hardly any gets that far.  What the warps have left at the end is ranked by
+// counting, for each key, the larger ones (every step of a sort waits for the one before).
 //
 // A row is one CTA's, or with few rows a cluster's: its CTAs take consecutive parts and
 // leave their results in the first one's shared memory.
@@ -139,9 +140,16 @@ struct Best {
     __device__ __forceinline__ void share(uint32_t o) {
         if (lane == 0) atomicMax(shared, static_cast<int32_t>(o ^ 0x80000000u));
     }
-    // from the first maxima of the lanes
+    // from the first maxima of the lanes: the k-th largest, by counting
     __device__ __forceinline__ void first(float cm) {
-        const uint32_t o = __shfl_sync(0xFFFFFFFFu, sort_warp(ordered(cm), lane), k - 1);
+        const uint32_t mine = ordered(cm);
+        int above = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const uint32_t other = __shfl_sync(0xFFFFFFFFu, mine, i);
+            above += other > mine || (other == mine && i < lane);
+        }
+        const uint32_t o = __shfl_sync(0xFFFFFFFFu, mine, __ffs(__ballot_sync(0xFFFFFFFFu, above == k - 1)) - 1);
         if (value_of(o) > -INFINITY) {
             bound = fmaxf(bound, below(o));
             share(o);
@@ -172,11 +180,33 @@ struct Best {
             share(static_cast<uint32_t>(kth >> 32));
         }
     }
-    __device__ __forceinline__ void finish() {
+    // What is left, appended to the CTA's (at most 63 a warp): keys below the bound are not
+    // among its k.
+    __device__ __forceinline__ void leave(uint64_t *all, int *count) {
+        const uint32_t least = static_cast<uint32_t>(*static_cast<volatile int32_t *>(shared)) ^ 0x80000000u;
         const uint64_t last = lane < pending ? buf[lane] : 0;
-        key = merge_sorted(key, sort_warp(last, lane), lane);
+        const uint32_t a = __ballot_sync(0xFFFFFFFFu, key != 0 && key >> 32 >= least);
+        const uint32_t b = __ballot_sync(0xFFFFFFFFu, last != 0 && last >> 32 >= least);
+        int at = 0;
+        if (lane == 0) at = atomicAdd(count, __popc(a) + __popc(b));
+        at = __shfl_sync(0xFFFFFFFFu, at, 0);
+        const uint32_t before = (1u << lane) - 1;
+        if (a >> lane & 1) all[at + __popc(a & before)] = key;
+        if (b >> lane & 1) all[at + __popc(a) + __popc(b & before)] = last;
     }
 };
+
+// the `top` largest of n different keys, in order, by counting the larger ones of each
+__device__ __forceinline__ void rank_keys(const uint64_t *keys, int n, int top, uint64_t *best) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t mine = keys[i];
+        if (mine == 0) continue;
+        int above = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) above += keys[j] > mine;
+        if (above < top) best[above] = mine;
+    }
+}
 
 __device__ __forceinline__ uint32_t rank_in_cluster() {
     uint32_t r;
@@ -208,11 +238,17 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
     __shared__ Part s_part[kMaxCluster];
     __shared__ float s_m[kWarps], s_S[kWarps], s_W[kWarps];
     __shared__ int32_t s_bound;
-    __shared__ int s_count[2];
+    __shared__ int s_count[2], s_left;
+    __shared__ uint64_t s_all[kWarps * 64], s_best[kMaxTop];
+    static_assert(kMaxCluster * kMaxTop <= kWarps * 64, "the cluster's keys");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t c = cluster_size(), rank = rank_in_cluster();
     const int64_t row = blockIdx.x / c;
-    if (threadIdx.x == 0) s_bound = static_cast<int32_t>(ordered(-INFINITY) ^ 0x80000000u);
+    if (threadIdx.x == 0) {
+        s_bound = static_cast<int32_t>(ordered(-INFINITY) ^ 0x80000000u);
+        s_left = 0;
+    }
+    if (threadIdx.x < kMaxTop) s_part[rank].best[threadIdx.x] = s_best[threadIdx.x] = 0;
     pdl_wait();
     pdl_trigger();
     __syncthreads();
@@ -274,12 +310,19 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
             if (step == step0) best.first(cm);
             best.look();
             if (__any_sync(0xFFFFFFFFu, cm > best.bound)) {
+                // a lane's values above the bound, one at a time (mostly there is one)
+                uint32_t mask = 0;
+#pragma unroll
+                for (int e = 0; e < kVecs * kN; ++e) mask |= static_cast<uint32_t>(v[e / kN][e % kN] > best.bound) << e;
                 const uint32_t i0 = static_cast<uint32_t>(head + ((step * kWarps + warp) * (32 * kVecs) + lane) * kN);
+                while (__any_sync(0xFFFFFFFFu, mask != 0)) {
+                    const int at = __ffs(mask) - 1;
+                    float x = v[0][0];
 #pragma unroll
-                for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-                    for (int i = 0; i < kN; ++i)
-                        best.push(v[u][i] > best.bound, v[u][i], i0 + u * 32 * kN + i);
+                    for (int e = 1; e < kVecs * kN; ++e) x = at == e ? v[e / kN][e % kN] : x;
+                    best.push(mask != 0, x, i0 + (at / kN) * 32 * kN + at % kN);
+                    mask &= mask - 1;
+                }
                 best.raise();
             }
         }
@@ -293,43 +336,40 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
         join(m, S, W, fmaxf(v, -FLT_MAX), v > -INFINITY ? 1.0f : v == v ? 0.0f : v, 0.0f);
         if (a.top > 0) best.push(v >= best.bound && v > -INFINITY, v, static_cast<uint32_t>(at));
     }
-    if (a.top > 0) best.finish();
+    if (a.top > 0) best.leave(s_all, &s_left);
 
     // the warp's, then the CTA's
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         join(m, S, W, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, S, o),
              __shfl_xor_sync(0xFFFFFFFFu, W, o));
-    __syncwarp();
-    s_buf[warp][lane] = best.key;
     if (lane == 0) {
         s_m[warp] = m;
         s_S[warp] = S;
         s_W[warp] = W;
     }
     __syncthreads();
-    if (warp == 0) {
-        m = s_m[0], S = s_S[0], W = s_W[0];
+    if (a.top > 0) rank_keys(s_all, s_left, a.top, s_part[rank].best);
+    m = s_m[0], S = s_S[0], W = s_W[0];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) join(m, S, W, s_m[w], s_S[w], s_W[w]);
-        if (a.top > 0)
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) best.key = merge_sorted(best.key, s_buf[w][lane], lane);
-        s_part[rank].best[lane] = best.key;
-        if (lane == 0) {
-            s_part[rank].m = m;
-            s_part[rank].S = S;
-            s_part[rank].W = W;
-        }
+    for (int w = 1; w < kWarps; ++w) join(m, S, W, s_m[w], s_S[w], s_W[w]);
+    if (threadIdx.x == 0) {
+        s_part[rank].m = m;
+        s_part[rank].S = S;
+        s_part[rank].W = W;
     }
     if (c > 1) {
         sync_cluster();   // (every CTA of the cluster runs, and its part is in its shared memory)
         if (rank != 0) to_first(&s_part[rank], &s_part[rank], sizeof(Part));
         sync_cluster();
         if (rank != 0) return;
-    } else {
-        __syncthreads();
+        if (a.top > 0) {
+            if (threadIdx.x < c * kMaxTop) s_all[threadIdx.x] = s_part[threadIdx.x / kMaxTop].best[threadIdx.x % kMaxTop];
+            __syncthreads();
+            rank_keys(s_all, c * kMaxTop, a.top, s_best);
+        }
     }
+    __syncthreads();
     // the row's
     m = s_part[0].m, S = s_part[0].S, W = s_part[0].W;
     for (uint32_t r = 1; r < c; ++r) join(m, S, W, s_part[r].m, s_part[r].S, s_part[r].W);
@@ -363,8 +403,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
         a.logprob[row * a.n + i] = t < 0 ? 0.0f : t >= a.V ? NAN : logprob_of(load_logit<kBf16>(l, t));
     }
     if (warp == 0 && a.top > 0) {
-        uint64_t key = s_part[0].best[lane];
-        for (uint32_t r = 1; r < c; ++r) key = merge_sorted(key, s_part[r].best[lane], lane);
+        const uint64_t key = c > 1 ? s_best[lane] : s_part[0].best[lane];
         const int found = min(a.top, __popc(__ballot_sync(0xFFFFFFFFu, key != 0)));
         int32_t *ids = a.top_id + row * a.top;
         float *lps = a.top_logprob + row * a.top;
