@@ -111,21 +111,62 @@ __global__ void __launch_bounds__(256) act_f8_kernel(const void *__restrict__ x,
     }
 }
 
-// One 128 x 128 block a CTA: four lanes hold a row's 128 values, 512 threads the block.
+// One 128 x 128 block a CTA: four lanes hold a row's 128 values, 512 threads the block.  It
+// comes through shared memory (16-byte copies of whole lines: a thread reading its own 128
+// bytes directly took twice the time, 264 us for 34816 x 5120 fp32), swizzled so that the
+// eight lanes of a quarter warp, two rows of four blocks, read eight different bank groups.
+__device__ __forceinline__ void copy16(void *smem_dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
+
+template <bool kBf16>
+struct WeightTile {
+    static constexpr int kPieces = kBf16 ? 16 : 32;   // 16-byte pieces of a row's 128 values
+    static constexpr int kBytes = 128 * kPieces * 16;
+    // where piece p of row r stands: its block's (p / (kPieces / 4)) and the row's low bits
+    // move it within the line
+    static __device__ __forceinline__ int at(int r, int p) {
+        const int turn = kBf16 ? ((p >> 3) + 2 * (r & 1)) & 3 : ((p >> 3) + 4 * (r & 1)) & 7;
+        return (r * kPieces + (p ^ turn)) * 16;
+    }
+};
+
 template <bool kBf16, int kRot>
-__global__ void __launch_bounds__(512) weights_f8_kernel(const void *__restrict__ w, uint32_t N, uint32_t nb,
-                                                         uint32_t groups, int64_t ldw,
-                                                         uint8_t *__restrict__ wq, float *__restrict__ wd) {
+__global__ void __launch_bounds__(512, 2) weights_f8_kernel(const void *__restrict__ w, uint32_t N, uint32_t nb,
+                                                            uint32_t groups, int64_t ldw,
+                                                            uint8_t *__restrict__ wq, float *__restrict__ wd) {
+    using T = WeightTile<kBf16>;
+    extern __shared__ __align__(128) uint8_t s_tile[];
     __shared__ float s_amax[16];
     const uint32_t tile_n = blockIdx.x / groups, g = blockIdx.x - tile_n * groups;
-    const uint32_t row = tile_n * 128 + (threadIdx.x >> 2), b = g * 4 + (threadIdx.x & 3);
-    const bool in = row < N && b < nb;
-    float v[32];
-    if (in) {
-        load_block<kBf16>(w, int64_t(row) * ldw + 32 * b, v);
-    } else {
+    constexpr int kSize = kBf16 ? 2 : 4, kRows = 512 / T::kPieces;   // rows a round of copies covers
+    const int p = threadIdx.x % T::kPieces;
+    const uint8_t *base = static_cast<const uint8_t *>(w) + (int64_t(tile_n) * 128 * ldw + g * 128) * kSize + p * 16;
+    const bool col_in = g * 128 + p * (16 / kSize) < nb * 32;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+    for (int i = 0; i < 128 / kRows; ++i) {
+        const int r = i * kRows + threadIdx.x / T::kPieces;
+        const bool in = col_in && tile_n * 128 + r < N;
+        copy16(s_tile + T::at(r, p), in ? base + r * ldw * kSize : w, in);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    const uint32_t r = threadIdx.x >> 2, j = threadIdx.x & 3, row = tile_n * 128 + r, b = g * 4 + j;
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < T::kPieces / 4; ++i) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(s_tile + T::at(r, j * (T::kPieces / 4) + i));
+        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if constexpr (kBf16) {
+                v[8 * i + 2 * q] = __uint_as_float(x[q] << 16);
+                v[8 * i + 2 * q + 1] = __uint_as_float(x[q] & 0xFFFF0000u);
+            } else {
+                v[4 * i + q] = __uint_as_float(x[q]);
+            }
+        }
     }
     rotate_block<kRot>(v, b, 0xFFFFFFFFu);
     float amax = block_amax(v);
@@ -138,7 +179,7 @@ __global__ void __launch_bounds__(512) weights_f8_kernel(const void *__restrict_
     for (int i = 1; i < 16; ++i) amax = fmaxf(amax, s_amax[i]);
     uint32_t c[8];
     const float d = f8_codes(v, amax, c);
-    if (in) store_codes(wq + (int64_t(row) * nb + b) * 32, c);
+    if (row < N && b < nb) store_codes(wq + (int64_t(row) * nb + b) * 32, c);
     if (threadIdx.x == 0) wd[int64_t(tile_n) * groups + g] = d;
 }
 
@@ -222,7 +263,10 @@ extern "C" h32_status h32_quantize_weights_f8(const void *w, h32_in_dtype dt, in
     int sms = 0;
     H32_TRY(check_device(&sms));
     const auto kernel = dt == H32_IN_BF16 ? weights_kernel<true>(rotate) : weights_kernel<false>(rotate);
-    kernel<<<static_cast<int>(tiles), 512, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+    const int smem = dt == H32_IN_BF16 ? WeightTile<true>::kBytes : WeightTile<false>::kBytes;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return launch_status(e);
+    kernel<<<static_cast<int>(tiles), 512, smem, reinterpret_cast<cudaStream_t>(stream)>>>(
         w, static_cast<uint32_t>(N), static_cast<uint32_t>(K / 32), static_cast<uint32_t>(groups), ldw, wq, wd);
     return launch_status(cudaGetLastError());
 }

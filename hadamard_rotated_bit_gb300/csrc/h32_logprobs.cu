@@ -140,8 +140,9 @@ struct Best {
     __device__ __forceinline__ void share(uint32_t o) {
         if (lane == 0) atomicMax(shared, static_cast<int32_t>(o ^ 0x80000000u));
     }
-    // from the first maxima of the lanes: the k-th largest, by counting
-    __device__ __forceinline__ void first(float cm) {
+    // The first bound, from the lanes' first maxima: their k-th largest, and the least of the
+    // warps' ceil(k / warps)-th largest (k values of the CTA are not below it).  Every warp.
+    __device__ __forceinline__ void first(float cm, int32_t *least) {
         const uint32_t mine = ordered(cm);
         int above = 0;
 #pragma unroll
@@ -149,11 +150,13 @@ struct Best {
             const uint32_t other = __shfl_sync(0xFFFFFFFFu, mine, i);
             above += other > mine || (other == mine && i < lane);
         }
+        if (above == (k + kWarps - 1) / kWarps - 1) atomicMin(least, static_cast<int32_t>(mine ^ 0x80000000u));
         const uint32_t o = __shfl_sync(0xFFFFFFFFu, mine, __ffs(__ballot_sync(0xFFFFFFFFu, above == k - 1)) - 1);
-        if (value_of(o) > -INFINITY) {
-            bound = fmaxf(bound, below(o));
-            share(o);
-        }
+        if (value_of(o) > -INFINITY) share(o);
+        __syncthreads();
+        if (threadIdx.x == 0) atomicMax(shared, *static_cast<volatile int32_t *>(least));
+        const uint32_t l = static_cast<uint32_t>(*static_cast<volatile int32_t *>(least)) ^ 0x80000000u;
+        if (value_of(l) > -INFINITY) bound = fmaxf(bound, below(l));
     }
     __device__ __forceinline__ void push(bool p, float v, uint32_t i) {
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, p);
@@ -196,15 +199,19 @@ struct Best {
     }
 };
 
-// the `top` largest of n different keys, in order, by counting the larger ones of each
+// the `top` largest of n different keys, in order, by counting the larger ones of each;
+// keys [n .. n + 3] are 0
 __device__ __forceinline__ void rank_keys(const uint64_t *keys, int n, int top, uint64_t *best) {
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const uint64_t mine = keys[i];
-        if (mine == 0) continue;
         int above = 0;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) above += keys[j] > mine;
-        if (above < top) best[above] = mine;
+#pragma unroll 2
+        for (int j = 0; j < n; j += 4) {
+            const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(keys + j);
+            const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(keys + j + 2);
+            above += (p.x > mine) + (p.y > mine) + (q.x > mine) + (q.y > mine);
+        }
+        if (above < top) best[above] = mine;   // (0, no key: above all that are)
     }
 }
 
@@ -237,15 +244,17 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
     __shared__ uint64_t s_buf[kWarps][64];
     __shared__ Part s_part[kMaxCluster];
     __shared__ float s_m[kWarps], s_S[kWarps], s_W[kWarps];
-    __shared__ int32_t s_bound;
+    __shared__ int32_t s_bound, s_least;
     __shared__ int s_count[2], s_left;
-    __shared__ uint64_t s_all[kWarps * 64], s_best[kMaxTop];
+    __shared__ __align__(16) uint64_t s_all[kWarps * 64 + 4];
+    __shared__ uint64_t s_best[kMaxTop];
     static_assert(kMaxCluster * kMaxTop <= kWarps * 64, "the cluster's keys");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t c = cluster_size(), rank = rank_in_cluster();
     const int64_t row = blockIdx.x / c;
     if (threadIdx.x == 0) {
         s_bound = static_cast<int32_t>(ordered(-INFINITY) ^ 0x80000000u);
+        s_least = INT32_MAX;
         s_left = 0;
     }
     if (threadIdx.x < kMaxTop) s_part[rank].best[threadIdx.x] = s_best[threadIdx.x] = 0;
@@ -286,11 +295,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
 #pragma unroll
         for (int u = 0; u < kVecs; ++u) v[u] = next[u];
         load(step + 1, next);
-        float cm = v[0][0];
+        float vm[kVecs], cm;
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u)
+        for (int u = 0; u < kVecs; ++u) {
+            vm[u] = v[u][0];
 #pragma unroll
-            for (int i = 0; i < kN; ++i) cm = fmaxf(cm, v[u][i]);
+            for (int i = 1; i < kN; ++i) vm[u] = fmaxf(vm[u], v[u][i]);
+            cm = u == 0 ? vm[0] : fmaxf(cm, vm[u]);
+        }
         // (what was summed so far, under the new maximum)
         const float top = fmaxf(m, cm);
         const float dm = fmaxf(m - top, kFar), f = exp2_fast(dm * kLog2e);
@@ -307,21 +319,26 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
                 W = fmaf(e, d, W);
             }
         if (a.top > 0) {
-            if (step == step0) best.first(cm);
+            if (step == step0) best.first(cm, &s_least);
             best.look();
             if (__any_sync(0xFFFFFFFFu, cm > best.bound)) {
-                // a lane's values above the bound, one at a time (mostly there is one)
-                uint32_t mask = 0;
 #pragma unroll
-                for (int e = 0; e < kVecs * kN; ++e) mask |= static_cast<uint32_t>(v[e / kN][e % kN] > best.bound) << e;
-                const uint32_t i0 = static_cast<uint32_t>(head + ((step * kWarps + warp) * (32 * kVecs) + lane) * kN);
-                while (__any_sync(0xFFFFFFFFu, mask != 0)) {
-                    const int at = __ffs(mask) - 1;
-                    float x = v[0][0];
+                for (int u = 0; u < kVecs; ++u) {
+                    if (!__any_sync(0xFFFFFFFFu, vm[u] > best.bound)) continue;
+                    // a lane's values above the bound, one at a time (mostly there is one)
+                    uint32_t mask = 0;
 #pragma unroll
-                    for (int e = 1; e < kVecs * kN; ++e) x = at == e ? v[e / kN][e % kN] : x;
-                    best.push(mask != 0, x, i0 + (at / kN) * 32 * kN + at % kN);
-                    mask &= mask - 1;
+                    for (int i = 0; i < kN; ++i) mask |= static_cast<uint32_t>(v[u][i] > best.bound) << i;
+                    const uint32_t i0 =
+                        static_cast<uint32_t>(head + ((step * kWarps + warp) * (32 * kVecs) + 32 * u + lane) * kN);
+                    while (__any_sync(0xFFFFFFFFu, mask != 0)) {
+                        const int at = __ffs(mask) - 1;
+                        float x = v[u][0];
+#pragma unroll
+                        for (int i = 1; i < kN; ++i) x = at == i ? v[u][i] : x;
+                        best.push(mask != 0, x, i0 + at);
+                        mask &= mask - 1;
+                    }
                 }
                 best.raise();
             }
@@ -349,7 +366,11 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
         s_W[warp] = W;
     }
     __syncthreads();
-    if (a.top > 0) rank_keys(s_all, s_left, a.top, s_part[rank].best);
+    if (a.top > 0) {
+        if (threadIdx.x < 4) s_all[s_left + threadIdx.x] = 0;
+        __syncthreads();
+        rank_keys(s_all, s_left, a.top, s_part[rank].best);
+    }
     m = s_m[0], S = s_S[0], W = s_W[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) join(m, S, W, s_m[w], s_S[w], s_W[w]);
@@ -364,9 +385,11 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
         sync_cluster();
         if (rank != 0) return;
         if (a.top > 0) {
-            if (threadIdx.x < c * kMaxTop) s_all[threadIdx.x] = s_part[threadIdx.x / kMaxTop].best[threadIdx.x % kMaxTop];
+            const int n = static_cast<int>(c) * a.top;
+            for (int i = threadIdx.x; i < n + 4; i += kThreads)
+                s_all[i] = i < n ? s_part[i / a.top].best[i % a.top] : 0;
             __syncthreads();
-            rank_keys(s_all, c * kMaxTop, a.top, s_best);
+            rank_keys(s_all, n, a.top, s_best);
         }
     }
     __syncthreads();
