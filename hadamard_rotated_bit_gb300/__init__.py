@@ -1195,6 +1195,17 @@ def _blocks128(n) -> int:
     return (int(n) + 127) // 128
 
 
+def _plain(dev, dtype, *tensors):
+    """Whether all are contiguous tensors of `dtype` on CUDA device `dev`: what most calls
+    pass, found out in a fraction of the time that the checks with their messages take
+    (their sizes are compared by the caller)."""
+    kind = _torch().Tensor
+    for t in tensors:
+        if not (isinstance(t, kind) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+            return False
+    return True
+
+
 def h32_quantize_act_f8(x, rotate=False, row_idx=None, xq=None, xd=None, stream=None):
     """x [T][K] bf16/fp32 -> (xq [R][K] uint8 e4m3 codes, xd [ceil(K/128)][ldxd] fp32):
     one scale amax / 448 for each 128 values of a row, group-major.
@@ -1203,28 +1214,32 @@ def h32_quantize_act_f8(x, rotate=False, row_idx=None, xq=None, xd=None, stream=
     product); None: R = T.  rotate as for the other quantizers, here off by default
     (weights quantized elsewhere are not rotated)."""
     torch = _torch()
-    f32 = (torch.float32,)
-    _need(x, "x", (torch.bfloat16, torch.float32), (_ge(0), _ge(0)), pitched=True)
+    bf16, f32, i32, u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+    if not (isinstance(x, torch.Tensor) and x.dim() == 2 and x.dtype in (bf16, f32) and x.is_cuda
+            and x.is_contiguous() and xq is None and xd is None
+            and (row_idx is None or (_plain(x.get_device(), i32, row_idx) and row_idx.dim() == 1))):
+        _need(x, "x", (bf16, f32), (_ge(0), _ge(0)), pitched=True)
+        R, K = x.shape
+        if row_idx is not None:
+            _need(row_idx, "row_idx", (i32,), (_ge(0),))
+            R = row_idx.shape[0]
+        if xq is not None:
+            _need(xq, "xq", (u8,), (_ge(R), K))
+        if xd is not None:
+            _need(xd, "xd", (f32,), (_ge(_blocks128(K)), _ge(R)))
+        _same_gpu(("x", x), ("row_idx", row_idx), ("xq", xq), ("xd", xd))
     T, K = x.shape
-    R = T
-    if row_idx is not None:
-        _need(row_idx, "row_idx", (torch.int32,), (_ge(0),))
-        R = row_idx.shape[0]
-    if xq is not None:
-        _need(xq, "xq", (torch.uint8,), (_ge(R), K))
-    if xd is not None:
-        _need(xd, "xd", f32, (_ge(_blocks128(K)), _ge(R)))
-    _same_gpu(("x", x), ("row_idx", row_idx), ("xq", xq), ("xd", xd))
+    R = T if row_idx is None else row_idx.shape[0]
     dev = x.device
     raw, guard = _enter_stream(dev, stream)
     try:
         if xq is None:
-            xq = torch.empty((R, K), dtype=torch.uint8, device=dev)
+            xq = torch.empty((R, K), dtype=u8, device=dev)
         if xd is None:
-            xd = torch.empty((_blocks128(K), (R + 3) // 4 * 4), dtype=torch.float32, device=dev)
-        st = lib().h32_quantize_act_f8(x.data_ptr(), x.dtype == torch.bfloat16, T, K, _pitch(x),
-                                       _raw(row_idx), R, xq.data_ptr(), xd.data_ptr(), xd.shape[1],
-                                       _rot_arg(rotate), raw)
+            xd = torch.empty(((K + 127) // 128, (R + 3) // 4 * 4), dtype=f32, device=dev)
+        st = lib().h32_quantize_act_f8(x.data_ptr(), x.dtype == bf16, T, K, x.stride(0) if T > 1 else K,
+                                       None if row_idx is None else row_idx.data_ptr(), R, xq.data_ptr(),
+                                       xd.data_ptr(), xd.shape[1], _rot_arg(rotate), raw)
     finally:
         if guard is not None:
             guard.__exit__(None, None, None)
@@ -1276,42 +1291,52 @@ def h32_f8_gemm_experts(wq, wd, xq, xd, expert_off, N, R=None, y=None, y_dtype=N
 
 def _f8_gemm(fn, wq, wd, xq, xd, off, N, M, y, y_dtype, stream):
     torch = _torch()
-    bf16, f32, u8 = torch.bfloat16, torch.float32, (torch.uint8,)
-    _need(wq, "wq", u8, (_ge(0), _ge(0)))
-    rows, K = wq.shape
-    _need(xq, "xq", u8, (_ge(0 if M is None else M), K))
+    bf16, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+    plain = False
+    if M is None and y is None and y_dtype in (None, bf16, f32) and (off is None or type(N) is int and N > 0) and \
+            isinstance(wq, torch.Tensor) and wq.is_cuda and wq.dim() == 2:
+        # the usual call, all sizes as the operands give them
+        (rows, K), dev = wq.shape, wq.get_device()
+        e, n = (1, rows) if off is None else (rows // N, N)
+        plain = (_plain(dev, u8, wq, xq) and _plain(dev, f32, wd, xd) and xq.dim() == 2 and xd.dim() == 2
+                 and xq.shape[1] == K and e * n == rows
+                 and wd.shape == (e * ((n + 127) // 128), (K + 127) // 128)
+                 and xd.shape[0] >= (K + 127) // 128 and xd.shape[1] >= xq.shape[0]
+                 and (off is None or (_plain(dev, i32, off) and off.dim() == 1 and off.shape[0] > e)))
+    if not plain:
+        _need(wq, "wq", (u8,), (_ge(0), _ge(0)))
+        rows, K = wq.shape
+        _need(xq, "xq", (u8,), (_ge(0 if M is None else M), K))
+        e, n = 1, rows
+        if off is not None:
+            n = int(N)
+            if n <= 0 or rows % n != 0:
+                raise ValueError("wq must have E * N rows")
+            e = rows // n
+            _need(off, "expert_off", (i32,), (_ge(e + 1),))
+        _need(wd, "wd", (f32,), (e * _blocks128(n), _blocks128(K)))
+        _need(xd, "xd", (f32,), (_ge(_blocks128(K)), _ge(xq.shape[0] if M is None else M)))
+        if y is not None:
+            _need(y, "y", (bf16, f32), (_ge(xq.shape[0] if M is None else M), _ge(n)), pitched=True)
+            if y_dtype is not None and y_dtype != y.dtype:
+                raise ValueError(f"y is {y.dtype}, y_dtype {y_dtype}")
+        elif y_dtype is not None and y_dtype not in (bf16, f32):
+            raise ValueError("y_dtype must be bf16 or fp32")
+        _same_gpu(("wq", wq), ("wd", wd), ("xq", xq), ("xd", xd), ("expert_off", off), ("y", y))
     if M is None:
         M = xq.shape[0]
-    E = 1
-    if off is None:
-        N = rows
-    else:
-        N = int(N)
-        if N <= 0 or rows % N != 0:
-            raise ValueError("wq must have E * N rows")
-        E = rows // N
-        _need(off, "expert_off", (torch.int32,), (_ge(E + 1),))
-    _need(wd, "wd", (f32,), (E * _blocks128(N), _blocks128(K)))
-    _need(xd, "xd", (f32,), (_ge(_blocks128(K)), _ge(M)))
-    if y is not None:
-        _need(y, "y", (bf16, f32), (_ge(M), _ge(N)), pitched=True)
-        if y_dtype is not None and y_dtype != y.dtype:
-            raise ValueError(f"y is {y.dtype}, y_dtype {y_dtype}")
-    elif y_dtype is not None and y_dtype not in (bf16, f32):
-        raise ValueError("y_dtype must be bf16 or fp32")
-    _same_gpu(("wq", wq), ("wd", wd), ("xq", xq), ("xd", xd), ("expert_off", off), ("y", y))
     dev = wq.device
     raw, guard = _enter_stream(dev, stream)
     try:
         if y is None:
-            y = torch.empty((M, N), dtype=y_dtype or f32, device=dev)
+            y = torch.empty((M, n), dtype=y_dtype or f32, device=dev)
         if off is None:
             st = lib().h32_f8_gemm(wq.data_ptr(), wd.data_ptr(), xq.data_ptr(), xd.data_ptr(),
-                                   xd.shape[1], M, N, K, y.data_ptr(), y.dtype == bf16, _pitch(y), raw)
+                                   xd.shape[1], M, n, K, y.data_ptr(), y.dtype == bf16, _pitch(y), raw)
         else:
             st = lib().h32_f8_gemm_experts(
-                wq.data_ptr(), wd.data_ptr(), E, xq.data_ptr(), xd.data_ptr(), xd.shape[1],
-                off.data_ptr(), M, N, K, y.data_ptr(), y.dtype == bf16, _pitch(y), raw)
+                wq.data_ptr(), wd.data_ptr(), e, xq.data_ptr(), xd.data_ptr(), xd.shape[1],
+                off.data_ptr(), M, n, K, y.data_ptr(), y.dtype == bf16, _pitch(y), raw)
     finally:
         if guard is not None:
             guard.__exit__(None, None, None)
@@ -1333,29 +1358,38 @@ def h32_token_logprobs(logits, targets=None, top=0, logprob=None, entropy=None, 
     fp32, by decreasing logit, ties to the lower id, or None with top = 0)."""
     torch = _torch()
     i32, f32 = (torch.int32,), (torch.float32,)
-    _need(logits, "logits", (torch.bfloat16, torch.float32), (_ge(0), _ge(1)), pitched=True)
-    T, V = logits.shape
     top = int(top)
-    if not 0 <= top <= min(LOGPROBS_MAX_TOP, V):
-        raise ValueError(f"top must be between 0 and {min(LOGPROBS_MAX_TOP, V)}")
-    n = 0
-    if targets is not None:
-        _need(targets, "targets", i32, (T,) if targets.dim() == 1 else (T, _ge(0)))
-        n = 1 if targets.dim() == 1 else targets.shape[1]
-        if logprob is not None:
-            _need(logprob, "logprob", f32, tuple(targets.shape))
-    elif logprob is not None:
-        raise ValueError("logprob needs targets")
-    if entropy is not None:
-        _need(entropy, "entropy", f32, (_ge(T),))
-    if top == 0 and (top_id is not None or top_logprob is not None):
-        raise ValueError("top_id and top_logprob need top")
-    if top_id is not None:
-        _need(top_id, "top_id", i32, (_ge(T), top))
-    if top_logprob is not None:
-        _need(top_logprob, "top_logprob", f32, (_ge(T), top))
-    _same_gpu(("logits", logits), ("targets", targets), ("logprob", logprob), ("entropy", entropy),
-              ("top_id", top_id), ("top_logprob", top_logprob))
+    plain = False
+    if logprob is None and entropy is None and top_id is None and top_logprob is None and \
+            isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() == 2:
+        # the usual call
+        T, V = logits.shape
+        plain = (logits.is_contiguous() and logits.dtype in (torch.bfloat16, torch.float32) and V > 0
+                 and 0 <= top <= min(LOGPROBS_MAX_TOP, V)
+                 and (targets is None or (_plain(logits.get_device(), torch.int32, targets)
+                                          and targets.dim() in (1, 2) and targets.shape[0] == T)))
+    if not plain:
+        _need(logits, "logits", (torch.bfloat16, torch.float32), (_ge(0), _ge(1)), pitched=True)
+        T, V = logits.shape
+        if not 0 <= top <= min(LOGPROBS_MAX_TOP, V):
+            raise ValueError(f"top must be between 0 and {min(LOGPROBS_MAX_TOP, V)}")
+        if targets is not None:
+            _need(targets, "targets", i32, (T,) if targets.dim() == 1 else (T, _ge(0)))
+            if logprob is not None:
+                _need(logprob, "logprob", f32, tuple(targets.shape))
+        elif logprob is not None:
+            raise ValueError("logprob needs targets")
+        if entropy is not None:
+            _need(entropy, "entropy", f32, (_ge(T),))
+        if top == 0 and (top_id is not None or top_logprob is not None):
+            raise ValueError("top_id and top_logprob need top")
+        if top_id is not None:
+            _need(top_id, "top_id", i32, (_ge(T), top))
+        if top_logprob is not None:
+            _need(top_logprob, "top_logprob", f32, (_ge(T), top))
+        _same_gpu(("logits", logits), ("targets", targets), ("logprob", logprob), ("entropy", entropy),
+                  ("top_id", top_id), ("top_logprob", top_logprob))
+    n = 0 if targets is None else 1 if targets.dim() == 1 else targets.shape[1]
     dev = logits.device
     raw, guard = _enter_stream(dev, stream)
     try:

@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 namespace h32 {
@@ -140,6 +141,18 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
             smem_u32(bar)),
         "h"(static_cast<uint16_t>(3))
         : "memory");
+}
+
+// Once a kernel and device: its dynamic shared memory may be up to `bytes`.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};   // a bit a device (check_device admits 64)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (done.load(std::memory_order_relaxed) >> dev & 1)) return e;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    return e;
 }
 
 // tensor maps ----------------------------------------------------------------

@@ -717,8 +717,8 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
 }
 
 // one launch in clusters of `cluster` CTAs, overlapping the tail of the stream's last kernel
-template <typename K>
-h32_status launch_clusters(K kernel, int grid, int threads, size_t smem, int cluster, cudaStream_t s,
+template <auto kKernel>
+h32_status launch_clusters(int grid, int threads, size_t smem, int cluster, cudaStream_t s,
                            const CUtensorMap *maps, const F8Args &a) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
@@ -733,8 +733,8 @@ h32_status launch_clusters(K kernel, int grid, int threads, size_t smem, int clu
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], a);
+    cudaError_t e = allow_smem<kKernel>(kMaxSmem);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kKernel, maps[0], maps[1], maps[2], a);
     return launch_status(e != cudaSuccess ? e : cudaGetLastError());
 }
 
@@ -761,7 +761,7 @@ h32_status launch_rows(const uint8_t *wq, const uint8_t *xq, const float *xd, in
         return H32_ERR_CUDA;
     }
     const int grid = a.cluster > 1 ? static_cast<int>(tiles * a.cluster) : static_cast<int>(tiles < sms ? tiles : sms);
-    return launch_clusters(rows_kernel<NC>, grid, kRowsWarps * 32, a.stages * C::kStage + rest, a.cluster, s, maps, a);
+    return launch_clusters<rows_kernel<NC>>(grid, kRowsWarps * 32, a.stages * C::kStage + rest, a.cluster, s, maps, a);
 }
 
 template <int kChunks>
@@ -789,7 +789,7 @@ h32_status launch_pair(const uint8_t *wq, const uint8_t *xq, const float *xd, in
         note_error("8-bit product compiled with fewer registers than its warpgroups hand over");
         return H32_ERR_CUDA;
     }
-    return launch_clusters(pair_kernel<kChunks>, 2 * pairs, kPairWarps * 32, a.stages * stage + rest, 2, s, maps, a);
+    return launch_clusters<pair_kernel<kChunks>>(2 * pairs, kPairWarps * 32, a.stages * stage + rest, 2, s, maps, a);
 }
 
 h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint8_t *xq, const float *xd,

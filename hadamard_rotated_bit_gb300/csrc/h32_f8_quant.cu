@@ -54,6 +54,26 @@ __device__ __forceinline__ float f8_codes(const float (&v)[32], float amax, uint
     return d;
 }
 
+// rotate_block of h32_quant_block.cuh with one fma a value for the strides across lanes:
+// v + c in the lower block, c - v in the upper one, the same bits (the product is exact)
+template <int kRot>
+__device__ __forceinline__ void rotate(float (&v)[32], uint32_t pos) {
+    if constexpr (kRot <= 32) {
+        rotate_block<kRot>(v, pos, 0xFFFFFFFFu);
+    } else {
+        butterfly32(v);
+#pragma unroll
+        for (int hb = 1; hb < kRot / 32; hb <<= 1) {
+            const float sign = (pos & hb) == 0 ? 1.0f : -1.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __fmaf_rn(v[i], sign, __shfl_xor_sync(0xFFFFFFFFu, v[i], hb));
+        }
+        const float sc = kRot == 64 ? 0.125f : kInvSqrt128;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(v[i], sc);
+    }
+}
+
 template <bool kBf16>
 __device__ __forceinline__ void load_block(const void *x, int64_t at, float (&v)[32]) {
     if constexpr (kBf16) load_block_bf16(static_cast<const uint16_t *>(x) + at, v);
@@ -98,7 +118,7 @@ __global__ void __launch_bounds__(256) act_f8_kernel(const void *__restrict__ x,
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.0f;
         }
-        rotate_block<kRot>(v, b, 0xFFFFFFFFu);
+        rotate<kRot>(v, b);
         float amax = block_amax(v);
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
@@ -111,7 +131,8 @@ __global__ void __launch_bounds__(256) act_f8_kernel(const void *__restrict__ x,
     }
 }
 
-// One 128 x 128 block a CTA: four lanes hold a row's 128 values, 512 threads the block.  It
+// One 128 x 128 block after another: four lanes hold a row's 128 values, 512 threads the
+// block, and the next one is copied while this one is rotated and rounded.  It
 // comes through shared memory (16-byte copies of whole lines: a thread reading its own 128
 // bytes directly took twice the time, 264 us for 34816 x 5120 fp32), swizzled so that the
 // eight lanes of a quarter warp, two rows of four blocks, read eight different bank groups.
@@ -139,48 +160,57 @@ __global__ void __launch_bounds__(512, 2) weights_f8_kernel(const void *__restri
     using T = WeightTile<kBf16>;
     extern __shared__ __align__(128) uint8_t s_tile[];
     __shared__ float s_amax[16];
-    const uint32_t tile_n = blockIdx.x / groups, g = blockIdx.x - tile_n * groups;
     constexpr int kSize = kBf16 ? 2 : 4, kRows = 512 / T::kPieces;   // rows a round of copies covers
-    const int p = threadIdx.x % T::kPieces;
-    const uint8_t *base = static_cast<const uint8_t *>(w) + (int64_t(tile_n) * 128 * ldw + g * 128) * kSize + p * 16;
-    const bool col_in = g * 128 + p * (16 / kSize) < nb * 32;
+    const int p = threadIdx.x % T::kPieces, r0 = threadIdx.x / T::kPieces;
+    const auto copy = [&](uint32_t t) {
+        const uint32_t tile_n = t / groups, g = t - tile_n * groups;
+        const uint8_t *base = static_cast<const uint8_t *>(w) + (int64_t(tile_n) * 128 * ldw + g * 128) * kSize + p * 16;
+        const bool col_in = g * 128 + p * (16 / kSize) < nb * 32;
 #pragma unroll
-    for (int i = 0; i < 128 / kRows; ++i) {
-        const int r = i * kRows + threadIdx.x / T::kPieces;
-        const bool in = col_in && tile_n * 128 + r < N;
-        copy16(s_tile + T::at(r, p), in ? base + r * ldw * kSize : w, in);
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
-    const uint32_t r = threadIdx.x >> 2, j = threadIdx.x & 3, row = tile_n * 128 + r, b = g * 4 + j;
-    float v[32];
+        for (int i = 0; i < 128 / kRows; ++i) {
+            const int r = i * kRows + r0;
+            const bool in = col_in && tile_n * 128 + r < N;
+            copy16(s_tile + T::at(r, p), in ? base + r * ldw * kSize : w, in);
+        }
+    };
+    const uint32_t tiles = (N + 127) / 128 * groups;
+    const uint32_t r = threadIdx.x >> 2, j = threadIdx.x & 3;
+    copy(blockIdx.x);
+    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const uint32_t tile_n = t / groups, g = t - tile_n * groups, row = tile_n * 128 + r, b = g * 4 + j;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        float v[32];
 #pragma unroll
-    for (int i = 0; i < T::kPieces / 4; ++i) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(s_tile + T::at(r, j * (T::kPieces / 4) + i));
-        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+        for (int i = 0; i < T::kPieces / 4; ++i) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(s_tile + T::at(r, j * (T::kPieces / 4) + i));
+            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if constexpr (kBf16) {
-                v[8 * i + 2 * q] = __uint_as_float(x[q] << 16);
-                v[8 * i + 2 * q + 1] = __uint_as_float(x[q] & 0xFFFF0000u);
-            } else {
-                v[4 * i + q] = __uint_as_float(x[q]);
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (kBf16) {
+                    v[8 * i + 2 * q] = __uint_as_float(x[q] << 16);
+                    v[8 * i + 2 * q + 1] = __uint_as_float(x[q] & 0xFFFF0000u);
+                } else {
+                    v[4 * i + q] = __uint_as_float(x[q]);
+                }
             }
         }
+        __syncthreads();
+        if (t + gridDim.x < tiles) copy(t + gridDim.x);   // (under this block's arithmetic)
+        rotate<kRot>(v, b);
+        float amax = block_amax(v);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        if ((threadIdx.x & 31) == 0) s_amax[threadIdx.x >> 5] = amax;
+        __syncthreads();   // (its next write is two barriers on)
+        amax = s_amax[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) amax = fmaxf(amax, s_amax[i]);
+        uint32_t c[8];
+        const float d = f8_codes(v, amax, c);
+        if (row < N && b < nb) store_codes(wq + (int64_t(row) * nb + b) * 32, c);
+        if (threadIdx.x == 0) wd[t] = d;
     }
-    rotate_block<kRot>(v, b, 0xFFFFFFFFu);
-    float amax = block_amax(v);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    if ((threadIdx.x & 31) == 0) s_amax[threadIdx.x >> 5] = amax;
-    __syncthreads();
-    amax = s_amax[0];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) amax = fmaxf(amax, s_amax[i]);
-    uint32_t c[8];
-    const float d = f8_codes(v, amax, c);
-    if (row < N && b < nb) store_codes(wq + (int64_t(row) * nb + b) * 32, c);
-    if (threadIdx.x == 0) wd[int64_t(tile_n) * groups + g] = d;
 }
 
 // what both quantizers ask of their sizes, types and rotation
@@ -259,14 +289,14 @@ extern "C" h32_status h32_quantize_weights_f8(const void *w, h32_in_dtype dt, in
     const int64_t esize = dt == H32_IN_BF16 ? 2 : 4;
     if (!aligned16(w) || !aligned16(wq) || !aligned16(wd) || (ldw * esize) % 16 != 0) return H32_ERR_ALIGNMENT;
     const int64_t groups = (K + 127) / 128, tiles = (N + 127) / 128 * groups;
-    if (tiles > 0x7FFFFFFFll || N > 0x7FFFFFFFll) return H32_ERR_INVALID_ARG;
+    if (tiles > 0x7FFFFFFFll || N > 0x7FFFFFFFll - 128) return H32_ERR_INVALID_ARG;
     int sms = 0;
     H32_TRY(check_device(&sms));
     const auto kernel = dt == H32_IN_BF16 ? weights_kernel<true>(rotate) : weights_kernel<false>(rotate);
     const int smem = dt == H32_IN_BF16 ? WeightTile<true>::kBytes : WeightTile<false>::kBytes;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return launch_status(e);
-    kernel<<<static_cast<int>(tiles), 512, smem, reinterpret_cast<cudaStream_t>(stream)>>>(
+    kernel<<<static_cast<int>(tiles < 2 * sms ? tiles : 2 * sms), 512, smem, reinterpret_cast<cudaStream_t>(stream)>>>(
         w, static_cast<uint32_t>(N), static_cast<uint32_t>(K / 32), static_cast<uint32_t>(groups), ldw, wq, wd);
     return launch_status(cudaGetLastError());
 }
