@@ -5,13 +5,13 @@
 //   log p(i) = (l_i - m) - log S,   H = log S - W / S
 //
 // One pass over the logits.  Each thread keeps m, S and W of what it has read (all fp32,
-// rescaled when m grows).  For the k largest, a warp keeps its best 32 as one sorted
-// 64-bit key a lane (the value as an ordered integer, then the lower index first); a value
-// above the warp's k-th goes to a short buffer, and each 32 of those are sorted and merged
-// by shuffles.  Before the first merge the k-th largest of the lanes' first maxima is
-// the bound, and the warps of a CTA share their bounds, so after the first few thousand
-// values hardly any gets that far.  What the warps have left at the end is ranked by
-// counting, for each key, the larger ones (every step of a sort waits for the one before).
+// rescaled when m grows) and, for the k most probable tokens, the largest value of each of its
+// chunks (16 or 32 values, more in rows beyond 2^15 vectors).  The k-th largest of the 64 maxima
+// of groups of four lanes bounds the k best from below, so only chunks that reach it, hardly
+// more than k, are read again (from L2) for their values above it, and of those the k largest
+// are found by counting, for each, the larger ones.  Nothing in the pass itself depends on
+// the values: buffers filled as candidates come cost 30 to 80% more time there.  Rows where too many
+// values reach the bound (ties, mostly) are read again by warps that keep sorted lists.
 //
 // A row is one CTA's, or with few rows a cluster's: its CTAs take consecutive parts and
 // leave their results in the first one's shared memory.
@@ -26,6 +26,8 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxTop = 32, kMaxCluster = 8;
 constexpr int kVecs = 4;             // 16-byte loads of a thread's step
+constexpr int kSlots = 32;           // chunks of a thread
+constexpr int kMaxChunks = 256, kMaxKeys = 512;   // chunks read again, keys ranked
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kFar = -200.0f;      // e^kFar is 0 in fp32
 
@@ -123,41 +125,15 @@ __device__ __forceinline__ float load_logit(const void *p, int64_t i) {
     else return static_cast<const float *>(p)[i];
 }
 
-// A warp's k best.
-struct Best {
-    uint64_t key = 0;      // the lane's of the sorted list
-    float bound = -INFINITY;   // values at or below it are not among the k
+// A warp's k best of what it is given: a sorted list, a key a lane, and a buffer of values
+// above its k-th, merged 32 at a time.
+struct List {
+    uint64_t key = 0;
+    float bound;           // values at or below it are not among the k
     int pending = 0;
     uint64_t *buf;         // [64], the warp's
-    int32_t *shared;       // the CTA's bound: the largest k-th of its warps, as ordered() - 2^31
     int k, lane;
 
-    // values equal to another warp's k-th may still be among the k by their index
-    __device__ __forceinline__ void look() {
-        const uint32_t o = static_cast<uint32_t>(*static_cast<volatile int32_t *>(shared)) ^ 0x80000000u;
-        bound = fmaxf(bound, below(o));   // (below -inf: NaN, which fmaxf passes over)
-    }
-    __device__ __forceinline__ void share(uint32_t o) {
-        if (lane == 0) atomicMax(shared, static_cast<int32_t>(o ^ 0x80000000u));
-    }
-    // The first bound, from the lanes' first maxima: their k-th largest, and the least of the
-    // warps' ceil(k / warps)-th largest (k values of the CTA are not below it).  Every warp.
-    __device__ __forceinline__ void first(float cm, int32_t *least) {
-        const uint32_t mine = ordered(cm);
-        int above = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const uint32_t other = __shfl_sync(0xFFFFFFFFu, mine, i);
-            above += other > mine || (other == mine && i < lane);
-        }
-        if (above == (k + kWarps - 1) / kWarps - 1) atomicMin(least, static_cast<int32_t>(mine ^ 0x80000000u));
-        const uint32_t o = __shfl_sync(0xFFFFFFFFu, mine, __ffs(__ballot_sync(0xFFFFFFFFu, above == k - 1)) - 1);
-        if (value_of(o) > -INFINITY) share(o);
-        __syncthreads();
-        if (threadIdx.x == 0) atomicMax(shared, *static_cast<volatile int32_t *>(least));
-        const uint32_t l = static_cast<uint32_t>(*static_cast<volatile int32_t *>(least)) ^ 0x80000000u;
-        if (value_of(l) > -INFINITY) bound = fmaxf(bound, below(l));
-    }
     __device__ __forceinline__ void push(bool p, float v, uint32_t i) {
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, p);
         if (mask == 0) return;
@@ -173,29 +149,14 @@ struct Best {
             __syncwarp();
         }
     }
-    // once a step's values are pushed: the k-th of the list is a bound
+    // once a run of ascending indices is pushed: the k-th of the list is a bound
     __device__ __forceinline__ void raise() {
-        const uint64_t kth = __shfl_sync(0xFFFFFFFFu, key, k - 1);
-        if (kth == 0) return;
-        const float v = value_of(static_cast<uint32_t>(kth >> 32));
-        if (v > bound) {
-            bound = v;
-            share(static_cast<uint32_t>(kth >> 32));
-        }
+        const uint32_t kth = static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, key, k - 1) >> 32);
+        if (kth != 0) bound = fmaxf(bound, value_of(kth));
     }
-    // What is left, appended to the CTA's (at most 63 a warp): keys below the bound are not
-    // among its k.
-    __device__ __forceinline__ void leave(uint64_t *all, int *count) {
-        const uint32_t least = static_cast<uint32_t>(*static_cast<volatile int32_t *>(shared)) ^ 0x80000000u;
-        const uint64_t last = lane < pending ? buf[lane] : 0;
-        const uint32_t a = __ballot_sync(0xFFFFFFFFu, key != 0 && key >> 32 >= least);
-        const uint32_t b = __ballot_sync(0xFFFFFFFFu, last != 0 && last >> 32 >= least);
-        int at = 0;
-        if (lane == 0) at = atomicAdd(count, __popc(a) + __popc(b));
-        at = __shfl_sync(0xFFFFFFFFu, at, 0);
-        const uint32_t before = (1u << lane) - 1;
-        if (a >> lane & 1) all[at + __popc(a & before)] = key;
-        if (b >> lane & 1) all[at + __popc(a) + __popc(b & before)] = last;
+    // what is left, as one sorted list
+    __device__ __forceinline__ uint64_t finish() {
+        return merge_sorted(key, sort_warp(lane < pending ? buf[lane] : 0, lane), lane);
     }
 };
 
@@ -241,26 +202,21 @@ template <bool kBf16>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a) {
     using V4 = Vec<kBf16>;
     constexpr int kN = V4::kN;
-    __shared__ uint64_t s_buf[kWarps][64];
+    __shared__ __align__(16) float s_chunk[kSlots][kThreads];   // largest values of the chunks
+    __shared__ __align__(16) uint64_t s_all[kMaxKeys + 4];
+    __shared__ uint64_t s_buf[kWarps][64], s_best[kMaxTop];
+    __shared__ uint32_t s_list[kMaxChunks];
     __shared__ Part s_part[kMaxCluster];
-    __shared__ float s_m[kWarps], s_S[kWarps], s_W[kWarps];
-    __shared__ int32_t s_bound, s_least;
-    __shared__ int s_count[2], s_left;
-    __shared__ __align__(16) uint64_t s_all[kWarps * 64 + 4];
-    __shared__ uint64_t s_best[kMaxTop];
-    static_assert(kMaxCluster * kMaxTop <= kWarps * 64, "the cluster's keys");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ __align__(16) float s_group[64];
+    __shared__ float s_m[kWarps], s_S[kWarps], s_W[kWarps], s_bound;
+    __shared__ int s_count[2], s_chunks, s_keys;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t c = cluster_size(), rank = rank_in_cluster();
     const int64_t row = blockIdx.x / c;
-    if (threadIdx.x == 0) {
-        s_bound = static_cast<int32_t>(ordered(-INFINITY) ^ 0x80000000u);
-        s_least = INT32_MAX;
-        s_left = 0;
-    }
-    if (threadIdx.x < kMaxTop) s_part[rank].best[threadIdx.x] = s_best[threadIdx.x] = 0;
+    if (tid == 0) s_chunks = s_keys = 0;
+    if (tid < kMaxTop) s_part[rank].best[tid] = s_best[tid] = 0;
     pdl_wait();
     pdl_trigger();
-    __syncthreads();
 
     constexpr int kSize = kBf16 ? 2 : 4;
     const uint8_t *l = static_cast<const uint8_t *>(a.logits) + row * a.ldl * kSize;
@@ -271,14 +227,9 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
     // this CTA's vectors: steps of kThreads x kVecs, dealt to the cluster in order
     const int64_t steps = (nvec + kThreads * kVecs - 1) / (kThreads * kVecs);
     const int64_t step0 = steps * rank / c, step1 = steps * (rank + 1) / c;
+    const int64_t per_slot = (step1 - step0 + kSlots - 1) / kSlots;   // steps of a chunk
 
     float m = -FLT_MAX, S = 0.0f, W = 0.0f;
-    Best best;
-    best.buf = s_buf[warp];
-    best.shared = &s_bound;
-    best.k = a.top;
-    best.lane = lane;
-
     // values read as what changes nothing: -inf
     constexpr uint32_t kNone = kBf16 ? 0xFF80FF80u : 0xFF800000u;
     auto load = [&](int64_t step, V4 (&v)[kVecs]) {
@@ -290,19 +241,19 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
     };
     V4 next[kVecs];
     load(step0, next);
+    float chunk = -INFINITY;
+    float *slot = &s_chunk[0][tid];
+    int in_slot = 0, slots = 0;
     for (int64_t step = step0; step < step1; ++step) {
         V4 v[kVecs];
 #pragma unroll
         for (int u = 0; u < kVecs; ++u) v[u] = next[u];
         load(step + 1, next);
-        float vm[kVecs], cm;
+        float cm = v[0][0];
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-            vm[u] = v[u][0];
+        for (int u = 0; u < kVecs; ++u)
 #pragma unroll
-            for (int i = 1; i < kN; ++i) vm[u] = fmaxf(vm[u], v[u][i]);
-            cm = u == 0 ? vm[0] : fmaxf(cm, vm[u]);
-        }
+            for (int i = 0; i < kN; ++i) cm = fmaxf(cm, v[u][i]);
         // (what was summed so far, under the new maximum)
         const float top = fmaxf(m, cm);
         const float dm = fmaxf(m - top, kFar), f = exp2_fast(dm * kLog2e);
@@ -318,44 +269,24 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
                 S += e;
                 W = fmaf(e, d, W);
             }
-        if (a.top > 0) {
-            if (step == step0) best.first(cm, &s_least);
-            best.look();
-            if (__any_sync(0xFFFFFFFFu, cm > best.bound)) {
-#pragma unroll
-                for (int u = 0; u < kVecs; ++u) {
-                    if (!__any_sync(0xFFFFFFFFu, vm[u] > best.bound)) continue;
-                    // a lane's values above the bound, one at a time (mostly there is one)
-                    uint32_t mask = 0;
-#pragma unroll
-                    for (int i = 0; i < kN; ++i) mask |= static_cast<uint32_t>(v[u][i] > best.bound) << i;
-                    const uint32_t i0 =
-                        static_cast<uint32_t>(head + ((step * kWarps + warp) * (32 * kVecs) + 32 * u + lane) * kN);
-                    while (__any_sync(0xFFFFFFFFu, mask != 0)) {
-                        const int at = __ffs(mask) - 1;
-                        float x = v[u][0];
-#pragma unroll
-                        for (int i = 1; i < kN; ++i) x = at == i ? v[u][i] : x;
-                        best.push(mask != 0, x, i0 + at);
-                        mask &= mask - 1;
-                    }
-                }
-                best.raise();
-            }
+        chunk = fmaxf(chunk, cm);
+        if (++in_slot == per_slot || step + 1 == step1) {
+            *slot = chunk;
+            slot += kThreads;
+            chunk = -INFINITY;
+            in_slot = 0;
+            ++slots;
         }
     }
-    // the values before and behind the vectors: fewer than 16, a lane each, last (their
-    // indices are out of order: equal values pass the bound, and the keys decide)
+    const float m_body = m;
+    // the values before and behind the vectors: fewer than 16, a lane each
+    float extra = -INFINITY;
+    const int64_t extra_at = lane < 16 ? lane : tail + (lane - 16);
     if (rank == 0 && warp == 0) {
-        const int64_t at = lane < 16 ? lane : tail + (lane - 16);
-        const bool in = lane < 16 ? lane < head : at < a.V;
-        const float v = in ? load_logit<kBf16>(l, at) : -INFINITY;
-        join(m, S, W, fmaxf(v, -FLT_MAX), v > -INFINITY ? 1.0f : v == v ? 0.0f : v, 0.0f);
-        if (a.top > 0) best.push(v >= best.bound && v > -INFINITY, v, static_cast<uint32_t>(at));
+        if (lane < 16 ? lane < head : extra_at < a.V) extra = load_logit<kBf16>(l, extra_at);
+        join(m, S, W, fmaxf(extra, -FLT_MAX), extra > -INFINITY ? 1.0f : extra == extra ? 0.0f : extra, 0.0f);
     }
-    if (a.top > 0) best.leave(s_all, &s_left);
-
-    // the warp's, then the CTA's
+    // the warp's sums, then the CTA's
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         join(m, S, W, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, S, o),
@@ -365,19 +296,101 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
         s_S[warp] = S;
         s_W[warp] = W;
     }
-    __syncthreads();
     if (a.top > 0) {
-        if (threadIdx.x < 4) s_all[s_left + threadIdx.x] = 0;
-        __syncthreads();
-        rank_keys(s_all, s_left, a.top, s_part[rank].best);
+        float g = fmaxf(m_body, __shfl_xor_sync(0xFFFFFFFFu, m_body, 1));
+        g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, 2));
+        if ((lane & 3) == 0) s_group[tid >> 2] = g;
     }
-    m = s_m[0], S = s_S[0], W = s_W[0];
+    __syncthreads();
+    if (warp == 0) {
+        if (a.top > 0) {
+            // the bound: the k-th largest of the groups' maxima (k <= 32 of 64)
+            const float g0 = s_group[lane], g1 = s_group[32 + lane];
+            int n0 = 0, n1 = 0;
+#pragma unroll 4
+            for (int i = 0; i < 64; ++i) {
+                const float o = s_group[i];
+                n0 += o > g0 || (o == g0 && i < lane);
+                n1 += o > g1 || (o == g1 && i < 32 + lane);
+            }
+            if (n0 == a.top - 1) s_bound = g0;
+            if (n1 == a.top - 1) s_bound = g1;
+        }
+        m = s_m[0], S = s_S[0], W = s_W[0];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) join(m, S, W, s_m[w], s_S[w], s_W[w]);
-    if (threadIdx.x == 0) {
-        s_part[rank].m = m;
-        s_part[rank].S = S;
-        s_part[rank].W = W;
+        for (int w = 1; w < kWarps; ++w) join(m, S, W, s_m[w], s_S[w], s_W[w]);
+        if (lane == 0) {
+            s_part[rank].m = m;
+            s_part[rank].S = S;
+            s_part[rank].W = W;
+        }
+    }
+    if (a.top > 0) {
+        __syncthreads();
+        // (at least the lowest number: -inf is no candidate)
+        const float bound = s_bound;
+        if (m_body >= bound)
+            for (int i = 0; i < slots; ++i)
+                if (s_chunk[i][tid] >= bound) {
+                    const int at = atomicAdd(&s_chunks, 1);
+                    if (at < kMaxChunks) s_list[at] = static_cast<uint32_t>(i) << 16 | tid;
+                }
+        __syncthreads();
+        const auto keep = [&](bool p, float v, uint32_t i) {
+            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, p);
+            if (mask == 0) return;
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&s_keys, __popc(mask));
+            at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(mask & ((1u << lane) - 1));
+            if (p && at < kMaxKeys) s_all[at] = key_of(v, i);
+        };
+        const int chunks = s_chunks;
+        for (int i = warp; i < min(chunks, kMaxChunks); i += kWarps) {
+            const uint32_t e = s_list[i];
+            const int64_t first = step0 + (e >> 16) * per_slot, last = min(first + per_slot, step1);
+            const int t = e & 0xFFFF;
+            for (int64_t step = first; step < last; ++step)
+#pragma unroll
+                for (int j = 0; j < kVecs * kN; j += 32) {
+                    const int u = (j + lane) / kN;
+                    const int64_t vec = (step * kWarps + (t >> 5)) * (32 * kVecs) + 32 * u + (t & 31);
+                    const bool in = u < kVecs && vec < nvec;
+                    const int64_t at = head + vec * kN + lane % kN;
+                    const float v = in ? load_logit<kBf16>(l, at) : -INFINITY;
+                    keep(v >= bound && v > -INFINITY, v, static_cast<uint32_t>(at));
+                }
+        }
+        if (warp == 0 && rank == 0) keep(extra >= bound && extra > -INFINITY, extra, static_cast<uint32_t>(extra_at));
+        __syncthreads();
+        int keys = s_keys;
+        if (chunks > kMaxChunks || keys > kMaxKeys) {
+            // too many: this CTA's values once more, each warp keeping its best, in ascending
+            // order of their indices (equal values behind the k-th are not better)
+            List list;
+            list.bound = below(ordered(bound));
+            list.buf = s_buf[warp];
+            list.k = a.top;
+            list.lane = lane;
+            for (int64_t step = step0; step < step1; ++step) {
+                V4 v[kVecs];
+                load(step, v);
+                const uint32_t i0 = static_cast<uint32_t>(head + ((step * kWarps + warp) * (32 * kVecs) + lane) * kN);
+#pragma unroll
+                for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+                    for (int i = 0; i < kN; ++i)
+                        list.push(v[u][i] > list.bound && v[u][i] > -INFINITY, v[u][i], i0 + u * 32 * kN + i);
+                list.raise();
+            }
+            if (warp == 0 && rank == 0)   // (out of order: equal values pass, and the keys decide)
+                list.push(extra >= list.bound && extra > -INFINITY, extra, static_cast<uint32_t>(extra_at));
+            s_all[tid] = list.finish();
+            keys = kThreads;
+            __syncthreads();
+        }
+        if (tid < 4) s_all[keys + tid] = 0;
+        __syncthreads();
+        rank_keys(s_all, keys, a.top, s_part[rank].best);
     }
     if (c > 1) {
         sync_cluster();   // (every CTA of the cluster runs, and its part is in its shared memory)
@@ -386,8 +399,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
         if (rank != 0) return;
         if (a.top > 0) {
             const int n = static_cast<int>(c) * a.top;
-            for (int i = threadIdx.x; i < n + 4; i += kThreads)
-                s_all[i] = i < n ? s_part[i / a.top].best[i % a.top] : 0;
+            for (int i = tid; i < n + 4; i += kThreads) s_all[i] = i < n ? s_part[i / a.top].best[i % a.top] : 0;
             __syncthreads();
             rank_keys(s_all, n, a.top, s_best);
         }
