@@ -34,7 +34,7 @@ __all__ = [
     "h32_add_rms_norm_quantize", "h32_moe_route_scored",
     "h32_moe_route_scored_workspace_bytes", "q4_0_x_q4_gemm_tc_epilogue", "q4_0_x_q8_gemm_tc_epilogue",
     "h32_quantize_act_f8", "h32_quantize_weights_f8", "h32_f8_gemm", "h32_f8_gemm_experts",
-    "h32_token_logprobs",
+    "h32_f8_gemm_workspace_bytes", "h32_token_logprobs",
 ]
 
 
@@ -109,7 +109,9 @@ _SIGS = {
                                          _I64, _P]),
     "h32_quantize_act_f8": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _INT, _P]),
     "h32_quantize_weights_f8": (_INT, [_P, _INT, _I64, _I64, _I64, _INT, _P, _P, _P]),
-    "h32_f8_gemm": (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _INT, _I64, _P]),
+    "h32_f8_gemm_workspace_bytes": (_INT, [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)]),
+    "h32_f8_gemm": (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _INT, _I64, _P,
+                           ctypes.c_size_t, _P]),
     "h32_f8_gemm_experts": (_INT, [_P, _P, _I32, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _INT,
                                    _I64, _P]),
     "h32_token_logprobs": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I32, _I32, _P, _P, _P, _P, _P]),
@@ -1276,6 +1278,22 @@ def h32_quantize_weights_f8(w, rotate=False, wq=None, wd=None, stream=None):
     return wq, wd
 
 
+F8_FEW_TOKENS = 32   # up to here h32_f8_gemm needs no workspace
+
+
+def h32_f8_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Workspace bytes of h32_f8_gemm on the current device (0 for most sizes)."""
+    n = ctypes.c_size_t(0)
+    _check("h32_f8_gemm_workspace_bytes",
+           lib().h32_f8_gemm_workspace_bytes(int(M), int(N), int(K), ctypes.byref(n)))
+    return int(n.value)
+
+
+@functools.lru_cache(maxsize=1024)
+def _f8_workspace_bytes(device, M, N, K):
+    return h32_f8_gemm_workspace_bytes(M, N, K) if K % 32 == 0 and N > 0 and K > 0 else 0
+
+
 def h32_f8_gemm(wq, wd, xq, xd, M=None, y=None, y_dtype=None, stream=None):
     """y [M][N] = the product of e4m3 codes wq [N][K] and xq [M][K] with their scales
     wd [ceil(N/128)][ceil(K/128)] and xd [ceil(K/128)][ldxd]; y bf16/fp32, by default
@@ -1331,8 +1349,16 @@ def _f8_gemm(fn, wq, wd, xq, xd, off, N, M, y, y_dtype, stream):
         if y is None:
             y = torch.empty((M, n), dtype=y_dtype or f32, device=dev)
         if off is None:
+            wp, ws_bytes = None, 0
+            if M > F8_FEW_TOKENS:
+                ws_bytes = _f8_workspace_bytes(dev.index, M, n, K)
+                if ws_bytes:
+                    # the call's own: freed with it, reused only by later work of the stream
+                    ws = torch.empty(ws_bytes, dtype=u8, device=dev)
+                    wp = ws.data_ptr()
             st = lib().h32_f8_gemm(wq.data_ptr(), wd.data_ptr(), xq.data_ptr(), xd.data_ptr(),
-                                   xd.shape[1], M, n, K, y.data_ptr(), y.dtype == bf16, _pitch(y), raw)
+                                   xd.shape[1], M, n, K, y.data_ptr(), y.dtype == bf16, _pitch(y),
+                                   wp, ws_bytes, raw)
         else:
             st = lib().h32_f8_gemm_experts(
                 wq.data_ptr(), wd.data_ptr(), e, xq.data_ptr(), xd.data_ptr(), xd.shape[1],

@@ -23,11 +23,12 @@ namespace {
 __device__ uint32_t g_f8_status;   // kStatusTimeout, kStatusGuard
 
 constexpr int kMaxStages = 12;
+constexpr int64_t kRowsTokens = 32;   // dense: up to here rows_kernel
 constexpr int kRowsWarps = 6;
 constexpr int kPairWarps = 12;
 // registers of pair_kernel: 12 warps of 168 at launch; the epilogue's two warpgroups take
 // over what the third, of the roles that issue, does not need
-constexpr int kPairIssueRegs = 72, kPairEpiRegs = 216;
+constexpr int kPairIssueRegs = 120, kPairEpiRegs = 192;
 static_assert(128 * kPairIssueRegs + 256 * kPairEpiRegs <= 384 * 168, "registers handed over");
 constexpr int kMaxSmem = 225 * 1024;
 constexpr uint64_t kDrainPolls = 1ull << 22;
@@ -38,6 +39,7 @@ struct F8Args {
     int32_t stages;
     int32_t bn;              // pair_kernel: weight rows of a tile
     int32_t cluster;         // rows_kernel: CTAs of a tile
+    uint8_t *ws;             // pair_kernel: partial sums and flags of split tiles, or null
     const int32_t *off;      // [E + 1] or null
     const float *wd;         // [E][ceil(N / 128)][ceil(K / 128)]
     void *y;
@@ -454,9 +456,98 @@ struct Pair {
     static __host__ __device__ uint32_t b_bytes(int bn) { return bn / 2 * 128; }
 };
 
+// A pair's work, as (tile, K steps): whole tiles in turn, or (kSplit) an equal run of all tiles'
+// steps, last piece first.  A tile may be in several pairs' runs: the pair with its last steps
+// adds the others' partial sums to its own, all of pairs before it, in their order.  They come
+// from those pairs' first pieces, and it needs them for its last one.
+template <bool kSplit>
+struct Walk {
+    int t, k0, k1;   // the piece: steps [k0, k1) of tile t
+    // the first step of pair p's run, of `all` steps
+    static __device__ __forceinline__ int64_t run(int64_t all, int p) { return all * p / (gridDim.x / 2); }
+    __device__ __forceinline__ Walk(int total, int nb) {
+        const int pair = blockIdx.x / 2;
+        if constexpr (kSplit) {
+            const int64_t all = int64_t(total) * nb, end = run(all, pair + 1);
+            left = static_cast<int>(end - run(all, pair));
+            t = static_cast<int>((end - 1) / nb) + 1;
+            k0 = 0;
+            last = static_cast<int>(end - int64_t(t - 1) * nb);
+        } else {
+            t = pair - static_cast<int>(gridDim.x / 2);
+        }
+    }
+    __device__ __forceinline__ bool next(int total, int nb) {
+        if constexpr (kSplit) {
+            if (left == 0) return false;
+            --t;
+            k1 = last;
+            last = nb;
+            k0 = max(0, k1 - left);
+            left -= k1 - k0;
+            return true;
+        }
+        t += gridDim.x / 2;
+        k0 = 0;
+        k1 = nb;
+        return t < total;
+    }
+
+private:
+    int left, last;   // steps of the run still to come, and where the next piece ends
+};
+
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Partial sums of a pair: a CTA's 8 epilogue warps, 32 pieces of 16 bytes a lane.  Behind all of
+// them a flag for each warp, set when its sums are written.
+struct Partials {
+    static constexpr size_t kPair = 2 * 8 * 32 * 32 * 16;
+    static __host__ __device__ size_t flags(int pairs) { return size_t(pairs) * 16 * 4; }
+    static __host__ __device__ size_t bytes(int pairs) { return pairs * kPair + flags(pairs); }
+    uint8_t *ws;
+    int pairs, warp;   // the warp's place in its pair, 0 .. 15
+    // piece i, four sums (volatile: one after another, not all held at once)
+    __device__ __forceinline__ uint8_t *piece(int pair, int i) const {
+        return ws + pair * kPair + ((warp * 32 + i) * 32 + (threadIdx.x & 31)) * 16;
+    }
+    __device__ __forceinline__ void put(int pair, int i, uint64_t lo, uint64_t hi) const {
+        asm volatile("st.global.cg.v2.b64 [%0], {%1, %2};" ::"l"(piece(pair, i)), "l"(lo), "l"(hi) : "memory");
+    }
+    __device__ __forceinline__ void get(int pair, int i, uint64_t &lo, uint64_t &hi) const {
+        asm volatile("ld.global.cg.v2.b64 {%0, %1}, [%2];" : "=l"(lo), "=l"(hi) : "l"(piece(pair, i)) : "memory");
+    }
+    __device__ uint32_t *flag(int pair) const {
+        return reinterpret_cast<uint32_t *>(ws + pairs * kPair) + pair * 16 + warp;
+    }
+    __device__ void publish(int pair) const {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            __threadfence();
+            asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(flag(pair)) : "memory");
+        }
+        __syncwarp();
+    }
+    __device__ bool wait(int pair, uint64_t limit, volatile int *abort) const {
+        bool ok = false;
+        if ((threadIdx.x & 31) == 0)
+            for (uint64_t i = 0; i < limit && !ok; ++i) {
+                uint32_t v;
+                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag(pair)) : "memory");
+                ok = v != 0;
+                if (!ok && *abort) break;
+            }
+        return __shfl_sync(0xFFFFFFFFu, ok, 0);
+    }
+};
+
 // kChunks: 32-column chunks of an epilogue warp, a.bn = 64 kChunks.  (Compiled in, as every
 // branch taken in the loop over the K steps costs about as much as a wait.)
-template <int kChunks>
+template <int kChunks, bool kSplit>
 __global__ void __launch_bounds__(kPairWarps * 32, 1)
     pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                 const __grid_constant__ CUtensorMap map_s, const F8Args a) {
@@ -479,7 +570,6 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int nb = (a.K + 127) / 128, nt = (a.N + a.bn - 1) / a.bn;
-    const int first = blockIdx.x / 2, step = gridDim.x / 2;
     const uint64_t lim = a.wait_limit;
     volatile int *abort = &s_abort;
     if (threadIdx.x == 0) {
@@ -527,10 +617,11 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
             Ring st(1), sl(0);   // (the first round's waits pass at once)
             int fed = 0;
             bool ok = true;
-            for (int t = first; t < total && ok; t += step) {
-                const Tile ti = tile_of(t, g, a.E, 256, a.bn);
+            Walk<kSplit> work(total, nb);
+            while (ok && work.next(total, nb)) {
+                const Tile ti = tile_of(work.t, g, a.E, 256, a.bn);
                 const int x_row = ti.g0 + 128 * rank, w_row = ti.e * a.N + ti.n0 + a.bn / 2 * rank;
-                for (int kb = 0; kb < nb; ++kb) {
+                for (int kb = kSplit ? work.k0 : 0; kb < (kSplit ? work.k1 : nb); ++kb) {
                     if (!warp_wait_or_look(&s_empty[st.i], st.ph, lim, abort)) {
                         ok = false;
                         break;
@@ -582,8 +673,9 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
             const uint64_t da0 = smem_desc_sw128(smem_u32(s_a)), db0 = smem_desc_sw128(smem_u32(s_b));
             Ring st(0), bf(1);
             bool ok = true;
-            for (int t = first; t < total && ok; t += step) {
-                for (int kb = 0; kb < nb; ++kb) {
+            Walk<kSplit> work(total, nb);
+            while (ok && work.next(total, nb)) {
+                for (int kb = kSplit ? work.k0 : 0; kb < (kSplit ? work.k1 : nb); ++kb) {
                     if (!warp_wait_or_look(&s_full[st.i], st.ph, lim, abort) ||
                         !warp_wait_or_look(&s_peer[st.i], st.ph, lim, abort) ||
                         !warp_wait_or_look(&s_free[bf.i], bf.ph, lim, abort)) {
@@ -615,8 +707,9 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
             // ------------------------------ CTA 1: its copies' arrival, passed on to CTA 0
             Ring st(0);
             bool ok = true;
-            for (int t = first; t < total && ok; t += step) {
-                for (int kb = 0; kb < nb; ++kb) {
+            Walk<kSplit> work(total, nb);
+            while (ok && work.next(total, nb)) {
+                for (int kb = kSplit ? work.k0 : 0; kb < (kSplit ? work.k1 : nb); ++kb) {
                     if (!warp_wait_or_look(&s_full[st.i], st.ph, lim, abort)) {
                         ok = false;
                         break;
@@ -640,34 +733,28 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
         const uint32_t free0 = peer_smem(&s_free[0], 0), free1 = peer_smem(&s_free[1], 0);
         Ring bf(0), sl(0);
         bool ok = true;
-        for (int t = first; t < total && ok; t += step) {
-            const Tile ti = tile_of(t, g, a.E, 256, a.bn);
+        Walk<kSplit> work(total, nb);
+        while (ok && work.next(total, nb)) {
+            const Tile ti = tile_of(work.t, g, a.E, 256, a.bn);
             uint64_t acc[kChunks][16];
-            const float *wd[kChunks];
-            float dw[kChunks];
 #pragma unroll
-            for (int j = 0; j < kChunks; ++j) {
+            for (int j = 0; j < kChunks; ++j)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[j][i] = 0ull;
-                // the chunk's row of weight scales (a chunk lies in one block of 128)
-                const int n = min(ti.n0 + 32 * (half * kChunks + j), a.N - 1);
-                wd[j] = a.wd + (int64_t(ti.e) * ((a.N + 127) / 128) + n / 128) * nb;
-                dw[j] = __ldg(wd[j]);
-            }
+            // the weight scales of the warp's columns: they lie in one block of 128
+            const float *wd = a.wd + (int64_t(ti.e) * ((a.N + 127) / 128) + min(ti.n0 + 32 * kChunks * half, a.N - 1) / 128) * nb;
+            float dw = __ldg(wd + (kSplit ? work.k0 : 0));
+            const int k0 = kSplit ? work.k0 : 0, k1 = kSplit ? work.k1 : nb;
 #pragma unroll 4
-            for (int kb = 0; kb < nb; ++kb) {
+            for (int kb = k0; kb < k1; ++kb) {
                 if (!warp_wait_or_look(&s_scale[sl.i], sl.ph, lim, abort)) {
                     ok = false;
                     break;
                 }
                 const float dx = *reinterpret_cast<const float *>(s_s + sl.i * 512 + row * 4);
-                uint64_t s2[kChunks];
-#pragma unroll
-                for (int j = 0; j < kChunks; ++j) {
-                    const uint32_t s = __float_as_uint(__fmul_rn(dx, dw[j]));
-                    s2[j] = pair_of(s, s);
-                    if (kb + 1 < nb) dw[j] = __ldg(wd[j] + kb + 1);
-                }
+                const uint32_t sc = __float_as_uint(__fmul_rn(dx, dw));
+                const uint64_t s2 = pair_of(sc, sc);
+                if (kb + 1 < k1) dw = __ldg(wd + kb + 1);
                 if (!warp_wait_or_look(&s_sum[bf.i], bf.ph, lim, abort)) {
                     ok = false;
                     break;
@@ -681,7 +768,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                     tmem_wait_for(v);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        acc[j][i] = fma_f32x2(s2[j], pair_of(v[2 * i], v[2 * i + 1]), acc[j][i]);
+                        acc[j][i] = fma_f32x2(s2, pair_of(v[2 * i], v[2 * i + 1]), acc[j][i]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -690,6 +777,36 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                 sl.next(slots);
             }
             if (!ok) break;
+            if (kSplit && (work.k1 < nb || work.k0 > 0)) {
+                // (the addresses are made here, not kept over the steps)
+                Partials parts{a.ws, static_cast<int>(gridDim.x / 2), static_cast<int>(rank) * 8 + warp};
+                asm volatile("" : "+l"(parts.ws), "+r"(parts.pairs), "+r"(parts.warp));
+                const int pair = blockIdx.x / 2;
+                if (work.k1 < nb) {
+                    // the tile's later steps are another pair's: it gets the sums so far
+#pragma unroll
+                    for (int i = 0; i < 8 * kChunks; ++i) parts.put(pair, i, acc[i / 8][2 * (i % 8)], acc[i / 8][2 * (i % 8) + 1]);
+                    parts.publish(pair);
+                    continue;
+                }
+                const int64_t all = int64_t(total) * nb;
+                int q0 = pair;   // the first pair with steps of the tile
+                while (q0 > 0 && Walk<kSplit>::run(all, q0) > int64_t(work.t) * nb) --q0;
+                for (int q = q0; q < pair && ok; ++q) {
+                    ok = parts.wait(q, lim, abort);
+                    if (ok) {
+#pragma unroll
+                        for (int j = 0; j < kChunks; ++j) {
+                            uint64_t part[16];   // (a chunk's loads under way together)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) parts.get(q, 8 * j + i, part[2 * i], part[2 * i + 1]);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) acc[j][i] = add_f32x2(acc[j][i], part[i]);
+                        }
+                    }
+                }
+                if (!ok) break;
+            }
             const int r0 = 128 * rank + (warp & 3) * 32;   // the warp's first row of the tile
 #pragma unroll
             for (int j = 0; j < kChunks; ++j) {
@@ -764,7 +881,7 @@ h32_status launch_rows(const uint8_t *wq, const uint8_t *xq, const float *xd, in
     return launch_clusters<rows_kernel<NC>>(grid, kRowsWarps * 32, a.stages * C::kStage + rest, a.cluster, s, maps, a);
 }
 
-template <int kChunks>
+template <int kChunks, bool kSplit = false>
 h32_status launch_pair(const uint8_t *wq, const uint8_t *xq, const float *xd, int64_t ldxd, F8Args a, int64_t tiles,
                        int sms, cudaStream_t s) {
     a.bn = 64 * kChunks;
@@ -783,31 +900,58 @@ h32_status launch_pair(const uint8_t *wq, const uint8_t *xq, const float *xd, in
     // with fewer registers a thread than the hand-over assumes
     static const int regs = [] {
         cudaFuncAttributes fa{};
-        return cudaFuncGetAttributes(&fa, pair_kernel<kChunks>) == cudaSuccess ? fa.numRegs : -1;
+        return cudaFuncGetAttributes(&fa, pair_kernel<kChunks, kSplit>) == cudaSuccess ? fa.numRegs : -1;
     }();
     if (regs < 168) {
         note_error("8-bit product compiled with fewer registers than its warpgroups hand over");
         return H32_ERR_CUDA;
     }
-    return launch_clusters<pair_kernel<kChunks>>(2 * pairs, kPairWarps * 32, a.stages * stage + rest, 2, s, maps, a);
+    return launch_clusters<pair_kernel<kChunks, kSplit>>(2 * pairs, kPairWarps * 32, a.stages * stage + rest, 2, s, maps, a);
+}
+
+// How pair_kernel takes `chunks` chunks of 256 tokens (as the host knows them).  A K step of 64, 128
+// and 256 weight rows takes 332, 355 and 406 ns (256 x 5120 against 5120 rows; 192 rows 444,
+// so never), a tile's end about 3 us for 256 rows.  The narrow ones pay where they fill pairs
+// that were idle (256 tokens x 8192 x 5120: 128 rows 29.5 us, 256 rows 33.6), and equal runs of
+// K steps where the last wave of whole tiles is long (333 x 5120 x 17408: 40 tiles on 76
+// pairs, 64 and 41 us); the partial sums cost about 5 us and 1.5 for each that a tile has.
+struct PairPlan {
+    int bn;
+    int pairs;   // > 0: runs of K steps for so many pairs, 12 steps at least
+};
+PairPlan plan_pairs(int64_t chunks, int64_t N, int64_t K, int sms) {
+    const int64_t nb = (K + 127) / 128, pairs = sms / 2;
+    const auto cost = [&](int64_t bn, int64_t step) {
+        const int64_t tiles = (N + bn - 1) / bn * chunks;
+        return (tiles + pairs - 1) / pairs * (nb * step + 12 * bn);
+    };
+    const int64_t c64 = cost(64, 332), c128 = cost(128, 355), c256 = cost(256, 406);
+    const int64_t best = c256 <= c128 && c256 <= c64 ? c256 : c128 <= c64 ? c128 : c64;
+    const int64_t tiles = (N + 255) / 256 * chunks, steps = tiles * nb;
+    PairPlan p{best == c256 ? 256 : best == c128 ? 128 : 64, 0};
+    const int64_t n = steps / 12 < pairs ? steps / 12 : pairs;
+    if (n < 2 || steps >= 0x7FFFFFFFll) return p;
+    const int64_t run = (steps + n - 1) / n;
+    if (run * 406 + (tiles / n + 1) * 3072 + 5000 + 1500 * ((nb + run - 1) / run) < best) p.pairs = static_cast<int>(n);
+    return p;
 }
 
 h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint8_t *xq, const float *xd,
                        int64_t ldxd, const int32_t *off, int64_t M, int64_t N, int64_t K, void *y,
-                       h32_in_dtype y_dt, int64_t ldy, void *stream) {
+                       h32_in_dtype y_dt, int64_t ldy, void *ws, size_t ws_bytes, void *stream) {
     if (M < 0 || N <= 0 || K <= 0 || K % 32 != 0 || E < 1 || E > kMaxExperts || ldxd < M || ldxd % 4 != 0 ||
         ldy < N || (y_dt != H32_IN_F32 && y_dt != H32_IN_BF16))
         return H32_ERR_INVALID_ARG;
     if (M == 0) return H32_OK;
     if (!wq || !wd || !xq || !xd || !y) return H32_ERR_INVALID_ARG;
-    if (!aligned16(wq) || !aligned16(wd) || !aligned16(xq) || !aligned16(xd) || !aligned16(y) ||
+    if (!aligned16(wq) || !aligned16(wd) || !aligned16(xq) || !aligned16(xd) || !aligned16(y) || !aligned16(ws) ||
         (off && reinterpret_cast<uintptr_t>(off) % 4 != 0))
         return H32_ERR_ALIGNMENT;
     // the kernels number rows and tiles in int (a group starts up to 3 rows early: at most
     // two chunks more than its rows fill)
-    const int64_t nt = (N + 127) / 128, tiles = nt * (M / 16 + 2 * int64_t(E));
+    const int64_t nt = (N + 127) / 128, most_tiles = nt * (M / 16 + 2 * int64_t(E));
     if (M > 0x7FFFFFFFll - 256 || K > 0x7FFFFFFFll - 256 || int64_t(E) * N > 0x7FFFFFFFll - 256 ||
-        ldxd > 0xFFFFFFFFll || tiles > 0x7FFFFFFFll)
+        ldxd > 0xFFFFFFFFll || most_tiles > 0x7FFFFFFFll)
         return H32_ERR_INVALID_ARG;
     int sms = 0;
     H32_TRY(check_device(&sms));
@@ -835,20 +979,21 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
     // (groups differ, and a second chunk reads the weights again).
     const int64_t per = (M + E - 1) / E;
     if (per <= (off ? 8 : 16)) return launch_rows<16>(wq, xq, xd, ldxd, a, nt * E, sms, s);
-    if (per <= (off ? 20 : 32)) return launch_rows<32>(wq, xq, xd, ldxd, a, nt * E, sms, s);
-    // The width of a tile: a K step of 64, 128 and 256 weight rows takes 332, 355 and
-    // 406 ns (256 x 5120 against 5120 rows; 192 rows 444, so never), a tile's end about 3 us
-    // for 256 rows; the narrow ones pay where they fill pairs that were idle (256 tokens x
-    // 8192 x 5120: 128 rows 29.5 us, 256 rows 33.6).
-    const int64_t chunks = off ? E + M / 256 : (M + 255) / 256, nb = (K + 127) / 128;
-    const auto cost = [&](int64_t bn, int64_t step) {
-        const int64_t tiles = (N + bn - 1) / bn * chunks;
-        return (tiles + sms / 2 - 1) / (sms / 2) * (nb * step + 12 * bn);
-    };
-    const int64_t c64 = cost(64, 332), c128 = cost(128, 355), c256 = cost(256, 406);
-    if (c256 <= c128 && c256 <= c64) return launch_pair<4>(wq, xq, xd, ldxd, a, (N + 255) / 256 * chunks, sms, s);
-    if (c128 <= c64) return launch_pair<2>(wq, xq, xd, ldxd, a, (N + 127) / 128 * chunks, sms, s);
-    return launch_pair<1>(wq, xq, xd, ldxd, a, (N + 63) / 64 * chunks, sms, s);
+    if (per <= (off ? 20 : kRowsTokens)) return launch_rows<32>(wq, xq, xd, ldxd, a, nt * E, sms, s);
+    const int64_t chunks = off ? E + M / 256 : (M + 255) / 256;
+    const PairPlan plan = plan_pairs(chunks, N, K, sms);
+    if (plan.pairs > 0 && ws && !off) {
+        if (ws_bytes < Partials::bytes(plan.pairs)) return H32_ERR_INVALID_ARG;
+        a.ws = static_cast<uint8_t *>(ws);
+        const size_t flags = Partials::flags(plan.pairs);
+        const cudaError_t e = cudaMemsetAsync(a.ws + Partials::bytes(plan.pairs) - flags, 0, flags, s);
+        if (e != cudaSuccess) return launch_status(e);
+        return launch_pair<4, true>(wq, xq, xd, ldxd, a, plan.pairs, sms, s);
+    }
+    const int64_t tiles = (N + plan.bn - 1) / plan.bn * chunks;
+    if (plan.bn == 256) return launch_pair<4>(wq, xq, xd, ldxd, a, tiles, sms, s);
+    if (plan.bn == 128) return launch_pair<2>(wq, xq, xd, ldxd, a, tiles, sms, s);
+    return launch_pair<1>(wq, xq, xd, ldxd, a, tiles, sms, s);
 }
 
 }  // namespace
@@ -866,10 +1011,21 @@ h32_status f8_read_and_clear_status(cudaStream_t s) {
 
 }  // namespace h32
 
+extern "C" h32_status h32_f8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes) {
+    using namespace h32;
+    if (M < 0 || N <= 0 || K <= 0 || K % 32 != 0 || !bytes) return H32_ERR_INVALID_ARG;
+    int sms = 0;
+    H32_TRY(check_device(&sms));
+    const int pairs = M > kRowsTokens ? plan_pairs((M + 255) / 256, N, K, sms).pairs : 0;
+    *bytes = pairs > 0 ? Partials::bytes(pairs) : 0;
+    return H32_OK;
+}
+
 extern "C" h32_status h32_f8_gemm(const uint8_t *wq, const float *wd, const uint8_t *xq, const float *xd,
                                   int64_t ldxd, int64_t M, int64_t N, int64_t K, void *y, h32_in_dtype y_dt,
-                                  int64_t ldy, void *stream) {
-    return h32::run_f8_gemm(wq, wd, 1, xq, xd, ldxd, nullptr, M, N, K, y, y_dt, ldy, stream);
+                                  int64_t ldy, void *workspace, size_t workspace_bytes, void *stream) {
+    return h32::run_f8_gemm(wq, wd, 1, xq, xd, ldxd, nullptr, M, N, K, y, y_dt, ldy, workspace, workspace_bytes,
+                            stream);
 }
 
 extern "C" h32_status h32_f8_gemm_experts(const uint8_t *wq, const float *wd, int32_t E, const uint8_t *xq,
@@ -877,5 +1033,5 @@ extern "C" h32_status h32_f8_gemm_experts(const uint8_t *wq, const float *wd, in
                                           int64_t N, int64_t K, void *y, h32_in_dtype y_dt, int64_t ldy,
                                           void *stream) {
     if (!expert_off) return H32_ERR_INVALID_ARG;
-    return h32::run_f8_gemm(wq, wd, E, xq, xd, ldxd, expert_off, R, N, K, y, y_dt, ldy, stream);
+    return h32::run_f8_gemm(wq, wd, E, xq, xd, ldxd, expert_off, R, N, K, y, y_dt, ldy, nullptr, 0, stream);
 }

@@ -687,20 +687,28 @@ h32_status h32_quantize_weights_f8(const void *w, h32_in_dtype dt, int64_t N, in
  * Products of e4m3 codes with a scale for each block of 128:
  *   y[m][n] = acc after acc = fma(fl(xd[b][m] * wd[n/128][b]), S_b, acc), b = 0 .. K/128,
  *   S_b = the fp32 sum of block b's products xq[m][k] * wq[n][k] (exact products; the sum's
- *   order and rounding are the tensor core's), rounded once to y's type.
+ *   order and rounding are the tensor core's), rounded once to y's type.  Where few tiles
+ *   share the GPU, runs of blocks are folded apart from +0 and then added in order; which
+ *   ones depends on the sizes and the device alone, so equal calls give equal bits.
  * For any M: one new token to long prompts (few tokens share one read of the weights).
  *   wq   [N][K] codes, wd [ceil(N/128)][ceil(K/128)] (h32_quantize_weights_f8)
  *   xq   [M][K] codes, xd [ceil(K/128)][ldxd], ldxd >= M a multiple of 4 (h32_quantize_act_f8)
  *   y    [M][ldy] out of type y_dt, any ldy >= N
+ *   workspace  nullable, 16-byte aligned device memory of at least
+ *        h32_f8_gemm_workspace_bytes (0 for most sizes); any contents, free again when the
+ *        call's work is done.  With it tiles that would leave much of the GPU idle are
+ *        shared out along K, their partial sums added in the order of K (without it the
+ *        same sums, slower and in one order over all of K)
  * Any N >= 1; K a multiple of 32.
  * The expert form multiplies rows r in [expert_off[e], expert_off[e+1]) by expert e's
  * weights: wq [E][N][K], wd [E][ceil(N/128)][ceil(K/128)], expert_off [E+1] int32 device,
  * 4-byte aligned, 0 = off[0] <= ... <= off[E] = R (else H32_ERR_DEVICE_GUARD is recorded
  * and nothing is computed), 1 <= E <= 1024.
  */
+h32_status h32_f8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes);
 h32_status h32_f8_gemm(const uint8_t *wq, const float *wd, const uint8_t *xq, const float *xd,
                        int64_t ldxd, int64_t M, int64_t N, int64_t K, void *y, h32_in_dtype y_dt,
-                       int64_t ldy, void *stream);
+                       int64_t ldy, void *workspace, size_t workspace_bytes, void *stream);
 h32_status h32_f8_gemm_experts(const uint8_t *wq, const float *wd, int32_t E, const uint8_t *xq,
                                const float *xd, int64_t ldxd, const int32_t *expert_off, int64_t R,
                                int64_t N, int64_t K, void *y, h32_in_dtype y_dt, int64_t ldy,

@@ -126,8 +126,9 @@ def test_library_refusals_quantizers(lib):
 def test_library_refusals_products(lib):
     P = 4096
 
-    def dense(wq=P, wd=2 * P, xq=3 * P, xd=4 * P, ldxd=4, M=4, N=100, K=256, y=5 * P, dt=0, ldy=100):
-        return lib.h32_f8_gemm(_p(wq), _p(wd), _p(xq), _p(xd), ldxd, M, N, K, _p(y), dt, ldy, _p(0))
+    def dense(wq=P, wd=2 * P, xq=3 * P, xd=4 * P, ldxd=4, M=4, N=100, K=256, y=5 * P, dt=0, ldy=100,
+              ws=None, ws_bytes=0):
+        return lib.h32_f8_gemm(_p(wq), _p(wd), _p(xq), _p(xd), ldxd, M, N, K, _p(y), dt, ldy, _p(ws), ws_bytes, _p(0))
 
     def experts(wq=P, wd=2 * P, E=3, xq=3 * P, xd=4 * P, ldxd=4, off=6 * P, M=4, N=100, K=256, y=5 * P, dt=0, ldy=100):
         return lib.h32_f8_gemm_experts(_p(wq), _p(wd), E, _p(xq), _p(xd), ldxd, _p(off), M, N, K, _p(y), dt, ldy, _p(0))
@@ -142,6 +143,13 @@ def test_library_refusals_products(lib):
         assert call(M=0) == OK
         _end(call)
         _end(call, N=1, ldy=1, K=32, dt=1)
+    assert dense(ws=P + 8, ws_bytes=1 << 30) == MIS
+    n = ctypes.c_size_t(7)
+    for kw in ((-1, 4, 128), (1, 0, 128), (1, 4, 0), (1, 4, 100)):
+        assert lib.h32_f8_gemm_workspace_bytes(*kw, ctypes.byref(n)) == BAD
+    assert lib.h32_f8_gemm_workspace_bytes(1, 4, 128, None) == BAD
+    if not torch.cuda.is_available():
+        assert lib.h32_f8_gemm_workspace_bytes(1, 4, 128, ctypes.byref(n)) == h32.H32_ERR_UNSUPPORTED
     assert experts(E=0) == BAD and experts(E=1025) == BAD and experts(off=None) == BAD
     assert experts(off=P + 2) == MIS
 

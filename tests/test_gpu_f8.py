@@ -162,6 +162,46 @@ def test_product_exact(h32, M, N, K, bf16):
     assert torch.equal(y.cpu(), ref.bfloat16() if bf16 else ref)
 
 
+@pytest.mark.parametrize("M,N,K", [(300, 5120, 8192), (1000, 5001, 5152), (40, 1024, 15904)])
+def test_product_shared_out_along_k(h32, M, N, K):
+    """Sizes whose tiles are cut along K between the pairs of CTAs: with the binding's
+    workspace, one of the caller's (dirty), and none; on two streams at once and from two
+    graphs replayed together."""
+    import torch
+    need = h32.h32_f8_gemm_workspace_bytes(M, N, K)
+    assert need > 0
+    wq, wd, xq, xd = _exact_operands(M, N, K, M + N)
+    t = torch_of(wq), torch_of(wd), torch_of(xq), _xd(xd, np.nan)
+    ref = torch.from_numpy(oracle.f8_gemm(wq, wd, xq, xd)[0]).float().cuda()
+    assert torch.equal(h32.h32_f8_gemm(*t), ref)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    y = torch.empty((M, N), device="cuda")
+    for p, n, want in ((ws.data_ptr(), need, 0), (ws.data_ptr(), need, 0), (None, 0, 0),
+                       (ws.data_ptr(), need - 16, h32.H32_ERR_INVALID_ARG)):
+        y.zero_()
+        st = h32.lib().h32_f8_gemm(t[0].data_ptr(), t[1].data_ptr(), t[2].data_ptr(), t[3].data_ptr(), t[3].shape[1],
+                                   M, N, K, y.data_ptr(), 0, N, p, n, torch.cuda.current_stream().cuda_stream)
+        assert st == want
+        _ok(h32)
+        assert torch.equal(y, ref) == (want == 0)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    ys = [h32.h32_f8_gemm(*t, stream=s) for _ in range(3) for s in (s1, s2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, ref) for y in ys)
+    graphs = []
+    for s in (s1, s2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            y = h32.h32_f8_gemm(*t)
+        graphs.append((g, y, s))
+    for _ in range(3):
+        for g, _, s in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+    _ok(h32)
+    assert all(torch.equal(y, ref) for _, y, _ in graphs)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 640, 5120), (5, 300, 17408), (40, 256, 2080), (100, 130, 4096), (300, 520, 5120)])
 def test_product_random_codes(h32, M, N, K):
     """Every finite code, scales over several octaves.  Per block the tensor core adds 128
@@ -301,11 +341,12 @@ def test_streams_and_graphs(h32, M, N, K):
     assert not torch.equal(want, first)
 
 
-@pytest.mark.parametrize("M", [2, 24, 60, 120, 700])
-def test_one_poll_wait_bound(h32, M):
+@pytest.mark.parametrize("M,N,K", [(2, 4096, 4096), (24, 4096, 4096), (60, 4096, 4096), (700, 4096, 4096),
+                                   (300, 5120, 8192)])
+def test_one_poll_wait_bound(h32, M, N, K):
     """A bound of one poll: waits give up, the status says so once, and the same context
     then computes exactly."""
-    wq, wd, xq, xd = _exact_operands(M, 4096, 4096, M)
+    wq, wd, xq, xd = _exact_operands(M, N, K, M)
     t = torch_of(wq), torch_of(wd), torch_of(xq), _xd(xd)
     ref = oracle.f8_gemm(wq[:256], wd[:2], xq, xd)[0].astype(np.float32)
     assert h32.h32_device_status() == 0
