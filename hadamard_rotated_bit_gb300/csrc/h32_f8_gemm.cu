@@ -25,21 +25,25 @@ __device__ uint32_t g_f8_status;   // kStatusTimeout, kStatusGuard
 constexpr int kMaxStages = 12;
 constexpr int64_t kRowsTokens = 32;   // dense: up to here rows_kernel
 constexpr int kRowsWarps = 6;
-constexpr int kPairWarps = 12;
-// registers of pair_kernel: 12 warps of 168 at launch; the epilogue's two warpgroups take
-// over what the third, of the roles that issue, does not need
-constexpr int kPairIssueRegs = 120, kPairEpiRegs = 192;
-static_assert(128 * kPairIssueRegs + 256 * kPairEpiRegs <= 384 * 168, "registers handed over");
+// lanes_kernel: two epilogue warps for each quarter of the lanes, and a warpgroup of the roles
+// that issue.  Of 12 warps with 168 registers at launch the epilogue's two warpgroups take over
+// what that one does not need.  (The shares and the unrolling of the K steps are those that
+// leave every instance without spills: a few spilled words cost it 12 to 20%.)
+constexpr int kPairWarps = 12, kPairRegs = 168;
+constexpr __host__ __device__ int issue_regs(bool split) { return split ? 104 : 120; }
+constexpr __host__ __device__ int epilogue_regs(bool split) { return split ? 200 : 192; }
+static_assert(128 * issue_regs(false) + 256 * epilogue_regs(false) <= kPairWarps * 32 * kPairRegs &&
+                  128 * issue_regs(true) + 256 * epilogue_regs(true) <= kPairWarps * 32 * kPairRegs,
+              "registers handed over");
 constexpr int kMaxSmem = 225 * 1024;
 constexpr uint64_t kDrainPolls = 1ull << 22;
 
 struct F8Args {
     int32_t M, N, K;         // token rows, weight rows (of an expert), reduction length
     int32_t E;               // experts; 1 and off null: all rows
-    int32_t stages;
-    int32_t bn;              // pair_kernel: weight rows of a tile
+    int32_t stages;          // rows_kernel
     int32_t cluster;         // rows_kernel: CTAs of a tile
-    uint8_t *ws;             // pair_kernel: partial sums and flags of split tiles, or null
+    uint8_t *ws;             // lanes_kernel: partial sums and flags of split tiles, or null
     const int32_t *off;      // [E + 1] or null
     const float *wd;         // [E][ceil(N / 128)][ceil(K / 128)]
     void *y;
@@ -54,7 +58,7 @@ struct F8Args {
 // the rows of a chunk outside the group are computed and not stored.
 struct Groups {
     int *off, *first;   // [E + 1] each
-    static __host__ __device__ size_t bytes(int E) { return (2 * size_t(E + 1) * 4 + 1023) / 1024 * 1024; }
+    static constexpr __host__ __device__ size_t bytes(int E) { return (2 * size_t(E + 1) * 4 + 1023) / 1024 * 1024; }
     __device__ int chunks(int e, int cols) const {
         const int lo = off[e], hi = off[e + 1];
         return hi > lo ? (hi - (lo & ~3) + cols - 1) / cols : 0;
@@ -448,25 +452,30 @@ __global__ void __launch_bounds__(kRowsWarps * 32, Rows<NC>::kPerSm)
 }
 
 // ----------------------------------------------------------------------------
-// token rows on the lanes, two CTAs a tile
+// token rows on the lanes, 128 to each of a tile's one or two CTAs
 // ----------------------------------------------------------------------------
-struct Pair {
-    static constexpr uint32_t kA = 128 * 128;          // codes of a CTA's tokens, a stage
-    static constexpr uint32_t kSlots = kMaxStages + 2; // scales of a K step each
-    static __host__ __device__ uint32_t b_bytes(int bn) { return bn / 2 * 128; }
+template <int kChunks, int kCtas>
+struct Lanes {
+    static constexpr int kBn = 64 * kChunks;             // weight rows of a tile
+    static constexpr uint32_t kA = 128 * 128, kB = kBn / kCtas * 128;   // a CTA's codes of a stage
+    static constexpr uint32_t kRest = Groups::bytes(kMaxExperts) + 2 * 1024 + 2 * 512 + 8 * 4096;
+    static constexpr int kFit = (kMaxSmem - kRest) / (kA + kB + 512);
+    static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+    static constexpr int kSlots = kStages + 2;           // scales of a K step each
+    static constexpr uint32_t kSmem = kStages * (kA + kB + 512) + kRest;
 };
 
 // A pair's work, as (tile, K steps): whole tiles in turn, or (kSplit) an equal run of all tiles'
 // steps, last piece first.  A tile may be in several pairs' runs: the pair with its last steps
 // adds the others' partial sums to its own, all of pairs before it, in their order.  They come
 // from those pairs' first pieces, and it needs them for its last one.
-template <bool kSplit>
+template <bool kSplit, int kCtas>
 struct Walk {
     int t, k0, k1;   // the piece: steps [k0, k1) of tile t
     // the first step of pair p's run, of `all` steps
-    static __device__ __forceinline__ int64_t run(int64_t all, int p) { return all * p / (gridDim.x / 2); }
+    static __device__ __forceinline__ int64_t run(int64_t all, int p) { return all * p / (gridDim.x / kCtas); }
     __device__ __forceinline__ Walk(int total, int nb) {
-        const int pair = blockIdx.x / 2;
+        const int pair = blockIdx.x / kCtas;
         if constexpr (kSplit) {
             const int64_t all = int64_t(total) * nb, end = run(all, pair + 1);
             left = static_cast<int>(end - run(all, pair));
@@ -474,7 +483,7 @@ struct Walk {
             k0 = 0;
             last = static_cast<int>(end - int64_t(t - 1) * nb);
         } else {
-            t = pair - static_cast<int>(gridDim.x / 2);
+            t = pair - static_cast<int>(gridDim.x / kCtas);
         }
     }
     __device__ __forceinline__ bool next(int total, int nb) {
@@ -487,7 +496,7 @@ struct Walk {
             left -= k1 - k0;
             return true;
         }
-        t += gridDim.x / 2;
+        t += gridDim.x / kCtas;
         k0 = 0;
         k1 = nb;
         return t < total;
@@ -545,54 +554,73 @@ struct Partials {
     }
 };
 
-// kChunks: 32-column chunks of an epilogue warp, a.bn = 64 kChunks.  (Compiled in, as every
+// kChunks: 32-column chunks of an epilogue warp (a tile has 64 kChunks weight rows).  (Compiled in, as every
 // branch taken in the loop over the K steps costs about as much as a wait.)
-template <int kChunks, bool kSplit>
+template <int kCtas>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (kCtas == 2) mma_pair_f8f6f4(d, a, b, idesc, accumulate);
+    else mma_f8f6f4(d, a, b, idesc, accumulate);
+}
+template <int kCtas>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    if constexpr (kCtas == 2) mma_commit_pair(bar);
+    else mma_commit(bar);
+}
+
+template <int kChunks, bool kSplit, int kCtas>
 __global__ void __launch_bounds__(kPairWarps * 32, 1)
-    pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+    lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                 const __grid_constant__ CUtensorMap map_s, const F8Args a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // s_full: this CTA's copies of a stage; s_peer (used in CTA 0): the other's are there too;
     // s_empty: the products have read the stage; s_sum: a K step's sums are in TMEM;
     // s_free (in CTA 0): both CTAs' epilogues have them in registers; s_scale: a slot's scales
-    __shared__ uint64_t s_full[kMaxStages], s_peer[kMaxStages], s_empty[kMaxStages], s_scale[Pair::kSlots], s_sum[2],
+    using C = Lanes<kChunks, kCtas>;
+    constexpr int S = C::kStages, slots = C::kSlots;
+    constexpr uint32_t b_bytes = C::kB;
+    __shared__ uint64_t s_full[S], s_peer[S], s_empty[S], s_scale[slots], s_sum[2],
         s_free[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_word;
     __shared__ volatile int s_abort;
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const int S = a.stages, slots = S + 2;
-    const uint32_t b_bytes = Pair::b_bytes(a.bn);
-    uint8_t *s_a = smem, *s_b = s_a + S * Pair::kA, *s_s = s_b + S * b_bytes;
+    uint8_t *s_a = smem, *s_b = s_a + S * C::kA, *s_s = s_b + S * b_bytes;
     uint8_t *s_y = s_s + (slots * 512 + 1023) / 1024 * 1024;   // 4 KB an epilogue warp
     int *s_table = reinterpret_cast<int *>(s_y + 8 * 4096);
     const Groups g{s_table, s_table + a.E + 1};
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
-    const int nb = (a.K + 127) / 128, nt = (a.N + a.bn - 1) / a.bn;
+    const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
+    const int nb = (a.K + 127) / 128, nt = (a.N + C::kBn - 1) / C::kBn;
     const uint64_t lim = a.wait_limit;
     volatile int *abort = &s_abort;
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int i = 0; i < S; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_peer[i], 1);
             mbar_init(&s_empty[i], 1);
         }
+#pragma unroll 1
         for (int i = 0; i < slots; ++i) mbar_init(&s_scale[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_sum[i], 1);
-            mbar_init(&s_free[i], 16);
+            mbar_init(&s_free[i], 8 * kCtas);
         }
         mbar_init(&s_drain, 1);
         s_abort = 0;
         fence_barrier_init();
     }
-    cluster_sync();   // both CTAs run, and their barriers are there
-    if (warp == 9) tmem_alloc_pair(&s_tmem, 512);
+    if constexpr (kCtas == 2) {
+        cluster_sync();   // both CTAs run, and their barriers are there
+        if (warp == 9) tmem_alloc_pair(&s_tmem, 512);
+    } else if (warp == 9) {
+        tmem_alloc(&s_tmem, 512);
+        tmem_relinquish();
+    }
     pdl_wait();
     pdl_trigger();
     tc_fence_before();
-    int total = load_groups(g, a, 256, nt, &s_word);
+    int total = load_groups(g, a, 128 * kCtas, nt, &s_word);
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     if (total < 0) {
@@ -605,7 +633,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
     };
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairIssueRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(issue_regs(kSplit)));
         if (warp == 8) {
             // ------------------------------------------------------------ TMA
             const bool leader = elect_one();
@@ -617,18 +645,19 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
             Ring st(1), sl(0);   // (the first round's waits pass at once)
             int fed = 0;
             bool ok = true;
-            Walk<kSplit> work(total, nb);
+            Walk<kSplit, kCtas> work(total, nb);
             while (ok && work.next(total, nb)) {
-                const Tile ti = tile_of(work.t, g, a.E, 256, a.bn);
-                const int x_row = ti.g0 + 128 * rank, w_row = ti.e * a.N + ti.n0 + a.bn / 2 * rank;
+                const Tile ti = tile_of(work.t, g, a.E, 128 * kCtas, C::kBn);
+                const int x_row = ti.g0 + 128 * rank, w_row = ti.e * a.N + ti.n0 + C::kBn / kCtas * rank;
+#pragma unroll 1
                 for (int kb = kSplit ? work.k0 : 0; kb < (kSplit ? work.k1 : nb); ++kb) {
                     if (!warp_wait_or_look(&s_empty[st.i], st.ph, lim, abort)) {
                         ok = false;
                         break;
                     }
                     if (leader) {
-                        mbar_arrive_expect_tx(&s_full[st.i], Pair::kA + b_bytes);
-                        tma_load_2d(s_a + st.i * Pair::kA, &map_x, &s_full[st.i], kb * 128, x_row);
+                        mbar_arrive_expect_tx(&s_full[st.i], C::kA + b_bytes);
+                        tma_load_2d(s_a + st.i * C::kA, &map_x, &s_full[st.i], kb * 128, x_row);
                         tma_load_2d(s_b + st.i * b_bytes, &map_w, &s_full[st.i], kb * 128, w_row);
                         // the slot's last scales were read before the sums two steps later
                         // were waited for, and those before this stage was free
@@ -645,11 +674,13 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                 if (!ok) give_up();
                 // leave only when the last products have read the stages (in a whole run: their
                 // arrivals come from CTA 0) and the copies under way have landed
+#pragma unroll 1
                 for (int i = 0; i < S && ok; ++i) {
                     mbar_wait_bounded(&s_empty[st.i], st.ph, kDrainPolls, nullptr);
                     st.next(S);
                 }
                 if (ok) st.ph ^= 1;   // (once around the ring)
+#pragma unroll 1
                 for (int i = 0; i < fed; ++i) {
                     if (i < S) {
                         if (--st.i < 0) {
@@ -669,15 +700,16 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
         } else if (warp == 9 && rank == 0) {
             // ------------------------------------------------------------ MMA
             const bool leader = elect_one();
-            const uint32_t idesc = idesc_e4m3_f32(256, a.bn);
+            const uint32_t idesc = idesc_e4m3_f32(128 * kCtas, C::kBn);
             const uint64_t da0 = smem_desc_sw128(smem_u32(s_a)), db0 = smem_desc_sw128(smem_u32(s_b));
             Ring st(0), bf(1);
             bool ok = true;
-            Walk<kSplit> work(total, nb);
+            Walk<kSplit, kCtas> work(total, nb);
             while (ok && work.next(total, nb)) {
+#pragma unroll 1
                 for (int kb = kSplit ? work.k0 : 0; kb < (kSplit ? work.k1 : nb); ++kb) {
                     if (!warp_wait_or_look(&s_full[st.i], st.ph, lim, abort) ||
-                        !warp_wait_or_look(&s_peer[st.i], st.ph, lim, abort) ||
+                        (kCtas == 2 && !warp_wait_or_look(&s_peer[st.i], st.ph, lim, abort)) ||
                         !warp_wait_or_look(&s_free[bf.i], bf.ph, lim, abort)) {
                         ok = false;
                         break;
@@ -685,12 +717,12 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                     tc_fence_after();
                     if (leader) {
                         // (columns behind K are zeros in both operands)
-                        const uint64_t da = da0 + st.i * (Pair::kA >> 4), db = db0 + st.i * (b_bytes >> 4);
+                        const uint64_t da = da0 + st.i * (C::kA >> 4), db = db0 + st.i * (b_bytes >> 4);
     #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            mma_pair_f8f6f4(tmem + bf.i * 256, da + 2 * j, db + 2 * j, idesc, j > 0);
-                        mma_commit_pair(&s_empty[st.i]);
-                        mma_commit_pair(&s_sum[bf.i]);
+                            mma<kCtas>(tmem + bf.i * 256, da + 2 * j, db + 2 * j, idesc, j > 0);
+                        commit<kCtas>(&s_empty[st.i]);
+                        commit<kCtas>(&s_sum[bf.i]);
                     }
                     __syncwarp();
                     st.next(S);
@@ -699,16 +731,17 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
             }
             if (leader) {
                 if (!ok) give_up();
-                mma_commit_pair(&s_drain);
+                commit<kCtas>(&s_drain);
                 mbar_wait_bounded(&s_drain, 0, kDrainPolls, nullptr);
             }
             __syncwarp();
-        } else if (warp == 9) {
+        } else if (kCtas == 2 && warp == 9) {
             // ------------------------------ CTA 1: its copies' arrival, passed on to CTA 0
             Ring st(0);
             bool ok = true;
-            Walk<kSplit> work(total, nb);
+            Walk<kSplit, kCtas> work(total, nb);
             while (ok && work.next(total, nb)) {
+#pragma unroll 1
                 for (int kb = kSplit ? work.k0 : 0; kb < (kSplit ? work.k1 : nb); ++kb) {
                     if (!warp_wait_or_look(&s_full[st.i], st.ph, lim, abort)) {
                         ok = false;
@@ -724,7 +757,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairEpiRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(epilogue_regs(kSplit)));
         // ------------------------------------------------------- epilogue
         // warp w: lanes of its quarter, half w / 4 of the columns in chunks of 32
         const int half = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -733,9 +766,9 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
         const uint32_t free0 = peer_smem(&s_free[0], 0), free1 = peer_smem(&s_free[1], 0);
         Ring bf(0), sl(0);
         bool ok = true;
-        Walk<kSplit> work(total, nb);
+        Walk<kSplit, kCtas> work(total, nb);
         while (ok && work.next(total, nb)) {
-            const Tile ti = tile_of(work.t, g, a.E, 256, a.bn);
+            const Tile ti = tile_of(work.t, g, a.E, 128 * kCtas, C::kBn);
             uint64_t acc[kChunks][16];
 #pragma unroll
             for (int j = 0; j < kChunks; ++j)
@@ -745,7 +778,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
             const float *wd = a.wd + (int64_t(ti.e) * ((a.N + 127) / 128) + min(ti.n0 + 32 * kChunks * half, a.N - 1) / 128) * nb;
             float dw = __ldg(wd + (kSplit ? work.k0 : 0));
             const int k0 = kSplit ? work.k0 : 0, k1 = kSplit ? work.k1 : nb;
-#pragma unroll 4
+#pragma unroll kSplit ? 4 : 3
             for (int kb = k0; kb < k1; ++kb) {
                 if (!warp_wait_or_look(&s_scale[sl.i], sl.ph, lim, abort)) {
                     ok = false;
@@ -791,7 +824,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                 }
                 const int64_t all = int64_t(total) * nb;
                 int q0 = pair;   // the first pair with steps of the tile
-                while (q0 > 0 && Walk<kSplit>::run(all, q0) > int64_t(work.t) * nb) --q0;
+                while (q0 > 0 && Walk<kSplit, kCtas>::run(all, q0) > int64_t(work.t) * nb) --q0;
                 for (int q = q0; q < pair && ok; ++q) {
                     ok = parts.wait(q, lim, abort);
                     if (ok) {
@@ -826,10 +859,12 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
         if (!ok && lane == 0) give_up();
     }
     tc_fence_before();
-    cluster_sync();   // nothing of either CTA reaches into the other any more
+    if constexpr (kCtas == 2) cluster_sync();   // nothing of either CTA reaches into the other any more
+    else __syncthreads();
     if (warp == 9) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, 512);
+        if constexpr (kCtas == 2) tmem_dealloc_pair(tmem, 512);
+        else tmem_dealloc(tmem, 512);
     }
 }
 
@@ -881,32 +916,28 @@ h32_status launch_rows(const uint8_t *wq, const uint8_t *xq, const float *xd, in
     return launch_clusters<rows_kernel<NC>>(grid, kRowsWarps * 32, a.stages * C::kStage + rest, a.cluster, s, maps, a);
 }
 
-template <int kChunks, bool kSplit = false>
-h32_status launch_pair(const uint8_t *wq, const uint8_t *xq, const float *xd, int64_t ldxd, F8Args a, int64_t tiles,
+template <int kChunks, int kCtas, bool kSplit = false>
+h32_status launch_lanes(const uint8_t *wq, const uint8_t *xq, const float *xd, int64_t ldxd, const F8Args &a, int64_t tiles,
                        int sms, cudaStream_t s) {
-    a.bn = 64 * kChunks;
-    const uint32_t stage = Pair::kA + Pair::b_bytes(a.bn) + 512;
-    const size_t rest = Groups::bytes(a.E) + 2 * 1024 + 2 * 512 + 8 * 4096;
-    const int fit = static_cast<int>((kMaxSmem - rest) / stage);
-    a.stages = fit < kMaxStages ? fit : kMaxStages;
+    using C = Lanes<kChunks, kCtas>;
     CUtensorMap maps[3];
-    if (!code_map(&maps[0], wq, a.K, int64_t(a.E) * a.N, a.bn / 2) || !code_map(&maps[1], xq, a.K, a.M, 128) ||
+    if (!code_map(&maps[0], wq, a.K, int64_t(a.E) * a.N, C::kBn / kCtas) || !code_map(&maps[1], xq, a.K, a.M, 128) ||
         !scale_map(&maps[2], xd, ldxd, (a.K + 127) / 128, 128)) {
         note_error("cuTensorMapEncodeTiled rejected a tensor map of the 8-bit product");
         return H32_ERR_CUDA;
     }
-    const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
+    const int units = static_cast<int>(tiles < sms / kCtas ? tiles : sms / kCtas);
     // the epilogue's setmaxnreg.inc waits until the pool holds its registers: never launch
     // with fewer registers a thread than the hand-over assumes
     static const int regs = [] {
         cudaFuncAttributes fa{};
-        return cudaFuncGetAttributes(&fa, pair_kernel<kChunks, kSplit>) == cudaSuccess ? fa.numRegs : -1;
+        return cudaFuncGetAttributes(&fa, lanes_kernel<kChunks, kSplit, kCtas>) == cudaSuccess ? fa.numRegs : -1;
     }();
-    if (regs < 168) {
+    if (regs < kPairRegs) {
         note_error("8-bit product compiled with fewer registers than its warpgroups hand over");
         return H32_ERR_CUDA;
     }
-    return launch_clusters<pair_kernel<kChunks, kSplit>>(2 * pairs, kPairWarps * 32, a.stages * stage + rest, 2, s, maps, a);
+    return launch_clusters<lanes_kernel<kChunks, kSplit, kCtas>>(kCtas * units, kPairWarps * 32, C::kSmem, kCtas, s, maps, a);
 }
 
 // How pair_kernel takes `chunks` chunks of 256 tokens (as the host knows them).  A K step of 64, 128
@@ -980,20 +1011,26 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
     const int64_t per = (M + E - 1) / E;
     if (per <= (off ? 8 : 16)) return launch_rows<16>(wq, xq, xd, ldxd, a, nt * E, sms, s);
     if (per <= (off ? 20 : kRowsTokens)) return launch_rows<32>(wq, xq, xd, ldxd, a, nt * E, sms, s);
-    const int64_t chunks = off ? E + M / 256 : (M + 255) / 256;
-    const PairPlan plan = plan_pairs(chunks, N, K, sms);
-    if (plan.pairs > 0 && ws && !off) {
+    const bool one = per <= (off ? 96 : 128);
+    const int64_t rows = one ? 128 : 256, chunks = off ? E + M / rows : (M + rows - 1) / rows;
+    const PairPlan plan = plan_pairs(chunks, N, K, one ? 2 * sms : sms);
+    if (plan.pairs > 0 && ws && !off && !one) {
         if (ws_bytes < Partials::bytes(plan.pairs)) return H32_ERR_INVALID_ARG;
         a.ws = static_cast<uint8_t *>(ws);
         const size_t flags = Partials::flags(plan.pairs);
         const cudaError_t e = cudaMemsetAsync(a.ws + Partials::bytes(plan.pairs) - flags, 0, flags, s);
         if (e != cudaSuccess) return launch_status(e);
-        return launch_pair<4, true>(wq, xq, xd, ldxd, a, plan.pairs, sms, s);
+        return launch_lanes<4, 2, true>(wq, xq, xd, ldxd, a, plan.pairs, sms, s);
     }
     const int64_t tiles = (N + plan.bn - 1) / plan.bn * chunks;
-    if (plan.bn == 256) return launch_pair<4>(wq, xq, xd, ldxd, a, tiles, sms, s);
-    if (plan.bn == 128) return launch_pair<2>(wq, xq, xd, ldxd, a, tiles, sms, s);
-    return launch_pair<1>(wq, xq, xd, ldxd, a, tiles, sms, s);
+    if (one) {
+        if (plan.bn == 256) return launch_lanes<4, 1>(wq, xq, xd, ldxd, a, tiles, sms, s);
+        if (plan.bn == 128) return launch_lanes<2, 1>(wq, xq, xd, ldxd, a, tiles, sms, s);
+        return launch_lanes<1, 1>(wq, xq, xd, ldxd, a, tiles, sms, s);
+    }
+    if (plan.bn == 256) return launch_lanes<4, 2>(wq, xq, xd, ldxd, a, tiles, sms, s);
+    if (plan.bn == 128) return launch_lanes<2, 2>(wq, xq, xd, ldxd, a, tiles, sms, s);
+    return launch_lanes<1, 2>(wq, xq, xd, ldxd, a, tiles, sms, s);
 }
 
 }  // namespace
@@ -1016,7 +1053,7 @@ extern "C" h32_status h32_f8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t 
     if (M < 0 || N <= 0 || K <= 0 || K % 32 != 0 || !bytes) return H32_ERR_INVALID_ARG;
     int sms = 0;
     H32_TRY(check_device(&sms));
-    const int pairs = M > kRowsTokens ? plan_pairs((M + 255) / 256, N, K, sms).pairs : 0;
+    const int pairs = M > 128 ? plan_pairs((M + 255) / 256, N, K, sms).pairs : 0;
     *bytes = pairs > 0 ? Partials::bytes(pairs) : 0;
     return H32_OK;
 }
