@@ -7,11 +7,29 @@
 // tile in TMEM, the epilogue warps read it back and fold it into registers while the
 // tensor core does the next one.
 //
-// rows_kernel: weight rows on the TMEM lanes, NC tokens as its columns.
-//   A tile is 128 weight rows (one block of scales: d_w is uniform) x NC tokens.
+// rows_kernel, for a few tokens: weight rows on the TMEM lanes, NC tokens as its columns.
+//   A tile is 128 weight rows (one block of scales: d_w is uniform) x NC tokens; with few
+//   tiles a cluster of CTAs shares its K steps out and adds up through shared memory.
 //   warps 0..3  epilogue, a lane quarter each
 //   warp 4      TMA producer: per K step the rows' and the tokens' codes and the tokens' scales
 //   warp 5      TMEM allocator and MMA issuer
+//   Bound: HBM, a byte a weight (131072 x 5120, one token: 108 us, 6.2 TB/s, 91% of the measured
+//   copy rate); a narrow projection by launch and the steps' latency (5120 x 5120, 7 tokens:
+//   9.4 us).
+//
+// lanes_kernel, for more: tokens on the lanes, so that a scale is one number a thread and K
+//   step; 128 tokens and one CTA, or 256 and a pair (cta_group::2), x 64, 128 or 256 weight rows.
+//   warps 0..7  epilogue: a lane quarter and half of the columns each
+//   warp 8      TMA producer
+//   warp 9      TMEM allocator; MMA issuer, in a pair's second CTA the messenger of its copies
+//   Bound: of the 406 ns of a pair's K step (256 x 256 x 128) the tensor core needs 270; the rest
+//   is the way from its last product to the epilogue and back, which two buffers of 256
+//   columns (all of TMEM) do not hide: without the loads of the sums and the folds a step
+//   took 445 ns when it took 610 with them.  4096 x 34816 x 5120: 555 us, 2630 TFLOP/s.  (Measured and left: four
+//   buffers of 128 columns, 913 us, as four dependent products of 128 columns take 350 clocks
+//   instead of 256; 16 epilogue warps, scales multiplied ahead of their step, scalar folds, and
+//   loads of sums two at a time, each 5 to 100% slower; arrivals across the pair with release, twice
+//   the time.)
 // Every wait is bounded.
 #include "h32_f8.cuh"
 
@@ -940,30 +958,31 @@ h32_status launch_lanes(const uint8_t *wq, const uint8_t *xq, const float *xd, i
     return launch_clusters<lanes_kernel<kChunks, kSplit, kCtas>>(kCtas * units, kPairWarps * 32, C::kSmem, kCtas, s, maps, a);
 }
 
-// How pair_kernel takes `chunks` chunks of 256 tokens (as the host knows them).  A K step of 64, 128
-// and 256 weight rows takes 332, 355 and 406 ns (256 x 5120 against 5120 rows; 192 rows 444,
-// so never), a tile's end about 3 us for 256 rows.  The narrow ones pay where they fill pairs
-// that were idle (256 tokens x 8192 x 5120: 128 rows 29.5 us, 256 rows 33.6), and equal runs of
-// K steps where the last wave of whole tiles is long (333 x 5120 x 17408: 40 tiles on 76
-// pairs, 64 and 41 us); the partial sums cost about 5 us and 1.5 for each that a tile has.
-struct PairPlan {
+// How lanes_kernel takes `chunks` chunks of tokens (as the host knows them) with so many units
+// (CTAs or pairs).  A K step of 64, 128 and 256 weight rows takes a pair 332, 355 and 406 ns (256
+// tokens x 5120 x 8192 and 16384; 192 rows 444, so never), a tile's end about 3 us for 256
+// rows.  The narrow ones pay where they fill units that were idle (256 tokens x 8192 x 5120: 128
+// rows 29.5 us, 256 rows 33.6), and equal runs of K steps where the last wave of whole tiles is
+// long (333 x 5120 x 17408: 40 tiles on 76 pairs, 64 and 53 us; 1000 tokens 81); the partial
+// sums cost about 5 us and 1.5 for each that a tile has.
+struct Plan {
     int bn;
-    int pairs;   // > 0: runs of K steps for so many pairs, 12 steps at least
+    int runs;   // > 0: runs of K steps for so many pairs, 12 steps at least
 };
-PairPlan plan_pairs(int64_t chunks, int64_t N, int64_t K, int sms) {
-    const int64_t nb = (K + 127) / 128, pairs = sms / 2;
+Plan plan_tiles(int64_t chunks, int64_t N, int64_t K, int units) {
+    const int64_t nb = (K + 127) / 128;
     const auto cost = [&](int64_t bn, int64_t step) {
         const int64_t tiles = (N + bn - 1) / bn * chunks;
-        return (tiles + pairs - 1) / pairs * (nb * step + 12 * bn);
+        return (tiles + units - 1) / units * (nb * step + 12 * bn);
     };
     const int64_t c64 = cost(64, 332), c128 = cost(128, 355), c256 = cost(256, 406);
     const int64_t best = c256 <= c128 && c256 <= c64 ? c256 : c128 <= c64 ? c128 : c64;
     const int64_t tiles = (N + 255) / 256 * chunks, steps = tiles * nb;
-    PairPlan p{best == c256 ? 256 : best == c128 ? 128 : 64, 0};
-    const int64_t n = steps / 12 < pairs ? steps / 12 : pairs;
+    Plan p{best == c256 ? 256 : best == c128 ? 128 : 64, 0};
+    const int64_t n = steps / 12 < units ? steps / 12 : units;
     if (n < 2 || steps >= 0x7FFFFFFFll) return p;
     const int64_t run = (steps + n - 1) / n;
-    if (run * 406 + (tiles / n + 1) * 3072 + 5000 + 1500 * ((nb + run - 1) / run) < best) p.pairs = static_cast<int>(n);
+    if (run * 406 + (tiles / n + 1) * 3072 + 5000 + 1500 * ((nb + run - 1) / run) < best) p.runs = static_cast<int>(n);
     return p;
 }
 
@@ -1004,23 +1023,27 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
     a.wait_limit = wait_limit();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // Tokens of a group, as far as the host knows them, decide the kernel.  Dense, 34816 x
-    // 5120: 32 tokens as columns 39 us, on the lanes 44; 50 tokens 42 (as 64 columns) and
-    // 44, but 5120 x 5120 27 and 21.  Experts (128 of 1536 x 2048) with 4, 16 and 32 tokens on
-    // average: 16 columns 67, 101 and 151 us, 32 columns 75, 85 and 129, lanes 100, 102 and 103
-    // (groups differ, and a second chunk reads the weights again).
+    // 5120: 16 tokens as columns 34 us, on the lanes 41; 32 tokens 39 and 35, but 5120 x 17408 25
+    // and 47 (K shared out over a cluster).  Experts (128 of 1536 x 2048) with 4, 16 and 32
+    // tokens on average: 16 columns 67, 101 and 151 us, lanes 74, 76 and 77 (groups differ, and a
+    // second chunk of columns reads the weights again).
     const int64_t per = (M + E - 1) / E;
     if (per <= (off ? 8 : 16)) return launch_rows<16>(wq, xq, xd, ldxd, a, nt * E, sms, s);
-    if (per <= (off ? 20 : kRowsTokens)) return launch_rows<32>(wq, xq, xd, ldxd, a, nt * E, sms, s);
+    if (!off && per <= kRowsTokens) return launch_rows<32>(wq, xq, xd, ldxd, a, nt, sms, s);
+    // One CTA a tile up to 128 tokens a group (experts: up to 96 on average), two beyond: of 256
+    // rows of a pair the half without tokens would idle (100 x 34816 x 5120: 36 and 45 us, 64
+    // tokens an expert 80 and 104; 4096 x 34816 x 5120 the other way, as a pair reads its
+    // weights once).
     const bool one = per <= (off ? 96 : 128);
     const int64_t rows = one ? 128 : 256, chunks = off ? E + M / rows : (M + rows - 1) / rows;
-    const PairPlan plan = plan_pairs(chunks, N, K, one ? 2 * sms : sms);
-    if (plan.pairs > 0 && ws && !off && !one) {
-        if (ws_bytes < Partials::bytes(plan.pairs)) return H32_ERR_INVALID_ARG;
+    const Plan plan = plan_tiles(chunks, N, K, one ? sms : sms / 2);
+    if (plan.runs > 0 && ws && !off && !one) {
+        if (ws_bytes < Partials::bytes(plan.runs)) return H32_ERR_INVALID_ARG;
         a.ws = static_cast<uint8_t *>(ws);
-        const size_t flags = Partials::flags(plan.pairs);
-        const cudaError_t e = cudaMemsetAsync(a.ws + Partials::bytes(plan.pairs) - flags, 0, flags, s);
+        const size_t flags = Partials::flags(plan.runs);
+        const cudaError_t e = cudaMemsetAsync(a.ws + Partials::bytes(plan.runs) - flags, 0, flags, s);
         if (e != cudaSuccess) return launch_status(e);
-        return launch_lanes<4, 2, true>(wq, xq, xd, ldxd, a, plan.pairs, sms, s);
+        return launch_lanes<4, 2, true>(wq, xq, xd, ldxd, a, plan.runs, sms, s);
     }
     const int64_t tiles = (N + plan.bn - 1) / plan.bn * chunks;
     if (one) {
@@ -1053,8 +1076,8 @@ extern "C" h32_status h32_f8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t 
     if (M < 0 || N <= 0 || K <= 0 || K % 32 != 0 || !bytes) return H32_ERR_INVALID_ARG;
     int sms = 0;
     H32_TRY(check_device(&sms));
-    const int pairs = M > 128 ? plan_pairs((M + 255) / 256, N, K, sms).pairs : 0;
-    *bytes = pairs > 0 ? Partials::bytes(pairs) : 0;
+    const int runs = M > 128 ? plan_tiles((M + 255) / 256, N, K, sms / 2).runs : 0;
+    *bytes = runs > 0 ? Partials::bytes(runs) : 0;
     return H32_OK;
 }
 
