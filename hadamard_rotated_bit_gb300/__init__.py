@@ -1197,15 +1197,35 @@ def _blocks128(n) -> int:
     return (int(n) + 127) // 128
 
 
+_usual = None   # what the usual calls need of torch, looked up once
+
+
+def _usual_torch():
+    global _usual
+    if _usual is None:
+        t = _torch()
+        _usual = (t.Tensor, t.empty, t.bfloat16, t.float32, t.int32, t.uint8,
+                  getattr(t._C, "_cuda_getDevice", None), getattr(t._C, "_cuda_getCurrentRawStream", None))
+    return _usual
+
+
 def _plain(dev, dtype, *tensors):
     """Whether all are contiguous tensors of `dtype` on CUDA device `dev`: what most calls
     pass, found out in a fraction of the time that the checks with their messages take
     (their sizes are compared by the caller)."""
-    kind = _torch().Tensor
+    kind = _usual_torch()[0]
     for t in tensors:
         if not (isinstance(t, kind) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
             return False
     return True
+
+
+def _stream_for(dev, stream):
+    """_enter_stream, with the usual case (no stream given, the tensors' device current) first."""
+    u = _usual_torch()
+    if stream is None and u[7] is not None and u[6] is not None and u[6]() == dev.index:
+        return u[7](dev.index), None
+    return _enter_stream(dev, stream)
 
 
 def h32_quantize_act_f8(x, rotate=False, row_idx=None, xq=None, xd=None, stream=None):
@@ -1215,10 +1235,9 @@ def h32_quantize_act_f8(x, rotate=False, row_idx=None, xq=None, xd=None, stream=
     row_idx [R] int32: output row r is x[row_idx[r]] (the grouped order of an expert
     product); None: R = T.  rotate as for the other quantizers, here off by default
     (weights quantized elsewhere are not rotated)."""
-    torch = _torch()
-    bf16, f32, i32, u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-    if not (isinstance(x, torch.Tensor) and x.dim() == 2 and x.dtype in (bf16, f32) and x.is_cuda
-            and x.is_contiguous() and xq is None and xd is None
+    kind, empty, bf16, f32, i32, u8 = _usual_torch()[:6]
+    if not (xq is None and xd is None and isinstance(x, kind) and (x.dtype is bf16 or x.dtype is f32)
+            and x.is_cuda and x.dim() == 2 and x.is_contiguous()
             and (row_idx is None or (_plain(x.get_device(), i32, row_idx) and row_idx.dim() == 1))):
         _need(x, "x", (bf16, f32), (_ge(0), _ge(0)), pitched=True)
         R, K = x.shape
@@ -1233,15 +1252,18 @@ def h32_quantize_act_f8(x, rotate=False, row_idx=None, xq=None, xd=None, stream=
     T, K = x.shape
     R = T if row_idx is None else row_idx.shape[0]
     dev = x.device
-    raw, guard = _enter_stream(dev, stream)
+    raw, guard = _stream_for(dev, stream)
     try:
         if xq is None:
-            xq = torch.empty((R, K), dtype=u8, device=dev)
+            xq = empty((R, K), dtype=u8, device=dev)
         if xd is None:
-            xd = torch.empty(((K + 127) // 128, (R + 3) // 4 * 4), dtype=f32, device=dev)
-        st = lib().h32_quantize_act_f8(x.data_ptr(), x.dtype == bf16, T, K, x.stride(0) if T > 1 else K,
+            ldxd = (R + 3) // 4 * 4
+            xd = empty(((K + 127) // 128, ldxd), dtype=f32, device=dev)
+        else:
+            ldxd = xd.shape[1]
+        st = lib().h32_quantize_act_f8(x.data_ptr(), x.dtype is bf16, T, K, x.stride(0) if T > 1 else K,
                                        None if row_idx is None else row_idx.data_ptr(), R, xq.data_ptr(),
-                                       xd.data_ptr(), xd.shape[1], _rot_arg(rotate), raw)
+                                       xd.data_ptr(), ldxd, _rot_arg(rotate), raw)
     finally:
         if guard is not None:
             guard.__exit__(None, None, None)
@@ -1308,11 +1330,10 @@ def h32_f8_gemm_experts(wq, wd, xq, xd, expert_off, N, R=None, y=None, y_dtype=N
 
 
 def _f8_gemm(fn, wq, wd, xq, xd, off, N, M, y, y_dtype, stream):
-    torch = _torch()
-    bf16, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+    kind, empty, bf16, f32, i32, u8 = _usual_torch()[:6]
     plain = False
-    if M is None and y is None and y_dtype in (None, bf16, f32) and (off is None or type(N) is int and N > 0) and \
-            isinstance(wq, torch.Tensor) and wq.is_cuda and wq.dim() == 2:
+    if M is None and y is None and (y_dtype is None or y_dtype is bf16 or y_dtype is f32) and (off is None or type(N) is int and N > 0) and \
+            isinstance(wq, kind) and wq.is_cuda and wq.dim() == 2:
         # the usual call, all sizes as the operands give them
         (rows, K), dev = wq.shape, wq.get_device()
         e, n = (1, rows) if off is None else (rows // N, N)
@@ -1344,25 +1365,28 @@ def _f8_gemm(fn, wq, wd, xq, xd, off, N, M, y, y_dtype, stream):
     if M is None:
         M = xq.shape[0]
     dev = wq.device
-    raw, guard = _enter_stream(dev, stream)
+    bf = (y_dtype if y is None else y.dtype) is bf16
+    raw, guard = _stream_for(dev, stream)
     try:
         if y is None:
-            y = torch.empty((M, n), dtype=y_dtype or f32, device=dev)
+            y, ldy = empty((M, n), dtype=y_dtype or f32, device=dev), n
+        else:
+            ldy = _pitch(y)
         if off is None:
             wp, ws_bytes = None, 0
             if M > F8_FEW_TOKENS:
                 ws_bytes = _f8_workspace_bytes(dev.index, M, n, K)
                 if ws_bytes:
                     # the call's own: freed with it, reused only by later work of the stream
-                    ws = torch.empty(ws_bytes, dtype=u8, device=dev)
+                    ws = empty(ws_bytes, dtype=u8, device=dev)
                     wp = ws.data_ptr()
             st = lib().h32_f8_gemm(wq.data_ptr(), wd.data_ptr(), xq.data_ptr(), xd.data_ptr(),
-                                   xd.shape[1], M, n, K, y.data_ptr(), y.dtype == bf16, _pitch(y),
+                                   xd.shape[1], M, n, K, y.data_ptr(), bf, ldy,
                                    wp, ws_bytes, raw)
         else:
             st = lib().h32_f8_gemm_experts(
                 wq.data_ptr(), wd.data_ptr(), e, xq.data_ptr(), xd.data_ptr(), xd.shape[1],
-                off.data_ptr(), M, n, K, y.data_ptr(), y.dtype == bf16, _pitch(y), raw)
+                off.data_ptr(), M, n, K, y.data_ptr(), bf, ldy, raw)
     finally:
         if guard is not None:
             guard.__exit__(None, None, None)
@@ -1382,54 +1406,53 @@ def h32_token_logprobs(logits, targets=None, top=0, logprob=None, entropy=None, 
     (negative: no token given, its result 0; V or more: NaN) -> (logprob, shaped as
     targets, or None; entropy [T] fp32; top_id [T][top] int32 and top_logprob [T][top]
     fp32, by decreasing logit, ties to the lower id, or None with top = 0)."""
-    torch = _torch()
-    i32, f32 = (torch.int32,), (torch.float32,)
+    kind, empty, bf16, f32, i32 = _usual_torch()[:5]
     top = int(top)
     plain = False
     if logprob is None and entropy is None and top_id is None and top_logprob is None and \
-            isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() == 2:
+            isinstance(logits, kind) and logits.is_cuda and logits.dim() == 2:
         # the usual call
         T, V = logits.shape
-        plain = (logits.is_contiguous() and logits.dtype in (torch.bfloat16, torch.float32) and V > 0
+        plain = (logits.is_contiguous() and (logits.dtype is f32 or logits.dtype is bf16) and V > 0
                  and 0 <= top <= min(LOGPROBS_MAX_TOP, V)
-                 and (targets is None or (_plain(logits.get_device(), torch.int32, targets)
+                 and (targets is None or (_plain(logits.get_device(), i32, targets)
                                           and targets.dim() in (1, 2) and targets.shape[0] == T)))
     if not plain:
-        _need(logits, "logits", (torch.bfloat16, torch.float32), (_ge(0), _ge(1)), pitched=True)
+        _need(logits, "logits", (bf16, f32), (_ge(0), _ge(1)), pitched=True)
         T, V = logits.shape
         if not 0 <= top <= min(LOGPROBS_MAX_TOP, V):
             raise ValueError(f"top must be between 0 and {min(LOGPROBS_MAX_TOP, V)}")
         if targets is not None:
-            _need(targets, "targets", i32, (T,) if targets.dim() == 1 else (T, _ge(0)))
+            _need(targets, "targets", (i32,), (T,) if targets.dim() == 1 else (T, _ge(0)))
             if logprob is not None:
-                _need(logprob, "logprob", f32, tuple(targets.shape))
+                _need(logprob, "logprob", (f32,), tuple(targets.shape))
         elif logprob is not None:
             raise ValueError("logprob needs targets")
         if entropy is not None:
-            _need(entropy, "entropy", f32, (_ge(T),))
+            _need(entropy, "entropy", (f32,), (_ge(T),))
         if top == 0 and (top_id is not None or top_logprob is not None):
             raise ValueError("top_id and top_logprob need top")
         if top_id is not None:
-            _need(top_id, "top_id", i32, (_ge(T), top))
+            _need(top_id, "top_id", (i32,), (_ge(T), top))
         if top_logprob is not None:
-            _need(top_logprob, "top_logprob", f32, (_ge(T), top))
+            _need(top_logprob, "top_logprob", (f32,), (_ge(T), top))
         _same_gpu(("logits", logits), ("targets", targets), ("logprob", logprob), ("entropy", entropy),
                   ("top_id", top_id), ("top_logprob", top_logprob))
     n = 0 if targets is None else 1 if targets.dim() == 1 else targets.shape[1]
     dev = logits.device
-    raw, guard = _enter_stream(dev, stream)
+    raw, guard = _stream_for(dev, stream)
     try:
         if targets is not None and logprob is None:
-            logprob = torch.empty(targets.shape, dtype=torch.float32, device=dev)
+            logprob = empty(targets.shape, dtype=f32, device=dev)
         if entropy is None:
-            entropy = torch.empty(T, dtype=torch.float32, device=dev)
+            entropy = empty(T, dtype=f32, device=dev)
         if top > 0:
             if top_id is None:
-                top_id = torch.empty((T, top), dtype=torch.int32, device=dev)
+                top_id = empty((T, top), dtype=i32, device=dev)
             if top_logprob is None:
-                top_logprob = torch.empty((T, top), dtype=torch.float32, device=dev)
+                top_logprob = empty((T, top), dtype=f32, device=dev)
         st = lib().h32_token_logprobs(
-            logits.data_ptr(), logits.dtype == torch.bfloat16, T, V, _pitch(logits), _raw(targets), n, top,
+            logits.data_ptr(), logits.dtype is bf16, T, V, _pitch(logits), _raw(targets), n, top,
             _raw(logprob), entropy.data_ptr(), _raw(top_id), _raw(top_logprob), raw)
     finally:
         if guard is not None:
