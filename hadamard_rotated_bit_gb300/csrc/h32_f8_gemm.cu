@@ -980,7 +980,9 @@ Plan plan_tiles(int64_t chunks, int64_t N, int64_t K, int units) {
     const int64_t tiles = (N + 255) / 256 * chunks, steps = tiles * nb;
     Plan p{best == c256 ? 256 : best == c128 ? 128 : 64, 0};
     const int64_t n = steps / 12 < units ? steps / 12 : units;
-    if (n < 2 || steps >= 0x7FFFFFFFll) return p;
+    // (not where every pair has many tiles: the runs then walk all weights at once, which no
+    // longer fit the L2; 2048 x 34816 x 5120 read them seven times)
+    if (n < 2 || steps >= 0x7FFFFFFFll || tiles > 4 * int64_t(units)) return p;
     const int64_t run = (steps + n - 1) / n;
     if (run * 406 + (tiles / n + 1) * 3072 + 5000 + 1500 * ((nb + run - 1) / run) < best) p.runs = static_cast<int>(n);
     return p;
