@@ -188,13 +188,25 @@ __device__ __forceinline__ void store_lines(const F8Args &a, const uint8_t *buf,
                     *reinterpret_cast<const uint4 *>(buf + r * 128 + ((p ^ (r & 7)) << 4));
         }
     } else {
+        // rows that start anywhere: a value a lane, whole rows a store (N odd, or the last columns)
         const int cols = min(bytes / es, a.N - n);
-        for (int r = max(0, lo - r0); r < min(32, hi - r0); ++r)
-            for (int c = lane; c < cols; c += 32) {
-                const uint8_t *v = buf + r * 128 + (((c * es >> 4) ^ (r & 7)) << 4) + (c * es & 15);
-                if (es == 2) reinterpret_cast<uint16_t *>(y + r * a.ldy * 2)[c] = *reinterpret_cast<const uint16_t *>(v);
-                else reinterpret_cast<uint32_t *>(y + r * a.ldy * 4)[c] = *reinterpret_cast<const uint32_t *>(v);
+        const int at = lane * es, rest = at & 15;
+#pragma unroll 4
+        for (int r = 0; r < 32; ++r) {
+            const bool in = r0 + r >= lo && r0 + r < hi;
+            const uint8_t *v = buf + r * 128 + rest;
+            if (es == 4) {
+                if (in && lane < cols)
+                    reinterpret_cast<uint32_t *>(y)[lane] = *reinterpret_cast<const uint32_t *>(v + (((at >> 4) ^ (r & 7)) << 4));
+            } else {
+                if (in && lane < cols)
+                    reinterpret_cast<uint16_t *>(y)[lane] = *reinterpret_cast<const uint16_t *>(v + (((at >> 4) ^ (r & 7)) << 4));
+                if (in && lane + 32 < cols)
+                    reinterpret_cast<uint16_t *>(y)[lane + 32] =
+                        *reinterpret_cast<const uint16_t *>(v + (((at >> 4) + 4 ^ (r & 7)) << 4));
             }
+            y += a.ldy * es;
+        }
     }
 }
 
@@ -963,8 +975,9 @@ h32_status launch_lanes(const uint8_t *wq, const uint8_t *xq, const float *xd, i
 // tokens x 5120 x 8192 and 16384; 192 rows 444, so never), a tile's end about 3 us for 256
 // rows.  The narrow ones pay where they fill units that were idle (256 tokens x 8192 x 5120: 128
 // rows 29.5 us, 256 rows 33.6), and equal runs of K steps where the last wave of whole tiles is
-// long (333 x 5120 x 17408: 40 tiles on 76 pairs, 64 and 53 us; 1000 tokens 81); the partial
-// sums cost about 5 us and 1.5 for each that a tile has.
+// long (333 x 5120 x 17408: 40 tiles on 76 pairs, 64 and 53 us; 1000 tokens 81); they cost about
+// 14 us (clearing the flags, and no overlap with the kernel before) and 3.2 for each partial
+// sum of a tile.
 struct Plan {
     int bn;
     int runs;   // > 0: runs of K steps for so many pairs, 12 steps at least
@@ -979,12 +992,18 @@ Plan plan_tiles(int64_t chunks, int64_t N, int64_t K, int units) {
     const int64_t best = c256 <= c128 && c256 <= c64 ? c256 : c128 <= c64 ? c128 : c64;
     const int64_t tiles = (N + 255) / 256 * chunks, steps = tiles * nb;
     Plan p{best == c256 ? 256 : best == c128 ? 128 : 64, 0};
-    const int64_t n = steps / 12 < units ? steps / 12 : units;
     // (not where every pair has many tiles: the runs then walk all weights at once, which no
     // longer fit the L2; 2048 x 34816 x 5120 read them seven times)
-    if (n < 2 || steps >= 0x7FFFFFFFll || tiles > 4 * int64_t(units)) return p;
-    const int64_t run = (steps + n - 1) / n;
-    if (run * 406 + (tiles / n + 1) * 3072 + 5000 + 1500 * ((nb + run - 1) / run) < best) p.runs = static_cast<int>(n);
+    if (steps >= 0x7FFFFFFFll || tiles > 4 * int64_t(units)) return p;
+    int64_t least = best;
+    for (int64_t n = steps / 12 < units ? steps / 12 : units; n >= 2; n = n * 3 / 4) {
+        const int64_t run = (steps + n - 1) / n;
+        const int64_t c = run * 406 + (tiles / n + 1) * 3072 + 14000 + 3200 * ((nb + run - 1) / run);
+        if (c < least) {
+            least = c;
+            p.runs = static_cast<int>(n);
+        }
+    }
     return p;
 }
 

@@ -162,7 +162,7 @@ def test_product_exact(h32, M, N, K, bf16):
     assert torch.equal(y.cpu(), ref.bfloat16() if bf16 else ref)
 
 
-@pytest.mark.parametrize("M,N,K", [(300, 5120, 8192), (1000, 5001, 5152), (140, 1024, 15904)])
+@pytest.mark.parametrize("M,N,K", [(300, 5120, 16000), (1000, 5001, 16000), (140, 5632, 16352)])
 def test_product_shared_out_along_k(h32, M, N, K):
     """Sizes whose tiles are cut along K between the pairs of CTAs: with the binding's
     workspace, one of the caller's (dirty), and none; on two streams at once and from two
@@ -342,7 +342,7 @@ def test_streams_and_graphs(h32, M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(2, 4096, 4096), (24, 4096, 4096), (60, 4096, 4096), (700, 4096, 4096),
-                                   (300, 5120, 8192)])
+                                   (300, 5120, 16000)])
 def test_one_poll_wait_bound(h32, M, N, K):
     """A bound of one poll: waits give up, the status says so once, and the same context
     then computes exactly."""
