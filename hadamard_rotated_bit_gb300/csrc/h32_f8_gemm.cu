@@ -236,7 +236,7 @@ struct Rows {
     static constexpr uint32_t kA = 128 * 128, kB = NC * 128;  // bytes of a stage's parts
     static constexpr uint32_t kS = NC * 4 < 128 ? 128 : NC * 4;
     static constexpr uint32_t kStage = kA + kB + kS;
-    static constexpr int kMaxCluster = 8, kPerSm = 2;         // CTAs of a tile, of an SM
+    static constexpr int kPerSm = 2;                          // CTAs of an SM
     // the partial sums that a CTA gets: [share][column][row]
     static __host__ __device__ uint32_t parts(int cluster) { return (cluster - 1) * (NC / cluster) * 512; }
 };
@@ -920,18 +920,21 @@ h32_status launch_clusters(int grid, int threads, size_t smem, int cluster, cuda
     return launch_status(e != cudaSuccess ? e : cudaGetLastError());
 }
 
+// CTAs that rows_kernel deals a tile's K steps to.  With few tiles a share of at least 4 steps
+// each, as long as all of them run at once.  (5120 x 5120 and 7 tokens: one CTA a tile 13.9 us, 4
+// 9.4.)
+int rows_cluster(int64_t tiles, int64_t nb, int sms) {
+    int c = 1;
+    while (2 * c <= 8 && tiles * 2 * c <= Rows<16>::kPerSm * int64_t(sms) && nb >= 8 * c) c *= 2;
+    return c;
+}
+
 template <int NC>
 h32_status launch_rows(const uint8_t *wq, const uint8_t *xq, const float *xd, int64_t ldxd, F8Args a, int64_t tiles,
                        int sms, cudaStream_t s) {
     using C = Rows<NC>;
     const int nb = (a.K + 127) / 128;
-    // Fewer tiles than SMs: a tile to the CTAs of a cluster, each a share of the K steps of at
-    // least 4, as long as all of them run at once.  (5120 x 5120 and 7 tokens:
-    // one CTA a tile 12.6 us, 4 7.2.)
-    a.cluster = 1;
-    if (!a.off)
-        while (2 * a.cluster <= C::kMaxCluster && tiles * 2 * a.cluster <= C::kPerSm * int64_t(sms) && nb >= 8 * a.cluster)
-            a.cluster *= 2;
+    a.cluster = a.off ? 1 : rows_cluster(tiles, nb, sms);
     const bool two = tiles * a.cluster > sms && a.cluster > 1;
     const size_t rest = Groups::bytes(a.E) + 1024 + C::parts(a.cluster);
     const int fit = static_cast<int>(((two ? kMaxSmem / 2 : kMaxSmem) - rest) / C::kStage);
@@ -979,10 +982,11 @@ h32_status launch_lanes(const uint8_t *wq, const uint8_t *xq, const float *xd, i
 // 14 us (clearing the flags, and no overlap with the kernel before) and 3.2 for each partial
 // sum of a tile.
 struct Plan {
-    int bn;
-    int runs;   // > 0: runs of K steps for so many pairs, 12 steps at least
+    int bn;         // weight rows of a tile; 0: rows_kernel
+    int runs;       // > 0: runs of K steps for so many pairs, 12 steps at least
+    int64_t cost;   // ns, without the launch
 };
-Plan plan_tiles(int64_t chunks, int64_t N, int64_t K, int units) {
+Plan plan_tiles(int64_t chunks, int64_t N, int64_t K, int units, bool may_run) {
     const int64_t nb = (K + 127) / 128;
     const auto cost = [&](int64_t bn, int64_t step) {
         const int64_t tiles = (N + bn - 1) / bn * chunks;
@@ -991,20 +995,33 @@ Plan plan_tiles(int64_t chunks, int64_t N, int64_t K, int units) {
     const int64_t c64 = cost(64, 332), c128 = cost(128, 355), c256 = cost(256, 406);
     const int64_t best = c256 <= c128 && c256 <= c64 ? c256 : c128 <= c64 ? c128 : c64;
     const int64_t tiles = (N + 255) / 256 * chunks, steps = tiles * nb;
-    Plan p{best == c256 ? 256 : best == c128 ? 128 : 64, 0};
+    Plan p{best == c256 ? 256 : best == c128 ? 128 : 64, 0, best};
     // (not where every pair has many tiles: the runs then walk all weights at once, which no
     // longer fit the L2; 2048 x 34816 x 5120 read them seven times)
-    if (steps >= 0x7FFFFFFFll || tiles > 4 * int64_t(units)) return p;
-    int64_t least = best;
+    if (!may_run || steps >= 0x7FFFFFFFll || tiles > 4 * int64_t(units)) return p;
     for (int64_t n = steps / 12 < units ? steps / 12 : units; n >= 2; n = n * 3 / 4) {
         const int64_t run = (steps + n - 1) / n;
-        const int64_t c = run * 406 + (tiles / n + 1) * 3072 + 14000 + 3200 * ((nb + run - 1) / run);
-        if (c < least) {
-            least = c;
+        const int64_t c = run * 406 + (tiles / n + 1) * (12 * 256) + 14000 + 3200 * ((nb + run - 1) / run);
+        if (c < p.cost) {
+            p.cost = c;
             p.runs = static_cast<int>(n);
         }
     }
     return p;
+}
+
+// Dense products of more tokens than rows_kernel has columns.  One CTA a tile up to 128 tokens, a
+// pair beyond.  Where the tiles are few and K is long, rows_kernel is faster with a tile for
+// each 32 tokens, as its clusters share K out: its steps take 430 ns of a CTA and its start 5 us
+// more than the other kernel's (128 x 783 x 8896 12.0 us, on the lanes 26.1; 64 x 5120 x 17408 36
+// and 47; 512 x 512 x 4096 12.5 and 15.3; but 723 x 418 x 1568 12.4 and 9.2).
+Plan plan_dense(int64_t M, int64_t N, int64_t K, int sms) {
+    const bool one = M <= 128;
+    Plan p = plan_tiles(one ? 1 : (M + 255) / 256, N, K, one ? sms : sms / 2, !one);
+    const int64_t nb = (K + 127) / 128;
+    const int c = rows_cluster((N + 127) / 128 * ((M + 31) / 32), nb, sms);
+    const int64_t rows = 5000 + 430 * ((nb + c - 1) / c);
+    return c > 1 && rows < p.cost ? Plan{0, 0, rows} : p;
 }
 
 h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint8_t *xq, const float *xd,
@@ -1050,15 +1067,15 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
     // second chunk of columns reads the weights again).
     const int64_t per = (M + E - 1) / E;
     if (per <= (off ? 8 : 16)) return launch_rows<16>(wq, xq, xd, ldxd, a, nt * E, sms, s);
-    if (!off && per <= kRowsTokens) return launch_rows<32>(wq, xq, xd, ldxd, a, nt, sms, s);
-    // One CTA a tile up to 128 tokens a group (experts: up to 96 on average), two beyond: of 256
-    // rows of a pair the half without tokens would idle (100 x 34816 x 5120: 36 and 45 us, 64
-    // tokens an expert 80 and 104; 4096 x 34816 x 5120 the other way, as a pair reads its
-    // weights once).
+    // Experts: up to 96 tokens on average one CTA a tile, two beyond, as of 256 rows of a pair the
+    // half without tokens would idle (64 tokens an expert: 80 and 104 us); dense, 100 x 34816 x 5120:
+    // 36 and 45, but 4096 x 34816 x 5120 the other way, as a pair reads its weights once.
     const bool one = per <= (off ? 96 : 128);
     const int64_t rows = one ? 128 : 256, chunks = off ? E + M / rows : (M + rows - 1) / rows;
-    const Plan plan = plan_tiles(chunks, N, K, one ? sms : sms / 2);
-    if (plan.runs > 0 && ws && !off && !one) {
+    const Plan plan = off ? plan_tiles(chunks, N, K, one ? sms : sms / 2, false) : plan_dense(M, N, K, sms);
+    if (!off && (per <= kRowsTokens || plan.bn == 0))
+        return launch_rows<32>(wq, xq, xd, ldxd, a, nt * ((M + 31) / 32), sms, s);
+    if (plan.runs > 0 && ws) {
         if (ws_bytes < Partials::bytes(plan.runs)) return H32_ERR_INVALID_ARG;
         a.ws = static_cast<uint8_t *>(ws);
         const size_t flags = Partials::flags(plan.runs);
@@ -1097,7 +1114,7 @@ extern "C" h32_status h32_f8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t 
     if (M < 0 || N <= 0 || K <= 0 || K % 32 != 0 || !bytes) return H32_ERR_INVALID_ARG;
     int sms = 0;
     H32_TRY(check_device(&sms));
-    const int runs = M > 128 ? plan_tiles((M + 255) / 256, N, K, sms / 2).runs : 0;
+    const int runs = M > kRowsTokens ? plan_dense(M, N, K, sms).runs : 0;
     *bytes = runs > 0 ? Partials::bytes(runs) : 0;
     return H32_OK;
 }

@@ -688,7 +688,7 @@ h32_status h32_quantize_weights_f8(const void *w, h32_in_dtype dt, int64_t N, in
  *   y[m][n] = acc after acc = fma(fl(xd[b][m] * wd[n/128][b]), S_b, acc), b = 0 .. K/128,
  *   S_b = the fp32 sum of block b's products xq[m][k] * wq[n][k] (exact products; the sum's
  *   order and rounding are the tensor core's), rounded once to y's type.  Where few tiles
- *   share the GPU, runs of blocks are folded apart from +0 and then added in order; which
+ *   share the GPU, runs of blocks are folded apart from +0 and then added in a fixed order; which
  *   ones depends on the sizes and the device alone, so equal calls give equal bits.
  * For any M: one new token to long prompts (few tokens share one read of the weights).
  *   wq   [N][K] codes, wd [ceil(N/128)][ceil(K/128)] (h32_quantize_weights_f8)
@@ -697,8 +697,8 @@ h32_status h32_quantize_weights_f8(const void *w, h32_in_dtype dt, int64_t N, in
  *   workspace  nullable, 16-byte aligned device memory of at least
  *        h32_f8_gemm_workspace_bytes (0 for most sizes); any contents, free again when the
  *        call's work is done.  With it tiles that would leave much of the GPU idle are
- *        shared out along K, their partial sums added in the order of K (without it the
- *        same sums, slower and in one order over all of K)
+ *        shared out along K, their partial sums added in a fixed order (without it the same
+ *        sums, slower and in one order over all of K)
  * Any N >= 1; K a multiple of 32.
  * The expert form multiplies rows r in [expert_off[e], expert_off[e+1]) by expert e's
  * weights: wq [E][N][K], wd [E][ceil(N/128)][ceil(K/128)], expert_off [E+1] int32 device,

@@ -147,7 +147,7 @@ def _xd(xd, pad=0.0):
 SHAPES = [(1, 1, 32), (1, 5120, 5120), (2, 129, 96), (7, 384, 4224), (15, 100, 160), (16, 128, 128), (17, 500, 640),
           (31, 1000, 2048), (33, 77, 1056), (64, 640, 512), (65, 2000, 384), (128, 257, 1024), (129, 128, 4096),
           (200, 1537, 96), (255, 4096, 320), (256, 256, 256), (257, 700, 5120), (333, 5120, 1024), (511, 96, 736),
-          (1030, 1300, 288), (2048, 8192, 128)]
+          (1030, 1300, 288), (2048, 8192, 128), (33, 831, 4032), (150, 783, 8896), (380, 269, 6464)]
 
 
 @pytest.mark.parametrize("bf16", [False, True])
@@ -341,8 +341,8 @@ def test_streams_and_graphs(h32, M, N, K):
     assert not torch.equal(want, first)
 
 
-@pytest.mark.parametrize("M,N,K", [(2, 4096, 4096), (24, 4096, 4096), (60, 4096, 4096), (700, 4096, 4096),
-                                   (300, 5120, 16000)])
+@pytest.mark.parametrize("M,N,K", [(2, 4096, 4096), (24, 4096, 4096), (60, 4096, 4096), (100, 8192, 4096),
+                                   (700, 4096, 4096), (300, 5120, 16000)])
 def test_one_poll_wait_bound(h32, M, N, K):
     """A bound of one poll: waits give up, the status says so once, and the same context
     then computes exactly."""
