@@ -6,12 +6,12 @@
 //
 // One pass over the logits.  Each thread keeps m, S and W of what it has read (all fp32,
 // rescaled when m grows) and, for the k most probable tokens, the largest value of each of its
-// chunks (32 values, more in rows beyond 2^14 vectors).  The k-th largest of the 64 maxima
-// of groups of four lanes bounds the k best from below, so only chunks that reach it, hardly
-// more than k, are read again (from L2) for their values above it, and of those the k largest
-// are found by counting, for each, the larger ones.  Nothing in the pass itself depends on
-// the values: buffers filled as candidates come cost 30 to 80% more time there.  Rows where too many
-// values reach the bound (ties, mostly) are read again by warps that keep sorted lists.
+// chunks (16 fp32 or 32 bf16 values, more where a CTA takes over 16 steps).  The k-th largest of
+// the 64 maxima of groups of lanes bounds the k best from below, so only chunks that reach it,
+// hardly more than k, are read again (from L2) for their values above it, and of those the k
+// largest are found by counting, for each, the larger ones.  Nothing in the pass itself depends
+// on the values: buffers filled as candidates come cost 30 to 80% more time there.  Rows where
+// too many values reach the bound (ties, mostly) are read again by warps that keep sorted lists.
 //
 // A row is one CTA's, or with few rows a cluster's: its CTAs take consecutive parts and
 // leave their results in the first one's shared memory.
@@ -25,7 +25,6 @@
 namespace h32 {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxTop = 32, kMaxCluster = 8;
 constexpr int kVecs = 4;             // 16-byte loads of a thread's step
 constexpr int kSlots = 16;           // chunks of a thread (32: 45 KB a CTA, f32 rows 10-40% slower)
@@ -185,6 +184,7 @@ struct List {
 
 // the `top` largest of n different keys, in order, by counting the larger ones of each;
 // keys [n .. n + 3] are 0
+template <int kThreads>
 __device__ __forceinline__ void rank_keys(const uint64_t *keys, int n, int top, uint64_t *best) {
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const uint64_t mine = keys[i];
@@ -213,6 +213,7 @@ __device__ __forceinline__ void sync_cluster() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 // `n` bytes (a multiple of 8) of this CTA's shared memory to the first CTA's
+template <int kThreads>
 __device__ __forceinline__ void to_first(void *dst, const void *src, int bytes) {
     uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst)), r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(d));
@@ -221,9 +222,10 @@ __device__ __forceinline__ void to_first(void *dst, const void *src, int bytes) 
                      : "memory");
 }
 
-template <bool kBf16>
+template <bool kBf16, int kThreads>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a) {
     using V4 = Vec<kBf16>;
+    constexpr int kWarps = kThreads / 32, kGroup = kThreads / 64;   // threads of a group
     constexpr int kN = V4::kN;
     __shared__ __align__(16) float s_chunk[kSlots][kThreads];   // largest values of the chunks
     __shared__ __align__(16) uint64_t s_all[kMaxKeys + 4];
@@ -327,9 +329,10 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
         s_W[warp] = W;
     }
     if (a.top > 0) {
-        float g = fmaxf(m_body, __shfl_xor_sync(0xFFFFFFFFu, m_body, 1));
-        g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, 2));
-        if ((lane & 3) == 0) s_group[tid >> 2] = g;
+        float g = m_body;
+#pragma unroll
+        for (int o = 1; o < kGroup; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
+        if (lane % kGroup == 0) s_group[tid / kGroup] = g;
     }
     __syncthreads();
     if (warp == 0) {
@@ -420,18 +423,18 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
         }
         if (tid < 4) s_all[keys + tid] = 0;
         __syncthreads();
-        rank_keys(s_all, keys, a.top, s_part[rank].best);
+        rank_keys<kThreads>(s_all, keys, a.top, s_part[rank].best);
     }
     if (c > 1) {
         sync_cluster();   // (every CTA of the cluster runs, and its part is in its shared memory)
-        if (rank != 0) to_first(&s_part[rank], &s_part[rank], sizeof(Part));
+        if (rank != 0) to_first<kThreads>(&s_part[rank], &s_part[rank], sizeof(Part));
         sync_cluster();
         if (rank != 0) return;
         if (a.top > 0) {
             const int n = static_cast<int>(c) * a.top;
             for (int i = tid; i < n + 4; i += kThreads) s_all[i] = i < n ? s_part[i / a.top].best[i % a.top] : 0;
             __syncthreads();
-            rank_keys(s_all, n, a.top, s_best);
+            rank_keys<kThreads>(s_all, n, a.top, s_best);
         }
     }
     __syncthreads();
@@ -514,13 +517,18 @@ extern "C" h32_status h32_token_logprobs(const void *logits, h32_in_dtype dt, in
     H32_TRY(check_device(&sms));
     // CTAs of a row: as many as leave each at least one whole step, while the grid
     // stays within one wave of 4 CTAs an SM
-    const int64_t steps = V / (kThreads * kVecs * (dt == H32_IN_BF16 ? 8 : 4));
+    const int64_t steps = V / (256 * kVecs * (dt == H32_IN_BF16 ? 8 : 4));
     int c = 1;
     while (c < kMaxCluster && 2 * c <= steps && T * 2 * c <= 4 * int64_t(sms)) c *= 2;
+    // Many rows: what follows the pass is steps that wait for one another, so more rows at once
+    // in CTAs of 128 threads (3989 x 11472 bf16, top 2: 34 us, with 256 threads 50; 4096 x 1000 25
+    // and 44; 2048 x 32768 36 and 40), unless the rows are long (2048 x 131072 fp32 170 and 163) or
+    // too few to fill the SMs (700 x 50000 fp32 32 and 26).  64 threads were slower throughout.
+    const bool half = c == 1 && T >= 7 * int64_t(sms) && V * (dt == H32_IN_BF16 ? 2 : 4) <= 256 * 1024;
     const LogprobArgs a{logits, V, ldl, targets, n, top, logprob, entropy, top_logprob, top_id};
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(T * c));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(half ? 128 : 256);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -530,7 +538,9 @@ extern "C" h32_status h32_token_logprobs(const void *logits, h32_in_dtype dt, in
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = dt == H32_IN_BF16 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<true>, a)
-                                            : cudaLaunchKernelEx(&cfg, logprobs_kernel<false>, a);
+    const auto kernel = dt == H32_IN_BF16 ? half ? logprobs_kernel<true, 128> : logprobs_kernel<true, 256>
+                        : half            ? logprobs_kernel<false, 128>
+                                          : logprobs_kernel<false, 256>;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     return launch_status(e != cudaSuccess ? e : cudaGetLastError());
 }

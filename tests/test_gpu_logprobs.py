@@ -98,9 +98,8 @@ def test_random_rows(h32, T, V, n, top, bf16):
     _compare(h32, l, t, targets, top)
 
 
-@pytest.mark.parametrize("bf16", [False, True])
-@pytest.mark.parametrize("V", [40, 3001, 70001])
-def test_rows_that_are_masked_or_not_finite(h32, V, bf16):
+def _odd_rows(V, bf16):
+    """16 rows, masked, tied or not finite: values and device tensor."""
     low = float(np.float32(-3.3895314e38))   # bf16's lowest number
     l, _ = _logits(16, V, V, bf16)
     r = np.random.default_rng(0)
@@ -129,9 +128,30 @@ def test_rows_that_are_masked_or_not_finite(h32, V, bf16):
     if bf16:
         bits = wl.f32_to_bf16_bits(l)
         t, l = torch_bf16(bits), oracle.bf16_to_f32(bits)
+    return l, t
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("V", [40, 3001, 70001])
+def test_rows_that_are_masked_or_not_finite(h32, V, bf16):
+    l, t = _odd_rows(V, bf16)
     targets = np.stack([np.full(16, 0), np.full(16, V - 1), np.full(16, 11), np.full(16, 3)], 1).astype(np.int32)
     for top in (1, 5, 32):
         _compare(h32, l, t, targets, top)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("V,top", [(40, 32), (1999, 3), (3001, 20), (12270, 32)])
+def test_many_rows(h32, V, top, bf16):
+    """More rows than run at once: each still gets its own results, whatever the rows around it."""
+    odd, todd = _odd_rows(V, bf16)
+    l, t = _logits(1101, V, V, bf16)
+    at = np.random.default_rng(V).permutation(1101)[:32]
+    for i in range(2):
+        l[at[16 * i:16 * i + 16]] = odd
+        t[torch_of(at[16 * i:16 * i + 16].copy())] = todd
+    targets = np.random.default_rng(2).integers(-1, V + 1, (1101, 2)).astype(np.int32)
+    _compare(h32, l, t, targets, top)
 
 
 @pytest.mark.parametrize("V", [2000, 50000])
