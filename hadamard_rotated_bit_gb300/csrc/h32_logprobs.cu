@@ -515,11 +515,17 @@ extern "C" h32_status h32_token_logprobs(const void *logits, h32_in_dtype dt, in
         return H32_ERR_ALIGNMENT;
     int sms = 0;
     H32_TRY(check_device(&sms));
-    // CTAs of a row: as many as leave each at least one whole step, while the grid
-    // stays within one wave of 4 CTAs an SM
+    // CTAs of a row.  With few rows up to 8, as long as each has a step and they are no more than
+    // 1.6 an SM, or 2 with at least 16 steps each: beyond, the steps behind the pass and the cluster's
+    // meeting cost more than the shorter pass gives (131072 bf16: 76 rows 10.0 us by twos, 15.7
+    // by eights; 150 rows 11.2 by one, 17.0 by fours, but fp32 15.8 by twos and 20.8 by one).  Long
+    // rows that come to nearly four CTAs an SM by twos are the exception (300 rows 21.6 and 28.0 us).
     const int64_t steps = V / (256 * kVecs * (dt == H32_IN_BF16 ? 8 : 4));
     int c = 1;
-    while (c < kMaxCluster && 2 * c <= steps && T * 2 * c <= 4 * int64_t(sms)) c *= 2;
+    while (c < kMaxCluster && 2 * c <= steps &&
+           (T * 2 * c * 5 <= 8 * int64_t(sms) || (T * 2 * c <= 2 * int64_t(sms) && steps >= 32 * c)))
+        c *= 2;
+    if (c == 1 && steps >= 16 && T * 4 > 7 * int64_t(sms) && T <= 2 * int64_t(sms)) c = 2;
     // Many rows: what follows the pass is steps that wait for one another, so more rows at once
     // in CTAs of 128 threads (3989 x 11472 bf16, top 2: 34 us, with 256 threads 50; 4096 x 1000 25
     // and 44; 2048 x 32768 36 and 40), unless the rows are long (2048 x 131072 fp32 170 and 163) or
