@@ -7,7 +7,7 @@
 // tile in TMEM, the epilogue warps read it back and fold it into registers while the
 // tensor core does the next one.
 //
-// rows_kernel, for a few tokens: weight rows on the TMEM lanes, NC tokens as its columns.
+// rows_kernel, for a few tokens (or few tiles of a long K): weight rows on the TMEM lanes, NC tokens as its columns.
 //   A tile is 128 weight rows (one block of scales: d_w is uniform) x NC tokens; with few
 //   tiles a cluster of CTAs shares its K steps out and adds up through shared memory.
 //   warps 0..3  epilogue, a lane quarter each
@@ -25,11 +25,12 @@
 //   Bound: of the 406 ns of a pair's K step (256 x 256 x 128) the tensor core needs 270; the rest
 //   is the way from its last product to the epilogue and back, which two buffers of 256
 //   columns (all of TMEM) do not hide: without the loads of the sums and the folds a step
-//   took 445 ns when it took 610 with them.  4096 x 34816 x 5120: 555 us, 2630 TFLOP/s.  (Measured and left: four
-//   buffers of 128 columns, 913 us, as four dependent products of 128 columns take 350 clocks
-//   instead of 256; 16 epilogue warps, scales multiplied ahead of their step, scalar folds, and
-//   loads of sums two at a time, each 5 to 100% slower; arrivals across the pair with release, twice
-//   the time.)
+//   took 445 ns when it took 610 with them.  4096 x 34816 x 5120: 555 to 595 us (the clock depends on
+//   the power the codes draw), 2460 to 2630 TFLOP/s.  (Measured and left: four buffers of 128
+//   columns, 913 us, as four dependent products of 128 columns take 350 clocks instead of 256; 16
+//   epilogue warps, scales multiplied ahead of their step, scalar folds, and loads of sums two
+//   at a time, each 5 to 100% slower; arrivals across the pair with release, twice the time; the
+//   outputs' stores are 5% of it, the first weight scales of a tile under 1%.)
 // Every wait is bounded.
 #include "h32_f8.cuh"
 
@@ -188,7 +189,8 @@ __device__ __forceinline__ void store_lines(const F8Args &a, const uint8_t *buf,
                     *reinterpret_cast<const uint4 *>(buf + r * 128 + ((p ^ (r & 7)) << 4));
         }
     } else {
-        // rows that start anywhere: a value a lane, whole rows a store (N odd, or the last columns)
+        // rows that start anywhere (N odd), or the last columns: a value a lane, a row of 32 or
+        // 64 columns a store (330 x 36226 x 96 fp32: 26 us, row by row without unrolling 69)
         const int cols = min(bytes / es, a.N - n);
         const int at = lane * es, rest = at & 15;
 #pragma unroll 4
@@ -497,7 +499,7 @@ struct Lanes {
 
 // A pair's work, as (tile, K steps): whole tiles in turn, or (kSplit) an equal run of all tiles'
 // steps, last piece first.  A tile may be in several pairs' runs: the pair with its last steps
-// adds the others' partial sums to its own, all of pairs before it, in their order.  They come
+// adds the others' partial sums, all of pairs before it, to its own in those pairs' order.  They come
 // from those pairs' first pieces, and it needs them for its last one.
 template <bool kSplit, int kCtas>
 struct Walk {
