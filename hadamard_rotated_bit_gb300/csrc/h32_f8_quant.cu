@@ -5,9 +5,9 @@
 // d = amax|v| / 448, code = the e4m3 number nearest to v * fl(1/d), ties to even.
 // 448 is e4m3's largest number, so the largest value of a group gets it.
 //
-// Both keep a 32-block in each thread's registers (the layout of h32_quant.cu: the
-// butterfly's strides 1..16 need no exchange, 32 and 64 one shuffle each) and read
-// every value once.  Bound: HBM, 3 bytes a bf16 value, 5 an fp32 one (16384 x 5120 bf16 activations,
+// Both keep 32-blocks in each thread's registers, activations one (the layout of h32_quant.cu:
+// the butterfly's strides 1..16 need no exchange, 32 and 64 one shuffle each), weights two,
+// and read every value once.  Bound: HBM, 3 bytes a bf16 value, 5 an fp32 one (16384 x 5120 bf16 activations,
 // no rotation: 39 us, 95% of the measured copy rate; weights below); one token by its launch, 2.1 us.
 #include "h32_common.cuh"
 #include "h32_quant_block.cuh"
@@ -75,6 +75,35 @@ __device__ __forceinline__ void rotate(float (&v)[32], uint32_t pos) {
     }
 }
 
+// the same for two blocks in a thread, `upper` in a row's upper half: the stride 32 needs no exchange
+template <int kRot>
+__device__ __forceinline__ void rotate_pair(float (&v)[2][32], uint32_t upper) {
+    if constexpr (kRot <= 32) {
+        rotate_block<kRot>(v[0], 0, 0xFFFFFFFFu);
+        rotate_block<kRot>(v[1], 0, 0xFFFFFFFFu);
+    } else {
+        butterfly32(v[0]);
+        butterfly32(v[1]);
+        const float sign = upper ? -1.0f : 1.0f, sc = kRot == 64 ? 0.125f : kInvSqrt128;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float a = __fadd_rn(v[0][i], v[1][i]), b = __fsub_rn(v[0][i], v[1][i]);
+            v[0][i] = a;
+            v[1][i] = b;
+        }
+        if constexpr (kRot == 128) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[k][i] = __fmaf_rn(v[k][i], sign, __shfl_xor_sync(0xFFFFFFFFu, v[k][i], 1));
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[k][i] = __fmul_rn(v[k][i], sc);
+    }
+}
+
 template <bool kBf16>
 __device__ __forceinline__ void load_block(const void *x, int64_t at, float (&v)[32]) {
     if constexpr (kBf16) load_block_bf16(static_cast<const uint16_t *>(x) + at, v);
@@ -132,12 +161,13 @@ __global__ void __launch_bounds__(256) act_f8_kernel(const void *__restrict__ x,
     }
 }
 
-// One 128 x 128 block after another: four lanes hold a row's 128 values, 512 threads the
-// block, and the next one is copied while this one is rotated and rounded.  It
-// comes through shared memory (16-byte copies of whole lines: a thread reading its own 128
-// bytes directly took 264 us for 34816 x 5120 fp32 and 128 points, staged ones 190, copied ahead 174;
-// without a rotation 135, 98% of the measured copy rate), swizzled so that the
-// eight lanes of a quarter warp, two rows of four blocks, read eight different bank groups.
+// One 128 x 128 block after another: two lanes hold a row's 128 values, 256 threads the block, and
+// the next one is copied while this one is rotated and rounded.  It comes through shared memory
+// (16-byte copies of whole lines: a thread reading its own 128 bytes directly took 264 us for 34816
+// x 5120 fp32 and 128 points, staged ones 190, copied ahead 172, all with four lanes a row; two
+// lanes, with half the exchange, 159; a lane 162; without a rotation 133, the measured copy rate),
+// swizzled so that the eight lanes of a quarter warp, four rows of two halves, read eight different
+// bank groups.
 __device__ __forceinline__ void copy16(void *smem_dst, const void *src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(in ? 16 : 0)
                  : "memory");
@@ -147,22 +177,21 @@ template <bool kBf16>
 struct WeightTile {
     static constexpr int kPieces = kBf16 ? 16 : 32;   // 16-byte pieces of a row's 128 values
     static constexpr int kBytes = 128 * kPieces * 16;
-    // where piece p of row r stands: its block's (p / (kPieces / 4)) and the row's low bits
-    // move it within the line
+    // where piece p of row r stands: its half of the row and the row's low bits move it within
+    // the line
     static __device__ __forceinline__ int at(int r, int p) {
-        const int turn = kBf16 ? ((p >> 3) + 2 * (r & 1)) & 3 : ((p >> 3) + 4 * (r & 1)) & 7;
-        return (r * kPieces + (p ^ turn)) * 16;
+        return (r * kPieces + (p ^ (p / (kPieces / 2) + 2 * (r & 3)))) * 16;
     }
 };
 
 template <bool kBf16, int kRot>
-__global__ void __launch_bounds__(512, 2) weights_f8_kernel(const void *__restrict__ w, uint32_t N, uint32_t nb,
+__global__ void __launch_bounds__(256, 2) weights_f8_kernel(const void *__restrict__ w, uint32_t N, uint32_t nb,
                                                             uint32_t groups, int64_t ldw,
                                                             uint8_t *__restrict__ wq, float *__restrict__ wd) {
     using T = WeightTile<kBf16>;
     extern __shared__ __align__(128) uint8_t s_tile[];
-    __shared__ float s_amax[16];
-    constexpr int kSize = kBf16 ? 2 : 4, kRows = 512 / T::kPieces;   // rows a round of copies covers
+    __shared__ float s_amax[8];
+    constexpr int kSize = kBf16 ? 2 : 4, kRows = 256 / T::kPieces;   // rows a round of copies covers
     const int p = threadIdx.x % T::kPieces, r0 = threadIdx.x / T::kPieces;
     const auto copy = [&](uint32_t t) {
         const uint32_t tile_n = t / groups, g = t - tile_n * groups;
@@ -176,41 +205,47 @@ __global__ void __launch_bounds__(512, 2) weights_f8_kernel(const void *__restri
         }
     };
     const uint32_t tiles = (N + 127) / 128 * groups;
-    const uint32_t r = threadIdx.x >> 2, j = threadIdx.x & 3;
+    const uint32_t r = threadIdx.x >> 1, j = threadIdx.x & 1;
     copy(blockIdx.x);
     for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const uint32_t tile_n = t / groups, g = t - tile_n * groups, row = tile_n * 128 + r, b = g * 4 + j;
+        const uint32_t tile_n = t / groups, g = t - tile_n * groups, row = tile_n * 128 + r, b = g * 4 + 2 * j;
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
-        float v[32];
+        float v[2][32];
 #pragma unroll
-        for (int i = 0; i < T::kPieces / 4; ++i) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(s_tile + T::at(r, j * (T::kPieces / 4) + i));
+        for (int i = 0; i < T::kPieces / 2; ++i) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(s_tile + T::at(r, j * (T::kPieces / 2) + i));
             const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+            constexpr int kIn = kBf16 ? 8 : 4;   // values of a piece
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
+                float *dst = v[i / (T::kPieces / 4)] + i % (T::kPieces / 4) * kIn + kIn / 4 * q;
                 if constexpr (kBf16) {
-                    v[8 * i + 2 * q] = __uint_as_float(x[q] << 16);
-                    v[8 * i + 2 * q + 1] = __uint_as_float(x[q] & 0xFFFF0000u);
+                    dst[0] = __uint_as_float(x[q] << 16);
+                    dst[1] = __uint_as_float(x[q] & 0xFFFF0000u);
                 } else {
-                    v[4 * i + q] = __uint_as_float(x[q]);
+                    dst[0] = __uint_as_float(x[q]);
                 }
             }
         }
         __syncthreads();
         if (t + gridDim.x < tiles) copy(t + gridDim.x);   // (under this block's arithmetic)
-        rotate<kRot>(v, b);
-        float amax = block_amax(v);
+        rotate_pair<kRot>(v, j);
+        float amax = fmaxf(block_amax(v[0]), block_amax(v[1]));
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
         if ((threadIdx.x & 31) == 0) s_amax[threadIdx.x >> 5] = amax;
         __syncthreads();   // (its next write is two barriers on)
         amax = s_amax[0];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) amax = fmaxf(amax, s_amax[i]);
-        uint32_t c[8];
-        const float d = f8_codes(v, amax, c);
-        if (row < N && b < nb) store_codes(wq + (int64_t(row) * nb + b) * 32, c);
+        for (int i = 1; i < 8; ++i) amax = fmaxf(amax, s_amax[i]);
+        float d = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t c[8];
+            d = f8_codes(v[i], amax, c);
+            if (row < N && b + i < nb) store_codes(wq + (int64_t(row) * nb + b + i) * 32, c);
+        }
         if (threadIdx.x == 0) wd[t] = d;
     }
 }
@@ -298,7 +333,7 @@ extern "C" h32_status h32_quantize_weights_f8(const void *w, h32_in_dtype dt, in
     const int smem = dt == H32_IN_BF16 ? WeightTile<true>::kBytes : WeightTile<false>::kBytes;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return launch_status(e);
-    kernel<<<static_cast<int>(tiles < 2 * sms ? tiles : 2 * sms), 512, smem, reinterpret_cast<cudaStream_t>(stream)>>>(
+    kernel<<<static_cast<int>(tiles < 2 * sms ? tiles : 2 * sms), 256, smem, reinterpret_cast<cudaStream_t>(stream)>>>(
         w, static_cast<uint32_t>(N), static_cast<uint32_t>(K / 32), static_cast<uint32_t>(groups), ldw, wq, wd);
     return launch_status(cudaGetLastError());
 }
