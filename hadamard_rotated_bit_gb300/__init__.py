@@ -1332,8 +1332,8 @@ def h32_f8_gemm_experts(wq, wd, xq, xd, expert_off, N, R=None, y=None, y_dtype=N
 def _f8_gemm(fn, wq, wd, xq, xd, off, N, M, y, y_dtype, stream):
     kind, empty, bf16, f32, i32, u8 = _usual_torch()[:6]
     plain = False
-    if M is None and y is None and (y_dtype is None or y_dtype is bf16 or y_dtype is f32) and (off is None or type(N) is int and N > 0) and \
-            isinstance(wq, kind) and wq.is_cuda and wq.dim() == 2:
+    if M is None and y is None and (y_dtype is None or y_dtype is bf16 or y_dtype is f32) and \
+            (off is None or type(N) is int and N > 0) and isinstance(wq, kind) and wq.is_cuda and wq.dim() == 2:
         # the usual call, all sizes as the operands give them
         (rows, K), dev = wq.shape, wq.get_device()
         e, n = (1, rows) if off is None else (rows // N, N)

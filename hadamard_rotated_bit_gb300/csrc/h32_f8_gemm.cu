@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                     if (leader) {
                         // (columns behind K are zeros in both operands)
                         const uint64_t da = da0 + st.i * (C::kA >> 4), db = db0 + st.i * (b_bytes >> 4);
-    #pragma unroll
+#pragma unroll
                         for (int j = 0; j < 4; ++j)
                             mma<kCtas>(tmem + bf.i * 256, da + 2 * j, db + 2 * j, idesc, j > 0);
                         commit<kCtas>(&s_empty[st.i]);
