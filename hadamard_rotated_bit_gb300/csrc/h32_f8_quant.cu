@@ -250,9 +250,11 @@ __global__ void __launch_bounds__(256, 2) weights_f8_kernel(const void *__restri
     }
 }
 
-// what both quantizers ask of their sizes, types and rotation
+// what both quantizers ask of their sizes, types and rotation: rows and K below 2^31, as the
+// products (the kernels number rows, blocks and a row's values in 32 bits)
 h32_status quant_args(h32_in_dtype dt, int64_t rows, int64_t K, int64_t ld, int rotate) {
-    if (rows < 0 || K <= 0 || K % 32 != 0 || ld < K) return H32_ERR_INVALID_ARG;
+    constexpr int64_t kMost = 0x7FFFFFFFll - 256;
+    if (rows < 0 || rows > kMost || K <= 0 || K > kMost || K % 32 != 0 || ld < K) return H32_ERR_INVALID_ARG;
     const int rot = rot_points(rotate);
     if (rot < 0 || (rot > 0 && K % rot != 0)) return H32_ERR_INVALID_ARG;
     if (dt != H32_IN_F32 && dt != H32_IN_BF16) return H32_ERR_INVALID_ARG;
@@ -297,14 +299,14 @@ extern "C" h32_status h32_quantize_act_f8(const void *x, h32_in_dtype dt, int64_
                                           int64_t ldxd, int rotate, void *stream) {
     using namespace h32;
     H32_TRY(quant_args(dt, T, K, ldx, rotate));
-    if (R < 0 || ldxd < R || ldxd % 4 != 0 || (!row_idx && R != T)) return H32_ERR_INVALID_ARG;
+    if (R < 0 || R > 0x7FFFFFFFll || ldxd < R || ldxd % 4 != 0 || (!row_idx && R != T)) return H32_ERR_INVALID_ARG;
     if (R == 0) return H32_OK;
     if (!x || !xq || !xd || T == 0) return H32_ERR_INVALID_ARG;
     const int64_t esize = dt == H32_IN_BF16 ? 2 : 4;
     if (!aligned16(x) || !aligned16(xq) || !aligned16(xd) || (ldx * esize) % 16 != 0 ||
         (row_idx && reinterpret_cast<uintptr_t>(row_idx) % 4 != 0))
         return H32_ERR_ALIGNMENT;
-    if (R * (K / 32) > 0x7FFFFFFFll || T > 0x7FFFFFFFll) return H32_ERR_INVALID_ARG;
+    if (R * (K / 32) > 0x7FFFFFFFll) return H32_ERR_INVALID_ARG;
     int sms = 0;
     H32_TRY(check_device(&sms));
     const uint32_t nb = static_cast<uint32_t>(K / 32);
@@ -326,7 +328,7 @@ extern "C" h32_status h32_quantize_weights_f8(const void *w, h32_in_dtype dt, in
     const int64_t esize = dt == H32_IN_BF16 ? 2 : 4;
     if (!aligned16(w) || !aligned16(wq) || !aligned16(wd) || (ldw * esize) % 16 != 0) return H32_ERR_ALIGNMENT;
     const int64_t groups = (K + 127) / 128, tiles = (N + 127) / 128 * groups;
-    if (tiles > 0x7FFFFFFFll || N > 0x7FFFFFFFll - 128) return H32_ERR_INVALID_ARG;
+    if (tiles > 0x7FFFFFFFll) return H32_ERR_INVALID_ARG;
     int sms = 0;
     H32_TRY(check_device(&sms));
     const auto kernel = dt == H32_IN_BF16 ? weights_kernel<true>(rotate) : weights_kernel<false>(rotate);

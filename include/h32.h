@@ -676,6 +676,7 @@ h32_status h32_add_rms_norm_quantize(const void *x, h32_in_dtype x_dt, int64_t l
  *            of 4; entries r >= R are left untouched
  * Weights: a block is 128 rows x 128 values (at the edges what is left).
  *   w        [N][ldw] of type dt;  wq [N][K] out;  wd [ceil(N/128)][ceil(K/128)] out
+ * K a multiple of 32; rows and K at most 2^31 - 257, and R (K / 32) below 2^31.
  */
 h32_status h32_quantize_act_f8(const void *x, h32_in_dtype dt, int64_t T, int64_t K, int64_t ldx,
                                const int32_t *row_idx, int64_t R, uint8_t *xq, float *xd,

@@ -123,6 +123,24 @@ def test_library_refusals_quantizers(lib):
     _end(weights, rot=1)
 
 
+def test_library_refusals_long_rows(lib):
+    """Rows of 2^31 values or more, which no product takes and whose places are numbered in 32
+    bits, and row counts whose product with the blocks of a row wraps around 64 bits."""
+    P = 4096
+    for K in (1 << 31, 1 << 32, (1 << 32) + 32, (1 << 33) + 128, 1 << 40):
+        for dt in (0, 1):
+            assert lib.h32_quantize_act_f8(_p(P), dt, 1, K, K, _p(None), 1, _p(2 * P), _p(3 * P), 4, 0, _p(0)) == BAD
+            assert lib.h32_quantize_weights_f8(_p(P), dt, 1, K, K, 0, _p(2 * P), _p(3 * P), _p(0)) == BAD
+    for R, K in ((1 << 38, 1 << 31), (1 << 40, 1 << 29), (1 << 60, 512), (1 << 32, 32)):
+        assert lib.h32_quantize_act_f8(_p(P), 0, 4, K, K, _p(5 * P), R, _p(2 * P), _p(3 * P), R, 0, _p(0)) == BAD
+    for N in ((1 << 31) - 128, 1 << 31, (1 << 63) - 1):
+        assert lib.h32_quantize_weights_f8(_p(P), 0, N, 256, 256, 0, _p(2 * P), _p(3 * P), _p(0)) == BAD
+    # the longest rows allowed get as far as the device (a call without a GPU)
+    if not torch.cuda.is_available():
+        K = (1 << 31) - 288
+        assert lib.h32_quantize_weights_f8(_p(P), 1, 1, K, K, 0, _p(2 * P), _p(3 * P), _p(0)) == h32.H32_ERR_UNSUPPORTED
+
+
 def test_library_refusals_products(lib):
     P = 4096
 
