@@ -724,8 +724,10 @@ h32_status h32_f8_gemm_experts(const uint8_t *wq, const float *wd, int32_t E, co
  *   entropy[t]        = -sum p log p
  *   top_id, top_logprob [t][j] = the `top` most probable tokens, by decreasing logit,
  *                       ties to the lower id, and their log p
- * Statistics are held in fp32; a log p is off by at most a few 2^-24 of |l - max l| +
- * log(sum), plus the rounding of the sum.  The ids are exact.
+ * Statistics are held in fp32; a log p is off by a few 2^-24 of |l - max l| + log(sum), plus
+ * the rounding of the sum: less than 64 2^-24 of it for its additions, whatever V, and at
+ * most 2^-22 more for each step of 16 (fp32) or 32 values at which the running maximum rises.
+ * So next to a certain token it is good to some 2^-24, not relative to itself.  The ids are exact.
  * Masked tokens (-inf) have log p = -inf and count for nothing; a row whose every logit is
  * -inf has log p = -inf throughout and entropy 0; +inf logits share the probability
  * equally; a NaN makes the row's log p (of given tokens and alternatives) and entropy NaN.

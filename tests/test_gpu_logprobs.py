@@ -185,6 +185,39 @@ def test_certain_tokens(h32):
     assert bool((lp <= 0).all())
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T", [1, 200])
+def test_a_certain_token_over_a_wide_floor(h32, T, bf16):
+    """One likely token and 131071 others whose e^(l - max) = 4.1e-8 is below half a step of the
+    sum next to 1: together they are 5.4e-3, however many of them one thread adds up (a CTA or
+    more to a row).  The sum's roundings, of about 1 + 5.4e-3 each, do not grow with the row:
+    within a step at most 4 of a vector's and 2 of the vectors' sums, 16 of a run's steps, 2 of
+    the compensated sum of the runs, 2 of the two halves, then 5 joins of lanes, 7 of warps, 7 of
+    CTAs and 1 of the values beside the vectors, one each as the part that is not scaled is the
+    large one: 46.  An exponential's own error is 3 |d| + 4 = 55 U of 5.4e-3.
+    W = 17 * 5.4e-3 comes of as many joins and, in a run, of at most 256 additions to partial
+    sums that are half of the run's on average: 128 U more."""
+    V, big, d = 131072, 12.0, 17.0
+    l = np.full((T, V), big - d, np.float32)
+    at = np.random.default_rng(T).integers(0, V, T)
+    at[0] = 0
+    l[np.arange(T), at] = big
+    bits = wl.f32_to_bf16_bits(l)
+    t = torch_bf16(bits) if bf16 else torch_of(l)
+    other = (at + 1) % V
+    lp, ent, ids, tlp = h32.h32_token_logprobs(t, torch_of(np.stack([at, other], 1).astype(np.int32)), top=2)
+    rest = (V - 1) * np.exp(-d)
+    log_s = np.log1p(rest)
+    assert np.array_equal(np_of(ids), np.stack([at, np.where(at == 0, 1, 0)], 1))
+    for got in (np_of(lp), np_of(tlp)):
+        err = np.abs(got.astype(np.float64) - [-log_s, -d - log_s])
+        print("log p off by, in U:", err.max(0) / U)
+        assert (err <= [52 * U, (52 + 2 * d) * U]).all()
+    err = np.abs(np_of(ent).astype(np.float64) - (log_s + d * rest / (1 + rest)))
+    print("entropy off by, in U:", err.max() / U)
+    assert (err <= 52 * (1 + 2 * d * rest) * U + (3 * d + 4 + 128) * d * rest * U).all()
+
+
 def test_given_outputs_streams_and_graphs(h32):
     import torch
     l, t = _logits(6, 30011, 5)
