@@ -35,6 +35,7 @@
 #include "h32_f8.cuh"
 
 #include "h32_epilogue.cuh"
+#include "h32_f8_plan.h"
 
 namespace h32 {
 namespace {
@@ -42,7 +43,6 @@ namespace {
 __device__ uint32_t g_f8_status;   // kStatusTimeout, kStatusGuard
 
 constexpr int kMaxStages = 12;
-constexpr int64_t kRowsTokens = 32;   // dense: up to here rows_kernel
 constexpr int kRowsWarps = 6;
 // lanes_kernel: two epilogue warps for each quarter of the lanes, and a warpgroup of the roles
 // that issue.  Of 12 warps with 168 registers at launch the epilogue's two warpgroups take over
@@ -238,13 +238,12 @@ struct Rows {
     static constexpr uint32_t kA = 128 * 128, kB = NC * 128;  // bytes of a stage's parts
     static constexpr uint32_t kS = NC * 4 < 128 ? 128 : NC * 4;
     static constexpr uint32_t kStage = kA + kB + kS;
-    static constexpr int kPerSm = 2;                          // CTAs of an SM
     // the partial sums that a CTA gets: [share][column][row]
     static __host__ __device__ uint32_t parts(int cluster) { return (cluster - 1) * (NC / cluster) * 512; }
 };
 
 template <int NC>
-__global__ void __launch_bounds__(kRowsWarps * 32, Rows<NC>::kPerSm)
+__global__ void __launch_bounds__(kRowsWarps * 32, kRowsPerSm)
     rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                 const __grid_constant__ CUtensorMap map_s, const F8Args a) {
     using C = Rows<NC>;
@@ -931,21 +930,12 @@ h32_status launch_clusters(int grid, int threads, size_t smem, int cluster, cuda
     return launch_status(e != cudaSuccess ? e : cudaGetLastError());
 }
 
-// CTAs that rows_kernel deals a tile's K steps to.  With few tiles a share of at least 4 steps
-// each, as long as all of them run at once.  (5120 x 5120 and 7 tokens: one CTA a tile 13.9 us, 4
-// 9.4.)
-int rows_cluster(int64_t tiles, int64_t nb, int sms) {
-    int c = 1;
-    while (2 * c <= 8 && tiles * 2 * c <= Rows<16>::kPerSm * int64_t(sms) && nb >= 8 * c) c *= 2;
-    return c;
-}
-
 template <int NC>
 h32_status launch_rows(const uint8_t *wq, const uint8_t *xq, const float *xd, int64_t ldxd, F8Args a, int64_t tiles,
-                       int sms, cudaStream_t s) {
+                       int cluster, int sms, cudaStream_t s) {
     using C = Rows<NC>;
     const int nb = (a.K + 127) / 128;
-    a.cluster = a.off ? 1 : rows_cluster(tiles, nb, sms);
+    a.cluster = cluster;
     const bool two = tiles * a.cluster > sms && a.cluster > 1;
     const size_t rest = Groups::bytes(a.E) + 1024 + C::parts(a.cluster);
     const int fit = static_cast<int>(((two ? kMaxSmem / 2 : kMaxSmem) - rest) / C::kStage);
@@ -984,61 +974,10 @@ h32_status launch_lanes(const uint8_t *wq, const uint8_t *xq, const float *xd, i
     return launch_clusters<lanes_kernel<kChunks, kSplit, kCtas>>(kCtas * units, kPairWarps * 32, C::kSmem, kCtas, s, maps, a);
 }
 
-// How lanes_kernel takes `chunks` chunks of tokens (as the host knows them) with so many units
-// (CTAs or pairs).  A K step of 64, 128 and 256 weight rows takes a pair 332, 355 and 406 ns (256
-// tokens x 5120 x 8192 and 16384; 192 rows 444, so never), a tile's end about 3 us for 256
-// rows.  The narrow ones pay where they fill units that were idle (256 tokens x 8192 x 5120: 128
-// rows 29.5 us, 256 rows 33.6), and equal runs of K steps where the last wave of whole tiles is
-// long (333 x 5120 x 17408: 40 tiles on 76 pairs, 64 and 47 us; 1000 tokens 76); they cost about
-// 14 us (clearing the flags, two ends of tiles in turn) and 3.2 for each partial
-// sum of a tile.
-struct Plan {
-    int bn;         // weight rows of a tile; 0: rows_kernel
-    int runs;       // > 0: runs of K steps for so many pairs, 12 steps at least
-    int64_t cost;   // ns, without the launch
-};
-Plan plan_tiles(int64_t chunks, int64_t N, int64_t K, int units, bool may_run) {
-    const int64_t nb = (K + 127) / 128;
-    const auto cost = [&](int64_t bn, int64_t step) {
-        const int64_t tiles = (N + bn - 1) / bn * chunks;
-        return (tiles + units - 1) / units * (nb * step + 12 * bn);
-    };
-    const int64_t c64 = cost(64, 332), c128 = cost(128, 355), c256 = cost(256, 406);
-    const int64_t best = c256 <= c128 && c256 <= c64 ? c256 : c128 <= c64 ? c128 : c64;
-    const int64_t tiles = (N + 255) / 256 * chunks, steps = tiles * nb;
-    Plan p{best == c256 ? 256 : best == c128 ? 128 : 64, 0, best};
-    // (not where every pair has many tiles: the runs then walk all weights at once, which no
-    // longer fit the L2; 2048 x 34816 x 5120 read them seven times)
-    if (!may_run || steps >= 0x7FFFFFFFll || tiles > 4 * int64_t(units)) return p;
-    for (int64_t n = steps / 12 < units ? steps / 12 : units; n >= 2; n = n * 3 / 4) {
-        const int64_t run = (steps + n - 1) / n;
-        const int64_t c = run * 406 + (tiles / n + 1) * (12 * 256) + 14000 + 3200 * ((nb + run - 1) / run);
-        if (c < p.cost) {
-            p.cost = c;
-            p.runs = static_cast<int>(n);
-        }
-    }
-    return p;
-}
-
-// Dense products of more tokens than rows_kernel has columns.  One CTA a tile up to 128 tokens, a
-// pair beyond.  Where the tiles are few and K is long, rows_kernel is faster with a tile for
-// each 32 tokens, as its clusters share K out: its steps take 430 ns of a CTA and its start 5 us
-// more than the other kernel's (128 x 783 x 8896 12.0 us, on the lanes 26.1; 64 x 5120 x 17408 36
-// and 47; 512 x 512 x 4096 12.5 and 15.3; but 723 x 418 x 1568 12.4 and 9.2).
-Plan plan_dense(int64_t M, int64_t N, int64_t K, int sms) {
-    const bool one = M <= 128;
-    Plan p = plan_tiles(one ? 1 : (M + 255) / 256, N, K, one ? sms : sms / 2, !one);
-    const int64_t nb = (K + 127) / 128;
-    const int c = rows_cluster((N + 127) / 128 * ((M + 31) / 32), nb, sms);
-    const int64_t rows = 5000 + 430 * ((nb + c - 1) / c);
-    return c > 1 && rows < p.cost ? Plan{0, 0, rows} : p;
-}
-
 h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint8_t *xq, const float *xd,
                        int64_t ldxd, const int32_t *off, int64_t M, int64_t N, int64_t K, void *y,
                        h32_in_dtype y_dt, int64_t ldy, void *ws, size_t ws_bytes, void *stream) {
-    if (M < 0 || N <= 0 || K <= 0 || K % 32 != 0 || E < 1 || E > kMaxExperts || ldxd < M || ldxd % 4 != 0 ||
+    if (E < 1 || E > kMaxExperts || !f8_sizes_fit(M, N, K, E) || ldxd < M || ldxd % 4 != 0 || ldxd > 0xFFFFFFFFll ||
         ldy < N || (y_dt != H32_IN_F32 && y_dt != H32_IN_BF16))
         return H32_ERR_INVALID_ARG;
     if (M == 0) return H32_OK;
@@ -1046,12 +985,6 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
     if (!aligned16(wq) || !aligned16(wd) || !aligned16(xq) || !aligned16(xd) || !aligned16(y) || !aligned16(ws) ||
         (off && reinterpret_cast<uintptr_t>(off) % 4 != 0))
         return H32_ERR_ALIGNMENT;
-    // the kernels number rows and tiles in int (a group starts up to 3 rows early: at most
-    // two chunks more than its rows fill)
-    const int64_t nt = (N + 127) / 128, most_tiles = nt * (M / 16 + 2 * int64_t(E));
-    if (M > 0x7FFFFFFFll - 256 || K > 0x7FFFFFFFll - 256 || int64_t(E) * N > 0x7FFFFFFFll - 256 ||
-        ldxd > 0xFFFFFFFFll || most_tiles > 0x7FFFFFFFll)
-        return H32_ERR_INVALID_ARG;
     int sms = 0;
     H32_TRY(check_device(&sms));
     if (!encoder()) {
@@ -1071,21 +1004,9 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
     a.y_vec = ldy * (a.y_bf16 ? 2 : 4) % 16 == 0;
     a.wait_limit = wait_limit();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // Tokens of a group, as far as the host knows them, decide the kernel.  Dense, 34816 x
-    // 5120: 16 tokens as columns 34 us, on the lanes 41; 32 tokens 39 and 35, but 5120 x 17408 25
-    // and 47 (K shared out over a cluster).  Experts (128 of 1536 x 2048) with 4, 16 and 32
-    // tokens on average: 16 columns 67, 101 and 151 us, lanes 74, 76 and 77 (groups differ, and a
-    // second chunk of columns reads the weights again).
-    const int64_t per = (M + E - 1) / E;
-    if (per <= (off ? 8 : 16)) return launch_rows<16>(wq, xq, xd, ldxd, a, nt * E, sms, s);
-    // Experts: up to 96 tokens on average one CTA a tile, two beyond, as of 256 rows of a pair the
-    // half without tokens would idle (64 tokens an expert: 80 and 104 us); dense, 100 x 34816 x 5120:
-    // 36 and 45, but 4096 x 34816 x 5120 the other way, as a pair reads its weights once.
-    const bool one = per <= (off ? 96 : 128);
-    const int64_t rows = one ? 128 : 256, chunks = off ? E + M / rows : (M + rows - 1) / rows;
-    const Plan plan = off ? plan_tiles(chunks, N, K, one ? sms : sms / 2, false) : plan_dense(M, N, K, sms);
-    if (!off && (per <= kRowsTokens || plan.bn == 0))
-        return launch_rows<32>(wq, xq, xd, ldxd, a, nt * ((M + 31) / 32), sms, s);
+    const F8Plan plan = plan_f8(M, N, K, E, off != nullptr, sms);
+    if (plan.columns == 16) return launch_rows<16>(wq, xq, xd, ldxd, a, plan.tiles, plan.cluster, sms, s);
+    if (plan.columns == 32) return launch_rows<32>(wq, xq, xd, ldxd, a, plan.tiles, plan.cluster, sms, s);
     if (plan.runs > 0 && ws) {
         if (ws_bytes < Partials::bytes(plan.runs)) return H32_ERR_INVALID_ARG;
         a.ws = static_cast<uint8_t *>(ws);
@@ -1096,15 +1017,14 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
         if (e != cudaSuccess) return launch_status(e);
         return launch_lanes<4, 2, true>(wq, xq, xd, ldxd, a, plan.runs, sms, s);
     }
-    const int64_t tiles = (N + plan.bn - 1) / plan.bn * chunks;
-    if (one) {
-        if (plan.bn == 256) return launch_lanes<4, 1>(wq, xq, xd, ldxd, a, tiles, sms, s);
-        if (plan.bn == 128) return launch_lanes<2, 1>(wq, xq, xd, ldxd, a, tiles, sms, s);
-        return launch_lanes<1, 1>(wq, xq, xd, ldxd, a, tiles, sms, s);
+    if (plan.ctas == 1) {
+        if (plan.bn == 256) return launch_lanes<4, 1>(wq, xq, xd, ldxd, a, plan.tiles, sms, s);
+        if (plan.bn == 128) return launch_lanes<2, 1>(wq, xq, xd, ldxd, a, plan.tiles, sms, s);
+        return launch_lanes<1, 1>(wq, xq, xd, ldxd, a, plan.tiles, sms, s);
     }
-    if (plan.bn == 256) return launch_lanes<4, 2>(wq, xq, xd, ldxd, a, tiles, sms, s);
-    if (plan.bn == 128) return launch_lanes<2, 2>(wq, xq, xd, ldxd, a, tiles, sms, s);
-    return launch_lanes<1, 2>(wq, xq, xd, ldxd, a, tiles, sms, s);
+    if (plan.bn == 256) return launch_lanes<4, 2>(wq, xq, xd, ldxd, a, plan.tiles, sms, s);
+    if (plan.bn == 128) return launch_lanes<2, 2>(wq, xq, xd, ldxd, a, plan.tiles, sms, s);
+    return launch_lanes<1, 2>(wq, xq, xd, ldxd, a, plan.tiles, sms, s);
 }
 
 }  // namespace
@@ -1124,10 +1044,10 @@ h32_status f8_read_and_clear_status(cudaStream_t s) {
 
 extern "C" h32_status h32_f8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes) {
     using namespace h32;
-    if (M < 0 || N <= 0 || K <= 0 || K % 32 != 0 || !bytes) return H32_ERR_INVALID_ARG;
+    if (!bytes || !f8_sizes_fit(M, N, K, 1)) return H32_ERR_INVALID_ARG;
     int sms = 0;
     H32_TRY(check_device(&sms));
-    const int runs = M > kRowsTokens ? plan_dense(M, N, K, sms).runs : 0;
+    const int runs = M > 0 ? plan_f8(M, N, K, 1, false, sms).runs : 0;
     *bytes = runs > 0 ? Partials::bytes(runs) : 0;
     return H32_OK;
 }

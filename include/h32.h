@@ -700,7 +700,8 @@ h32_status h32_quantize_weights_f8(const void *w, h32_in_dtype dt, int64_t N, in
  *        call's work is done.  With it tiles that would leave much of the GPU idle are
  *        shared out along K, their partial sums added in a fixed order (without it the same
  *        sums, slower and in one order over all of K)
- * Any N >= 1; K a multiple of 32.
+ * Any N >= 1; K a multiple of 32; M, K and E N at most 2^31 - 257 (the workspace query refuses
+ * what the products refuse).
  * The expert form multiplies rows r in [expert_off[e], expert_off[e+1]) by expert e's
  * weights: wq [E][N][K], wd [E][ceil(N/128)][ceil(K/128)], expert_off [E+1] int32 device,
  * 4-byte aligned, 0 = off[0] <= ... <= off[E] = R (else H32_ERR_DEVICE_GUARD is recorded

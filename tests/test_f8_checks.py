@@ -166,6 +166,12 @@ def test_library_refusals_products(lib):
     for kw in ((-1, 4, 128), (1, 0, 128), (1, 4, 0), (1, 4, 100)):
         assert lib.h32_f8_gemm_workspace_bytes(*kw, ctypes.byref(n)) == BAD
     assert lib.h32_f8_gemm_workspace_bytes(1, 4, 128, None) == BAD
+    # sizes that the product refuses, some of which would wrap around 64 bits in its plan
+    for kw in ((1 << 31, 4, 128), (1, 1 << 31, 128), (1, 4, 1 << 31), (1 << 62, 1 << 40, 1 << 40),
+               ((1 << 63) - 1, 4, 128), (1, (1 << 63) - 1, 128), (1, 4, (1 << 63) - 32), (1 << 30, 1 << 30, 128)):
+        assert lib.h32_f8_gemm_workspace_bytes(*kw, ctypes.byref(n)) == BAD, kw
+        M, N, K = kw
+        assert dense(M=M, N=N, K=K, ldy=N, ldxd=(M + 3) // 4 * 4 if M < 1 << 62 else M // 4 * 4) == BAD, kw
     if not torch.cuda.is_available():
         assert lib.h32_f8_gemm_workspace_bytes(1, 4, 128, ctypes.byref(n)) == h32.H32_ERR_UNSUPPORTED
     assert experts(E=0) == BAD and experts(E=1025) == BAD and experts(off=None) == BAD
