@@ -121,6 +121,20 @@ def test_quantize_weights(h32, N, K, rotate, bf16):
     assert np.array_equal(np_of(wq), q) and np.array_equal(np_of(wd), d)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("rotate,K", [(0, 416), (32, 416), (64, 448), (128, 384)])
+def test_quantize_weights_many_blocks(h32, K, rotate, bf16):
+    """More blocks of 128 x 128 than run at once: the next one is copied under this one."""
+    import torch
+    N = 20001
+    assert (N + 127) // 128 * ((K + 127) // 128) > 2 * 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    w = _rows(N, K, N + K, bf16, 0.02)
+    wq, wd = h32.h32_quantize_weights_f8(_dev(w), rotate=rotate)
+    _ok(h32)
+    q, d = oracle.quantize_weights_f8(w, rotate)
+    assert np.array_equal(np_of(wq), q) and np.array_equal(np_of(wd), d)
+
+
 # --------------------------------------------------------------------------
 # products
 # --------------------------------------------------------------------------
@@ -148,6 +162,18 @@ SHAPES = [(1, 1, 32), (1, 5120, 5120), (2, 129, 96), (7, 384, 4224), (15, 100, 1
           (31, 1000, 2048), (33, 77, 1056), (64, 640, 512), (65, 2000, 384), (128, 257, 1024), (129, 128, 4096),
           (200, 1537, 96), (255, 4096, 320), (256, 256, 256), (257, 700, 5120), (333, 5120, 1024), (511, 96, 736),
           (1030, 1300, 288), (2048, 8192, 128), (33, 831, 4032), (150, 783, 8896), (380, 269, 6464)]
+
+
+# more tiles than run at once, of several K steps each, on every kernel instance
+# (tests/test_f8_plan.py holds this list and EXPERTS_MANY_TILES to that)
+MANY_TILES = [(1, 40001, 2080), (20, 20103, 672), (50, 39001, 160), (100, 39001, 800), (300, 10001, 288),
+              (140, 39001, 288), (300, 39001, 416)]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("M,N,K", MANY_TILES)
+def test_product_exact_many_tiles(h32, M, N, K, bf16):
+    test_product_exact(h32, M, N, K, bf16)
 
 
 @pytest.mark.parametrize("bf16", [False, True])
@@ -265,6 +291,27 @@ def _experts_ref(wq, wd, xq, xd, off, N):
     E, nt = len(off) - 1, (N + 127) // 128
     return np.concatenate([oracle.f8_gemm(wq[e * N:(e + 1) * N], wd[e * nt:(e + 1) * nt], xq[off[e]:off[e + 1]],
                                           xd[off[e]:off[e + 1]])[0] for e in range(E)])
+
+
+def _uneven(E, per):
+    """Counts of E groups, `per` on average, a few of them 0 or 1."""
+    c = [per] * E
+    for i in range(0, E - 3, 4):
+        d = min(per, 3 * i // 4 + 1)
+        c[i], c[i + 1] = per - d, per + d
+    return c
+
+
+# two rows or so each (tokens as columns), 20 to 120 (on the lanes, tiles of every width)
+EXPERTS_MANY_TILES = [(_uneven(160, 2), 200, 416), (_uneven(64, 20), 1000, 288), (_uneven(64, 60), 260, 288),
+                      (_uneven(64, 90), 260, 288), (_uneven(20, 120), 260, 288), (_uneven(64, 120), 260, 160),
+                      (_uneven(20, 120), 1000, 416), (_uneven(20, 120), 2000, 416)]
+
+
+@pytest.mark.parametrize("counts,N,K", EXPERTS_MANY_TILES)
+@pytest.mark.parametrize("bf16", [False, True])
+def test_experts_exact_many_tiles(h32, counts, N, K, bf16):
+    test_experts_exact(h32, counts, N, K, bf16)
 
 
 @pytest.mark.parametrize("counts,N,K", [([1], 128, 128), ([0, 5, 0, 1, 16], 130, 288), ([3, 17, 29, 0, 2, 15], 300, 512),
