@@ -581,6 +581,7 @@ struct Partials {
                 ok = v != 0;
                 if (!ok && *abort) break;
             }
+        __syncwarp();   // (the other lanes' loads of the sums come after lane 0's acquire)
         return __shfl_sync(0xFFFFFFFFu, ok, 0);
     }
 };

@@ -228,6 +228,34 @@ def test_product_shared_out_along_k(h32, M, N, K):
     assert all(torch.equal(y, ref) for _, y, _ in graphs)
 
 
+def _same_every_time(h32, M, N, K, calls):
+    """Equal calls give equal bits, call after call, while other calls come between them."""
+    import torch
+    fin = np.setdiff1d(np.arange(256), [127, 255]).astype(np.uint8)
+    r = np.random.default_rng(M + N)
+    wq, xq = fin[r.integers(0, 254, (N, K))], fin[r.integers(0, 254, (M, K))]
+    nb = (K + 127) // 128
+    wd = (10.0 ** r.uniform(-4, 0, ((N + 127) // 128, nb))).astype(np.float32)
+    xd = (10.0 ** r.uniform(-4, 0, (M, nb))).astype(np.float32)
+    a = torch_of(wq), torch_of(wd), torch_of(xq), _xd(xd)
+    b = a[0].flip(1).contiguous(), a[1].flip(1).contiguous(), a[2].flip(0).contiguous(), a[3]
+    first = [h32.h32_f8_gemm(*a), h32.h32_f8_gemm(*b)]
+    rows = r.integers(0, M, 6)
+    ref, mag = oracle.f8_gemm(wq, wd, xq[rows], xd[rows])
+    assert (np.abs(np_of(first[0])[rows].astype(np.float64) - ref) <= (256 + nb + 2) * U * mag).all()
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(calls):
+        differ += (h32.h32_f8_gemm(*(a, b)[i % 2]) != first[i % 2]).sum()
+    _ok(h32)
+    assert int(differ) == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 5120, 16000), (1000, 5001, 16000)])
+def test_partial_sums_are_the_same_every_time(h32, M, N, K):
+    assert h32.h32_f8_gemm_workspace_bytes(M, N, K) > 0
+    _same_every_time(h32, M, N, K, 60)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 640, 5120), (5, 300, 17408), (40, 256, 2080), (100, 130, 4096), (300, 520, 5120)])
 def test_product_random_codes(h32, M, N, K):
     """Every finite code, scales over several octaves.  Per block the tensor core adds 128
