@@ -606,11 +606,12 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // s_full: this CTA's copies of a stage; s_peer (used in CTA 0): the other's are there too;
     // s_empty: the products have read the stage; s_sum: a K step's sums are in TMEM;
-    // s_free (in CTA 0): both CTAs' epilogues have them in registers; s_scale: a slot's scales
+    // s_free (in CTA 0): both CTAs' epilogues have them in registers; s_scale: a slot's scales;
+    // s_taken: this CTA's epilogue has read them
     using C = Lanes<kChunks, kCtas>;
     constexpr int S = C::kStages, slots = C::kSlots;
     constexpr uint32_t b_bytes = C::kB;
-    __shared__ uint64_t s_full[S], s_peer[S], s_empty[S], s_scale[slots], s_sum[2],
+    __shared__ uint64_t s_full[S], s_peer[S], s_empty[S], s_scale[slots], s_taken[slots], s_sum[2],
         s_free[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_word;
@@ -633,7 +634,10 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
             mbar_init(&s_empty[i], 1);
         }
 #pragma unroll 1
-        for (int i = 0; i < slots; ++i) mbar_init(&s_scale[i], 1);
+        for (int i = 0; i < slots; ++i) {
+            mbar_init(&s_scale[i], 1);
+            mbar_init(&s_taken[i], 8);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_sum[i], 1);
             mbar_init(&s_free[i], 8 * kCtas);
@@ -674,7 +678,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                 prefetch_tmap(&map_x);
                 prefetch_tmap(&map_s);
             }
-            Ring st(1), sl(0);   // (the first round's waits pass at once)
+            Ring st(1), sl(1);   // (the first round's waits pass at once)
             int fed = 0;
             bool ok = true;
             Walk<kSplit, kCtas> work(total, nb);
@@ -683,7 +687,9 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                 const int x_row = ti.g0 + 128 * rank, w_row = ti.e * a.N + ti.n0 + C::kBn / kCtas * rank;
 #pragma unroll 1
                 for (int kb = kSplit ? work.k0 : 0; kb < (kSplit ? work.k1 : nb); ++kb) {
-                    if (!warp_wait_or_look(&s_empty[st.i], st.ph, lim, abort)) {
+                    // (the slot's last scales were read two steps before this stage was free)
+                    if (!warp_wait_or_look(&s_empty[st.i], st.ph, lim, abort) ||
+                        !warp_wait_or_look(&s_taken[sl.i], sl.ph, lim, abort)) {
                         ok = false;
                         break;
                     }
@@ -691,8 +697,6 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                         mbar_arrive_expect_tx(&s_full[st.i], C::kA + b_bytes);
                         tma_load_2d(s_a + st.i * C::kA, &map_x, &s_full[st.i], kb * 128, x_row);
                         tma_load_2d(s_b + st.i * b_bytes, &map_w, &s_full[st.i], kb * 128, w_row);
-                        // the slot's last scales were read before the sums two steps later
-                        // were waited for, and those before this stage was free
                         mbar_arrive_expect_tx(&s_scale[sl.i], 512);
                         tma_load_2d(s_s + sl.i * 512, &map_s, &s_scale[sl.i], x_row, kb);
                     }
@@ -725,7 +729,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                         sl.i = slots - 1;
                         sl.ph ^= 1;
                     }
-                    mbar_wait_bounded(&s_scale[sl.i], sl.ph, kDrainPolls, nullptr);
+                    mbar_wait_bounded(&s_scale[sl.i], sl.ph ^ 1, kDrainPolls, nullptr);
                 }
             }
             __syncwarp();
@@ -837,7 +841,10 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) peer_arrive(bf.i ? free1 : free0);
+                if (lane == 0) {
+                    peer_arrive(bf.i ? free1 : free0);
+                    mbar_arrive(&s_taken[sl.i]);
+                }
                 bf.next(2);
                 sl.next(slots);
             }
