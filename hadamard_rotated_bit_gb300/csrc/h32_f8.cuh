@@ -81,6 +81,9 @@ __device__ __forceinline__ uint32_t peer_smem(const void *p, uint32_t q) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(q));
     return r;
 }
+__device__ __forceinline__ void peer_store(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void peer_store(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -105,12 +108,11 @@ __device__ __forceinline__ bool warp_wait_cluster(uint64_t *bar, uint32_t parity
     }
     return __all_sync(0xFFFFFFFFu, ok);
 }
-// Arrive on another CTA's barrier.  Nothing this thread wrote is handed over by it (the
-// copy engine's writes and the tensor-core loads it stands for were waited for), so it
-// carries no release: that waits for more than the thread's own accesses (4096 x 34816 x 5120 took
-// twice the time, even with releases by the messenger warp alone, 1130 us for 576).  What the copies
-// brought to a CTA's shared memory is read by that CTA's own tensor core, after the wait
-// for them in that CTA.
+// Arrive on another CTA's barrier, handing over tensor memory that this warp has read: its loads
+// were waited for (tcgen05.wait::ld) and fenced (tcgen05.fence::before_thread_sync), and the
+// issuer of the products that overwrite it fences behind its wait.  That pattern orders tensor
+// memory with relaxed arrivals; nothing else may rest on this one.  (A release, which waits for
+// more than the thread's own accesses, doubled the time of 4096 x 34816 x 5120.)
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -126,6 +128,19 @@ __device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst_smem, uint32_t nco
 }
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// a box of a tensor to this CTA's shared memory, complete on a barrier in either CTA of the pair
+// (`bar`: its address there)
+__device__ __forceinline__ void tma_load_2d_pair(void *smem_dst, const void *tmap, uint32_t bar, int32_t x, int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+// counts `bytes` as arrived, without a copy
+__device__ __forceinline__ void mbar_complete_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 // the descriptors' addresses hold in both CTAs; one thread of the first one issues
 __device__ __forceinline__ void mma_pair_f8f6f4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,

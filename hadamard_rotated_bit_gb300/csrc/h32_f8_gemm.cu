@@ -21,7 +21,7 @@
 //   step; 128 tokens and one CTA, or 256 and a pair (cta_group::2), x 64, 128 or 256 weight rows.
 //   warps 0..7  epilogue: a lane quarter and half of the columns each
 //   warp 8      TMA producer
-//   warp 9      TMEM allocator; MMA issuer, in a pair's second CTA the messenger of its copies
+//   warp 9      TMEM allocator; in the first CTA MMA issuer
 //   Bound: of the 406 ns of a pair's K step (256 x 256 x 128) the tensor core needs 270; the rest
 //   is the way from its last product to the epilogue and back, which two buffers of 256
 //   columns (all of TMEM) do not hide: without the loads of the sums and the folds a step
@@ -599,20 +599,41 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
     else mma_commit(bar);
 }
 
+// a box of codes to this CTA's shared memory; of a pair's it completes on CTA 0's barrier
+template <int kCtas>
+__device__ __forceinline__ void copy_codes(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
+    if constexpr (kCtas == 2) tma_load_2d_pair(dst, map, peer_smem(bar, 0), x, y);
+    else tma_load_2d(dst, map, bar, x, y);
+}
+// Waits until what is under way to the stages has landed, `mine` and `peer` stages being fed by
+// this CTA, which announced a stage's copies, and by the other (without one: the same).  They
+// differ by a stage ring at most, as neither goes round without the products of both; what only one
+// of them fed, of `bytes`, is made up for.
+__device__ __forceinline__ void drain_codes(uint64_t *full, int stages, uint32_t mine, uint32_t peer, uint32_t bytes = 0) {
+    const uint32_t least = min(mine, peer), most = max(mine, peer);
+#pragma unroll 1
+    for (uint32_t k = least; k != most; ++k) {
+        if (mine > peer) mbar_complete_tx(&full[k % stages], bytes);
+        else mbar_arrive_expect_tx(&full[k % stages], bytes);
+    }
+#pragma unroll 1
+    for (uint32_t k = most > uint32_t(stages) ? most - stages : 0; k != most; ++k)
+        mbar_wait_bounded(&full[k % stages], k / stages & 1, kDrainPolls, nullptr);
+}
+
 template <int kChunks, bool kSplit, int kCtas>
 __global__ void __launch_bounds__(kPairWarps * 32, 1)
     lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                 const __grid_constant__ CUtensorMap map_s, const F8Args a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    // s_full: this CTA's copies of a stage; s_peer (used in CTA 0): the other's are there too;
-    // s_empty: the products have read the stage; s_sum: a K step's sums are in TMEM;
+    // s_full (in CTA 0): both CTAs' copies of a stage; s_empty: the products have read the stage; s_sum: a K step's sums are in TMEM;
     // s_free (in CTA 0): both CTAs' epilogues have them in registers; s_scale: a slot's scales;
     // s_taken: this CTA's epilogue has read them
     using C = Lanes<kChunks, kCtas>;
     constexpr int S = C::kStages, slots = C::kSlots;
     constexpr uint32_t b_bytes = C::kB;
-    __shared__ uint64_t s_full[S], s_peer[S], s_empty[S], s_scale[slots], s_taken[slots], s_sum[2],
-        s_free[2], s_drain;
+    __shared__ uint64_t s_full[S], s_empty[S], s_scale[slots], s_taken[slots], s_sum[2], s_free[2], s_drain;
+    __shared__ uint32_t s_fed[2];   // in CTA 0: stages that each CTA's copies went to
     __shared__ uint32_t s_tmem;
     __shared__ int s_word;
     __shared__ volatile int s_abort;
@@ -630,7 +651,6 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
 #pragma unroll 1
         for (int i = 0; i < S; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_peer[i], 1);
             mbar_init(&s_empty[i], 1);
         }
 #pragma unroll 1
@@ -667,6 +687,11 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
         s_abort = 1;
         atomicOr(&g_f8_status, kStatusTimeout);
     };
+    // (a pair gives up together, and neither CTA waits for the other in vain)
+    auto tell_peer = [&]() {
+        if constexpr (kCtas == 2)
+            if (s_abort) peer_store(peer_smem(const_cast<int *>(&s_abort), cluster_rank() ^ 1), 1u);
+    };
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(issue_regs(kSplit)));
@@ -679,7 +704,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                 prefetch_tmap(&map_s);
             }
             Ring st(1), sl(1);   // (the first round's waits pass at once)
-            int fed = 0;
+            uint32_t fed = 0;
             bool ok = true;
             Walk<kSplit, kCtas> work(total, nb);
             while (ok && work.next(total, nb)) {
@@ -694,37 +719,37 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                         break;
                     }
                     if (leader) {
-                        mbar_arrive_expect_tx(&s_full[st.i], C::kA + b_bytes);
-                        tma_load_2d(s_a + st.i * C::kA, &map_x, &s_full[st.i], kb * 128, x_row);
-                        tma_load_2d(s_b + st.i * b_bytes, &map_w, &s_full[st.i], kb * 128, w_row);
+                        if (rank == 0) mbar_arrive_expect_tx(&s_full[st.i], kCtas * (C::kA + b_bytes));
+                        copy_codes<kCtas>(s_a + st.i * C::kA, &map_x, &s_full[st.i], kb * 128, x_row);
+                        copy_codes<kCtas>(s_b + st.i * b_bytes, &map_w, &s_full[st.i], kb * 128, w_row);
                         mbar_arrive_expect_tx(&s_scale[sl.i], 512);
                         tma_load_2d(s_s + sl.i * 512, &map_s, &s_scale[sl.i], x_row, kb);
                     }
                     __syncwarp();
-                    if (fed < slots) ++fed;
+                    ++fed;
                     st.next(S);
                     sl.next(slots);
                 }
             }
             if (leader) {
                 if (!ok) give_up();
-                // leave only when the last products have read the stages (in a whole run: their
-                // arrivals come from CTA 0) and the copies under way have landed
+                // leave only when the last products have read the stages (their arrivals come from
+                // CTA 0) and the copies under way have landed
 #pragma unroll 1
                 for (int i = 0; i < S && ok; ++i) {
-                    mbar_wait_bounded(&s_empty[st.i], st.ph, kDrainPolls, nullptr);
+                    ok = mbar_wait_bounded(&s_empty[st.i], st.ph, kDrainPolls, abort);
                     st.next(S);
                 }
-                if (ok) st.ph ^= 1;   // (once around the ring)
+                tell_peer();
+                if constexpr (kCtas == 2) {
+                    // (what is left of a pair's codes: below, once both CTAs are here)
+                    peer_store(peer_smem(&s_fed[rank], 0), fed);
+                    mbar_wait_bounded(&s_drain, 0, kDrainPolls, nullptr);   // CTA 0's last arrival
+                } else {
+                    drain_codes(s_full, S, fed, fed);
+                }
 #pragma unroll 1
-                for (int i = 0; i < fed; ++i) {
-                    if (i < S) {
-                        if (--st.i < 0) {
-                            st.i = S - 1;
-                            st.ph ^= 1;
-                        }
-                        mbar_wait_bounded(&s_full[st.i], st.ph ^ 1, kDrainPolls, nullptr);
-                    }
+                for (int i = 0; i < slots && static_cast<uint32_t>(i) < fed; ++i) {
                     if (--sl.i < 0) {
                         sl.i = slots - 1;
                         sl.ph ^= 1;
@@ -745,7 +770,6 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
 #pragma unroll 1
                 for (int kb = kSplit ? work.k0 : 0; kb < (kSplit ? work.k1 : nb); ++kb) {
                     if (!warp_wait_or_look(&s_full[st.i], st.ph, lim, abort) ||
-                        (kCtas == 2 && !warp_wait_or_look(&s_peer[st.i], st.ph, lim, abort)) ||
                         !warp_wait_or_look(&s_free[bf.i], bf.ph, lim, abort)) {
                         ok = false;
                         break;
@@ -770,26 +794,6 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                 commit<kCtas>(&s_drain);
                 mbar_wait_bounded(&s_drain, 0, kDrainPolls, nullptr);
             }
-            __syncwarp();
-        } else if (kCtas == 2 && warp == 9) {
-            // ------------------------------ CTA 1: its copies' arrival, passed on to CTA 0
-            Ring st(0);
-            bool ok = true;
-            Walk<kSplit, kCtas> work(total, nb);
-            while (ok && work.next(total, nb)) {
-#pragma unroll 1
-                for (int kb = kSplit ? work.k0 : 0; kb < (kSplit ? work.k1 : nb); ++kb) {
-                    if (!warp_wait_or_look(&s_full[st.i], st.ph, lim, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) peer_arrive(peer_smem(&s_peer[st.i], 0));
-                    __syncwarp();
-                    st.next(S);
-                }
-            }
-            if (!ok && lane == 0) give_up();
-            if (lane == 0) mbar_wait_bounded(&s_drain, 0, kDrainPolls, nullptr);   // CTA 0's last arrival
             __syncwarp();
         }
     } else {
@@ -897,9 +901,22 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
         }
         if (!ok && lane == 0) give_up();
     }
+    __syncwarp();
+    if (lane == 0) tell_peer();
     tc_fence_before();
-    if constexpr (kCtas == 2) cluster_sync();   // nothing of either CTA reaches into the other any more
-    else __syncthreads();
+    __syncwarp();
+    if constexpr (kCtas == 2) {
+        cluster_sync();   // nothing of either CTA reaches into the other any more, but copies:
+        if (s_abort) {    // (of both or neither) a wait gave up, some may be under way
+            // (the rank read anew: kept for this over the steps it cost spills)
+            if (cluster_rank() == 0 && warp == 8 && lane == 0)
+                drain_codes(s_full, S, s_fed[0], s_fed[1], C::kA + b_bytes);
+            __syncwarp();
+            cluster_sync();
+        }
+    } else {
+        __syncthreads();
+    }
     if (warp == 9) {
         tc_fence_after();
         if constexpr (kCtas == 2) tmem_dealloc_pair(tmem, 512);

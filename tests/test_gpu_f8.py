@@ -127,7 +127,7 @@ def test_quantize_weights_many_blocks(h32, K, rotate, bf16):
     """More blocks of 128 x 128 than run at once: the next one is copied under this one."""
     import torch
     N = 20001
-    assert (N + 127) // 128 * ((K + 127) // 128) > 2 * 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    assert (N + 127) // 128 * ((K + 127) // 128) > 2 * torch.cuda.get_device_properties(0).multi_processor_count
     w = _rows(N, K, N + K, bf16, 0.02)
     wq, wd = h32.h32_quantize_weights_f8(_dev(w), rotate=rotate)
     _ok(h32)
@@ -248,6 +248,13 @@ def _same_every_time(h32, M, N, K, calls):
         differ += (h32.h32_f8_gemm(*(a, b)[i % 2]) != first[i % 2]).sum()
     _ok(h32)
     assert int(differ) == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 9001, 4096), (700, 30001, 1056), (2000, 5001, 2080)])
+def test_pairs_give_the_same_bits_every_time(h32, M, N, K):
+    """Tiles of two CTAs, several a pair, of many K steps."""
+    assert h32.h32_f8_gemm_workspace_bytes(M, N, K) == 0
+    _same_every_time(h32, M, N, K, 100)
 
 
 @pytest.mark.parametrize("M,N,K", [(300, 5120, 16000), (1000, 5001, 16000)])
