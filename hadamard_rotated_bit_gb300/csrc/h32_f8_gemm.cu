@@ -988,10 +988,9 @@ h32_status launch_lanes(const uint8_t *wq, const uint8_t *xq, const float *xd, i
     const int units = static_cast<int>(tiles < sms / kCtas ? tiles : sms / kCtas);
     // the epilogue's setmaxnreg.inc waits until the pool holds its registers: never launch
     // with fewer registers a thread than the hand-over assumes
-    static const int regs = [] {
-        cudaFuncAttributes fa{};
-        return cudaFuncGetAttributes(&fa, lanes_kernel<kChunks, kSplit, kCtas>) == cudaSuccess ? fa.numRegs : -1;
-    }();
+    int regs = 0;
+    const cudaError_t e = kernel_regs<lanes_kernel<kChunks, kSplit, kCtas>>(&regs);
+    if (e != cudaSuccess) return launch_status(e);
     if (regs < kPairRegs) {
         note_error("8-bit product compiled with fewer registers than its warpgroups hand over");
         return H32_ERR_CUDA;
