@@ -22,15 +22,14 @@
 //   warps 0..7  epilogue: a lane quarter and half of the columns each
 //   warp 8      TMA producer
 //   warp 9      TMEM allocator; in the first CTA MMA issuer
-//   Bound: of the 406 ns of a pair's K step (256 x 256 x 128) the tensor core needs 270; the rest
-//   is the way from its last product to the epilogue and back, which two buffers of 256
-//   columns (all of TMEM) do not hide: without the loads of the sums and the folds a step
-//   took 445 ns when it took 610 with them.  4096 x 34816 x 5120: 555 to 595 us (the clock depends on
-//   the power the codes draw), 2460 to 2630 TFLOP/s.  (Measured and left: four buffers of 128
-//   columns, 913 us, as four dependent products of 128 columns take 350 clocks instead of 256; 16
-//   epilogue warps, scales multiplied ahead of their step, scalar folds, and loads of sums two
-//   at a time, each 5 to 100% slower; arrivals across the pair with release, twice the time; the
-//   outputs' stores are 5% of it, the first weight scales of a tile under 1%.)
+//   Bound: of the 420 to 480 ns of a pair's K step (256 x 256 x 128; the clock depends on the power
+//   the codes draw) the tensor core needs 270; the rest is the way from its last product to the
+//   epilogue and back, which two buffers of 256 columns (all of TMEM) do not hide.  4096 x 34816 x
+//   5120: 510 to 520 us, 2810 to 2860 TFLOP/s.  (Measured and left, in an earlier form: four buffers
+//   of 128 columns, 913 us for 555, as four dependent products of 128 columns take 350 clocks instead
+//   of 256; 16 epilogue warps, scales multiplied ahead of their step, scalar folds, and loads of
+//   sums two at a time, each 5 to 100% slower; arrivals across the pair with release, twice the
+//   time; the outputs' stores are 5% of it, the first weight scales of a tile under 1%.)
 // Every wait is bounded.
 #include "h32_f8.cuh"
 
@@ -47,12 +46,12 @@ constexpr int kRowsWarps = 6;
 // lanes_kernel: two epilogue warps for each quarter of the lanes, and a warpgroup of the roles
 // that issue.  Of 12 warps with 168 registers at launch the epilogue's two warpgroups take over
 // what that one does not need.  (The shares and the unrolling of the K steps are those that
-// leave every instance without spills: a few spilled words cost it 12 to 20%.)
+// leave every instance without spills: a few spilled words cost it 12 to 30%.)
 constexpr int kPairWarps = 12, kPairRegs = 168;
-constexpr __host__ __device__ int issue_regs(bool split) { return split ? 104 : 120; }
-constexpr __host__ __device__ int epilogue_regs(bool split) { return split ? 200 : 192; }
-static_assert(128 * issue_regs(false) + 256 * epilogue_regs(false) <= kPairWarps * 32 * kPairRegs &&
-                  128 * issue_regs(true) + 256 * epilogue_regs(true) <= kPairWarps * 32 * kPairRegs,
+constexpr __host__ __device__ int issue_regs(int ctas) { return ctas == 2 ? 104 : 120; }
+constexpr __host__ __device__ int epilogue_regs(int ctas) { return ctas == 2 ? 200 : 192; }
+static_assert(128 * issue_regs(1) + 256 * epilogue_regs(1) <= kPairWarps * 32 * kPairRegs &&
+                  128 * issue_regs(2) + 256 * epilogue_regs(2) <= kPairWarps * 32 * kPairRegs,
               "registers handed over");
 constexpr int kMaxSmem = 225 * 1024;
 constexpr uint64_t kDrainPolls = 1ull << 22;
@@ -65,6 +64,8 @@ struct F8Args {
     uint8_t *ws;             // lanes_kernel: partial sums and flags of split tiles, or null
     const int32_t *off;      // [E + 1] or null
     const float *wd;         // [E][ceil(N / 128)][ceil(K / 128)]
+    const float *xd;         // [ceil(K / 128)][ldxd]
+    int64_t ldxd;
     void *y;
     int64_t ldy;
     uint8_t y_bf16, y_vec;   // y_vec: every row of y starts on 16 bytes
@@ -489,11 +490,10 @@ template <int kChunks, int kCtas>
 struct Lanes {
     static constexpr int kBn = 64 * kChunks;             // weight rows of a tile
     static constexpr uint32_t kA = 128 * 128, kB = kBn / kCtas * 128;   // a CTA's codes of a stage
-    static constexpr uint32_t kRest = Groups::bytes(kMaxExperts) + 2 * 1024 + 2 * 512 + 8 * 4096;
-    static constexpr int kFit = (kMaxSmem - kRest) / (kA + kB + 512);
+    static constexpr uint32_t kRest = Groups::bytes(kMaxExperts) + 1024 + 8 * 4096;
+    static constexpr int kFit = (kMaxSmem - kRest) / (kA + kB);
     static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-    static constexpr int kSlots = kStages + 2;           // scales of a K step each
-    static constexpr uint32_t kSmem = kStages * (kA + kB + 512) + kRest;
+    static constexpr uint32_t kSmem = kStages * (kA + kB) + kRest;
 };
 
 // A pair's work, as (tile, K steps): whole tiles in turn, or (kSplit) an equal run of all tiles'
@@ -623,23 +623,20 @@ __device__ __forceinline__ void drain_codes(uint64_t *full, int stages, uint32_t
 
 template <int kChunks, bool kSplit, int kCtas>
 __global__ void __launch_bounds__(kPairWarps * 32, 1)
-    lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                const __grid_constant__ CUtensorMap map_s, const F8Args a) {
+    lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const F8Args a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // s_full (in CTA 0): both CTAs' copies of a stage; s_empty: the products have read the stage; s_sum: a K step's sums are in TMEM;
-    // s_free (in CTA 0): both CTAs' epilogues have them in registers; s_scale: a slot's scales;
-    // s_taken: this CTA's epilogue has read them
+    // s_free (in CTA 0): both CTAs' epilogues have them in registers
     using C = Lanes<kChunks, kCtas>;
-    constexpr int S = C::kStages, slots = C::kSlots;
+    constexpr int S = C::kStages;
     constexpr uint32_t b_bytes = C::kB;
-    __shared__ uint64_t s_full[S], s_empty[S], s_scale[slots], s_taken[slots], s_sum[2], s_free[2], s_drain;
+    __shared__ uint64_t s_full[S], s_empty[S], s_sum[2], s_free[2], s_drain;
     __shared__ uint32_t s_fed[2];   // in CTA 0: stages that each CTA's copies went to
     __shared__ uint32_t s_tmem;
     __shared__ int s_word;
     __shared__ volatile int s_abort;
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t *s_a = smem, *s_b = s_a + S * C::kA, *s_s = s_b + S * b_bytes;
-    uint8_t *s_y = s_s + (slots * 512 + 1023) / 1024 * 1024;   // 4 KB an epilogue warp
+    uint8_t *s_a = smem, *s_b = s_a + S * C::kA, *s_y = s_b + S * b_bytes;   // (s_y: 4 KB an epilogue warp)
     int *s_table = reinterpret_cast<int *>(s_y + 8 * 4096);
     const Groups g{s_table, s_table + a.E + 1};
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -652,11 +649,6 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
         for (int i = 0; i < S; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_empty[i], 1);
-        }
-#pragma unroll 1
-        for (int i = 0; i < slots; ++i) {
-            mbar_init(&s_scale[i], 1);
-            mbar_init(&s_taken[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_sum[i], 1);
@@ -694,16 +686,15 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
     };
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(issue_regs(kSplit)));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(issue_regs(kCtas)));
         if (warp == 8) {
             // ------------------------------------------------------------ TMA
             const bool leader = elect_one();
             if (leader) {
                 prefetch_tmap(&map_w);
                 prefetch_tmap(&map_x);
-                prefetch_tmap(&map_s);
             }
-            Ring st(1), sl(1);   // (the first round's waits pass at once)
+            Ring st(1);   // (the first round's waits pass at once)
             uint32_t fed = 0;
             bool ok = true;
             Walk<kSplit, kCtas> work(total, nb);
@@ -712,9 +703,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                 const int x_row = ti.g0 + 128 * rank, w_row = ti.e * a.N + ti.n0 + C::kBn / kCtas * rank;
 #pragma unroll 1
                 for (int kb = kSplit ? work.k0 : 0; kb < (kSplit ? work.k1 : nb); ++kb) {
-                    // (the slot's last scales were read two steps before this stage was free)
-                    if (!warp_wait_or_look(&s_empty[st.i], st.ph, lim, abort) ||
-                        !warp_wait_or_look(&s_taken[sl.i], sl.ph, lim, abort)) {
+                    if (!warp_wait_or_look(&s_empty[st.i], st.ph, lim, abort)) {
                         ok = false;
                         break;
                     }
@@ -722,13 +711,10 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                         if (rank == 0) mbar_arrive_expect_tx(&s_full[st.i], kCtas * (C::kA + b_bytes));
                         copy_codes<kCtas>(s_a + st.i * C::kA, &map_x, &s_full[st.i], kb * 128, x_row);
                         copy_codes<kCtas>(s_b + st.i * b_bytes, &map_w, &s_full[st.i], kb * 128, w_row);
-                        mbar_arrive_expect_tx(&s_scale[sl.i], 512);
-                        tma_load_2d(s_s + sl.i * 512, &map_s, &s_scale[sl.i], x_row, kb);
                     }
                     __syncwarp();
                     ++fed;
                     st.next(S);
-                    sl.next(slots);
                 }
             }
             if (leader) {
@@ -747,14 +733,6 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                     mbar_wait_bounded(&s_drain, 0, kDrainPolls, nullptr);   // CTA 0's last arrival
                 } else {
                     drain_codes(s_full, S, fed, fed);
-                }
-#pragma unroll 1
-                for (int i = 0; i < slots && static_cast<uint32_t>(i) < fed; ++i) {
-                    if (--sl.i < 0) {
-                        sl.i = slots - 1;
-                        sl.ph ^= 1;
-                    }
-                    mbar_wait_bounded(&s_scale[sl.i], sl.ph ^ 1, kDrainPolls, nullptr);
                 }
             }
             __syncwarp();
@@ -797,14 +775,14 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(epilogue_regs(kSplit)));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(epilogue_regs(kCtas)));
         // ------------------------------------------------------- epilogue
         // warp w: lanes of its quarter, half w / 4 of the columns in chunks of 32
         const int half = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
         uint8_t *buf = s_y + warp * 4096;
         const uint32_t free0 = peer_smem(&s_free[0], 0), free1 = peer_smem(&s_free[1], 0);
-        Ring bf(0), sl(0);
+        Ring bf(0);
         bool ok = true;
         Walk<kSplit, kCtas> work(total, nb);
         while (ok && work.next(total, nb)) {
@@ -816,18 +794,21 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                 for (int i = 0; i < 16; ++i) acc[j][i] = 0ull;
             // the weight scales of the warp's columns: they lie in one block of 128
             const float *wd = a.wd + (int64_t(ti.e) * ((a.N + 127) / 128) + min(ti.n0 + 32 * kChunks * half, a.N - 1) / 128) * nb;
-            float dw = __ldg(wd + (kSplit ? work.k0 : 0));
             const int k0 = kSplit ? work.k0 : 0, k1 = kSplit ? work.k1 : nb;
-#pragma unroll kSplit ? 4 : 3
+            // the scales of the lane's token (behind the last one: any) and of the columns, a step ahead
+            // (the tokens' through shared memory, with barriers for their arrival and their being
+            // read: 4096 x 34816 x 5120 581 us, now 515; loaded two steps ahead 523)
+            const float *xd = a.xd + k0 * a.ldxd + min(ti.g0 + 128 * static_cast<int>(rank) + row, a.M - 1);
+            float dw = __ldg(wd + k0), dx = __ldg(xd);
+#pragma unroll 4
             for (int kb = k0; kb < k1; ++kb) {
-                if (!warp_wait_or_look(&s_scale[sl.i], sl.ph, lim, abort)) {
-                    ok = false;
-                    break;
-                }
-                const float dx = *reinterpret_cast<const float *>(s_s + sl.i * 512 + row * 4);
                 const uint32_t sc = __float_as_uint(__fmul_rn(dx, dw));
                 const uint64_t s2 = pair_of(sc, sc);
-                if (kb + 1 < k1) dw = __ldg(wd + kb + 1);
+                xd += a.ldxd;
+                if (kb + 1 < k1) {
+                    dw = __ldg(wd + kb + 1);
+                    dx = __ldg(xd);
+                }
                 if (!warp_wait_or_look(&s_sum[bf.i], bf.ph, lim, abort)) {
                     ok = false;
                     break;
@@ -845,12 +826,8 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    peer_arrive(bf.i ? free1 : free0);
-                    mbar_arrive(&s_taken[sl.i]);
-                }
+                if (lane == 0) peer_arrive(bf.i ? free1 : free0);
                 bf.next(2);
-                sl.next(slots);
             }
             if (!ok) break;
             if (kSplit && (work.k1 < nb || work.k0 > 0)) {
@@ -934,9 +911,8 @@ __global__ void __launch_bounds__(256) clear_flags(uint4 *flags, int n) {
 }
 
 // one launch in clusters of `cluster` CTAs, overlapping the tail of the stream's last kernel
-template <auto kKernel>
-h32_status launch_clusters(int grid, int threads, size_t smem, int cluster, cudaStream_t s,
-                           const CUtensorMap *maps, const F8Args &a) {
+template <auto kKernel, typename... Args>
+h32_status launch_clusters(int grid, int threads, size_t smem, int cluster, cudaStream_t s, const Args &...args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
@@ -951,13 +927,13 @@ h32_status launch_clusters(int grid, int threads, size_t smem, int cluster, cuda
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     cudaError_t e = allow_smem<kKernel>(kMaxSmem);
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kKernel, maps[0], maps[1], maps[2], a);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kKernel, args...);
     return launch_status(e != cudaSuccess ? e : cudaGetLastError());
 }
 
 template <int NC>
-h32_status launch_rows(const uint8_t *wq, const uint8_t *xq, const float *xd, int64_t ldxd, F8Args a, int64_t tiles,
-                       int cluster, int sms, cudaStream_t s) {
+h32_status launch_rows(const uint8_t *wq, const uint8_t *xq, F8Args a, int64_t tiles, int cluster, int sms,
+                       cudaStream_t s) {
     using C = Rows<NC>;
     const int nb = (a.K + 127) / 128;
     a.cluster = cluster;
@@ -967,21 +943,20 @@ h32_status launch_rows(const uint8_t *wq, const uint8_t *xq, const float *xd, in
     a.stages = fit < kMaxStages ? fit : kMaxStages;
     CUtensorMap maps[3];
     if (!code_map(&maps[0], wq, a.K, int64_t(a.E) * a.N, 128) || !code_map(&maps[1], xq, a.K, a.M, NC) ||
-        !scale_map(&maps[2], xd, ldxd, nb, NC)) {
+        !scale_map(&maps[2], a.xd, a.ldxd, nb, NC)) {
         note_error("cuTensorMapEncodeTiled rejected a tensor map of the 8-bit product");
         return H32_ERR_CUDA;
     }
     const int grid = a.cluster > 1 ? static_cast<int>(tiles * a.cluster) : static_cast<int>(tiles < sms ? tiles : sms);
-    return launch_clusters<rows_kernel<NC>>(grid, kRowsWarps * 32, a.stages * C::kStage + rest, a.cluster, s, maps, a);
+    return launch_clusters<rows_kernel<NC>>(grid, kRowsWarps * 32, a.stages * C::kStage + rest, a.cluster, s, maps[0], maps[1],
+                                            maps[2], a);
 }
 
 template <int kChunks, int kCtas, bool kSplit = false>
-h32_status launch_lanes(const uint8_t *wq, const uint8_t *xq, const float *xd, int64_t ldxd, const F8Args &a, int64_t tiles,
-                       int sms, cudaStream_t s) {
+h32_status launch_lanes(const uint8_t *wq, const uint8_t *xq, const F8Args &a, int64_t tiles, int sms, cudaStream_t s) {
     using C = Lanes<kChunks, kCtas>;
-    CUtensorMap maps[3];
-    if (!code_map(&maps[0], wq, a.K, int64_t(a.E) * a.N, C::kBn / kCtas) || !code_map(&maps[1], xq, a.K, a.M, 128) ||
-        !scale_map(&maps[2], xd, ldxd, (a.K + 127) / 128, 128)) {
+    CUtensorMap maps[2];
+    if (!code_map(&maps[0], wq, a.K, int64_t(a.E) * a.N, C::kBn / kCtas) || !code_map(&maps[1], xq, a.K, a.M, 128)) {
         note_error("cuTensorMapEncodeTiled rejected a tensor map of the 8-bit product");
         return H32_ERR_CUDA;
     }
@@ -995,7 +970,8 @@ h32_status launch_lanes(const uint8_t *wq, const uint8_t *xq, const float *xd, i
         note_error("8-bit product compiled with fewer registers than its warpgroups hand over");
         return H32_ERR_CUDA;
     }
-    return launch_clusters<lanes_kernel<kChunks, kSplit, kCtas>>(kCtas * units, kPairWarps * 32, C::kSmem, kCtas, s, maps, a);
+    return launch_clusters<lanes_kernel<kChunks, kSplit, kCtas>>(kCtas * units, kPairWarps * 32, C::kSmem, kCtas, s, maps[0], maps[1],
+                                                                a);
 }
 
 h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint8_t *xq, const float *xd,
@@ -1022,6 +998,8 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
     a.E = E;
     a.off = off;
     a.wd = wd;
+    a.xd = xd;
+    a.ldxd = ldxd;
     a.y = y;
     a.ldy = ldy;
     a.y_bf16 = y_dt == H32_IN_BF16;
@@ -1029,8 +1007,8 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
     a.wait_limit = wait_limit();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const F8Plan plan = plan_f8(M, N, K, E, off != nullptr, sms);
-    if (plan.columns == 16) return launch_rows<16>(wq, xq, xd, ldxd, a, plan.tiles, plan.cluster, sms, s);
-    if (plan.columns == 32) return launch_rows<32>(wq, xq, xd, ldxd, a, plan.tiles, plan.cluster, sms, s);
+    if (plan.columns == 16) return launch_rows<16>(wq, xq, a, plan.tiles, plan.cluster, sms, s);
+    if (plan.columns == 32) return launch_rows<32>(wq, xq, a, plan.tiles, plan.cluster, sms, s);
     if (plan.runs > 0 && ws) {
         if (ws_bytes < Partials::bytes(plan.runs)) return H32_ERR_INVALID_ARG;
         a.ws = static_cast<uint8_t *>(ws);
@@ -1039,16 +1017,16 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
                                          reinterpret_cast<uint4 *>(a.ws + Partials::bytes(plan.runs) - flags),
                                          static_cast<int>(flags / 16));
         if (e != cudaSuccess) return launch_status(e);
-        return launch_lanes<4, 2, true>(wq, xq, xd, ldxd, a, plan.runs, sms, s);
+        return launch_lanes<4, 2, true>(wq, xq, a, plan.runs, sms, s);
     }
     if (plan.ctas == 1) {
-        if (plan.bn == 256) return launch_lanes<4, 1>(wq, xq, xd, ldxd, a, plan.tiles, sms, s);
-        if (plan.bn == 128) return launch_lanes<2, 1>(wq, xq, xd, ldxd, a, plan.tiles, sms, s);
-        return launch_lanes<1, 1>(wq, xq, xd, ldxd, a, plan.tiles, sms, s);
+        if (plan.bn == 256) return launch_lanes<4, 1>(wq, xq, a, plan.tiles, sms, s);
+        if (plan.bn == 128) return launch_lanes<2, 1>(wq, xq, a, plan.tiles, sms, s);
+        return launch_lanes<1, 1>(wq, xq, a, plan.tiles, sms, s);
     }
-    if (plan.bn == 256) return launch_lanes<4, 2>(wq, xq, xd, ldxd, a, plan.tiles, sms, s);
-    if (plan.bn == 128) return launch_lanes<2, 2>(wq, xq, xd, ldxd, a, plan.tiles, sms, s);
-    return launch_lanes<1, 2>(wq, xq, xd, ldxd, a, plan.tiles, sms, s);
+    if (plan.bn == 256) return launch_lanes<4, 2>(wq, xq, a, plan.tiles, sms, s);
+    if (plan.bn == 128) return launch_lanes<2, 2>(wq, xq, a, plan.tiles, sms, s);
+    return launch_lanes<1, 2>(wq, xq, a, plan.tiles, sms, s);
 }
 
 }  // namespace
