@@ -282,6 +282,44 @@ def test_product_random_codes(h32, M, N, K):
     assert (err <= (256 + nb + 2) * U * mag).all()
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("M", [3, 20, 40, 140, 300])
+def test_product_scales_outside_the_normal_range(h32, M, bf16):
+    """The product of two scales is rounded as it stands: to a multiple of 2^-149 below fp32's
+    normal range (sums of codes are then exact), to infinity above."""
+    import torch
+    N, K = 300, 416
+    wq, _, xq, _ = _exact_operands(M, N, K, M)
+    nb, nt = (K + 127) // 128, (N + 127) // 128
+    r = np.random.default_rng(M)
+    wd = (r.integers(64, 128, (nt, nb)) * 2.0 ** -80).astype(np.float32)
+    xd = (r.integers(64, 128, (M, nb)) * 2.0 ** -81).astype(np.float32)
+    val = oracle.e4m3_values()
+    sums = np.stack([val[xq[:, 128 * b:128 * b + 128]] @ val[wq[:, 128 * b:128 * b + 128]].T for b in range(nb)])
+
+    def fold(xd, wd):
+        acc = np.zeros((M, N), np.float32)
+        with np.errstate(all="ignore"):
+            for b in range(nb):
+                acc = acc + (xd[:, b, None] * np.repeat(wd[:, b], 128)[None, :N]) * sums[b].astype(np.float32)
+        return torch.from_numpy(acc)
+
+    def run(xd, wd):
+        y = h32.h32_f8_gemm(torch_of(wq), torch_of(wd), torch_of(xq), _xd(xd), y_dtype=torch.bfloat16 if bf16 else None)
+        _ok(h32)
+        return y.cpu()
+
+    # 64^2 to 127^2 times 2^-161, so 1 to 4 times 2^-149: sums of at most 4 * 8192 * 4 steps
+    ref = fold(xd, wd)
+    assert bool((ref != 0).any()) and float(ref.abs().max()) < 2.0 ** -126
+    assert torch.equal(run(xd, wd), ref.bfloat16() if bf16 else ref)
+    xd[M // 2], wd[1] = 2.0 ** 70, 2.0 ** 70
+    ref = fold(xd, wd)
+    assert bool(torch.isinf(ref[M // 2, 128:256]).any())
+    assert torch.equal(torch.nan_to_num(run(xd, wd).float(), nan=1234.0),
+                       torch.nan_to_num((ref.bfloat16() if bf16 else ref).float(), nan=1234.0))
+
+
 def test_product_nan_stays_in_its_row_and_column(h32):
     wq, wd, xq, xd = _exact_operands(40, 300, 256, 1)
     wq[7, 3], xq[5, 200] = 0x7F, 0xFF

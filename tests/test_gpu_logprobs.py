@@ -218,6 +218,36 @@ def test_a_certain_token_over_a_wide_floor(h32, T, bf16):
     assert (err <= 52 * (1 + 2 * d * rest) * U + (3 * d + 4 + 128) * d * rest * U).all()
 
 
+@pytest.mark.parametrize("T,V,bf16", [(267, 65600, False), (300, 70001, False), (304, 131073, True), (305, 131073, True),
+                                      (121, 131072, True), (122, 131072, True), (152, 70001, False), (153, 70001, False),
+                                      (1063, 40000, False), (1064, 40000, False), (1064, 131072, True),
+                                      (1064, 131080, True), (2100, 65536, False)])
+def test_row_counts_around_the_choices_of_a_rows_ctas(h32, T, V, bf16):
+    """How many CTAs a row is split over and how large they are depend on the number of rows."""
+    import torch
+    n, top = 7, 6
+    l, base = _logits(n, V, T + V, bf16)
+    odd = n - 1
+    l[odd, : V - 3], base[odd, : V - 3] = -INF, -INF        # fewer left than asked for
+    rows = np.random.default_rng(T).integers(0, n, T)
+    rows[:n] = np.arange(n)
+    targets = np.stack([l.argmax(1), np.full(n, V // 2), np.full(n, V - 1)], 1).astype(np.int32)
+    at = torch_of(rows)
+    got = h32.h32_token_logprobs(base[at], torch_of(targets)[at], top=top)
+    torch.cuda.synchronize()
+    assert h32.h32_device_status() == 0
+    rlp, rent, rids, rtlp = oracle.token_logprobs(l, targets, top)
+    lp, ent, ids, tlp = (np_of(g).astype(np.float64) for g in got)
+    assert np.array_equal(ids, rids[rows])
+    # at most 64 roundings of the sum and 4 more at each of a thread's rises of its maximum (a few
+    # of its up to 64 steps), 3 |l - m| + 4 of an exponential (p |l - m| adds up to less than 3 here),
+    # and of the values themselves: 400 U in all for values up to 20
+    for g, want in ((lp, rlp[rows]), (ent, rent[rows]), (tlp, rtlp[rows])):
+        odd = ~np.isfinite(want)
+        assert np.array_equal(g[odd], want[odd], equal_nan=True)
+        assert (np.abs(g[~odd] - want[~odd]) <= 400 * U * np.maximum(1, np.abs(want[~odd]) / 20)).all()
+
+
 def test_given_outputs_streams_and_graphs(h32):
     import torch
     l, t = _logits(6, 30011, 5)
