@@ -237,10 +237,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
     constexpr int kWarps = kThreads / 32, kGroup = kThreads / 64;   // threads of a group
     constexpr int kN = V4::kN;
     __shared__ __align__(16) float s_chunk[kSlots][kThreads];   // largest values of the chunks
-    __shared__ __align__(16) uint64_t s_all[kMaxKeys + 4];
-    __shared__ uint64_t s_buf[kWarps][64], s_best[kMaxTop];
+    // keys and the warps' lists behind the pass; in it, for each thread, m, S, W and what the
+    // roundings of S and W left over (no memory of their own: the pass is faster with more L1)
+    __shared__ __align__(16) uint64_t s_pool[kMaxKeys + 4 + kWarps * 64];
+    static_assert(sizeof(s_pool) >= 5 * kThreads * sizeof(float), "a thread's sums of runs");
+    uint64_t *s_all = s_pool, *s_buf = s_pool + kMaxKeys + 4;
+    float(*s_run)[kThreads] = reinterpret_cast<float(*)[kThreads]>(s_pool);
+    __shared__ uint64_t s_best[kMaxTop];
     __shared__ uint32_t s_list[kMaxChunks];
-    __shared__ float s_run[5][kThreads];   // m, S, W and what the roundings of S and W left over
     __shared__ Part s_part[kMaxCluster];
     __shared__ __align__(16) float s_group[64];
     __shared__ float s_m[kWarps], s_S[kWarps], s_W[kWarps], s_bound;
@@ -269,8 +273,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
     // steps' sums plainly for kRun steps, and the runs' with compensation: terms below half a step
     // of the sum, the floor under a likely token, would all be lost if they were added to it one by
     // one (131071 of e^-17 next to 1: 1e-5 of log p).  W has no such 1, its terms are added as they
-    // come.  (512 x 100003 fp32 37.9 us, one by one 37.5; every step with compensation 40.9;
-    // 4096 x 131072 bf16, top 8: 182.5, 179 and 184.)
+    // come.  (512 x 100003 fp32 36.2 us, one by one 37.4, every step with compensation 40.9;
+    // 4096 x 131072 bf16, top 8: 184, 178 and 184.)
     uint64_t S2 = 0, W2 = 0;
     const auto end_run = [&](bool first) {
         float run_s = low(S2) + high(S2), run_w = low(W2) + high(W2), rest_s = 0.0f, rest_w = 0.0f;
@@ -453,7 +457,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
             // order of their indices (equal values behind the k-th are not better)
             List list;
             list.bound = below(ordered(bound));
-            list.buf = s_buf[warp];
+            list.buf = s_buf + 64 * warp;
             list.k = a.top;
             list.lane = lane;
             for (int64_t step = step0; step < step1; ++step) {
