@@ -6,19 +6,19 @@
 //
 // One pass over the logits.  Each thread keeps m, S and W of what it has read (all fp32,
 // rescaled when m grows, summed by steps and runs of steps) and, for the k most probable tokens, the
-// largest value of each of its
-// chunks (16 fp32 or 32 bf16 values, more where a CTA takes over 16 steps).  The k-th largest of
-// the 64 maxima of groups of lanes bounds the k best from below, so only chunks that reach it,
-// hardly more than k, are read again (from L2) for their values above it, and of those the k
-// largest are found by counting, for each, the larger ones.  Nothing in the pass itself depends
-// on the values: buffers filled as candidates come cost 30 to 80% more time there.  Rows where
-// too many values reach the bound (ties, mostly) are read again by warps that keep sorted lists.
+// largest value of each of its chunks (16 fp32 or 32 bf16 values, more where a CTA takes over 16
+// steps).  The k-th largest of the 64 maxima of groups of lanes bounds the k best from below, so only
+// chunks that reach it, hardly more than k, are read again (from L2) for their values above it, and
+// of those the k largest are found by counting, for each, the larger ones.  Nothing in the pass
+// itself depends on the values: buffers filled as candidates come cost 30 to 80% more time there.
+// Rows where too many values reach the bound (ties, mostly) are read again by warps that keep sorted
+// lists.
 //
 // A row is one CTA's, or with few rows a cluster's: its CTAs take consecutive parts and
 // leave their results in the first one's shared memory.
 // Bound: HBM, one read of the logits, and next to it instruction issue (2048 x 131072 fp32, top 8:
-// 163 us, 97% of the measured copy rate; 4096 x 131072 bf16, top 8: 182 us, 87%, with the sums not
-// in packed pairs 191); one row: about 9 us of steps that wait for one another.
+// 161 us, 99% of the measured copy rate; 4096 x 131072 bf16, top 8: 184 us, 86%); one row: about 9 us
+// of steps that wait for one another.
 #include "h32_common.cuh"
 
 #include <float.h>
@@ -576,18 +576,26 @@ extern "C" h32_status h32_token_logprobs(const void *logits, h32_in_dtype dt, in
     // 1.6 an SM, or 2 with at least 16 steps each: beyond, the steps behind the pass and the cluster's
     // meeting cost more than the shorter pass gives (131072 bf16: 76 rows 10.0 us by twos, 15.7
     // by eights; 150 rows 11.2 by one, 17.0 by fours, but fp32 15.8 by twos and 20.8 by one).  Long
-    // rows that come to nearly four CTAs an SM by twos are the exception (300 rows 21.6 and 28.0 us).
+    // rows go by twos as long as all of them run at once, five CTAs an SM (131072 fp32 by one and by
+    // twos: 160 rows 26.8 and 20.4 us, 240 28.7 and 27.0, 300 30.7 and 29.1, 380 33.9 and 33.1, 400 40.1
+    // and 50.9; bf16 160 rows 21.6 and 17.4, 300 23.7 and 20.6, 380 30.4 and 30.0, 400 30.4 and
+    // 31.0; rows of 8 steps, 65536 bf16, 420 18.1 and 22.9, 160 the same).
     const int64_t steps = V / (256 * kVecs * (dt == H32_IN_BF16 ? 8 : 4));
     int c = 1;
     while (c < kMaxCluster && 2 * c <= steps &&
            (T * 2 * c * 5 <= 8 * int64_t(sms) || (T * 2 * c <= 2 * int64_t(sms) && steps >= 32 * c)))
         c *= 2;
-    if (c == 1 && steps >= 16 && T * 4 > 7 * int64_t(sms) && T <= 2 * int64_t(sms)) c = 2;
-    // Many rows: what follows the pass is steps that wait for one another, so more rows at once
-    // in CTAs of 128 threads (3989 x 11472 bf16, top 2: 34 us, with 256 threads 50; 4096 x 1000 25
-    // and 44; 2048 x 32768 36 and 40), unless the rows are long (2048 x 131072 fp32 170 and 163) or
-    // too few to fill the SMs (700 x 50000 fp32 32 and 26).  64 threads were slower throughout.
-    const bool half = c == 1 && T >= 7 * int64_t(sms) && V * (dt == H32_IN_BF16 ? 2 : 4) <= 256 * 1024;
+    if (c == 1 && steps >= 16 && 2 * T <= 5 * int64_t(sms)) c = 2;
+    // Many rows: what follows the pass is steps that wait for one another, so more rows at once in
+    // CTAs of 128 threads (4096 rows, with 128 and 256 threads: 1000 fp32 24 and 33 us, 11472 bf16 37
+    // and 52, 32768 bf16 61 and 70, 65536 bf16 101 and 107, 131072 bf16 and 65536 fp32, 256 KB, equal;
+    // beyond, 90000 fp32 275 and 226), unless they are too few to fill the SMs (700 x 50000 fp32 46 and
+    // 26) or, of 48 KB or more, between half a wave of such CTAs and one, which then all end together
+    // (32768 fp32: 1064 rows 26 and 32 us, but 1250 36 and 34, 1500 46 and 36, 2048 50 and 51; 131072
+    // bf16 1500 rows 81 and 74).
+    const int64_t bytes = V * (dt == H32_IN_BF16 ? 2 : 4);
+    const bool half = c == 1 && T >= 7 * int64_t(sms) && bytes <= 256 * 1024 &&
+                      (bytes < 48 * 1024 || T <= 8 * int64_t(sms) || T >= 12 * int64_t(sms));
     const LogprobArgs a{logits, V, ldl, targets, n, top, logprob, entropy, top_logprob, top_id};
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(T * c));
