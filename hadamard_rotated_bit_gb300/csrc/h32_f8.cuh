@@ -9,36 +9,16 @@
 
 #include "h32_common.cuh"
 #include "h32_once.h"
+#include "h32_tmap.cuh"
 
-#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cudaTypedefs.h>
 
 #include <atomic>
-#include <mutex>
 
 namespace h32 {
 namespace {
 
 constexpr int kMaxExperts = 1024;
-
-// one leader lane of a converged warp
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
-    return r != 0;
-}
-
-// K-major operand in 128B-swizzled 8-row x 128-byte atoms, as TMA writes it
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(1) << 16;            // leading byte offset (unused here)
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;    // 8-row group stride: 1024 bytes
-    d |= static_cast<uint64_t>(1) << 46;            // descriptor version
-    d |= static_cast<uint64_t>(2) << 61;            // swizzle: 128 bytes
-    return d;
-}
 
 // 32 lanes x 32 bit, 32 consecutive columns per thread
 __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -67,21 +47,6 @@ __device__ __forceinline__ void tmem_wait_for(uint32_t (&r)[32]) {
 
 
 // clusters -------------------------------------------------------------------
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// every thread of every CTA of the cluster
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
-// the address of this CTA's shared location `p` in the CTA of rank q
-__device__ __forceinline__ uint32_t peer_smem(const void *p, uint32_t q) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(q));
-    return r;
-}
 __device__ __forceinline__ void peer_store(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -186,26 +151,12 @@ cudaError_t kernel_regs(int *regs) {
 }
 
 // tensor maps ----------------------------------------------------------------
-inline PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 // rows of K code bytes, boxes of `box_rows` rows x 128 bytes, 128B-swizzled; rows and
 // columns outside the array read as zero
 inline bool code_map(CUtensorMap *map, const void *base, uint64_t K, uint64_t rows, uint32_t box_rows) {
     const cuuint64_t dims[2] = {K, rows}, strides[1] = {K};
     const cuuint32_t box[2] = {128, box_rows}, estr[2] = {1, 1};
-    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+    return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -213,7 +164,7 @@ inline bool code_map(CUtensorMap *map, const void *base, uint64_t K, uint64_t ro
 inline bool scale_map(CUtensorMap *map, const void *base, uint64_t ld, uint64_t groups, uint32_t box_cols) {
     const cuuint64_t dims[2] = {ld, groups}, strides[1] = {ld * 4};
     const cuuint32_t box[2] = {box_cols, 1}, estr[2] = {1, 1};
-    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base), dims, strides, box, estr,
+    return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

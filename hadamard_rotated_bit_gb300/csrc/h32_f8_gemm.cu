@@ -537,12 +537,6 @@ private:
     int left, last;   // steps of the run still to come, and where the next piece ends
 };
 
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // Partial sums of a pair: a CTA's 8 epilogue warps, 32 pieces of 16 bytes a lane.  Behind all of
 // them a flag for each warp, set when its sums are written.
 struct Partials {
@@ -987,7 +981,7 @@ h32_status run_f8_gemm(const uint8_t *wq, const float *wd, int32_t E, const uint
         return H32_ERR_ALIGNMENT;
     int sms = 0;
     H32_TRY(check_device(&sms));
-    if (!encoder()) {
+    if (!tensor_map_encoder()) {
         note_error("cuTensorMapEncodeTiled is not available from the driver");
         return H32_ERR_CUDA;
     }

@@ -37,13 +37,8 @@
 #endif
 
 #include "h32_few.cuh"
-
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
 #include "h32_epilogue.cuh"
+#include "h32_tmap.cuh"
 
 namespace h32 {
 namespace {
@@ -80,23 +75,6 @@ __device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, ui
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
         : "memory");
-}
-
-// K-major operand in 128B-swizzled 8-row x 128-byte atoms, as TMA writes it
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(1) << 16;            // leading byte offset (unused here)
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;    // 8-row group stride: 1024 bytes
-    d |= static_cast<uint64_t>(1) << 46;            // descriptor version
-    d |= static_cast<uint64_t>(2) << 61;            // swizzle: 128 bytes
-    return d;
-}
-
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
-    return r != 0;
 }
 
 // 2 PT consecutive columns of the warp's 32 lanes
@@ -398,27 +376,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 // rows of `row_bytes` as [row_bytes / 128][rows][128 bytes], boxes of `box_rows` rows
 // and `box_cols` 128-byte columns, 128B-swizzled
 bool code_map(CUtensorMap *map, const void *base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows,
               uint32_t box_cols) {
     const cuuint64_t dims[3] = {128, rows, row_bytes / 128}, strides[2] = {row_bytes, 128};
     const cuuint32_t box[3] = {128, box_rows, box_cols}, estr[3] = {1, 1, 1};
-    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
+    return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
                      estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -427,7 +391,7 @@ bool scale_map(CUtensorMap *map, const void *base, uint64_t inner, uint64_t oute
                uint32_t box_outer) {
     const cuuint64_t dims[2] = {inner, outer}, strides[1] = {inner * 4};
     const cuuint32_t box[2] = {box_inner, box_outer}, estr[2] = {1, 1};
-    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base), dims, strides, box,
+    return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base), dims, strides, box,
                      estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -475,7 +439,7 @@ h32_status launch_few(int xbits, const uint8_t *wp, const float *wsc, int64_t ld
     const int fit = (kMaxSmem - 1024) / static_cast<int>(z.stage());
     a.stages = fit < kMaxStages ? fit : kMaxStages;
     const int smem = a.stages * static_cast<int>(z.stage()) + 1024;
-    if (!encoder()) {
+    if (!tensor_map_encoder()) {
         note_error("cuTensorMapEncodeTiled is not available from the driver");
         return H32_ERR_CUDA;
     }

@@ -34,8 +34,6 @@
 // Every wait is bounded; a wait that gives up records a status bit, makes the
 // other roles leave their loops, drains the CTA's own TMA copies and MMAs,
 // frees its tensor memory and returns.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
 #include <map>
@@ -44,6 +42,7 @@
 
 #include "h32_common.cuh"
 #include "h32_epilogue.cuh"
+#include "h32_tmap.cuh"
 
 namespace h32 {
 namespace {
@@ -767,20 +766,6 @@ __global__ void __launch_bounds__(Cfg<XB>::kThreads, 1)
 // ----------------------------------------------------------------------------
 // host side
 // ----------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 // 128 rows x 64 bytes boxes over the weight nibbles viewed as [rows][K/2] bytes
 h32_status make_weight_map(CUtensorMap *map, const uint8_t *wq, int64_t rows, int64_t K) {
     auto enc = tensor_map_encoder();

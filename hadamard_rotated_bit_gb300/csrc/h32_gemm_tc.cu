@@ -58,8 +58,6 @@
 #define H32_WAIT_SLEEP 0
 #endif
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <cstdint>
 #include <map>
@@ -71,6 +69,7 @@
 #include "h32_few.cuh"
 #include "h32_finish.cuh"
 #include "h32_tcform.cuh"
+#include "h32_tmap.cuh"
 
 namespace h32 {
 namespace {
@@ -194,17 +193,6 @@ __device__ __forceinline__ void reg_alloc() {
 __device__ __forceinline__ void set_abort(volatile int *misc) {
     misc[kMiscAbort] = 1;
     record(kStatusTimeout);
-}
-
-// K-major operand in 128B-swizzled 8-row x 128-byte atoms, as TMA writes it
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(1) << 16;            // leading byte offset (unused here)
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;    // 8-row group stride: 1024 bytes
-    d |= static_cast<uint64_t>(1) << 46;            // descriptor version
-    d |= static_cast<uint64_t>(2) << 61;            // swizzle: 128 bytes
-    return d;
 }
 
 // one elected lane of the (converged) warp arrives on `bar`; no branch
@@ -1387,24 +1375,10 @@ __global__ void __launch_bounds__(TcCfg<EPQ, XB, kEpi == 2, kWQ, kEpi == 3>::kTh
 // ----------------------------------------------------------------------------
 // host side
 // ----------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 h32_status make_map(CUtensorMap *map, CUtensorMapDataType type, int esize, const void *base,
                     uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
                     uint32_t box_outer, bool swizzle) {
-    auto enc = encoder();
+    auto enc = tensor_map_encoder();
     if (!enc) {
         note_error("cuTensorMapEncodeTiled is not available from the driver");
         return H32_ERR_CUDA;

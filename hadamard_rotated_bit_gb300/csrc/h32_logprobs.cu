@@ -20,6 +20,7 @@
 // 161 us, 99% of the measured copy rate; 4096 x 131072 bf16, top 8: 184 us, 86%); one row: about 9 us
 // of steps that wait for one another.
 #include "h32_common.cuh"
+#include "h32_epilogue.cuh"
 
 #include <float.h>
 
@@ -60,21 +61,6 @@ __device__ __forceinline__ uint64_t pair(float a, float b) {
 }
 __device__ __forceinline__ float low(uint64_t p) { return __uint_as_float(static_cast<uint32_t>(p)); }
 __device__ __forceinline__ float high(uint64_t p) { return __uint_as_float(static_cast<uint32_t>(p >> 32)); }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
 // the larger one; NaN if either is
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
@@ -208,18 +194,10 @@ __device__ __forceinline__ void rank_keys(const uint64_t *keys, int n, int top, 
     }
 }
 
-__device__ __forceinline__ uint32_t rank_in_cluster() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
-}
-__device__ __forceinline__ void sync_cluster() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 // `n` bytes (a multiple of 8) of this CTA's shared memory to the first CTA's
 template <int kThreads>
@@ -250,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
     __shared__ float s_m[kWarps], s_S[kWarps], s_W[kWarps], s_bound;
     __shared__ int s_count[2], s_chunks, s_keys;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t c = cluster_size(), rank = rank_in_cluster();
+    const uint32_t c = cluster_size(), rank = cluster_rank();
     const int64_t row = blockIdx.x / c;
     if (tid == 0) s_chunks = s_keys = 0;
     if (tid < kMaxTop) s_part[rank].best[tid] = s_best[tid] = 0;
@@ -326,8 +304,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
         // (what was summed so far, under the new maximum)
         const float top = fmaxf(m, cm);
         const float dm = fmaxf(m - top, kFar), f = exp2_fast(dm * kLog2e);
-        W2 = mul2(pair(f, f), fma2(S2, pair(dm, dm), W2));
-        S2 = mul2(S2, pair(f, f));
+        W2 = mul_f32x2(pair(f, f), fma_f32x2(S2, pair(dm, dm), W2));
+        S2 = mul_f32x2(S2, pair(f, f));
         m = top;
         const uint64_t less = pair(-m, -m);
         uint64_t s[kVecs];
@@ -336,15 +314,15 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
 #pragma unroll
             for (int i = 0; i < kN; i += 2) {
                 // (-inf and far values: e = 0, and 0 times a finite d)
-                const uint64_t x = add2(pair(v[u][i], v[u][i + 1]), less);
+                const uint64_t x = add_f32x2(pair(v[u][i], v[u][i + 1]), less);
                 const uint64_t d = pair(max_nan(low(x), kFar), max_nan(high(x), kFar));
-                const uint64_t t = mul2(d, pair(kLog2e, kLog2e));
+                const uint64_t t = mul_f32x2(d, pair(kLog2e, kLog2e));
                 const uint64_t e = pair(exp2_fast(low(t)), exp2_fast(high(t)));
-                s[u] = i == 0 ? e : add2(s[u], e);
-                W2 = fma2(e, d, W2);
+                s[u] = i == 0 ? e : add_f32x2(s[u], e);
+                W2 = fma_f32x2(e, d, W2);
             }
         static_assert(kVecs == 4, "vectors of a step");
-        S2 = add2(S2, add2(add2(s[0], s[1]), add2(s[2], s[3])));
+        S2 = add_f32x2(S2, add_f32x2(add_f32x2(s[0], s[1]), add_f32x2(s[2], s[3])));
         if (++in_run == kRun && step + 1 < step1) {
             end_run(runs++ == 0);
             in_run = 0;
@@ -482,9 +460,9 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
         rank_keys<kThreads>(s_all, keys, a.top, s_part[rank].best);
     }
     if (c > 1) {
-        sync_cluster();   // (every CTA of the cluster runs, and its part is in its shared memory)
+        cluster_sync();   // (every CTA of the cluster runs, and its part is in its shared memory)
         if (rank != 0) to_first<kThreads>(&s_part[rank], &s_part[rank], sizeof(Part));
-        sync_cluster();
+        cluster_sync();
         if (rank != 0) return;
         if (a.top > 0) {
             const int n = static_cast<int>(c) * a.top;

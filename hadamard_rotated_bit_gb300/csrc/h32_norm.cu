@@ -56,11 +56,6 @@ struct NormArgs {
 __device__ uint32_t g_norm_status;   // kStatusTimeout: a wait for a row's copy gave up
 constexpr uint64_t kDrainPolls = 1ull << 22;
 
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ uint64_t pair_f(float lo, float hi) {
     return pair_of(__float_as_uint(lo), __float_as_uint(hi));
 }
