@@ -221,7 +221,8 @@ def test_a_certain_token_over_a_wide_floor(h32, T, bf16):
 @pytest.mark.parametrize("T,V,bf16", [(267, 65600, False), (300, 70001, False), (304, 131073, True), (305, 131073, True),
                                       (121, 131072, True), (122, 131072, True), (152, 70001, False), (153, 70001, False),
                                       (1063, 40000, False), (1064, 40000, False), (1064, 131072, True),
-                                      (1064, 131080, True), (2100, 65536, False)])
+                                      (1064, 131080, True), (2100, 65536, False), (380, 70001, False), (381, 70001, False),
+                                      (1217, 12500, False), (1824, 12500, False)])
 def test_row_counts_around_the_choices_of_a_rows_ctas(h32, T, V, bf16):
     """How many CTAs a row is split over and how large they are depend on the number of rows."""
     import torch
