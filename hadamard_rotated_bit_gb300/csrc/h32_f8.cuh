@@ -1,5 +1,5 @@
-// Device and host helpers of the 8-bit floating-point products (sm_103a): swizzled
-// operand descriptors, clusters, tensor maps, the table of expert groups.
+// Device and host helpers of the 8-bit floating-point products (sm_103a): hand-overs across clusters
+// and pairs of CTAs, tensor memory, tensor maps.
 #pragma once
 
 // poll without sleeping: the waits are short and on the critical path

@@ -7,7 +7,8 @@
 // tile in TMEM, the epilogue warps read it back and fold it into registers while the
 // tensor core does the next one.
 //
-// rows_kernel, for a few tokens (or few tiles of a long K): weight rows on the TMEM lanes, NC tokens as its columns.
+// rows_kernel, for a few tokens (or few tiles of a long K): weight rows on the TMEM lanes, NC tokens as
+//   its columns.
 //   A tile is 128 weight rows (one block of scales: d_w is uniform) x NC tokens; with few
 //   tiles a cluster of CTAs shares its K steps out and adds up through shared memory.
 //   warps 0..3  epilogue, a lane quarter each
@@ -25,11 +26,12 @@
 //   Bound: of the 420 to 480 ns of a pair's K step (256 x 256 x 128; the clock depends on the power
 //   the codes draw) the tensor core needs 270; the rest is the way from its last product to the
 //   epilogue and back, which two buffers of 256 columns (all of TMEM) do not hide.  4096 x 34816 x
-//   5120: 510 to 520 us, 2810 to 2860 TFLOP/s.  (Measured and left, in an earlier form: four buffers
-//   of 128 columns, 913 us for 555, as four dependent products of 128 columns take 350 clocks instead
-//   of 256; 16 epilogue warps, scales multiplied ahead of their step, scalar folds, and loads of
-//   sums two at a time, each 5 to 100% slower; arrivals across the pair with release, twice the
-//   time; the outputs' stores are 5% of it, the first weight scales of a tile under 1%.)
+//   5120: 508 to 525 us, 2780 to 2870 TFLOP/s (back to back for more than half a second 563 to 575).
+//   (Measured and left, in an earlier form: four buffers of 128 columns, 913 us for 555, as four
+//   dependent products of 128 columns take 350 clocks instead of 256; 16 epilogue warps, scales
+//   multiplied ahead of their step, scalar folds, and loads of sums two at a time, each 5 to 100%
+//   slower; arrivals across the pair with release, twice the time; the outputs' stores are 5% of it,
+//   the first weight scales of a tile under 1%.)
 // Every wait is bounded.
 #include "h32_f8.cuh"
 

@@ -31,7 +31,7 @@ inline int rows_cluster(int64_t tiles, int64_t nb, int sms) {
 // tokens x 5120 x 8192 and 16384; 192 rows 444, so never), a tile's end about 3 us for 256
 // rows.  The narrow ones pay where they fill units that were idle (256 tokens x 8192 x 5120: 128
 // rows 29.5 us, 256 rows 33.6), and equal runs of K steps where the last wave of whole tiles is
-// long (333 x 5120 x 17408: 40 tiles on 76 pairs, 64 and 47 us; 1000 tokens 76); they cost about
+// long (333 x 5120 x 17408: 40 tiles on 76 pairs, 64 and 48 us; 1000 tokens 80); they cost about
 // 14 us (clearing the flags, two ends of tiles in turn) and 3.2 for each partial
 // sum of a tile.
 struct TilePlan {
@@ -66,7 +66,7 @@ inline TilePlan plan_tiles(int64_t chunks, int64_t N, int64_t K, int units, bool
 // Dense products of more tokens than rows_kernel has columns.  One CTA a tile up to 128 tokens, a
 // pair beyond.  Where the tiles are few and K is long, rows_kernel is faster with a tile for
 // each 32 tokens, as its clusters share K out: its steps take 430 ns of a CTA and its start 5 us
-// more than the other kernel's (128 x 783 x 8896 12.0 us, on the lanes 26.1; 64 x 5120 x 17408 36
+// more than the other kernel's (128 x 783 x 8896 12.0 us, on the lanes 26.1; 64 x 5120 x 17408 37
 // and 47; 512 x 512 x 4096 12.5 and 15.3; but 723 x 418 x 1568 12.4 and 9.2).
 inline TilePlan plan_dense(int64_t M, int64_t N, int64_t K, int sms) {
     const bool one = M <= 128;

@@ -676,6 +676,7 @@ h32_status h32_add_rms_norm_quantize(const void *x, h32_in_dtype x_dt, int64_t l
  *            of 4; entries r >= R are left untouched
  * Weights: a block is 128 rows x 128 values (at the edges what is left).
  *   w        [N][ldw] of type dt;  wq [N][K] out;  wd [ceil(N/128)][ceil(K/128)] out
+ *            (stacked weights of several experts whose rows are no multiple of 128: a call each)
  * K a multiple of 32; rows and K at most 2^31 - 257, and R (K / 32) below 2^31.
  */
 h32_status h32_quantize_act_f8(const void *x, h32_in_dtype dt, int64_t T, int64_t K, int64_t ldx,
@@ -688,7 +689,8 @@ h32_status h32_quantize_weights_f8(const void *w, h32_in_dtype dt, int64_t N, in
  * Products of e4m3 codes with a scale for each block of 128:
  *   y[m][n] = acc after acc = fma(fl(xd[b][m] * wd[n/128][b]), S_b, acc), b = 0 .. K/128,
  *   S_b = the fp32 sum of block b's products xq[m][k] * wq[n][k] (exact products; the sum's
- *   order and rounding are the tensor core's), rounded once to y's type.  Where few tiles
+ *   order and rounding are the tensor core's), rounded once to y's type.  The scales' product
+ *   is rounded by itself, so it is subnormal, 0 or infinite where it leaves fp32's range.  Where few tiles
  *   share the GPU, runs of blocks are folded apart from +0 and then added in a fixed order; which
  *   ones depends on the sizes and the device alone, so equal calls give equal bits.
  * For any M: one new token to long prompts (few tokens share one read of the weights).
