@@ -74,6 +74,20 @@ __device__ __forceinline__ bool warp_wait_cluster(uint64_t *bar, uint32_t parity
     }
     return __all_sync(0xFFFFFFFFu, ok);
 }
+// the same for what other CTAs release, as warp_wait_or_look
+__device__ __forceinline__ bool warp_wait_or_look_cluster(uint64_t *bar, uint32_t parity, uint64_t limit,
+                                                          volatile int *abort) {
+    uint32_t all;
+    asm volatile(
+        "{\n.reg .pred p, q;\nmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "vote.sync.all.pred q, p, 0xffffffff;\nselp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(all)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (all) return true;
+    if (limit == 1) return false;
+    return warp_wait_cluster(bar, parity, limit, abort);
+}
 // Arrive on another CTA's barrier, handing over tensor memory that this warp has read: its loads
 // were waited for (tcgen05.wait::ld) and fenced (tcgen05.fence::before_thread_sync), and the
 // issuer of the products that overwrite it fences behind its wait.  That pattern orders tensor

@@ -601,6 +601,12 @@ __device__ __forceinline__ void copy_codes(void *dst, const CUtensorMap *map, ui
     if constexpr (kCtas == 2) tma_load_2d_pair(dst, map, peer_smem(bar, 0), x, y);
     else tma_load_2d(dst, map, bar, x, y);
 }
+// (a pair's come from both CTAs)
+template <int kCtas>
+__device__ __forceinline__ bool wait_codes(uint64_t *bar, uint32_t parity, uint64_t limit, volatile int *abort) {
+    if constexpr (kCtas == 2) return warp_wait_or_look_cluster(bar, parity, limit, abort);
+    else return warp_wait_or_look(bar, parity, limit, abort);
+}
 // Waits until what is under way to the stages has landed, `mine` and `peer` stages being fed by
 // this CTA, which announced a stage's copies, and by the other (without one: the same).  They
 // differ by a stage ring at most, as neither goes round without the products of both; what only one
@@ -621,8 +627,9 @@ template <int kChunks, bool kSplit, int kCtas>
 __global__ void __launch_bounds__(kPairWarps * 32, 1)
     lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const F8Args a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    // s_full (in CTA 0): both CTAs' copies of a stage; s_empty: the products have read the stage; s_sum: a K step's sums are in TMEM;
-    // s_free (in CTA 0): both CTAs' epilogues have them in registers
+    // s_full (in CTA 0): both CTAs' copies of a stage; s_empty: the products have read the stage;
+    // s_sum: a K step's sums are in TMEM; s_free (in CTA 0): both CTAs' epilogues have them in
+    // registers
     using C = Lanes<kChunks, kCtas>;
     constexpr int S = C::kStages;
     constexpr uint32_t b_bytes = C::kB;
@@ -743,7 +750,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
             while (ok && work.next(total, nb)) {
 #pragma unroll 1
                 for (int kb = kSplit ? work.k0 : 0; kb < (kSplit ? work.k1 : nb); ++kb) {
-                    if (!warp_wait_or_look(&s_full[st.i], st.ph, lim, abort) ||
+                    if (!wait_codes<kCtas>(&s_full[st.i], st.ph, lim, abort) ||
                         !warp_wait_or_look(&s_free[bf.i], bf.ph, lim, abort)) {
                         ok = false;
                         break;
