@@ -10,6 +10,7 @@
 #include <stdint.h>
 
 #include "../../include/h32.h"
+#include "h32_once.h"
 
 #if defined(__CUDA_ARCH__) && (__CUDA_ARCH__ != 1030)
 #error "h32 kernels are written for sm_103a only"
@@ -59,6 +60,18 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 #endif
 
 #if defined(__CUDACC__)
+// Registers of a thread of the kernel.
+template <auto kKernel>
+cudaError_t kernel_regs(int *regs) {
+    static std::atomic<int> known{0};
+    return ask_once(known, [](int *r) {
+        cudaFuncAttributes fa{};
+        const cudaError_t e = cudaFuncGetAttributes(&fa, kKernel);
+        *r = fa.numRegs;
+        return e;
+    }, regs);
+}
+
 // Read and clear a kernel status word in one atomic step: `take` is a
 // one-thread kernel that swaps the word with 0 and leaves the old value in the
 // device word `taken`, which is then copied out.  A bit that a kernel on

@@ -8,7 +8,6 @@
 #endif
 
 #include "h32_common.cuh"
-#include "h32_once.h"
 #include "h32_tmap.cuh"
 
 #include <cuda_bf16.h>
@@ -150,18 +149,6 @@ cudaError_t allow_smem(int bytes) {
     e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     return e;
-}
-
-// Registers of a thread of the kernel.
-template <auto kKernel>
-cudaError_t kernel_regs(int *regs) {
-    static std::atomic<int> known{0};
-    return ask_once(known, [](int *r) {
-        cudaFuncAttributes fa{};
-        const cudaError_t e = cudaFuncGetAttributes(&fa, kKernel);
-        *r = fa.numRegs;
-        return e;
-    }, regs);
 }
 
 // tensor maps ----------------------------------------------------------------
